@@ -1,8 +1,9 @@
 /*
  * scan.h - C ABI of the stream_compaction_amd library (libscan_amd.so):
  * row-wise prefix scan, device-wide exclusive and inclusive scan, device-wide
- * reduction, reduce-by-key, radix sort and stream compaction on one AMD
- * Instinct MI355X (gfx950).
+ * reduction, reduce-by-key, radix sort and stream compaction, and the sequence
+ * operators built on them (causal convolution, selective scan, token
+ * embedding), on one AMD Instinct MI355X (gfx950).
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -275,6 +276,165 @@ scan_status radix_sort_devn(void* keys, void* tmp_keys, void* values, void* tmp_
 scan_status select_compact_devn(const void* in, const uint8_t* flags, void* out, int32_t* num_out,
                                 const int32_t* n_live, int64_t capacity, size_t elem_bytes,
                                 void* scratch, size_t scratch_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Sequence operators: the scan whose combine is an affine map (the selective
+ * state space scan), the short causal convolution that stands before it, and
+ * the token embedding whose gradient is a sorted segmented sum.  They share
+ * the conventions above, and:
+ *  - Activations are [batch, length, channels] of one `dtype` (SCAN_F32,
+ *    SCAN_F16 or SCAN_BF16, else SCAN_ENOTSUP) with contiguous channels;
+ *    inputs may have any non-negative batch and token strides (in elements; 0
+ *    repeats), the arrays a call writes are contiguous.  Parameters and states
+ *    of the scan are contiguous float32.  All arithmetic and every sum is
+ *    float32; each output is rounded once, to nearest even.
+ *  - Inputs may overlap one another; outputs and scratch overlap nothing
+ *    (SCAN_EALIAS), but a step may update its state in place.
+ *  - lengths: NULL, or device pointer to `batch` int32, read by the kernels and
+ *    clamped to [0, length].  Tokens at and past lengths[b] do not exist: they
+ *    are not read, their outputs and gradients are 0 and states do not move.
+ *  - 0 <= batch, length <= INT32_MAX and 1 <= channels <= 2^22.  batch == 0 is
+ *    a no-op, except that a gradient's sums over the batch are then 0;
+ *    length == 0 copies the initial state to the final one.
+ *  - Results do not depend on timing: no floating atomics, the same bits for
+ *    the same arguments.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Causal convolution along time, one filter per channel:
+ *   pre[b,t,c] = bias[c] + sum_{k < width} weight[c,k] x[b, t-width+1+k, c],
+ *   y = silu ? pre / (1 + exp(-pre)) : pre.
+ *   x              activations; x_stride = {batch, token} strides
+ *   weight, bias   float32 [channels, width] and [channels] (bias may be NULL)
+ *   initial_state  [batch, width - 1, channels] of dtype, the inputs before
+ *                  t = 0, oldest first (NULL: zeros)
+ *   width          1 .. 8 (else SCAN_ENOTSUP)
+ */
+typedef struct {
+    const void* x;
+    const float* weight;
+    const float* bias;
+    const void* initial_state;
+    const int32_t* lengths;
+    int64_t batch, length, channels, width;
+    int64_t x_stride[2];
+    int32_t silu;
+    scan_dtype dtype;
+} causal_conv_args;
+
+/* y: [batch, length, channels].  final_state: [batch, width - 1, channels], the
+ * last inputs of each sequence (NULL: not written). */
+scan_status causal_conv(const causal_conv_args* args, void* y, void* final_state, void* stream);
+
+/* Gradient: from dy (strides {batch, token}) and dfinal (of final_state's
+ * shape; NULL: zeros) to dx [batch, length, channels], dweight [channels,
+ * width] and dbias [channels] (float32; dbias may be NULL) and dinitial (of
+ * initial_state's shape; NULL: not written). */
+size_t causal_conv_grad_scratch_bytes(const causal_conv_args* args);
+scan_status causal_conv_grad(const causal_conv_args* args, const void* dy,
+                             const int64_t* dy_stride, const void* dfinal, void* dx,
+                             float* dweight, float* dbias, void* dinitial, void* scratch,
+                             size_t scratch_bytes, void* stream);
+
+/* One token per sequence: x is [batch, channels] (x_stride[0] between rows;
+ * args->length, lengths and initial_state are not used).  state and new_state
+ * are [batch, width - 1, channels] and either the same array or disjoint; y is
+ * [batch, channels]. */
+scan_status causal_conv_step(const causal_conv_args* args, const void* state, void* new_state,
+                             void* y, void* stream);
+
+/*
+ * Selective scan: with `states` states per channel, and channel c using row
+ * g = c / (channels / groups) of B and C,
+ *   s[b,t,c] = dt[b,t,c] + dt_bias[c], through softplus when asked
+ *   h[b,t,c,n] = exp(s A[c,n]) h[b,t-1,c,n] + s x[b,t,c] B[b,t,g,n]
+ *   y[b,t,c] = (sum_n C[b,t,g,n] h[b,t,c,n] + D[c] x) * silu(z[b,t,c]).
+ *   x, dt, z       activations (z may be NULL: no gate)
+ *   B, C           [batch, length, groups, states] of dtype, states contiguous;
+ *                  strides {batch, token, group}
+ *   A              float32 [channels, states]
+ *   D, dt_bias     float32 [channels] (each may be NULL)
+ *   initial_state  float32 [batch, channels, states] (NULL: zeros)
+ *   states         1 .. 64 (else SCAN_ENOTSUP); groups divides channels
+ */
+typedef struct {
+    const void* x;
+    const void* dt;
+    const void* B;
+    const void* C;
+    const void* z;
+    const float* A;
+    const float* D;
+    const float* dt_bias;
+    const float* initial_state;
+    const int32_t* lengths;
+    int64_t batch, length, channels, states, groups;
+    int64_t x_stride[2], dt_stride[2], z_stride[2], B_stride[3], C_stride[3];
+    int32_t softplus;
+    scan_dtype dtype;
+} selective_scan_args;
+
+/* y: [batch, length, channels].  final_state: float32 [batch, channels, states]
+ * (NULL: not written).  starts (NULL: not written): what the gradient needs,
+ * selective_scan_starts_bytes(length, ...) bytes, the states before each block
+ * of tokens. */
+size_t selective_scan_starts_bytes(const selective_scan_args* args);
+scan_status selective_scan(const selective_scan_args* args, void* y, float* final_state,
+                           float* starts, void* stream);
+
+/* Gradients of a forward call with the same args that wrote `starts`, from dy
+ * (strides {batch, token}) and dfinal (of final_state's shape; NULL: zeros).
+ * dx, ddt [batch, length, channels] and dB, dC [batch, length, groups, states]
+ * of dtype, dz of dtype (required exactly when z is given), dA float32
+ * [channels, states]; dD, ddt_bias (float32 [channels]) and dinitial (float32
+ * [batch, channels, states]) are not written when NULL. */
+typedef struct {
+    const void* dy;
+    int64_t dy_stride[2];
+    const float* dfinal;
+    const float* starts;
+    void* dx;
+    void* ddt;
+    void* dB;
+    void* dC;
+    void* dz;
+    float* dA;
+    float* dD;
+    float* ddt_bias;
+    float* dinitial;
+} selective_scan_grads;
+size_t selective_scan_grad_scratch_bytes(const selective_scan_args* args);
+scan_status selective_scan_grad(const selective_scan_args* args, const selective_scan_grads* grads,
+                                void* scratch, size_t scratch_bytes, void* stream);
+
+/* One token per sequence: x, dt, z are [batch, channels] and B, C [batch,
+ * groups, states] (token strides, length, lengths and initial_state are not
+ * used).  state and new_state are float32 [batch, channels, states] and either
+ * the same array or disjoint; y is [batch, channels]. */
+scan_status selective_scan_step(const selective_scan_args* args, const float* state,
+                                float* new_state, void* y, void* stream);
+
+/*
+ * Token embedding: out[i,:] = scale * weight[ids[i],:]; an id outside [0, rows)
+ * is a masked token, whose output is 0.
+ *   weight     [rows, channels] of dtype, row_stride elements between rows
+ *   ids        `tokens` int32 (id_dtype SCAN_I32) or int64 (SCAN_I64)
+ *   out        [tokens, channels] of dtype
+ *   1 <= rows <= INT32_MAX, 0 <= tokens <= INT32_MAX
+ */
+scan_status embedding(const void* weight, const void* ids, void* out, int64_t tokens, int64_t rows,
+                      int64_t channels, int64_t row_stride, scan_dtype dtype, scan_dtype id_dtype,
+                      float scale, void* stream);
+
+/* Its gradient: dweight[v,:] = scale * the sum of dout[i,:] over the tokens with
+ * ids[i] = v, in token order within fixed segments of the sorted tokens; every
+ * row is written.  dout: [tokens, channels] of dtype, row_stride elements
+ * between rows; dweight: [rows, channels] of out_dtype (dtype or SCAN_F32). */
+size_t embedding_grad_scratch_bytes(int64_t tokens, int64_t rows, int64_t channels);
+scan_status embedding_grad(const void* dout, const void* ids, void* dweight, int64_t tokens,
+                           int64_t rows, int64_t channels, int64_t row_stride, scan_dtype dtype,
+                           scan_dtype id_dtype, scan_dtype out_dtype, float scale, void* scratch,
+                           size_t scratch_bytes, void* stream);
 
 /* Static string naming a status code (never NULL). */
 const char* scan_status_str(scan_status s);

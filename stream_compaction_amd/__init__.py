@@ -34,6 +34,11 @@ Entry points (same names as the C ABI):
   capacity.  Python wrappers: ``scan_device(..., n_live=t)`` and likewise.
 * ``scan_device_scratch_bytes(n, dtype)``, ``reduce_device_scratch_bytes(n,
   dtype)``, ``reduce_by_key_scratch_bytes(n)``, ``select_compact_scratch_bytes(n)``.
+
+Sequence operators (module ``sequence``, reached by the same names from here; each
+described there): ``causal_conv``, ``causal_conv_grad``, ``causal_conv_step``,
+``selective_scan``, ``selective_scan_grad``, ``selective_scan_step``, ``embedding``,
+``embedding_grad``; module ``autograd`` has the differentiable forms.
 """
 import ctypes
 import os
@@ -51,8 +56,15 @@ EXPORTS = ("scan_rows", "scan_device", "scan_device_inclusive", "scan_device_scr
            "reduce_by_key_scratch_bytes", "radix_sort", "radix_sort_scratch_bytes",
            "select_compact", "select_compact_scratch_bytes", "scan_device_devn",
            "scan_device_inclusive_devn", "reduce_device_devn", "reduce_by_key_devn",
-           "radix_sort_devn", "select_compact_devn", "scan_device_noalloc", "scan_status_str",
+           "radix_sort_devn", "select_compact_devn", "scan_device_noalloc", "causal_conv",
+           "causal_conv_grad", "causal_conv_grad_scratch_bytes", "causal_conv_step",
+           "selective_scan", "selective_scan_starts_bytes", "selective_scan_grad",
+           "selective_scan_grad_scratch_bytes", "selective_scan_step", "embedding",
+           "embedding_grad", "embedding_grad_scratch_bytes", "scan_status_str",
            "scan_last_hip_error")
+# entry points whose wrappers live in the module `sequence`, loaded on first use
+_SEQUENCE = ("causal_conv", "causal_conv_grad", "causal_conv_step", "selective_scan",
+             "selective_scan_grad", "selective_scan_step", "embedding", "embedding_grad")
 
 _lib = None
 
@@ -111,11 +123,21 @@ def load(path):
     L.radix_sort_devn.restype = i32
     L.select_compact_devn.argtypes = [vp, vp, vp, vp, vp, i64, sz, vp, sz, vp]
     L.select_compact_devn.restype = i32
+    from ._sequence_abi import declare
+    declare(L)
     L.scan_status_str.argtypes = [i32]
     L.scan_status_str.restype = ctypes.c_char_p
     L.scan_last_hip_error.argtypes = []
     L.scan_last_hip_error.restype = i32
     return L
+
+
+def __getattr__(name):
+    if name in _SEQUENCE:
+        from . import sequence
+        globals()[name] = getattr(sequence, name)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def check(status):

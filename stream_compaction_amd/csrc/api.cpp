@@ -4,7 +4,11 @@
 
 #include <hip/hip_runtime.h>
 
+#include "api_common.hpp"
 #include "launch.hpp"
+
+using sca::api::aligned;
+using sca::api::hip_status;
 
 namespace {
 
@@ -41,8 +45,6 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return x < y + nb && y < x + na;
 }
 
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
 size_t round16(size_t b) { return (b + 15) & ~(size_t)15; }
 
 // The device count of the *_devn entry points: present, 4-byte aligned and
@@ -56,15 +58,15 @@ scan_status devn_check(const int32_t* n_dev, const void* const* written, const s
   return SCAN_OK;
 }
 
-scan_status hip_status(hipError_t e) {
+constexpr int64_t kMaxN = 2147483647;  // INT32_MAX
+
+}  // namespace
+
+scan_status sca::api::hip_status(hipError_t e) {
   if (e == hipSuccess) return SCAN_OK;
   g_last_hip_error = (int)e;
   return SCAN_EHIP;
 }
-
-constexpr int64_t kMaxN = 2147483647;  // INT32_MAX
-
-}  // namespace
 
 extern "C" {
 

@@ -1,0 +1,446 @@
+// Short causal convolution along time, one filter per channel:
+//   pre[t] = bias + sum_{k < W} w[k] x[t - W + 1 + k],   y = silu(pre) or pre,
+// its gradient, and its step for one token.  Tokens before the first come from
+// an initial state of W - 1 tokens (or are zero); tokens at and past a
+// sequence's length do not exist (their outputs are zero).
+//
+// All three are bound by memory: 2 W operations per element against 4 bytes.
+// A lane owns E neighbouring channels (one load of up to 16 bytes per token)
+// and walks T tokens with the last W inputs in registers, so each input is
+// read once but for the W - 1 tokens before a run.
+#include "sequence.hpp"
+
+namespace sca {
+
+namespace {
+
+__device__ __forceinline__ int64_t conv_length(const ConvProblem& p, int64_t b) {
+  if (p.lengths == nullptr) return p.length;
+  const int64_t v = p.lengths[b];
+  return v < 0 ? 0 : (v > p.length ? p.length : v);
+}
+
+// The filters of E channels, channel c's tap k in w[k][c].
+template <int E, int W>
+__device__ __forceinline__ void load_filters(const ConvProblem& p, int64_t ch, int64_t n,
+                                             float (&w)[W][E], float (&bias)[E]) {
+#pragma unroll
+  for (int c = 0; c < E; ++c) {
+#pragma unroll
+    for (int k = 0; k < W; ++k) w[k][c] = c < n ? p.weight[(ch + c) * W + k] : 0.0f;
+    bias[c] = c < n && p.bias != nullptr ? p.bias[ch + c] : 0.0f;
+  }
+}
+
+// Input token t of sequence b: the initial state before 0, zero past `len`.
+template <class F, int E, int W>
+__device__ __forceinline__ typename RowIO<F, E>::Raw conv_input(const ConvProblem& p, int64_t b,
+                                                               int64_t t, int64_t len, int64_t ch,
+                                                               int64_t n, bool vec) {
+  using S = typename F::S;
+  const S* src = nullptr;
+  if (t >= 0) {
+    if (t < len) src = (const S*)p.x + b * p.x_batch + t * p.x_token + ch;
+  } else if (p.initial_state != nullptr) {
+    src = (const S*)p.initial_state + (b * (W - 1) + t + W - 1) * p.channels + ch;
+  }
+  if (src == nullptr) return typename RowIO<F, E>::Raw{};
+  return RowIO<F, E>::load(src, n, vec);
+}
+
+}  // namespace
+
+constexpr int kConvRun = 16;      // tokens per lane
+constexpr int kConvAhead = 4;     // token rows loaded together
+
+template <class F, int E, int W>
+__global__ __launch_bounds__(256) void causal_conv_kernel(ConvProblem p, void* yv,
+                                                         void* final_state) {
+  using S = typename F::S;
+  using IO = RowIO<F, E>;
+  constexpr bool vec = E > 1;
+  const int64_t vecs = (p.channels + E - 1) / E;
+  const int64_t runs = p.length > 0 ? (p.length + kConvRun - 1) / kConvRun : 1;
+  const int64_t total = p.batch * runs * vecs;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * 256) {
+    const int64_t ch = i % vecs * E, run = i / vecs % runs, b = i / vecs / runs;
+    const int64_t n = p.channels - ch;
+    const int64_t len = conv_length(p, b);
+    const int64_t t0 = run * kConvRun;
+    const int64_t end = t0 + kConvRun < p.length ? t0 + kConvRun : p.length;
+    S* y = (S*)yv + b * p.length * p.channels + ch;
+    float w[W][E], bias[E], win[W][E];
+    load_filters<E, W>(p, ch, n, w, bias);
+#pragma unroll
+    for (int k = 0; k + 1 < W; ++k)
+      IO::unpack(conv_input<F, E, W>(p, b, t0 - W + 1 + k, len, ch, n, vec), win[k + 1]);
+    for (int64_t t = t0; t < end; t += kConvAhead) {
+      typename IO::Raw raw[kConvAhead];
+#pragma unroll
+      for (int j = 0; j < kConvAhead; ++j)
+        raw[j] = conv_input<F, E, W>(p, b, t + j, len, ch, n, vec);
+#pragma unroll
+      for (int j = 0; j < kConvAhead; ++j) {
+#pragma unroll
+        for (int k = 0; k + 1 < W; ++k)
+#pragma unroll
+          for (int c = 0; c < E; ++c) win[k][c] = win[k + 1][c];
+        IO::unpack(raw[j], win[W - 1]);
+        float out[E];
+#pragma unroll
+        for (int c = 0; c < E; ++c) {
+          float a = bias[c];
+#pragma unroll
+          for (int k = 0; k < W; ++k) a = __builtin_fmaf(w[k][c], win[k][c], a);
+          if (p.silu) a = silu(a);
+          out[c] = t + j < len ? a : 0.0f;
+        }
+        if (t + j < end) IO::store(y + (t + j) * p.channels, IO::pack(out), n, vec);
+      }
+    }
+    if (run == 0 && final_state != nullptr) {
+      S* fs = (S*)final_state + b * (W - 1) * p.channels + ch;
+#pragma unroll
+      for (int k = 0; k + 1 < W; ++k)
+        IO::store(fs + k * p.channels,
+                  conv_input<F, E, W>(p, b, len - W + 1 + k, len, ch, n, vec), n, vec);
+    }
+  }
+}
+
+// Gradient.  With g = dy * slope(pre), dx[t] = sum_k w[k] g[t + W - 1 - k]: a
+// lane recomputes g for its run and the W - 1 tokens after it.  Filter sums
+// over a run stay in registers; the four waves of a workgroup (four runs of
+// the same channels) add theirs in LDS, and a second kernel adds the
+// workgroups' sums in a fixed order, so results are the same every time.
+constexpr int kConvGradRun = 16;
+constexpr int kConvGradWaves = 4;
+
+// Gradients with respect to the final state reach line token t (x for t >= 0,
+// the initial state for t < 0) when t is among the last W - 1 before len.
+template <class F, int E, int W>
+__device__ __forceinline__ void add_final(const ConvProblem& p, const void* dfinal, int64_t b,
+                                          int64_t t, int64_t len, int64_t ch, int64_t n, bool vec,
+                                          float (&d)[E]) {
+  using S = typename F::S;
+  const int64_t j = t - len + W - 1;
+  if (dfinal == nullptr || j < 0 || j >= W - 1) return;
+  float v[E];
+  RowIO<F, E>::unpack(
+      RowIO<F, E>::load((const S*)dfinal + (b * (W - 1) + j) * p.channels + ch, n, vec), v);
+#pragma unroll
+  for (int c = 0; c < E; ++c) d[c] += v[c];
+}
+
+template <class F, int E, int W>
+__global__ __launch_bounds__(64 * kConvGradWaves) void causal_conv_grad_kernel(
+    ConvProblem p, const void* dyv, int64_t dy_batch, int64_t dy_token, const void* dfinal,
+    void* dxv, void* dinitial, float* part) {
+  using S = typename F::S;
+  using IO = RowIO<F, E>;
+  constexpr bool vec = E > 1;
+  constexpr int M = W + 1;                          // sums per channel
+  __shared__ float s_sum[kConvGradWaves][E * M][64];
+  const int lane = lane_id(), wave = wave_id();
+  const int64_t vecs = (p.channels + E - 1) / E, cols = (vecs + 63) / 64;
+  const int64_t runs = p.length > 0 ? (p.length + kConvGradRun - 1) / kConvGradRun : 1;
+  const int64_t total = p.batch * runs;             // runs of all sequences
+  const int64_t col = blockIdx.x % cols, set = blockIdx.x / cols;
+  const int64_t sets = gridDim.x / cols;
+  const int64_t ch = (col * 64 + lane) * E;
+  const int64_t n = p.channels - ch;                // may be <= 0: a lane past the last channel
+  float w[W][E], bias[E], dw[W][E] = {}, db[E] = {};
+  load_filters<E, W>(p, ch, n, w, bias);
+  for (int64_t r = set * kConvGradWaves + wave; r < total; r += sets * kConvGradWaves) {
+    if (n <= 0) break;
+    const int64_t b = r / runs, t0 = r % runs * kConvGradRun;
+    const int64_t len = conv_length(p, b);
+    const int64_t end = t0 + kConvGradRun < p.length ? t0 + kConvGradRun : p.length;
+    const S* dy = (const S*)dyv + b * dy_batch + ch;
+    S* dx = (S*)dxv + b * p.length * p.channels + ch;
+    float win[W][E], g[W][E] = {};                  // inputs and gradients, newest last
+#pragma unroll
+    for (int k = 0; k + 1 < W; ++k)
+      IO::unpack(conv_input<F, E, W>(p, b, t0 - W + 1 + k, len, ch, n, vec), win[k + 1]);
+    constexpr int STEPS = kConvGradRun + W - 1;
+    for (int s0 = 0; s0 < STEPS; s0 += kConvAhead) {
+      typename IO::Raw rx[kConvAhead], rdy[kConvAhead];
+#pragma unroll
+      for (int j = 0; j < kConvAhead; ++j) {
+        const int64_t t = t0 + s0 + j;
+        rx[j] = conv_input<F, E, W>(p, b, t, len, ch, n, vec);
+        rdy[j] = t < len ? IO::load(dy + t * dy_token, n, vec) : typename IO::Raw{};
+      }
+#pragma unroll
+      for (int j = 0; j < kConvAhead; ++j) {
+        const int64_t t = t0 + s0 + j;
+#pragma unroll
+        for (int k = 0; k + 1 < W; ++k)
+#pragma unroll
+          for (int c = 0; c < E; ++c) {
+            win[k][c] = win[k + 1][c];
+            g[k][c] = g[k + 1][c];
+          }
+        IO::unpack(rx[j], win[W - 1]);
+        IO::unpack(rdy[j], g[W - 1]);
+        if (p.silu) {
+#pragma unroll
+          for (int c = 0; c < E; ++c) {
+            float a = bias[c];
+#pragma unroll
+            for (int k = 0; k < W; ++k) a = __builtin_fmaf(w[k][c], win[k][c], a);
+            g[W - 1][c] = t < len ? g[W - 1][c] * silu_slope(a) : 0.0f;
+          }
+        }
+        if (s0 + j < kConvGradRun) {                 // the run's own tokens
+#pragma unroll
+          for (int c = 0; c < E; ++c) {
+            db[c] += g[W - 1][c];
+#pragma unroll
+            for (int k = 0; k < W; ++k) dw[k][c] = __builtin_fmaf(g[W - 1][c], win[k][c], dw[k][c]);
+          }
+        }
+        // line token t - W + 1 now has all its gradients
+        const int64_t u = t - W + 1;
+        if (u < end && (u >= t0 || (t0 == 0 && dinitial != nullptr))) {
+          float d[E];
+#pragma unroll
+          for (int c = 0; c < E; ++c) {
+            d[c] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < W; ++k) d[c] = __builtin_fmaf(w[k][c], g[W - 1 - k][c], d[c]);
+          }
+          add_final<F, E, W>(p, dfinal, b, u, len, ch, n, vec, d);
+          S* to = u >= 0 ? dx + u * p.channels
+                         : (S*)dinitial + (b * (W - 1) + u + W - 1) * p.channels + ch;
+          if (u < len) {
+            IO::store(to, IO::pack(d), n, vec);
+          } else {
+            IO::store(to, typename IO::Raw{}, n, vec);
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < E; ++c) {
+#pragma unroll
+    for (int k = 0; k < W; ++k) s_sum[wave][c * M + k][lane] = dw[k][c];
+    s_sum[wave][c * M + W][lane] = db[c];
+  }
+  __syncthreads();
+  // channel-major sums of this workgroup: [set][channel][M]
+  for (int i = threadIdx.x; i < 64 * E * M; i += 64 * kConvGradWaves) {
+    const int l = i / (E * M), m = i % (E * M);
+    const int64_t c = (col * 64 + l) * E + m / M;
+    if (c >= p.channels) continue;
+    float v = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kConvGradWaves; ++q) v += s_sum[q][m][l];
+    part[set * p.channels * M + c * M + m % M] = v;
+  }
+}
+
+// dweight and dbias from the workgroups' sums, in the order of the sets: 64
+// values per workgroup, four strided partial sums each.
+__global__ __launch_bounds__(256) void conv_filter_sum_kernel(const float* part, int64_t sets,
+                                                             int64_t count, int M, float* dweight,
+                                                             float* dbias) {
+  __shared__ float s[4][64];
+  const int l = threadIdx.x % 64, q = threadIdx.x / 64;
+  const int64_t i = (int64_t)blockIdx.x * 64 + l;
+  float v = 0.0f;
+  if (i < count)
+    for (int64_t k = q; k < sets; k += 4) v += part[k * count + i];
+  s[q][l] = v;
+  __syncthreads();
+  if (q != 0 || i >= count) return;
+  v = (s[0][l] + s[1][l]) + (s[2][l] + s[3][l]);
+  const int64_t c = i / M;
+  const int m = (int)(i % M);
+  if (m + 1 < M) {
+    dweight[c * (M - 1) + m] = v;
+  } else if (dbias != nullptr) {
+    dbias[c] = v;
+  }
+}
+
+// One token: the state's W - 1 rows and the new input, each read once.
+template <class F, int E, int W>
+__global__ __launch_bounds__(256) void causal_conv_step_kernel(ConvProblem p, const void* state,
+                                                              void* new_state, void* yv) {
+  using S = typename F::S;
+  using IO = RowIO<F, E>;
+  constexpr bool vec = E > 1;
+  const int64_t vecs = (p.channels + E - 1) / E;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= p.batch * vecs) return;
+  const int64_t ch = i % vecs * E, b = i / vecs, n = p.channels - ch;
+  float w[W][E], bias[E], a[E];
+  typename IO::Raw row[W];
+#pragma unroll
+  for (int k = 0; k + 1 < W; ++k)
+    row[k] = IO::load((const S*)state + (b * (W - 1) + k) * p.channels + ch, n, vec);
+  row[W - 1] = IO::load((const S*)p.x + b * p.x_batch + ch, n, vec);
+  load_filters<E, W>(p, ch, n, w, bias);
+#pragma unroll
+  for (int c = 0; c < E; ++c) a[c] = bias[c];
+#pragma unroll
+  for (int k = 0; k < W; ++k) {
+    float v[E];
+    IO::unpack(row[k], v);
+#pragma unroll
+    for (int c = 0; c < E; ++c) a[c] = __builtin_fmaf(w[k][c], v[c], a[c]);
+  }
+  if (p.silu) {
+#pragma unroll
+    for (int c = 0; c < E; ++c) a[c] = silu(a[c]);
+  }
+  IO::store((S*)yv + b * p.channels + ch, IO::pack(a), n, vec);
+#pragma unroll
+  for (int k = 0; k + 1 < W; ++k)
+    IO::store((S*)new_state + (b * (W - 1) + k) * p.channels + ch, row[k + 1], n, vec);
+}
+
+// Vectors of E channels can be used when every row starts on E elements.
+template <class F> static bool rows_aligned(int E, int64_t channels, const void* a, int64_t s0 = 0,
+                                            int64_t s1 = 0) {
+  const int64_t bytes = (int64_t)E * (int64_t)sizeof(typename F::S);
+  return a == nullptr || ((uintptr_t)a % bytes == 0 && channels % E == 0 && s0 % E == 0 &&
+                          s1 % E == 0);
+}
+
+constexpr int64_t kGridMost = 1 << 20;              // workgroups; kernels loop beyond it
+
+template <class F, int E, int W>
+static void fwd_go(const ConvProblem& p, void* y, void* final_state, hipStream_t stream) {
+  const int64_t runs = p.length > 0 ? (p.length + kConvRun - 1) / kConvRun : 1;
+  const int64_t blocks = (p.batch * runs * ((p.channels + E - 1) / E) + 255) / 256;
+  causal_conv_kernel<F, E, W><<<dim3((unsigned)(blocks < kGridMost ? blocks : kGridMost)),
+                                dim3(256), 0, stream>>>(p, y, final_state);
+}
+template <class F, int W>
+static hipError_t fwd_w(const ConvProblem& p, void* y, void* fs, hipStream_t stream) {
+  constexpr int E = kVecElems<F>;
+  if (rows_aligned<F>(E, p.channels, p.x, p.x_batch, p.x_token) && rows_aligned<F>(E, p.channels, y) &&
+      rows_aligned<F>(E, p.channels, fs) && rows_aligned<F>(E, p.channels, p.initial_state)) {
+    fwd_go<F, E, W>(p, y, fs, stream);
+  } else {
+    fwd_go<F, 1, W>(p, y, fs, stream);
+  }
+  return hipGetLastError();
+}
+
+static int64_t grad_sets(const ConvProblem& p) {
+  const int64_t per = p.length > 0 ? (p.length + kConvGradRun - 1) / kConvGradRun : 1;
+  const int64_t runs = per * p.batch;
+  const int64_t sets = (runs + kConvGradWaves - 1) / kConvGradWaves;
+  // at most 1024 partial sums per channel, and a grid of at most 2^22 workgroups
+  const int64_t cols = (p.channels + 63) / 64, most = (1ll << 22) / cols;
+  const int64_t cap = most < 1024 ? most : 1024;
+  return sets < cap ? sets : cap;
+}
+size_t conv_grad_scratch(const ConvProblem& p) {
+  return (size_t)(grad_sets(p) * p.channels * (p.width + 1)) * 4;
+}
+
+template <class F, int W>
+static hipError_t grad_w(const ConvProblem& p, const void* dy, int64_t dy_batch, int64_t dy_token,
+                         const void* dfinal, void* dx, float* dweight, float* dbias,
+                         void* dinitial, void* scratch, hipStream_t stream) {
+  // four channels per lane: eight would hold 5 * 8 * W values in registers
+  constexpr int E = 4;
+  const int64_t sets = grad_sets(p);
+  float* part = (float*)scratch;
+  auto cols = [&](int e) { return ((p.channels + e - 1) / e + 63) / 64; };
+  if (sets == 0) {
+    // no sequence: the filter sums below are zero
+  } else if (rows_aligned<F>(E, p.channels, p.x, p.x_batch, p.x_token) &&
+      rows_aligned<F>(E, p.channels, dy, dy_batch, dy_token) &&
+      rows_aligned<F>(E, p.channels, dx) && rows_aligned<F>(E, p.channels, dinitial) &&
+      rows_aligned<F>(E, p.channels, dfinal) && rows_aligned<F>(E, p.channels, p.initial_state)) {
+    causal_conv_grad_kernel<F, E, W><<<dim3((unsigned)(sets * cols(E))), dim3(64 * kConvGradWaves),
+                                       0, stream>>>(p, dy, dy_batch, dy_token, dfinal, dx, dinitial,
+                                                    part);
+  } else {
+    causal_conv_grad_kernel<F, 1, W><<<dim3((unsigned)(sets * cols(1))), dim3(64 * kConvGradWaves),
+                                       0, stream>>>(p, dy, dy_batch, dy_token, dfinal, dx, dinitial,
+                                                    part);
+  }
+  const int64_t count = p.channels * (W + 1);
+  conv_filter_sum_kernel<<<dim3((unsigned)((count + 63) / 64)), dim3(256), 0, stream>>>(
+      part, sets, count, W + 1, dweight, dbias);
+  return hipGetLastError();
+}
+
+template <class F, int W>
+static hipError_t step_w(const ConvProblem& p, const void* state, void* new_state, void* y,
+                         hipStream_t stream) {
+  constexpr int E = kVecElems<F>;
+  if (rows_aligned<F>(E, p.channels, p.x, p.x_batch) && rows_aligned<F>(E, p.channels, y) &&
+      rows_aligned<F>(E, p.channels, state) && rows_aligned<F>(E, p.channels, new_state)) {
+    const int64_t blocks = (p.batch * (p.channels / E) + 255) / 256;
+    causal_conv_step_kernel<F, E, W><<<dim3((unsigned)blocks), dim3(256), 0, stream>>>(
+        p, state, new_state, y);
+  } else {
+    const int64_t blocks = (p.batch * p.channels + 255) / 256;
+    causal_conv_step_kernel<F, 1, W><<<dim3((unsigned)blocks), dim3(256), 0, stream>>>(
+        p, state, new_state, y);
+  }
+  return hipGetLastError();
+}
+
+// Calls fn with the format and the filter width as constants.
+template <class Fn> static hipError_t by_width(int64_t width, Fn&& fn) {
+  switch (width) {
+    case 1: return fn(std::integral_constant<int, 1>{});
+    case 2: return fn(std::integral_constant<int, 2>{});
+    case 3: return fn(std::integral_constant<int, 3>{});
+    case 4: return fn(std::integral_constant<int, 4>{});
+    case 5: return fn(std::integral_constant<int, 5>{});
+    case 6: return fn(std::integral_constant<int, 6>{});
+    case 7: return fn(std::integral_constant<int, 7>{});
+    case 8: return fn(std::integral_constant<int, 8>{});
+    default: return hipErrorInvalidValue;
+  }
+}
+template <class Fn> static hipError_t by_format(Fmt fmt, Fn&& fn) {
+  switch (fmt) {
+    case Fmt::F32: return fn(FmtF32{});
+    case Fmt::F16: return fn(FmtF16{});
+    case Fmt::BF16: return fn(FmtBF16{});
+    default: return hipErrorInvalidValue;
+  }
+}
+
+hipError_t launch_conv(const ConvProblem& p, Fmt fmt, void* y, void* final_state,
+                       hipStream_t stream) {
+  return by_format(fmt, [&](auto f) {
+    return by_width(p.width, [&](auto w) {
+      return fwd_w<decltype(f), decltype(w)::value>(p, y, final_state, stream);
+    });
+  });
+}
+
+hipError_t launch_conv_grad(const ConvProblem& p, Fmt fmt, const void* dy, int64_t dy_batch,
+                            int64_t dy_token, const void* dfinal, void* dx, float* dweight,
+                            float* dbias, void* dinitial, void* scratch, hipStream_t stream) {
+  return by_format(fmt, [&](auto f) {
+    return by_width(p.width, [&](auto w) {
+      return grad_w<decltype(f), decltype(w)::value>(p, dy, dy_batch, dy_token, dfinal, dx, dweight,
+                                                     dbias, dinitial, scratch, stream);
+    });
+  });
+}
+
+hipError_t launch_conv_step(const ConvProblem& p, Fmt fmt, const void* state, void* new_state,
+                            void* y, hipStream_t stream) {
+  return by_format(fmt, [&](auto f) {
+    return by_width(p.width, [&](auto w) {
+      return step_w<decltype(f), decltype(w)::value>(p, state, new_state, y, stream);
+    });
+  });
+}
+
+}  // namespace sca

@@ -55,6 +55,66 @@ hipError_t launch_select(const void* in, const uint8_t* flags, void* out, int32_
                          int64_t n, size_t elem_bytes, void* scratch, hipStream_t stream,
                          const int32_t* n_dev = nullptr);
 
+// ---- sequence operators (f32 / f16 / bf16 activations; see scan.h) ----
+// Strides count elements; the last axis of every array is contiguous and the
+// arrays a call writes are contiguous throughout.
+struct ConvProblem {
+  const void* x;
+  const float* weight;              // [channels, width]
+  const float* bias;                // [channels] or null
+  const void* initial_state;        // [batch, width - 1, channels] or null (zeros)
+  const int32_t* lengths;           // [batch] or null (all tokens exist)
+  int64_t batch, length, channels, width;
+  int64_t x_batch, x_token;
+  bool silu;
+};
+hipError_t launch_conv(const ConvProblem& p, Fmt fmt, void* y, void* final_state,
+                       hipStream_t stream);
+size_t conv_grad_scratch(const ConvProblem& p);
+hipError_t launch_conv_grad(const ConvProblem& p, Fmt fmt, const void* dy, int64_t dy_batch,
+                            int64_t dy_token, const void* dfinal, void* dx, float* dweight,
+                            float* dbias, void* dinitial, void* scratch, hipStream_t stream);
+hipError_t launch_conv_step(const ConvProblem& p, Fmt fmt, const void* state, void* new_state,
+                            void* y, hipStream_t stream);
+
+struct ScanProblem {
+  const void *x, *dt, *B, *C, *z;   // z may be null
+  const float *A, *D, *dt_bias;     // [channels, states], [channels] or null (both)
+  const float* initial_state;       // [batch, channels, states] or null (zeros)
+  const int32_t* lengths;           // [batch] or null
+  int64_t batch, length, channels, states, groups;
+  int64_t x_batch, x_token, dt_batch, dt_token, z_batch, z_token;
+  int64_t B_batch, B_token, B_group, C_batch, C_token, C_group;
+  bool softplus;
+};
+// Tokens per block: the forward keeps the states at the start of every block
+// for the gradient.
+int64_t scan_block_tokens(int64_t length, Fmt fmt);
+hipError_t launch_selective_scan(const ScanProblem& p, Fmt fmt, void* y, float* final_state,
+                                 float* starts, hipStream_t stream);
+struct ScanGrads {
+  const void* dy;
+  int64_t dy_batch, dy_token;
+  const float* dfinal;              // [batch, channels, states] or null
+  const float* starts;
+  void *dx, *ddt, *dB, *dC, *dz;    // dz null without z
+  float *dA, *dD, *ddt_bias, *dinitial;   // any of the last three may be null
+};
+size_t selective_scan_grad_scratch(const ScanProblem& p, Fmt fmt);
+hipError_t launch_selective_scan_grad(const ScanProblem& p, Fmt fmt, const ScanGrads& g,
+                                      void* scratch, hipStream_t stream);
+hipError_t launch_selective_scan_step(const ScanProblem& p, Fmt fmt, const float* state,
+                                      float* new_state, void* y, hipStream_t stream);
+
+hipError_t launch_embedding(const void* weight, const void* ids, bool wide_ids, void* out,
+                            int64_t tokens, int64_t rows, int64_t channels, int64_t row_stride,
+                            Fmt fmt, float scale, hipStream_t stream);
+size_t embedding_grad_scratch(int64_t tokens, int64_t rows, int64_t channels);
+hipError_t launch_embedding_grad(const void* dout, const void* ids, bool wide_ids, void* dweight,
+                                 int64_t tokens, int64_t rows, int64_t channels,
+                                 int64_t row_stride, Fmt fmt, Fmt out_fmt, float scale,
+                                 void* scratch, hipStream_t stream);
+
 // Scratch of the look-back kernels holds only the tile descriptors, one per
 // 128-byte line (kDescBytes), whose used words are zeroed at the start of
 // every call by a small fill kernel (no hipMemsetAsync, so the call can sit

@@ -1,0 +1,137 @@
+// Shared by the sequence kernels (causal convolution, selective scan,
+// embedding): problem descriptions as the kernels take them, strided loads of
+// 16-byte vectors, and the elementwise functions of a gated state space layer.
+#pragma once
+
+#include "device.hpp"
+#include "launch.hpp"
+
+namespace sca {
+
+// The combine type is float everywhere here: activations widen exactly,
+// parameters and states are float32, and each output is rounded once.
+template <class F> constexpr int kVecElems = 16 / (int)sizeof(typename F::S);
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// 2^v with the hardware instruction (1 ulp; results below 2^-126 flush to 0,
+// which a decay factor that small may do).
+__device__ __forceinline__ float exp2_hw(float v) { return __builtin_amdgcn_exp2f(v); }
+__device__ __forceinline__ float rcp_hw(float v) { return __builtin_amdgcn_rcpf(v); }
+
+// sigmoid(v); v -> -inf gives rcp(inf) = 0, v -> inf gives 1.
+__device__ __forceinline__ float sigmoid(float v) { return rcp_hw(1.0f + exp2_hw(-v * kLog2e)); }
+// silu(v) = v sigmoid(v).  Below -104 the sigmoid underflows (v = -inf would
+// give -inf * 0): there the limit, a signed zero, is returned.
+__device__ __forceinline__ float silu(float v) { return v < -104.0f ? -0.0f : v * sigmoid(v); }
+// d silu / dv = s (1 + v (1 - s)), with the same limits at the two ends.
+__device__ __forceinline__ float silu_slope(float v) {
+  const float s = sigmoid(v);
+  const float r = s * (1.0f + v * (1.0f - s));
+  return v < -104.0f ? 0.0f : (v > 104.0f ? 1.0f : r);
+}
+
+// softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|) in (0, 1].  The steps of
+// a state space layer are small (1e-3 to 1e-1), where log(1 + e) rounded
+// through 1 + e would keep few digits, so it is taken as 2 atanh(s) with
+// s = e / (2 + e) <= 1/3: of the odd series (1 + q/3 + q^2/5 + ..., q = s^2)
+// the terms past q^7/15 add less than 2e-9, well under float32's half step.
+__device__ __forceinline__ float softplus(float v) {
+  const float e = exp2_hw(-__builtin_fabsf(v) * kLog2e);
+  const float s = e * rcp_hw(2.0f + e);
+  const float q = s * s;
+  float p = 1.0f / 15.0f;
+  p = __builtin_fmaf(p, q, 1.0f / 13.0f);
+  p = __builtin_fmaf(p, q, 1.0f / 11.0f);
+  p = __builtin_fmaf(p, q, 1.0f / 9.0f);
+  p = __builtin_fmaf(p, q, 1.0f / 7.0f);
+  p = __builtin_fmaf(p, q, 1.0f / 5.0f);
+  p = __builtin_fmaf(p, q, 1.0f / 3.0f);
+  p = __builtin_fmaf(p, q, 1.0f);
+  const float r = __builtin_fmaf(2.0f * s, p, v > 0.0f ? v : 0.0f);
+  return v != v ? v : r;
+}
+
+// The E = 16 / sizeof(S) elements at `p` whose count `n` (may exceed E) exist;
+// the others read as zero bits.  vec: p is 16-byte aligned.
+template <class F>
+__device__ __forceinline__ uint4 load_vec(const typename F::S* p, int64_t n, bool vec) {
+  constexpr int E = kVecElems<F>;
+  if (vec && n >= E) return __builtin_bit_cast(uint4, *gptr<const u32x4>((uintptr_t)p));
+  typename F::S e[E] = {};
+#pragma unroll
+  for (int k = 0; k < E; ++k)
+    if (k < n) e[k] = *gptr<const typename F::S>((uintptr_t)(p + k));
+  return __builtin_bit_cast(uint4, e);
+}
+
+// Stores the first n elements of r.
+template <class F>
+__device__ __forceinline__ void store_vec(typename F::S* p, uint4 r, int64_t n, bool vec) {
+  constexpr int E = kVecElems<F>;
+  if (vec && n >= E) {
+    *gptr<u32x4>((uintptr_t)p) = __builtin_bit_cast(u32x4, r);
+    return;
+  }
+  struct Elems { typename F::S e[E]; };
+  const Elems s = __builtin_bit_cast(Elems, r);
+#pragma unroll
+  for (int k = 0; k < E; ++k)
+    if (k < n) *gptr<typename F::S>((uintptr_t)(p + k)) = s.e[k];
+}
+
+// E consecutive elements as one load or store of 2 to 16 bytes (`vec`: p is
+// aligned to that), or one by one.  `n` of them exist: others read as zero.
+template <class F, int E> struct RowIO {
+  using S = typename F::S;
+  struct Elems { S e[E]; };
+  typedef uint32_t vec2 __attribute__((ext_vector_type(2)));
+  using Raw = std::conditional_t<sizeof(Elems) == 16, u32x4,
+              std::conditional_t<sizeof(Elems) == 8, vec2,
+              std::conditional_t<sizeof(Elems) == 4, uint32_t, uint16_t>>>;
+  static __device__ __forceinline__ Raw load(const S* p, int64_t n, bool vec) {
+    if (vec && n >= E) return *gptr<const Raw>((uintptr_t)p);
+    Elems s = {};
+#pragma unroll
+    for (int k = 0; k < E; ++k)
+      if (k < n) s.e[k] = *gptr<const S>((uintptr_t)(p + k));
+    return __builtin_bit_cast(Raw, s);
+  }
+  static __device__ __forceinline__ void unpack(Raw r, float (&x)[E]) {
+    const Elems s = __builtin_bit_cast(Elems, r);
+#pragma unroll
+    for (int k = 0; k < E; ++k) x[k] = widen<F>(s.e[k]);
+  }
+  static __device__ __forceinline__ Raw pack(const float (&x)[E]) {
+    Elems s;
+#pragma unroll
+    for (int k = 0; k < E; ++k) s.e[k] = narrow<F>(x[k]);
+    return __builtin_bit_cast(Raw, s);
+  }
+  static __device__ __forceinline__ void store(S* p, Raw r, int64_t n, bool vec) {
+    if (vec && n >= E) {
+      *gptr<Raw>((uintptr_t)p) = r;
+      return;
+    }
+    const Elems s = __builtin_bit_cast(Elems, r);
+#pragma unroll
+    for (int k = 0; k < E; ++k)
+      if (k < n) *gptr<S>((uintptr_t)(p + k)) = s.e[k];
+  }
+};
+
+// Sum over the 64 lanes, the same value in every lane of the wave.
+__device__ __forceinline__ float wave_sum(float v) {
+  return readlane(wave_scan_incl<Op::Add>(v), kWave - 1);
+}
+
+// Logical workgroup index: hardware deals consecutive workgroups to the 8
+// XCDs in turn, each with its own L2, so neighbours in the logical order
+// (which share cache lines of the activations) are put on one XCD.
+__device__ __forceinline__ uint32_t xcd_order(uint32_t bid, uint32_t count) {
+  constexpr uint32_t X = 8;
+  const uint32_t per = count / X, rem = count % X, x = bid % X, i = bid / X;
+  return x < rem ? x * (per + 1) + i : rem * (per + 1) + (x - rem) * per + i;
+}
+
+}  // namespace sca

@@ -1,0 +1,308 @@
+"""Sequence operators of the library: causal convolution, selective scan and token
+embedding, each with its gradient, and the first two with their single-token step.
+
+Thin wrappers over the C ABI (``include/scan.h`` has every definition and rule): they
+check shapes and types, allocate what is not given, and pass pointers, strides and the
+current HIP stream.  Activations are ``[batch, length, channels]`` float32, float16 or
+bfloat16 tensors with contiguous channels; parameters and the scan's states are float32.
+``stream_compaction_amd.autograd`` has the same operators for torch's automatic
+differentiation.
+"""
+import ctypes
+
+import torch
+
+from . import DTYPE_CODES, _stream, check, lib
+from ._sequence_abi import ConvArgs, ScanArgs, ScanGrads
+
+_ACT = {torch.float32: DTYPE_CODES["f32"], torch.float16: DTYPE_CODES["f16"],
+        torch.bfloat16: DTYPE_CODES["bf16"]}
+_IDS = {torch.int32: DTYPE_CODES["i32"], torch.int64: DTYPE_CODES["i64"]}
+
+_i64 = ctypes.c_int64
+
+
+def _require(ok, message):
+    if not ok:
+        raise ValueError(message)
+
+
+def _code(x, what):
+    if x.dtype not in _ACT:
+        raise NotImplementedError(f"{what}: dtype {x.dtype} is not supported")
+    return _ACT[x.dtype]
+
+
+def _like(t, what, shape, dtype, device):
+    """Pointer of a contiguous tensor of this shape, type and device."""
+    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+    return t.data_ptr()
+
+
+def _opt(t, what, shape, dtype, device):
+    return None if t is None else _like(t, what, shape, dtype, device)
+
+
+def _out(t, what, shape, dtype, device):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _like(t, what, shape, dtype, device)
+    return t
+
+
+def _rows(t, what, shape, dtype, device):
+    """An activation tensor: shape, type, device, contiguous last axis."""
+    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{what} must be a {dtype} tensor of shape {shape} on {device}")
+    if shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{what} must have a contiguous last axis")
+    return t.data_ptr()
+
+
+def _scratch(scratch, need, device):
+    if scratch is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    if scratch.dtype != torch.uint8 or scratch.device != device or not scratch.is_contiguous():
+        raise ValueError("scratch must be a contiguous uint8 tensor on the data's device")
+    return scratch
+
+
+def _conv_args(x, weight, bias, initial_state, lengths, silu, step):
+    if x.dim() != (2 if step else 3):
+        raise ValueError("x must be [batch, channels]" if step else
+                         "x must be [batch, length, channels]")
+    _require(x.is_cuda, "x must be a GPU tensor")
+    code = _code(x, "x")
+    b, d, dev = x.shape[0], x.shape[-1], x.device
+    _require(weight.dim() == 2, "weight must be [channels, width]")
+    w = weight.shape[1]
+    a = ConvArgs()
+    a.x = _rows(x, "x", tuple(x.shape), x.dtype, dev)
+    a.weight = _like(weight, "weight", (d, w), torch.float32, dev)
+    a.bias = _opt(bias, "bias", (d,), torch.float32, dev)
+    a.initial_state = _opt(initial_state, "initial_state", (b, w - 1, d), x.dtype, dev)
+    a.lengths = _opt(lengths, "lengths", (b,), torch.int32, dev)
+    a.batch, a.length, a.channels, a.width = b, 1 if step else x.shape[1], d, w
+    a.x_stride[:] = x.stride()[:2] if not step else (x.stride(0), 0)
+    a.silu, a.dtype = int(bool(silu)), code
+    return a
+
+
+def causal_conv(x, weight, bias=None, initial_state=None, lengths=None, silu=True, out=None,
+                final_state=None, stream=None):
+    """Causal convolution of ``x`` along time, one filter ``weight[channel]`` (float32
+    ``[channels, width]``, width 1 to 8) per channel, then ``silu`` when asked.
+
+    ``initial_state`` (``[batch, width - 1, channels]``) holds the inputs before the first
+    token; ``lengths`` (int32 ``[batch]``) the tokens of each sequence that exist.  Returns
+    ``(y, final_state)``: the second is the next call's initial state.
+    """
+    a = _conv_args(x, weight, bias, initial_state, lengths, silu, False)
+    y = _out(out, "out", tuple(x.shape), x.dtype, x.device)
+    fs = _out(final_state, "final_state", (a.batch, a.width - 1, a.channels), x.dtype, x.device)
+    check(lib().causal_conv(a, y.data_ptr(), fs.data_ptr(), _stream(stream)))
+    return y, fs
+
+
+def causal_conv_grad(dy, x, weight, bias=None, initial_state=None, lengths=None, silu=True,
+                     dfinal=None, scratch=None, stream=None):
+    """Gradients of ``causal_conv`` from ``dy`` (and ``dfinal``, of the final state): a dict
+    with ``dx``, ``dweight``, ``dbias`` and ``dstate`` (of the initial state; both None when
+    that input is)."""
+    a = _conv_args(x, weight, bias, initial_state, lengths, silu, False)
+    dev, state = x.device, (a.batch, a.width - 1, a.channels)
+    dyp = _rows(dy, "dy", tuple(x.shape), x.dtype, dev)
+    df = _opt(dfinal, "dfinal", state, x.dtype, dev)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    dw = torch.empty(weight.shape, dtype=torch.float32, device=dev)
+    db = None if bias is None else torch.empty(bias.shape, dtype=torch.float32, device=dev)
+    ds = None if initial_state is None else torch.empty(state, dtype=x.dtype, device=dev)
+    L = lib()
+    scratch = _scratch(scratch, L.causal_conv_grad_scratch_bytes(a), dev)
+    check(L.causal_conv_grad(a, dyp, (_i64 * 2)(*dy.stride()[:2]), df, dx.data_ptr(),
+                             dw.data_ptr(), None if db is None else db.data_ptr(),
+                             None if ds is None else ds.data_ptr(), scratch.data_ptr(),
+                             scratch.numel(), _stream(stream)))
+    return {"dx": dx, "dweight": dw, "dbias": db, "dstate": ds}
+
+
+def causal_conv_step(state, x, weight, bias=None, silu=True, new_state=None, out=None,
+                     stream=None):
+    """One token of ``causal_conv``: ``x`` is ``[batch, channels]`` and ``state`` the last
+    ``width - 1`` inputs, replaced by those that include ``x`` (in place, or into
+    ``new_state``).  Returns ``y``."""
+    a = _conv_args(x, weight, bias, None, None, silu, True)
+    shape = (a.batch, a.width - 1, a.channels)
+    sp = _like(state, "state", shape, x.dtype, x.device)
+    np_ = sp if new_state is None else _like(new_state, "new_state", shape, x.dtype, x.device)
+    y = _out(out, "out", tuple(x.shape), x.dtype, x.device)
+    check(lib().causal_conv_step(a, sp, np_, y.data_ptr(), _stream(stream)))
+    return y
+
+
+def _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, lengths, step):
+    if x.dim() != (2 if step else 3):
+        raise ValueError("x must be [batch, channels]" if step else
+                         "x must be [batch, length, channels]")
+    _require(x.is_cuda, "x must be a GPU tensor")
+    code = _code(x, "x")
+    dev, ty = x.device, x.dtype
+    shape = tuple(x.shape)
+    b, d = shape[0], shape[-1]
+    _require(A.dim() == 2, "A must be [channels, states]")
+    n = A.shape[1]
+    _require(B.dim() == x.dim() + 1, "B must be [batch, length, groups, states] (a step: "
+                                     "[batch, groups, states])")
+    rows = shape[:-1] + (B.shape[-2], n)
+    a = ScanArgs()
+    a.x = _rows(x, "x", shape, ty, dev)
+    a.dt = _rows(dt, "dt", shape, ty, dev)
+    a.B = _rows(B, "B", rows, ty, dev)
+    a.C = _rows(C, "C", rows, ty, dev)
+    a.A = _like(A, "A", (d, n), torch.float32, dev)
+    a.D = _opt(D, "D", (d,), torch.float32, dev)
+    a.dt_bias = _opt(dt_bias, "dt_bias", (d,), torch.float32, dev)
+    a.initial_state = _opt(initial_state, "initial_state", (b, d, n), torch.float32, dev)
+    a.lengths = _opt(lengths, "lengths", (b,), torch.int32, dev)
+    a.batch, a.length, a.channels = b, 1 if step else shape[1], d
+    a.states, a.groups = n, B.shape[-2]
+    if step:
+        a.x_stride[0], a.dt_stride[0] = x.stride(0), dt.stride(0)
+        a.B_stride[:] = (B.stride(0), 0, B.stride(1))
+        a.C_stride[:] = (C.stride(0), 0, C.stride(1))
+    else:
+        a.x_stride[:], a.dt_stride[:] = x.stride()[:2], dt.stride()[:2]
+        a.B_stride[:], a.C_stride[:] = B.stride()[:3], C.stride()[:3]
+    if z is not None:
+        a.z = _rows(z, "z", shape, ty, dev)
+        a.z_stride[:] = (z.stride(0), 0) if step else z.stride()[:2]
+    a.softplus, a.dtype = int(bool(softplus)), code
+    return a
+
+
+def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=False,
+                   initial_state=None, lengths=None, keep_starts=False, out=None,
+                   final_state=None, stream=None):
+    """Selective state space scan.
+
+    ``x``, ``dt`` and the gate ``z`` are ``[batch, length, channels]``, ``B`` and ``C``
+    ``[batch, length, groups, states]`` (channel ``c`` uses group ``c // (channels //
+    groups)``), ``A`` float32 ``[channels, states]`` (1 to 64 states), ``D`` and ``dt_bias``
+    float32 ``[channels]``.  Per channel, ``s = dt + dt_bias`` (through softplus when asked),
+    ``h = exp(s A) h + s x B`` and ``y = (C . h + D x) silu(z)``.
+
+    Returns ``(y, final_state)``, the state float32 ``[batch, channels, states]``; with
+    ``keep_starts`` also what ``selective_scan_grad`` needs of this call.
+    """
+    a = _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, lengths, False)
+    y = _out(out, "out", tuple(x.shape), x.dtype, x.device)
+    fs = _out(final_state, "final_state", (a.batch, a.channels, a.states), torch.float32, x.device)
+    L = lib()
+    if not keep_starts:
+        check(L.selective_scan(a, y.data_ptr(), fs.data_ptr(), None, _stream(stream)))
+        return y, fs
+    starts = torch.empty(L.selective_scan_starts_bytes(a) // 4, dtype=torch.float32,
+                         device=x.device)
+    check(L.selective_scan(a, y.data_ptr(), fs.data_ptr(), starts.data_ptr(), _stream(stream)))
+    return y, fs, starts
+
+
+def selective_scan_grad(dy, x, dt, A, B, C, starts, D=None, z=None, dt_bias=None, softplus=False,
+                        lengths=None, dfinal=None, scratch=None, stream=None):
+    """Gradients of ``selective_scan`` called with the same arguments and ``keep_starts``,
+    from ``dy`` (and ``dfinal``, of the final state): a dict with ``dx``, ``ddt``, ``dA``,
+    ``dB``, ``dC``, ``dD``, ``dz``, ``ddt_bias`` (None where that input is) and ``dstate``
+    (of the initial state)."""
+    a = _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, None, lengths, False)
+    dev, ty, f32 = x.device, x.dtype, torch.float32
+    state = (a.batch, a.channels, a.states)
+    L = lib()
+    g = ScanGrads()
+    g.dy = _rows(dy, "dy", tuple(x.shape), ty, dev)
+    g.dy_stride[:] = dy.stride()[:2]
+    g.dfinal = _opt(dfinal, "dfinal", state, f32, dev)
+    g.starts = _like(starts, "starts", (L.selective_scan_starts_bytes(a) // 4,), f32, dev)
+    out = {"dx": torch.empty(x.shape, dtype=ty, device=dev),
+           "ddt": torch.empty(x.shape, dtype=ty, device=dev),
+           "dA": torch.empty(A.shape, dtype=f32, device=dev),
+           "dB": torch.empty(B.shape, dtype=ty, device=dev),
+           "dC": torch.empty(B.shape, dtype=ty, device=dev),
+           "dD": None if D is None else torch.empty(D.shape, dtype=f32, device=dev),
+           "dz": None if z is None else torch.empty(x.shape, dtype=ty, device=dev),
+           "ddt_bias": None if dt_bias is None else torch.empty(dt_bias.shape, dtype=f32,
+                                                                device=dev),
+           "dstate": torch.empty(state, dtype=f32, device=dev)}
+    g.dx, g.ddt, g.dA = out["dx"].data_ptr(), out["ddt"].data_ptr(), out["dA"].data_ptr()
+    g.dB, g.dC, g.dinitial = out["dB"].data_ptr(), out["dC"].data_ptr(), out["dstate"].data_ptr()
+    for name in ("dD", "dz", "ddt_bias"):
+        if out[name] is not None:
+            setattr(g, name, out[name].data_ptr())
+    scratch = _scratch(scratch, L.selective_scan_grad_scratch_bytes(a), dev)
+    check(L.selective_scan_grad(a, g, scratch.data_ptr(), scratch.numel(), _stream(stream)))
+    return out
+
+
+def selective_scan_step(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=False,
+                        new_state=None, out=None, stream=None):
+    """One token of ``selective_scan``: ``x``, ``dt``, ``z`` are ``[batch, channels]``, ``B``
+    and ``C`` ``[batch, groups, states]``; ``state`` (float32 ``[batch, channels, states]``)
+    moves on in place, or into ``new_state``.  Returns ``y``."""
+    a = _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, None, None, True)
+    shape = (a.batch, a.channels, a.states)
+    sp = _like(state, "state", shape, torch.float32, x.device)
+    np_ = sp if new_state is None else _like(new_state, "new_state", shape, torch.float32, x.device)
+    y = _out(out, "out", tuple(x.shape), x.dtype, x.device)
+    check(lib().selective_scan_step(a, sp, np_, y.data_ptr(), _stream(stream)))
+    return y
+
+
+def _table(t, what):
+    """A [rows, channels] tensor with contiguous channels: its type code and row stride."""
+    _require(t.dim() == 2 and t.is_cuda, f"{what} must be a 2-D GPU tensor")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    return _code(t, what), t.stride(0)
+
+
+def _id_code(ids, device):
+    if ids.dtype not in _IDS:
+        raise NotImplementedError(f"ids: dtype {ids.dtype} is not supported")
+    if ids.device != device or not ids.is_contiguous():
+        raise ValueError(f"ids must be a contiguous tensor on {device}")
+    return _IDS[ids.dtype]
+
+
+def embedding(weight, ids, scale=1.0, out=None, stream=None):
+    """``scale * weight[ids]`` for int32 or int64 ``ids`` of any shape; ids outside the table
+    are masked tokens and give zeros.  Returns ``[*ids.shape, channels]`` in weight's type."""
+    code, stride = _table(weight, "weight")
+    idc = _id_code(ids, weight.device)
+    rows, d = weight.shape
+    out = _out(out, "out", tuple(ids.shape) + (d,), weight.dtype, weight.device)
+    check(lib().embedding(weight.data_ptr(), ids.data_ptr(), out.data_ptr(), ids.numel(), rows, d,
+                          stride, code, idc, float(scale), _stream(stream)))
+    return out
+
+
+def embedding_grad(dout, ids, rows, scale=1.0, dtype=None, out=None, scratch=None, stream=None):
+    """Gradient of ``embedding``'s table: ``[rows, channels]`` in ``dtype`` (dout's, or
+    float32), row ``v`` being ``scale`` times the sum of ``dout`` over the tokens with id
+    ``v``; masked tokens add nothing.  The same bits every time."""
+    d = dout.shape[-1]
+    if dout.shape[:-1] != ids.shape:
+        raise ValueError("dout must be [*ids.shape, channels]")
+    flat = dout.view(-1, d) if dout.dim() != 2 else dout
+    code, stride = _table(flat, "dout")
+    idc = _id_code(ids, dout.device)
+    dtype = dtype or (out.dtype if out is not None else dout.dtype)
+    if dtype not in (dout.dtype, torch.float32):
+        raise NotImplementedError("the gradient is of dout's type or float32")
+    out = _out(out, "out", (int(rows), d), dtype, dout.device)
+    L = lib()
+    n = ids.numel()
+    scratch = _scratch(scratch, L.embedding_grad_scratch_bytes(n, rows, d), dout.device)
+    check(L.embedding_grad(flat.data_ptr(), ids.data_ptr(), out.data_ptr(), n, rows, d, stride,
+                           code, idc, _ACT[dtype], float(scale), scratch.data_ptr(),
+                           scratch.numel(), _stream(stream)))
+    return out
