@@ -20,15 +20,36 @@ __device__ __forceinline__ int64_t conv_length(const ConvProblem& p, int64_t b) 
   return v < 0 ? 0 : (v > p.length ? p.length : v);
 }
 
-// The filters of E channels, channel c's tap k in w[k][c].
+// The filters of E channels, channel c's tap k in w[k][c].  E W consecutive
+// floats (the lane's channels all exist when E > 1), 16 bytes at a time where
+// the arrays are aligned: one by one they cost more than a run's input.
 template <int E, int W>
-__device__ __forceinline__ void load_filters(const ConvProblem& p, int64_t ch, int64_t n,
-                                             float (&w)[W][E], float (&bias)[E]) {
+__device__ __forceinline__ void load_filters(const ConvProblem& p, int64_t ch, float (&w)[W][E],
+                                             float (&bias)[E]) {
+  const bool wide = E > 1 && (((uintptr_t)p.weight | (uintptr_t)p.bias) % 16 == 0);
+  typedef float vec4 __attribute__((ext_vector_type(4)));
+  if (wide) {
+#pragma unroll
+    for (int j = 0; j < E * W; j += 4) {
+      const vec4 v = *gptr<const vec4>((uintptr_t)(p.weight + ch * W + j));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[(j + i) % W][(j + i) / W] = v[i];
+    }
+#pragma unroll
+    for (int j = 0; j < E; j += 4) {
+      vec4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (p.bias != nullptr) v = *gptr<const vec4>((uintptr_t)(p.bias + ch + j));
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (j + i < E) bias[j + i] = v[i];
+    }
+    return;
+  }
 #pragma unroll
   for (int c = 0; c < E; ++c) {
 #pragma unroll
-    for (int k = 0; k < W; ++k) w[k][c] = c < n ? p.weight[(ch + c) * W + k] : 0.0f;
-    bias[c] = c < n && p.bias != nullptr ? p.bias[ch + c] : 0.0f;
+    for (int k = 0; k < W; ++k) w[k][c] = p.weight[(ch + c) * W + k];
+    bias[c] = p.bias != nullptr ? p.bias[ch + c] : 0.0f;
   }
 }
 
@@ -50,55 +71,69 @@ __device__ __forceinline__ typename RowIO<F, E>::Raw conv_input(const ConvProble
 
 }  // namespace
 
-constexpr int kConvRun = 16;      // tokens per lane
 constexpr int kConvAhead = 4;     // token rows loaded together
 
 template <class F, int E, int W>
 __global__ __launch_bounds__(256) void causal_conv_kernel(ConvProblem p, void* yv,
-                                                         void* final_state) {
+                                                         void* final_state, int run_tokens) {
   using S = typename F::S;
   using IO = RowIO<F, E>;
   constexpr bool vec = E > 1;
   const int64_t vecs = (p.channels + E - 1) / E;
-  const int64_t runs = p.length > 0 ? (p.length + kConvRun - 1) / kConvRun : 1;
+  const int64_t runs = p.length > 0 ? (p.length + run_tokens - 1) / run_tokens : 1;
   const int64_t total = p.batch * runs * vecs;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * 256) {
-    const int64_t ch = i % vecs * E, run = i / vecs % runs, b = i / vecs / runs;
+    int64_t ch, run;
+    const int64_t b = divide(divide(i, vecs, &ch), runs, &run);
+    ch *= E;
     const int64_t n = p.channels - ch;
     const int64_t len = conv_length(p, b);
-    const int64_t t0 = run * kConvRun;
-    const int64_t end = t0 + kConvRun < p.length ? t0 + kConvRun : p.length;
+    const int64_t t0 = run * run_tokens;
+    const int64_t end = t0 + run_tokens < p.length ? t0 + run_tokens : p.length;
+    const int64_t last = end < len ? end : len;        // tokens of the run that exist
+    const S* x = (const S*)p.x + b * p.x_batch + ch;
     S* y = (S*)yv + b * p.length * p.channels + ch;
-    float w[W][E], bias[E], win[W][E];
-    load_filters<E, W>(p, ch, n, w, bias);
+    int64_t t = t0;
+    if (t < last) {
+      auto row = [&](int64_t at) {
+        return at < last ? IO::load(x + at * p.x_token, n, vec) : typename IO::Raw{};
+      };
+      typename IO::Raw next[kConvAhead];
 #pragma unroll
-    for (int k = 0; k + 1 < W; ++k)
-      IO::unpack(conv_input<F, E, W>(p, b, t0 - W + 1 + k, len, ch, n, vec), win[k + 1]);
-    for (int64_t t = t0; t < end; t += kConvAhead) {
-      typename IO::Raw raw[kConvAhead];
+      for (int j = 0; j < kConvAhead; ++j) next[j] = row(t + j);
+      float w[W][E], bias[E], win[W][E];
+      load_filters<E, W>(p, ch, w, bias);
 #pragma unroll
-      for (int j = 0; j < kConvAhead; ++j)
-        raw[j] = conv_input<F, E, W>(p, b, t + j, len, ch, n, vec);
+      for (int k = 0; k + 1 < W; ++k)
+        IO::unpack(conv_input<F, E, W>(p, b, t0 - W + 1 + k, len, ch, n, vec), win[k + 1]);
+      for (; t < last; t += kConvAhead) {
+        typename IO::Raw raw[kConvAhead];
 #pragma unroll
-      for (int j = 0; j < kConvAhead; ++j) {
+        for (int j = 0; j < kConvAhead; ++j) raw[j] = next[j];
 #pragma unroll
-        for (int k = 0; k + 1 < W; ++k)
+        for (int j = 0; j < kConvAhead; ++j) next[j] = row(t + kConvAhead + j);
 #pragma unroll
-          for (int c = 0; c < E; ++c) win[k][c] = win[k + 1][c];
-        IO::unpack(raw[j], win[W - 1]);
-        float out[E];
+        for (int j = 0; j < kConvAhead; ++j) {
 #pragma unroll
-        for (int c = 0; c < E; ++c) {
-          float a = bias[c];
+          for (int k = 0; k + 1 < W; ++k)
 #pragma unroll
-          for (int k = 0; k < W; ++k) a = __builtin_fmaf(w[k][c], win[k][c], a);
-          if (p.silu) a = silu(a);
-          out[c] = t + j < len ? a : 0.0f;
+            for (int c = 0; c < E; ++c) win[k][c] = win[k + 1][c];
+          IO::unpack(raw[j], win[W - 1]);
+          float out[E];
+#pragma unroll
+          for (int c = 0; c < E; ++c) {
+            float a = bias[c];
+#pragma unroll
+            for (int k = 0; k < W; ++k) a = __builtin_fmaf(w[k][c], win[k][c], a);
+            out[c] = p.silu ? silu(a) : a;
+          }
+          if (t + j < last) IO::store(y + (t + j) * p.channels, IO::pack(out), n, vec);
         }
-        if (t + j < end) IO::store(y + (t + j) * p.channels, IO::pack(out), n, vec);
       }
+      t = last;
     }
+    for (; t < end; ++t) IO::store(y + t * p.channels, typename IO::Raw{}, n, vec);
     if (run == 0 && final_state != nullptr) {
       S* fs = (S*)final_state + b * (W - 1) * p.channels + ch;
 #pragma unroll
@@ -114,7 +149,6 @@ __global__ __launch_bounds__(256) void causal_conv_kernel(ConvProblem p, void* y
 // over a run stay in registers; the four waves of a workgroup (four runs of
 // the same channels) add theirs in LDS, and a second kernel adds the
 // workgroups' sums in a fixed order, so results are the same every time.
-constexpr int kConvGradRun = 16;
 constexpr int kConvGradWaves = 4;
 
 // Gradients with respect to the final state reach line token t (x for t >= 0,
@@ -136,7 +170,7 @@ __device__ __forceinline__ void add_final(const ConvProblem& p, const void* dfin
 template <class F, int E, int W>
 __global__ __launch_bounds__(64 * kConvGradWaves) void causal_conv_grad_kernel(
     ConvProblem p, const void* dyv, int64_t dy_batch, int64_t dy_token, const void* dfinal,
-    void* dxv, void* dinitial, float* part) {
+    void* dxv, void* dinitial, float* part, int run_tokens) {
   using S = typename F::S;
   using IO = RowIO<F, E>;
   constexpr bool vec = E > 1;
@@ -144,27 +178,29 @@ __global__ __launch_bounds__(64 * kConvGradWaves) void causal_conv_grad_kernel(
   __shared__ float s_sum[kConvGradWaves][E * M][64];
   const int lane = lane_id(), wave = wave_id();
   const int64_t vecs = (p.channels + E - 1) / E, cols = (vecs + 63) / 64;
-  const int64_t runs = p.length > 0 ? (p.length + kConvGradRun - 1) / kConvGradRun : 1;
+  const int64_t runs = p.length > 0 ? (p.length + run_tokens - 1) / run_tokens : 1;
   const int64_t total = p.batch * runs;             // runs of all sequences
   const int64_t col = blockIdx.x % cols, set = blockIdx.x / cols;
   const int64_t sets = gridDim.x / cols;
   const int64_t ch = (col * 64 + lane) * E;
   const int64_t n = p.channels - ch;                // may be <= 0: a lane past the last channel
   float w[W][E], bias[E], dw[W][E] = {}, db[E] = {};
-  load_filters<E, W>(p, ch, n, w, bias);
+  if (n > 0) load_filters<E, W>(p, ch, w, bias);
   for (int64_t r = set * kConvGradWaves + wave; r < total; r += sets * kConvGradWaves) {
     if (n <= 0) break;
-    const int64_t b = r / runs, t0 = r % runs * kConvGradRun;
+    int64_t t0;
+    const int64_t b = divide(r, runs, &t0);
+    t0 *= run_tokens;
     const int64_t len = conv_length(p, b);
-    const int64_t end = t0 + kConvGradRun < p.length ? t0 + kConvGradRun : p.length;
+    const int64_t end = t0 + run_tokens < p.length ? t0 + run_tokens : p.length;
     const S* dy = (const S*)dyv + b * dy_batch + ch;
     S* dx = (S*)dxv + b * p.length * p.channels + ch;
     float win[W][E], g[W][E] = {};                  // inputs and gradients, newest last
 #pragma unroll
     for (int k = 0; k + 1 < W; ++k)
       IO::unpack(conv_input<F, E, W>(p, b, t0 - W + 1 + k, len, ch, n, vec), win[k + 1]);
-    constexpr int STEPS = kConvGradRun + W - 1;
-    for (int s0 = 0; s0 < STEPS; s0 += kConvAhead) {
+    const int steps = run_tokens + W - 1;
+    for (int s0 = 0; s0 < steps; s0 += kConvAhead) {
       typename IO::Raw rx[kConvAhead], rdy[kConvAhead];
 #pragma unroll
       for (int j = 0; j < kConvAhead; ++j) {
@@ -193,7 +229,7 @@ __global__ __launch_bounds__(64 * kConvGradWaves) void causal_conv_grad_kernel(
             g[W - 1][c] = t < len ? g[W - 1][c] * silu_slope(a) : 0.0f;
           }
         }
-        if (s0 + j < kConvGradRun) {                 // the run's own tokens
+        if (s0 + j < run_tokens) {                 // the run's own tokens
 #pragma unroll
           for (int c = 0; c < E; ++c) {
             db[c] += g[W - 1][c];
@@ -242,21 +278,24 @@ __global__ __launch_bounds__(64 * kConvGradWaves) void causal_conv_grad_kernel(
   }
 }
 
-// dweight and dbias from the workgroups' sums, in the order of the sets: 64
-// values per workgroup, four strided partial sums each.
-__global__ __launch_bounds__(256) void conv_filter_sum_kernel(const float* part, int64_t sets,
-                                                             int64_t count, int M, float* dweight,
-                                                             float* dbias) {
-  __shared__ float s[4][64];
+// dweight and dbias from the workgroups' sums, in a fixed order: 64 values per
+// workgroup, 16 strided partial sums each, whose loads travel four at a time.
+constexpr int kSumStrands = 16;
+__global__ __launch_bounds__(64 * kSumStrands) void conv_filter_sum_kernel(
+    const float* part, int64_t sets, int64_t count, int M, float* dweight, float* dbias) {
+  __shared__ float s[kSumStrands][64];
   const int l = threadIdx.x % 64, q = threadIdx.x / 64;
   const int64_t i = (int64_t)blockIdx.x * 64 + l;
   float v = 0.0f;
-  if (i < count)
-    for (int64_t k = q; k < sets; k += 4) v += part[k * count + i];
+  if (i < count) {
+#pragma unroll 4
+    for (int64_t k = q; k < sets; k += kSumStrands) v += part[k * count + i];
+  }
   s[q][l] = v;
   __syncthreads();
   if (q != 0 || i >= count) return;
-  v = (s[0][l] + s[1][l]) + (s[2][l] + s[3][l]);
+#pragma unroll
+  for (int k = 1; k < kSumStrands; ++k) v += s[k][l];
   const int64_t c = i / M;
   const int m = (int)(i % M);
   if (m + 1 < M) {
@@ -276,14 +315,17 @@ __global__ __launch_bounds__(256) void causal_conv_step_kernel(ConvProblem p, co
   const int64_t vecs = (p.channels + E - 1) / E;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= p.batch * vecs) return;
-  const int64_t ch = i % vecs * E, b = i / vecs, n = p.channels - ch;
+  int64_t ch;
+  const int64_t b = divide(i, vecs, &ch);
+  ch *= E;
+  const int64_t n = p.channels - ch;
   float w[W][E], bias[E], a[E];
   typename IO::Raw row[W];
 #pragma unroll
   for (int k = 0; k + 1 < W; ++k)
     row[k] = IO::load((const S*)state + (b * (W - 1) + k) * p.channels + ch, n, vec);
   row[W - 1] = IO::load((const S*)p.x + b * p.x_batch + ch, n, vec);
-  load_filters<E, W>(p, ch, n, w, bias);
+  load_filters<E, W>(p, ch, w, bias);
 #pragma unroll
   for (int c = 0; c < E; ++c) a[c] = bias[c];
 #pragma unroll
@@ -313,12 +355,22 @@ template <class F> static bool rows_aligned(int E, int64_t channels, const void*
 
 constexpr int64_t kGridMost = 1 << 20;              // workgroups; kernels loop beyond it
 
+// Tokens a lane walks: a longer run reads fewer rows and filters twice, as long
+// as it leaves enough workgroups.
+static int conv_run(const ConvProblem& p, int E, int64_t most, int64_t workgroups) {
+  const int64_t lanes = p.batch * ((p.channels + E - 1) / E);
+  int run = (int)most;
+  while (run > 4 && lanes * ((p.length + run - 1) / run) < workgroups * 256) run /= 2;
+  return run;
+}
+
 template <class F, int E, int W>
 static void fwd_go(const ConvProblem& p, void* y, void* final_state, hipStream_t stream) {
-  const int64_t runs = p.length > 0 ? (p.length + kConvRun - 1) / kConvRun : 1;
+  const int run = conv_run(p, E, 32, 1024);
+  const int64_t runs = p.length > 0 ? (p.length + run - 1) / run : 1;
   const int64_t blocks = (p.batch * runs * ((p.channels + E - 1) / E) + 255) / 256;
   causal_conv_kernel<F, E, W><<<dim3((unsigned)(blocks < kGridMost ? blocks : kGridMost)),
-                                dim3(256), 0, stream>>>(p, y, final_state);
+                                dim3(256), 0, stream>>>(p, y, final_state, run);
 }
 template <class F, int W>
 static hipError_t fwd_w(const ConvProblem& p, void* y, void* fs, hipStream_t stream) {
@@ -332,8 +384,11 @@ static hipError_t fwd_w(const ConvProblem& p, void* y, void* fs, hipStream_t str
   return hipGetLastError();
 }
 
+constexpr int kConvGradE = 4;   // channels per lane: eight would hold 5 * 8 * W values in registers
+static int grad_run(const ConvProblem& p) { return conv_run(p, kConvGradE, 32, 1024); }
 static int64_t grad_sets(const ConvProblem& p) {
-  const int64_t per = p.length > 0 ? (p.length + kConvGradRun - 1) / kConvGradRun : 1;
+  const int run = grad_run(p);
+  const int64_t per = p.length > 0 ? (p.length + run - 1) / run : 1;
   const int64_t runs = per * p.batch;
   const int64_t sets = (runs + kConvGradWaves - 1) / kConvGradWaves;
   // at most 1024 partial sums per channel, and a grid of at most 2^22 workgroups
@@ -349,8 +404,8 @@ template <class F, int W>
 static hipError_t grad_w(const ConvProblem& p, const void* dy, int64_t dy_batch, int64_t dy_token,
                          const void* dfinal, void* dx, float* dweight, float* dbias,
                          void* dinitial, void* scratch, hipStream_t stream) {
-  // four channels per lane: eight would hold 5 * 8 * W values in registers
-  constexpr int E = 4;
+  constexpr int E = kConvGradE;
+  const int run = grad_run(p);
   const int64_t sets = grad_sets(p);
   float* part = (float*)scratch;
   auto cols = [&](int e) { return ((p.channels + e - 1) / e + 63) / 64; };
@@ -362,14 +417,14 @@ static hipError_t grad_w(const ConvProblem& p, const void* dy, int64_t dy_batch,
       rows_aligned<F>(E, p.channels, dfinal) && rows_aligned<F>(E, p.channels, p.initial_state)) {
     causal_conv_grad_kernel<F, E, W><<<dim3((unsigned)(sets * cols(E))), dim3(64 * kConvGradWaves),
                                        0, stream>>>(p, dy, dy_batch, dy_token, dfinal, dx, dinitial,
-                                                    part);
+                                                    part, run);
   } else {
     causal_conv_grad_kernel<F, 1, W><<<dim3((unsigned)(sets * cols(1))), dim3(64 * kConvGradWaves),
                                        0, stream>>>(p, dy, dy_batch, dy_token, dfinal, dx, dinitial,
-                                                    part);
+                                                    part, run);
   }
   const int64_t count = p.channels * (W + 1);
-  conv_filter_sum_kernel<<<dim3((unsigned)((count + 63) / 64)), dim3(256), 0, stream>>>(
+  conv_filter_sum_kernel<<<dim3((unsigned)((count + 63) / 64)), dim3(64 * kSumStrands), 0, stream>>>(
       part, sets, count, W + 1, dweight, dbias);
   return hipGetLastError();
 }

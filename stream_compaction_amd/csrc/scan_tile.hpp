@@ -246,8 +246,8 @@ template <class F, int K, int NG> struct RowStage {
 struct ScanPlace {
   int64_t b, g, ch, nch, tile;
 };
-__device__ __forceinline__ ScanPlace scan_place(const ScanProblem& p, int64_t b0, int64_t tiles) {
-  const uint32_t id = xcd_order(blockIdx.x, gridDim.x);
+__device__ __forceinline__ ScanPlace scan_place(const ScanProblem& p, int64_t b0, int64_t tiles,
+                                                uint32_t id) {
   ScanPlace s;
   const int64_t per = p.channels / p.groups;
   const int64_t w = id / (uint32_t)tiles;

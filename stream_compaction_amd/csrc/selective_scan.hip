@@ -10,7 +10,8 @@ template <class F, int K, int NG>
 __global__ __launch_bounds__(kScanThreads) void selective_scan_kernel(ScanProblem p, void* yv,
                                                                      float* final_state,
                                                                      float* starts, int64_t b0,
-                                                                     int64_t tiles) {
+                                                                     int64_t tiles,
+                                                                     uint32_t count) {
   using S = typename F::S;
   using Tile = TileStage<F, K>;
   using Rows = RowStage<F, K, NG>;
@@ -19,7 +20,9 @@ __global__ __launch_bounds__(kScanThreads) void selective_scan_kernel(ScanProble
   __shared__ alignas(16) uint32_t s_x[Tile::WORDS], s_dt[Tile::WORDS], s_z[Tile::WORDS];
 
   const int lane = lane_id(), wave = wave_id();
-  const ScanPlace at = scan_place(p, b0, tiles);
+  const uint32_t id = xcd_order(blockIdx.x);
+  if (id >= count) return;
+  const ScanPlace at = scan_place(p, b0, tiles, id);
   const int64_t len = scan_length(p, at.b);
   const int N = (int)p.states;
   const bool gate = p.z != nullptr;
@@ -190,8 +193,8 @@ static hipError_t launch_fwd(const ScanProblem& p, void* y, float* final_state, 
   for (int64_t b0 = 0; b0 < p.batch; b0 += step) {
     const int64_t nb = p.batch - b0 < step ? p.batch - b0 : step;
     selective_scan_kernel<F, K, sizeof(typename F::S) == 2 ? 16 : 8>
-        <<<dim3((unsigned)(nb * per)), dim3(kScanThreads), 0, stream>>>(p, y, final_state, starts,
-                                                                       b0, tiles);
+        <<<dim3(xcd_grid(nb * per)), dim3(kScanThreads), 0, stream>>>(
+            p, y, final_state, starts, b0, tiles, (uint32_t)(nb * per));
   }
   return hipGetLastError();
 }
@@ -222,51 +225,126 @@ hipError_t launch_selective_scan(const ScanProblem& p, Fmt fmt, void* y, float* 
 }
 
 // ---------------------------------------------------------------------------
-// One token: G lanes (a power of two) share a channel, lane q of them owning
-// states q, q + G, ...; the state is read and written once.
+// One token.  Bound by the state: 8 bytes per state and sequence against some
+// six operations.  G lanes (a power of two) share a channel, lane q of them
+// owning the V states at q V, (q + G) V, ...; V = 4 makes the state's loads and
+// stores 16 bytes wide and a wave's contiguous.  A lane takes R sequences of
+// its channel at once: A, D and the bias are read once for them and R loads of
+// the state are in flight.
 // ---------------------------------------------------------------------------
-template <class F, int G>
+template <class F, int V, int G, int R>
 __global__ __launch_bounds__(256) void selective_scan_step_kernel(ScanProblem p,
                                                                  const float* state,
-                                                                 float* new_state, void* yv) {
+                                                                 float* new_state, void* yv,
+                                                                 int64_t first) {
   using S = typename F::S;
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) / G;   // (sequence, channel)
-  const int q = threadIdx.x % G;
-  const int N = (int)p.states;
-  if (i >= p.batch * p.channels) return;                // whole groups of G lanes leave together
-  const int64_t b = i / p.channels, ch = i % p.channels;
-  const int64_t g = ch / (p.channels / p.groups);
-  const float x = widen<F>(((const S*)p.x)[b * p.x_batch + ch]);
-  float dt = widen<F>(((const S*)p.dt)[b * p.dt_batch + ch]);
-  if (p.dt_bias != nullptr) dt += p.dt_bias[ch];
-  if (p.softplus) dt = softplus(dt);
-  const float u = dt * x;
-  const S* Bp = (const S*)p.B + b * p.B_batch + g * p.B_group;
-  const S* Cp = (const S*)p.C + b * p.C_batch + g * p.C_group;
-  float acc = 0.0f;
-  for (int n = q; n < N; n += G) {
-    const float a = exp2_hw(dt * (p.A[ch * N + n] * kLog2e));
-    const float h = __builtin_fmaf(a, state[i * N + n], u * widen<F>(Bp[n]));
-    new_state[i * N + n] = h;
-    acc = __builtin_fmaf(h, widen<F>(Cp[n]), acc);
+  using IO = RowIO<FmtF32, V>;
+  using BIO = RowIO<F, V>;
+  const uint32_t per = (uint32_t)p.channels * G;        // lanes of one sequence
+  const uint32_t cols = (per + 255) / 256;
+  const uint32_t at = blockIdx.x % cols * 256 + threadIdx.x;
+  const int64_t b0 = first + (int64_t)(blockIdx.x / cols) * R;
+  if (at >= per) return;                                // whole groups of G lanes leave together
+  const int64_t ch = at / G;
+  const int q = at % G, N = (int)p.states;
+  const int64_t g = p.groups == 1 ? 0 : (int64_t)((uint32_t)ch / (uint32_t)(p.channels / p.groups));
+  const float bias = p.dt_bias != nullptr ? p.dt_bias[ch] : 0.0f;
+  float x[R], dt[R], z[R], acc[R];
+  bool on[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t b = b0 + r;
+    on[r] = b < p.batch;
+    x[r] = on[r] ? widen<F>(((const S*)p.x)[b * p.x_batch + ch]) : 0.0f;
+    dt[r] = on[r] ? widen<F>(((const S*)p.dt)[b * p.dt_batch + ch]) : 0.0f;
+    z[r] = on[r] && p.z != nullptr ? widen<F>(((const S*)p.z)[b * p.z_batch + ch]) : 0.0f;
+    acc[r] = 0.0f;
   }
 #pragma unroll
-  for (int m = G / 2; m > 0; m /= 2) acc += __shfl_xor(acc, m);
-  if (q == 0) {
-    float v = p.D != nullptr ? __builtin_fmaf(p.D[ch], x, acc) : acc;
-    if (p.z != nullptr) v *= silu(widen<F>(((const S*)p.z)[b * p.z_batch + ch]));
-    ((S*)yv)[i] = narrow<F>(v);
+  for (int r = 0; r < R; ++r) {
+    dt[r] += bias;
+    if (p.softplus) dt[r] = softplus(dt[r]);
   }
+  for (int n = q * V; n < N; n += G * V) {
+    float A[V];
+    IO::unpack(IO::load(p.A + ch * N + n, V, V > 1), A);
+    typename IO::Raw h0[R];
+    typename BIO::Raw Bn[R], Cn[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t b = b0 + r;
+      h0[r] = typename IO::Raw{};
+      Bn[r] = Cn[r] = typename BIO::Raw{};
+      if (!on[r]) continue;
+      h0[r] = IO::load(state + (b * p.channels + ch) * N + n, V, V > 1);
+      Bn[r] = BIO::load((const S*)p.B + b * p.B_batch + g * p.B_group + n, V, V > 1);
+      Cn[r] = BIO::load((const S*)p.C + b * p.C_batch + g * p.C_group + n, V, V > 1);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) A[v] *= kLog2e;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float h[V], Bv[V], Cv[V];
+      IO::unpack(h0[r], h);
+      BIO::unpack(Bn[r], Bv);
+      BIO::unpack(Cn[r], Cv);
+      const float u = dt[r] * x[r];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        h[v] = __builtin_fmaf(exp2_hw(dt[r] * A[v]), h[v], u * Bv[v]);
+        acc[r] = __builtin_fmaf(h[v], Cv[v], acc[r]);
+      }
+      if (on[r])
+        IO::store(new_state + ((b0 + r) * p.channels + ch) * N + n, IO::pack(h), V, V > 1);
+    }
+  }
+  const float D = p.D != nullptr ? p.D[ch] : 0.0f;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float a = acc[r];
+#pragma unroll
+    for (int m = G / 2; m > 0; m /= 2) a += __shfl_xor(a, m);
+    if (p.D != nullptr) a = __builtin_fmaf(D, x[r], a);
+    if (p.z != nullptr) a *= silu(z[r]);
+    if (q == 0 && on[r]) ((S*)yv)[(b0 + r) * p.channels + ch] = narrow<F>(a);
+  }
+}
+
+template <class F, int V, int G>
+static hipError_t launch_step_g(const ScanProblem& p, const float* state, float* new_state,
+                                void* y, hipStream_t stream) {
+  const int64_t cols = (p.channels * G + 255) / 256;
+  // several sequences a lane once that still leaves 2048 workgroups, 8 waves a SIMD
+  constexpr int R = 4;
+  const bool many = p.batch * cols >= 2048 * R;
+  const int64_t step = kMaxGroups / cols < 1 ? 1 : kMaxGroups / cols;
+  for (int64_t b0 = 0; b0 < p.batch; b0 += step) {
+    const int64_t nb = p.batch - b0 < step ? p.batch - b0 : step;
+    if (many) {
+      selective_scan_step_kernel<F, V, G, R><<<dim3((unsigned)((nb + R - 1) / R * cols)), dim3(256), 0,
+                                               stream>>>(p, state, new_state, y, b0);
+    } else {
+      selective_scan_step_kernel<F, V, G, 1><<<dim3((unsigned)(nb * cols)), dim3(256), 0, stream>>>(
+          p, state, new_state, y, b0);
+    }
+  }
+  return hipGetLastError();
 }
 
 template <class F>
 static hipError_t launch_step_f(const ScanProblem& p, const float* state, float* new_state,
                                 void* y, hipStream_t stream) {
-  constexpr int G = 16;
-  const int64_t blocks = (p.batch * p.channels * G + 255) / 256;
-  selective_scan_step_kernel<F, G><<<dim3((unsigned)blocks), dim3(256), 0, stream>>>(
-      p, state, new_state, y);
-  return hipGetLastError();
+  using S = typename F::S;
+  const int64_t bc = 4 * (int64_t)sizeof(S);            // bytes of four states of B or C
+  auto rows4 = [&](const void* a, int64_t batch, int64_t group) {
+    return (uintptr_t)a % bc == 0 && batch % 4 == 0 && group % 4 == 0;
+  };
+  const bool vec = p.states % 4 == 0 && (uintptr_t)state % 16 == 0 &&
+                   (uintptr_t)new_state % 16 == 0 && (uintptr_t)p.A % 16 == 0 &&
+                   rows4(p.B, p.B_batch, p.B_group) && rows4(p.C, p.C_batch, p.C_group);
+  if (!vec) return launch_step_g<F, 1, 16>(p, state, new_state, y, stream);
+  if (p.states <= 8) return launch_step_g<F, 4, 2>(p, state, new_state, y, stream);
+  return launch_step_g<F, 4, 4>(p, state, new_state, y, stream);
 }
 
 hipError_t launch_selective_scan_step(const ScanProblem& p, Fmt fmt, const float* state,

@@ -32,7 +32,8 @@ __device__ __forceinline__ float lane_from(float v, int from) {
 
 template <class F, int K>
 __global__ __launch_bounds__(kScanThreads) void selective_scan_grad_kernel(
-    ScanProblem p, ScanGrads g, float* part, float* part_params, int64_t b0, int64_t tiles) {
+    ScanProblem p, ScanGrads g, float* part, float* part_params, int64_t b0, int64_t tiles,
+    uint32_t count) {
   using S = typename F::S;
   using Tile = TileStage<F, K>;
   constexpr int NG = GradShape<F, K>::NG, TB = GradShape<F, K>::TB;
@@ -41,7 +42,9 @@ __global__ __launch_bounds__(kScanThreads) void selective_scan_grad_kernel(
   __shared__ alignas(16) uint32_t s_x[Tile::WORDS], s_dt[Tile::WORDS], s_z[Tile::WORDS], s_dy[Tile::WORDS];
 
   const int lane = lane_id(), wave = wave_id();
-  const ScanPlace at = scan_place(p, b0, tiles);
+  const uint32_t id = xcd_order(blockIdx.x);
+  if (id >= count) return;
+  const ScanPlace at = scan_place(p, b0, tiles, id);
   const int64_t len = scan_length(p, at.b);
   const int N = (int)p.states;
   const bool gate = p.z != nullptr;
@@ -369,8 +372,8 @@ static hipError_t launch_grad(const ScanProblem& p, Fmt fmt, const ScanGrads& g,
   float* params = part + rows_part_floats(p, fmt);
   for (int64_t b0 = 0; b0 < p.batch; b0 += step) {
     const int64_t nb = p.batch - b0 < step ? p.batch - b0 : step;
-    selective_scan_grad_kernel<F, K><<<dim3((unsigned)(nb * per)), dim3(kScanThreads), 0, stream>>>(
-        p, g, part, params, b0, tiles);
+    selective_scan_grad_kernel<F, K><<<dim3(xcd_grid(nb * per)), dim3(kScanThreads), 0, stream>>>(
+        p, g, part, params, b0, tiles, (uint32_t)(nb * per));
   }
   constexpr int TB = 64 * K;
   const int64_t nblk = (p.length + TB - 1) / TB;

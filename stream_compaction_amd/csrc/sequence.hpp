@@ -103,10 +103,17 @@ template <class F, int E> struct RowIO {
     for (int k = 0; k < E; ++k) x[k] = widen<F>(s.e[k]);
   }
   static __device__ __forceinline__ Raw pack(const float (&x)[E]) {
-    Elems s;
+    if constexpr (sizeof(S) == 2 && E > 1) {
+      struct Words { uint32_t w[E / 2]; } s;
 #pragma unroll
-    for (int k = 0; k < E; ++k) s.e[k] = narrow<F>(x[k]);
-    return __builtin_bit_cast(Raw, s);
+      for (int k = 0; k < E / 2; ++k) s.w[k] = narrow2<F>(x[2 * k], x[2 * k + 1]);
+      return __builtin_bit_cast(Raw, s);
+    } else {
+      Elems s;
+#pragma unroll
+      for (int k = 0; k < E; ++k) s.e[k] = narrow<F>(x[k]);
+      return __builtin_bit_cast(Raw, s);
+    }
   }
   static __device__ __forceinline__ void store(S* p, Raw r, int64_t n, bool vec) {
     if (vec && n >= E) {
@@ -120,18 +127,32 @@ template <class F, int E> struct RowIO {
   }
 };
 
+// i = q d + r.  A 64-bit division costs some 150 instructions, a 32-bit one 25.
+__device__ __forceinline__ int64_t divide(int64_t i, int64_t d, int64_t* r) {
+  int64_t q;
+  if (((uint64_t)(i | d) >> 32) == 0) {
+    q = (int64_t)((uint32_t)i / (uint32_t)d);
+  } else {
+    q = i / d;
+  }
+  *r = i - q * d;
+  return q;
+}
+
 // Sum over the 64 lanes, the same value in every lane of the wave.
 __device__ __forceinline__ float wave_sum(float v) {
   return readlane(wave_scan_incl<Op::Add>(v), kWave - 1);
 }
 
 // Logical workgroup index: hardware deals consecutive workgroups to the 8
-// XCDs in turn, each with its own L2, so neighbours in the logical order
-// (which share cache lines of the activations) are put on one XCD.
-__device__ __forceinline__ uint32_t xcd_order(uint32_t bid, uint32_t count) {
-  constexpr uint32_t X = 8;
-  const uint32_t per = count / X, rem = count % X, x = bid % X, i = bid / X;
-  return x < rem ? x * (per + 1) + i : rem * (per + 1) + (x - rem) * per + i;
+// XCDs in turn, each with its own L2.  Runs of 4 logical neighbours (which share
+// the 128-byte lines of the activations) are put on one XCD and the runs dealt
+// in turn, so that every XCD gets its part of each sequence, however long.  The
+// grid is a multiple of 32 workgroups; logical indices may pass the last one.
+__device__ __forceinline__ uint32_t xcd_order(uint32_t bid) {
+  const uint32_t x = bid % 8, i = bid / 8;
+  return (i / 4 * 8 + x) * 4 + i % 4;
 }
+inline unsigned xcd_grid(int64_t count) { return (unsigned)((count + 31) / 32 * 32); }
 
 }  // namespace sca
