@@ -171,10 +171,12 @@ def dtype_name(dt):
 
 
 def _stream(stream):
-    torch = _torch()
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    # the current device's current stream, as torch.cuda.current_stream() has it, without
+    # building the Stream object (which costs more than the rest of a small call)
+    c = _torch()._C
+    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
 def _dev_ptr(t, what):

@@ -6,7 +6,7 @@
 // The gradient sorts the tokens by id (the library's radix sort, stable), so
 // that each table row is the sum of one run of sorted tokens, taken in token
 // order: no float atomics, the same bits every time.  The sorted tokens are cut
-// into segments of kSeg; a wave sums the runs of its segment (one table column
+// into segments; a wave sums the runs of its segment (one table column
 // block), writes the rows whose run lies inside, and leaves the sums of runs
 // that cross a border to a second kernel.
 #include "sequence.hpp"
@@ -67,7 +67,133 @@ __global__ __launch_bounds__(256) void embedding_zero_kernel(uint4* out, int64_t
   if (blockIdx.x == 0 && (int)threadIdx.x < tail_bytes) tail[threadIdx.x] = 0;
 }
 
-constexpr int kSeg = 32;          // sorted tokens per wave
+// The sort of a short list, in one launch.  A workgroup owns `bucket` (at most
+// 256) table rows and reads all ids: those below its rows tell where its part
+// of the sorted list begins, so workgroups need nothing of one another.  It
+// counts its rows per wave (a wave owns consecutive tokens) and places its
+// tokens in token order.  It also writes zeros to its rows: the segments'
+// kernel overwrites those that have a token, which costs less than waiting for
+// the counts before the first store.  Every id is read by every workgroup, from
+// L2: 64 MB for 16384 ids and 512 workgroups, against the four passes over the
+// list and the seven launches of the general path.
+constexpr int kBucketRows = 256;
+constexpr int kBucketWaves = 16;
+constexpr int kBucketIds = 16;           // ids per lane
+constexpr int64_t kBucketTokens = 64 * kBucketWaves * kBucketIds;
+
+// The workgroup's threads write zeros to [a, e), whose ends are multiples of
+// `unit` (2 or 4) bytes.
+__device__ __forceinline__ void zero_span(uintptr_t a, uintptr_t e, int unit) {
+  const uintptr_t a16 = (a + 15) & ~(uintptr_t)15;
+  const uintptr_t lo = a16 < e ? a16 : e, hi = lo + ((e - lo) & ~(uintptr_t)15);
+  const uintptr_t t = threadIdx.x;
+  for (uintptr_t i = lo + t * 16; i < hi; i += 64 * kBucketWaves * 16)
+    __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, gptr<u32x4>(i));
+  const uintptr_t head = a + t * unit, tail = hi + t * unit;
+  if (unit == 4) {
+    if (head < lo) *gptr<uint32_t>(head) = 0;
+    if (tail < e) *gptr<uint32_t>(tail) = 0;
+  } else {
+    if (head < lo) *gptr<uint16_t>(head) = 0;
+    if (tail < e) *gptr<uint16_t>(tail) = 0;
+  }
+}
+
+template <class I>
+__global__ __launch_bounds__(64 * kBucketWaves) void embedding_bucket_kernel(
+    const I* ids, int tokens, int64_t rows, int bucket, uint32_t* __restrict__ keys,
+    uint32_t* __restrict__ pos, char* __restrict__ dweight,
+    int64_t row_bytes, int unit) {
+  __shared__ uint32_t s_off[kBucketWaves][kBucketRows];
+  __shared__ uint32_t s_start[kBucketRows];
+  __shared__ uint32_t s_below[kBucketWaves], s_sum[kBucketRows / 64];
+  const int lane = lane_id(), wave = wave_id();
+  const uint32_t lo = blockIdx.x * (uint32_t)bucket;      // rows are at most 2^17 here
+  const int its = (tokens + 64 * kBucketWaves - 1) / (64 * kBucketWaves);
+  const int first = wave * its * 64 + lane;
+  constexpr uint32_t kNone = ~0u;
+  uint32_t rel[kBucketIds];              // row within the bucket
+  uint32_t below = 0;
+#pragma unroll
+  for (int b = 0; b < kBucketRows; b += 64) s_off[wave][b + lane] = 0;
+  uint32_t row[kBucketIds];              // masked tokens are above every row
+#pragma unroll
+  for (int k = 0; k < kBucketIds; ++k) {
+    const int i = first + k * 64;
+    row[k] = k < its && i < tokens ? (uint32_t)token_row(ids, i, rows) : kNone;
+  }
+  {
+    const int64_t left = rows - lo, mine = left < bucket ? left : bucket;
+    const uintptr_t a = (uintptr_t)dweight + (uintptr_t)(lo * row_bytes);
+    zero_span(a, a + (uintptr_t)(mine * row_bytes), unit);
+  }
+#pragma unroll
+  for (int k = 0; k < kBucketIds; ++k) {
+    below += (uint32_t)__popcll(__ballot(row[k] < lo));
+    rel[k] = row[k] - lo < (uint32_t)bucket ? row[k] - lo : kNone;
+    if (rel[k] != kNone) atomicAdd(&s_off[wave][rel[k]], 1u);
+  }
+  if (lane == 0) s_below[wave] = below;
+  __syncthreads();
+  uint32_t count = 0, incl = 0;
+  if (threadIdx.x < kBucketRows) {
+    // per row: where each wave's tokens begin among the row's, and their number
+#pragma unroll
+    for (int w = 0; w < kBucketWaves; ++w) {
+      const uint32_t v = s_off[w][threadIdx.x];
+      s_off[w][threadIdx.x] = count;
+      count += v;
+    }
+    incl = wave_scan_incl<Op::Add>(count);
+    if (lane == kWave - 1) s_sum[wave] = incl;
+  }
+  __syncthreads();
+  uint32_t base = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kBucketWaves; ++w) base += s_below[w];
+#pragma unroll
+  for (int w = 0; w < kBucketRows / 64; ++w) {
+    if (threadIdx.x < kBucketRows && w < wave) incl += s_sum[w];
+    all += s_sum[w];
+  }
+  if (threadIdx.x < kBucketRows) s_start[threadIdx.x] = base + incl - count;
+  __syncthreads();
+
+#pragma unroll
+  for (int k = 0; k < kBucketIds; ++k) {
+    const uint32_t r = rel[k];
+    const bool on = r != kNone;
+    uint64_t same = __ballot(on);
+    if (same == 0) continue;
+    // lanes with the same row
+#pragma unroll
+    for (int bit = 0; bit < 8; ++bit) {
+      const uint64_t set = __ballot((r >> bit & 1) != 0);
+      same &= (r >> bit & 1) != 0 ? set : ~set;
+    }
+    if (on) {
+      const int rank = __popcll(same & ((1ull << lane) - 1));
+      uint32_t* mine = &s_off[wave][r];
+      const uint32_t before = __hip_atomic_load(mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
+      const uint32_t at = s_start[r] + before + rank;
+      keys[at] = lo + r;
+      pos[at] = (uint32_t)(first + k * 64);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      // the wave's LDS accesses are in order: all lanes have read
+      if (rank == 0)
+        __hip_atomic_store(mine, before + (uint32_t)__popcll(same), __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_WAVEFRONT);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+  }
+  // masked tokens sort last
+  if (blockIdx.x == gridDim.x - 1)
+    for (int i = (int)(base + all) + (int)threadIdx.x; i < tokens; i += 64 * kBucketWaves) {
+      keys[i] = (uint32_t)rows;
+      pos[i] = 0;
+    }
+}
+
 constexpr int kSegAhead = 8;      // gradient rows loaded together
 
 // A wave sums segment `seg` of the sorted tokens over one block of 64 E
@@ -77,19 +203,20 @@ constexpr int kSegAhead = 8;      // gradient rows loaded together
 template <class F, class G, int E>
 __global__ __launch_bounds__(256) void embedding_segment_kernel(
     const void* dout, const uint32_t* keys, const uint32_t* pos, void* dweight, float* part,
-    int64_t tokens, int64_t rows, int64_t channels, int64_t row_stride, float scale) {
+    int64_t tokens, int64_t rows, int64_t channels, int64_t row_stride, float scale, int seg_tokens) {
   using S = typename F::S;
   using IO = RowIO<F, E>;
   constexpr int OE = E < kVecElems<G> ? E : kVecElems<G>;   // outputs per store
   using OIO = RowIO<G, OE>;
   const int lane = lane_id();
   const int64_t blocks = (channels + 64 * E - 1) / (64 * E);
-  const int64_t total = (tokens + kSeg - 1) / kSeg * blocks;
+  const int64_t total = (tokens + seg_tokens - 1) / seg_tokens * blocks;
   for (int64_t w = (int64_t)blockIdx.x * 4 + wave_id(); w < total; w += (int64_t)gridDim.x * 4) {
-    const int64_t seg = w / blocks, s0 = seg * kSeg;
-    const int64_t ch = (w % blocks * 64 + lane) * E, n = channels - ch;
-    const int cnt = (int)(tokens - s0 < kSeg ? tokens - s0 : kSeg);
-    // lane l holds the key and position of token s0 + l, lane kSeg the next
+    int64_t col;
+    const int64_t seg = divide(w, blocks, &col), s0 = seg * seg_tokens;
+    const int64_t ch = (col * 64 + lane) * E, n = channels - ch;
+    const int cnt = (int)(tokens - s0 < seg_tokens ? tokens - s0 : seg_tokens);
+    // lane l holds the key and position of token s0 + l, lane seg_tokens the next
     // segment's first key, and `before` the last segment's last
     uint32_t key = ~0u, at = 0;
     if (lane <= cnt && s0 + lane < tokens) {
@@ -151,30 +278,56 @@ __global__ __launch_bounds__(256) void embedding_segment_kernel(
   }
 }
 
-// Runs that cross segments: the wave of the segment in which such a run begins
-// adds its pieces in order and writes the row.
-template <class G>
-__global__ __launch_bounds__(256) void embedding_border_kernel(const uint32_t* keys, void* dweight,
-                                                              const float* part, int64_t tokens,
-                                                              int64_t rows, int64_t channels,
-                                                              float scale) {
-  const int64_t blocks = (channels + 63) / 64;
-  const int64_t total = (tokens + kSeg - 1) / kSeg * blocks;
-  for (int64_t w = (int64_t)blockIdx.x * 4 + wave_id(); w < total; w += (int64_t)gridDim.x * 4) {
-    const int64_t seg = w / blocks, s0 = seg * kSeg, end = s0 + kSeg;
+// Runs that cross segments: the workgroup of the segment in which such a run
+// begins adds its pieces in order and writes the row (256 E channels of it).  A
+// frequent token's run crosses many segments: kAhead of them are looked at
+// together.
+template <class G, int E>
+__global__ __launch_bounds__(256) void embedding_border_kernel(const uint32_t* __restrict__ keys,
+                                                              void* __restrict__ dweight,
+                                                              const float* __restrict__ part,
+                                                              int64_t tokens, int64_t rows,
+                                                              int64_t channels, float scale,
+                                                              int seg_tokens) {
+  using IO = RowIO<FmtF32, E>;
+  constexpr int kAhead = 16;
+  const int64_t cols = (channels + 256 * E - 1) / (256 * E);
+  const int64_t segs = (tokens + seg_tokens - 1) / seg_tokens;
+  for (int64_t w = blockIdx.x; w < segs * cols; w += gridDim.x) {
+    int64_t col;
+    const int64_t seg = divide(w, cols, &col), s0 = seg * seg_tokens, end = s0 + seg_tokens;
     if (end >= tokens) continue;                          // nothing follows the last segment
     const uint32_t k = keys[end - 1];
     if (k >= (uint32_t)rows || keys[end] != k) continue;  // no run continues past this segment
     if (s0 > 0 && keys[s0 - 1] == k) continue;            // it began in an earlier one
-    const int64_t ch = w % blocks * 64 + lane_id();
+    const int64_t ch = (col * 256 + threadIdx.x) * E;
     if (ch >= channels) continue;
-    float sum = part[(seg * 2 + 1) * channels + ch];
-    for (int64_t s = seg + 1;; ++s) {
-      sum += part[s * 2 * channels + ch];
-      const int64_t e = (s + 1) * kSeg;
-      if (e >= tokens || keys[e - 1] != k || keys[e] != k) break;
+    float sum[E];
+    IO::unpack(IO::load(part + (seg * 2 + 1) * channels + ch, E, E > 1), sum);
+    bool more = true;
+    for (int64_t s = seg + 1; more; s += kAhead) {
+      typename IO::Raw v[kAhead];
+      bool on[kAhead];                                    // the run goes on past segment s + j
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        // past the list's end the last entries are read again, without use
+        const int64_t e = (s + j + 1) * seg_tokens, r = s + j < segs ? s + j : segs - 1;
+        v[j] = IO::load(part + r * 2 * channels + ch, E, E > 1);
+        const int64_t i = e < tokens ? e : tokens - 1;
+        on[j] = (keys[i - 1] == k) & (keys[i] == k) & (e < tokens);
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        float x[E];
+        IO::unpack(v[j], x);
+#pragma unroll
+        for (int c = 0; c < E; ++c) sum[c] = more ? sum[c] + x[c] : sum[c];
+        more = more && on[j];
+      }
     }
-    ((typename G::S*)dweight)[(int64_t)k * channels + ch] = narrow<G>(sum * scale);
+#pragma unroll
+    for (int c = 0; c < E; ++c)
+      ((typename G::S*)dweight)[(int64_t)k * channels + ch + c] = narrow<G>(sum[c] * scale);
   }
 }
 
@@ -217,29 +370,39 @@ hipError_t launch_embedding(const void* weight, const void* ids, bool wide_ids, 
   });
 }
 
+// Sorted tokens per wave: short segments leave more waves to a short list, long
+// ones fewer runs that cross a border.
+static int embedding_seg(int64_t tokens, int64_t channels) {
+  const int64_t cols = (channels + 511) / 512;
+  return tokens * cols >= 4096 * 32 ? 32 : tokens * cols >= 4096 * 16 ? 16 : 8;
+}
+static bool embedding_short(int64_t tokens, int64_t rows) {
+  return tokens <= kBucketTokens && rows <= 512 * kBucketRows;
+}
+
 // Scratch: keys, positions and their sort temporaries; the sort's own scratch;
 // two float32 rows per segment.
 namespace {
 struct GradScratch {
   size_t keys, pos, tmp_keys, tmp_pos, sort, part, bytes;
 };
-GradScratch grad_scratch(int64_t tokens, int64_t channels) {
+GradScratch grad_scratch(int64_t tokens, int64_t rows, int64_t channels) {
   auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
   GradScratch s;
   const size_t list = up((size_t)tokens * 4);
+  const int seg = embedding_seg(tokens, channels);
   s.keys = 0;
   s.pos = list;
   s.tmp_keys = 2 * list;
   s.tmp_pos = 3 * list;
   s.sort = 4 * list;
-  s.part = s.sort + up(radix_sort_scratch(tokens, 4));
-  s.bytes = s.part + up((size_t)((tokens + kSeg - 1) / kSeg) * 2 * (size_t)channels * 4);
+  s.part = embedding_short(tokens, rows) ? s.tmp_keys : s.sort + up(radix_sort_scratch(tokens, 4));
+  s.bytes = s.part + up((size_t)((tokens + seg - 1) / seg) * 2 * (size_t)channels * 4);
   return s;
 }
 }  // namespace
 size_t embedding_grad_scratch(int64_t tokens, int64_t rows, int64_t channels) {
-  (void)rows;
-  return tokens == 0 ? 0 : grad_scratch(tokens, channels).bytes;
+  return tokens == 0 ? 0 : grad_scratch(tokens, rows, channels).bytes;
 }
 
 hipError_t launch_embedding_grad(const void* dout, const void* ids, bool wide_ids, void* dweight,
@@ -247,7 +410,8 @@ hipError_t launch_embedding_grad(const void* dout, const void* ids, bool wide_id
                                  int64_t row_stride, Fmt fmt, Fmt out_fmt, float scale,
                                  void* scratch, hipStream_t stream) {
   const int out_bytes = out_fmt == Fmt::F32 ? 4 : 2;
-  {
+  const bool one_launch = tokens > 0 && embedding_short(tokens, rows);
+  if (!one_launch) {
     // rows without a token are zero; the others are overwritten below
     const uintptr_t a = (uintptr_t)dweight, e = a + (uintptr_t)(rows * channels * out_bytes);
     const uintptr_t a16 = (a + 15) & ~(uintptr_t)15;
@@ -261,23 +425,40 @@ hipError_t launch_embedding_grad(const void* dout, const void* ids, bool wide_id
                             dim3(256), 0, stream>>>((uint4*)lo, vecs, (uint8_t*)hi, (int)(e - hi));
   }
   if (tokens == 0) return hipGetLastError();
-  const GradScratch g = grad_scratch(tokens, channels);
+  const GradScratch g = grad_scratch(tokens, rows, channels);
   char* base = (char*)scratch;
   uint32_t* keys = (uint32_t*)(base + g.keys);
   uint32_t* pos = (uint32_t*)(base + g.pos);
-  const dim3 tgrid((unsigned)((tokens + 255) / 256));
-  if (wide_ids) {
-    embedding_keys_kernel<<<tgrid, dim3(256), 0, stream>>>((const int64_t*)ids, tokens, rows, keys, pos);
+  auto with_ids = [&](auto&& fn) {
+    if (wide_ids) {
+      fn((const int64_t*)ids);
+    } else {
+      fn((const int32_t*)ids);
+    }
+  };
+  if (one_launch) {
+    // two workgroups per CU as long as a workgroup's rows fit its counters
+    const int64_t even = (rows + 511) / 512;
+    const int bucket = (int)(even < kBucketRows ? even : kBucketRows);
+    with_ids([&](auto* id) {
+      embedding_bucket_kernel<<<dim3((unsigned)((rows + bucket - 1) / bucket)),
+                                dim3(64 * kBucketWaves), 0, stream>>>(
+          id, (int)tokens, rows, bucket, keys, pos, (char*)dweight, channels * out_bytes, out_bytes);
+    });
   } else {
-    embedding_keys_kernel<<<tgrid, dim3(256), 0, stream>>>((const int32_t*)ids, tokens, rows, keys, pos);
+    with_ids([&](auto* id) {
+      embedding_keys_kernel<<<dim3((unsigned)((tokens + 255) / 256)), dim3(256), 0, stream>>>(
+          id, tokens, rows, keys, pos);
+    });
+    int bits = 8;                       // keys go up to `rows`
+    while (bits < 32 && ((uint64_t)rows >> bits) != 0) bits += 8;
+    const hipError_t e = launch_radix_sort(keys, base + g.tmp_keys, pos, base + g.tmp_pos, tokens,
+                                           Fmt::U32, 4, bits, base + g.sort, stream);
+    if (e != hipSuccess) return e;
   }
-  int bits = 8;                       // keys go up to `rows`
-  while (bits < 32 && ((uint64_t)rows >> bits) != 0) bits += 8;
-  hipError_t e = launch_radix_sort(keys, base + g.tmp_keys, pos, base + g.tmp_pos, tokens, Fmt::U32,
-                                   4, bits, base + g.sort, stream);
-  if (e != hipSuccess) return e;
   float* part = (float*)(base + g.part);
-  const int64_t segs = (tokens + kSeg - 1) / kSeg;
+  const int seg = embedding_seg(tokens, channels);
+  const int64_t segs = (tokens + seg - 1) / seg;
   return by_format(fmt, [&](auto f) {
     using F = decltype(f);
     auto go = [&](auto o) {
@@ -293,14 +474,23 @@ hipError_t launch_embedding_grad(const void* dout, const void* ids, bool wide_id
       const dim3 grid = grid_of(waves);
       if (vec) {
         embedding_segment_kernel<F, G, E><<<grid, dim3(256), 0, stream>>>(
-            dout, keys, pos, dweight, part, tokens, rows, channels, row_stride, scale);
+            dout, keys, pos, dweight, part, tokens, rows, channels, row_stride, scale, seg);
       } else {
         embedding_segment_kernel<F, G, 1><<<grid, dim3(256), 0, stream>>>(
-            dout, keys, pos, dweight, part, tokens, rows, channels, row_stride, scale);
+            dout, keys, pos, dweight, part, tokens, rows, channels, row_stride, scale, seg);
       }
-      const int64_t bw = segs * ((channels + 63) / 64);
-      embedding_border_kernel<G><<<grid_of(bw), dim3(256), 0, stream>>>(
-          keys, dweight, part, tokens, rows, channels, scale);
+      auto border = [&](auto e) {
+        constexpr int BE = decltype(e)::value;
+        const int64_t b = segs * ((channels + 256 * BE - 1) / (256 * BE));
+        embedding_border_kernel<G, BE><<<dim3((unsigned)(b < kGridMost ? b : kGridMost)), dim3(256), 0,
+                                         stream>>>(keys, dweight, part, tokens, rows, channels,
+                                                   scale, seg);
+      };
+      if (channels % 4 == 0) {
+        border(std::integral_constant<int, 4>{});
+      } else {
+        border(std::integral_constant<int, 1>{});
+      }
       return hipGetLastError();
     };
     // the table's gradient in the activations' type or in float32

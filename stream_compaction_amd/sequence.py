@@ -35,7 +35,7 @@ def _code(x, what):
 
 def _like(t, what, shape, dtype, device):
     """Pointer of a contiguous tensor of this shape, type and device."""
-    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape} on {device}")
     return t.data_ptr()
 
@@ -44,25 +44,34 @@ def _opt(t, what, shape, dtype, device):
     return None if t is None else _like(t, what, shape, dtype, device)
 
 
-def _out(t, what, shape, dtype, device):
-    if t is None:
+def _new(shape, dtype, device, stream):
+    """A new tensor.  Memory for an explicit stream comes from that stream's pool, so that it
+    is not handed on while the stream still works on it."""
+    if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _out(t, what, shape, dtype, device, stream):
+    if t is None:
+        return _new(shape, dtype, device, stream)
     _like(t, what, shape, dtype, device)
     return t
 
 
 def _rows(t, what, shape, dtype, device):
     """An activation tensor: shape, type, device, contiguous last axis."""
-    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device:
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
         raise ValueError(f"{what} must be a {dtype} tensor of shape {shape} on {device}")
     if shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{what} must have a contiguous last axis")
     return t.data_ptr()
 
 
-def _scratch(scratch, need, device):
+def _scratch(scratch, need, device, stream):
     if scratch is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        return _new(max(need, 16), torch.uint8, device, stream)
     if scratch.dtype != torch.uint8 or scratch.device != device or not scratch.is_contiguous():
         raise ValueError("scratch must be a contiguous uint8 tensor on the data's device")
     return scratch
@@ -74,19 +83,18 @@ def _conv_args(x, weight, bias, initial_state, lengths, silu, step):
                          "x must be [batch, length, channels]")
     _require(x.is_cuda, "x must be a GPU tensor")
     code = _code(x, "x")
-    b, d, dev = x.shape[0], x.shape[-1], x.device
+    shape, dev, stride = x.shape, x.device, x.stride()
+    b, d = shape[0], shape[-1]
     _require(weight.dim() == 2, "weight must be [channels, width]")
     w = weight.shape[1]
-    a = ConvArgs()
-    a.x = _rows(x, "x", tuple(x.shape), x.dtype, dev)
-    a.weight = _like(weight, "weight", (d, w), torch.float32, dev)
-    a.bias = _opt(bias, "bias", (d,), torch.float32, dev)
-    a.initial_state = _opt(initial_state, "initial_state", (b, w - 1, d), x.dtype, dev)
-    a.lengths = _opt(lengths, "lengths", (b,), torch.int32, dev)
-    a.batch, a.length, a.channels, a.width = b, 1 if step else x.shape[1], d, w
-    a.x_stride[:] = x.stride()[:2] if not step else (x.stride(0), 0)
-    a.silu, a.dtype = int(bool(silu)), code
-    return a
+    return ConvArgs(
+        _rows(x, "x", shape, x.dtype, dev),
+        _like(weight, "weight", (d, w), torch.float32, dev),
+        _opt(bias, "bias", (d,), torch.float32, dev),
+        _opt(initial_state, "initial_state", (b, w - 1, d), x.dtype, dev),
+        _opt(lengths, "lengths", (b,), torch.int32, dev),
+        b, 1 if step else shape[1], d, w,
+        (stride[0], 0 if step else stride[1]), 1 if silu else 0, code)
 
 
 def causal_conv(x, weight, bias=None, initial_state=None, lengths=None, silu=True, out=None,
@@ -99,8 +107,9 @@ def causal_conv(x, weight, bias=None, initial_state=None, lengths=None, silu=Tru
     ``(y, final_state)``: the second is the next call's initial state.
     """
     a = _conv_args(x, weight, bias, initial_state, lengths, silu, False)
-    y = _out(out, "out", tuple(x.shape), x.dtype, x.device)
-    fs = _out(final_state, "final_state", (a.batch, a.width - 1, a.channels), x.dtype, x.device)
+    y = _out(out, "out", x.shape, x.dtype, x.device, stream)
+    fs = _out(final_state, "final_state", (a.batch, a.width - 1, a.channels), x.dtype, x.device,
+              stream)
     check(lib().causal_conv(a, y.data_ptr(), fs.data_ptr(), _stream(stream)))
     return y, fs
 
@@ -112,14 +121,14 @@ def causal_conv_grad(dy, x, weight, bias=None, initial_state=None, lengths=None,
     that input is)."""
     a = _conv_args(x, weight, bias, initial_state, lengths, silu, False)
     dev, state = x.device, (a.batch, a.width - 1, a.channels)
-    dyp = _rows(dy, "dy", tuple(x.shape), x.dtype, dev)
+    dyp = _rows(dy, "dy", x.shape, x.dtype, dev)
     df = _opt(dfinal, "dfinal", state, x.dtype, dev)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    dw = torch.empty(weight.shape, dtype=torch.float32, device=dev)
-    db = None if bias is None else torch.empty(bias.shape, dtype=torch.float32, device=dev)
-    ds = None if initial_state is None else torch.empty(state, dtype=x.dtype, device=dev)
+    dx = _new(x.shape, x.dtype, dev, stream)
+    dw = _new(weight.shape, torch.float32, dev, stream)
+    db = None if bias is None else _new(bias.shape, torch.float32, dev, stream)
+    ds = None if initial_state is None else _new(state, x.dtype, dev, stream)
     L = lib()
-    scratch = _scratch(scratch, L.causal_conv_grad_scratch_bytes(a), dev)
+    scratch = _scratch(scratch, L.causal_conv_grad_scratch_bytes(a), dev, stream)
     check(L.causal_conv_grad(a, dyp, (_i64 * 2)(*dy.stride()[:2]), df, dx.data_ptr(),
                              dw.data_ptr(), None if db is None else db.data_ptr(),
                              None if ds is None else ds.data_ptr(), scratch.data_ptr(),
@@ -136,7 +145,7 @@ def causal_conv_step(state, x, weight, bias=None, silu=True, new_state=None, out
     shape = (a.batch, a.width - 1, a.channels)
     sp = _like(state, "state", shape, x.dtype, x.device)
     np_ = sp if new_state is None else _like(new_state, "new_state", shape, x.dtype, x.device)
-    y = _out(out, "out", tuple(x.shape), x.dtype, x.device)
+    y = _out(out, "out", x.shape, x.dtype, x.device, stream)
     check(lib().causal_conv_step(a, sp, np_, y.data_ptr(), _stream(stream)))
     return y
 
@@ -148,37 +157,38 @@ def _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, lengths, 
     _require(x.is_cuda, "x must be a GPU tensor")
     code = _code(x, "x")
     dev, ty = x.device, x.dtype
-    shape = tuple(x.shape)
+    shape = x.shape
     b, d = shape[0], shape[-1]
     _require(A.dim() == 2, "A must be [channels, states]")
     n = A.shape[1]
     _require(B.dim() == x.dim() + 1, "B must be [batch, length, groups, states] (a step: "
                                      "[batch, groups, states])")
-    rows = shape[:-1] + (B.shape[-2], n)
-    a = ScanArgs()
-    a.x = _rows(x, "x", shape, ty, dev)
-    a.dt = _rows(dt, "dt", shape, ty, dev)
-    a.B = _rows(B, "B", rows, ty, dev)
-    a.C = _rows(C, "C", rows, ty, dev)
-    a.A = _like(A, "A", (d, n), torch.float32, dev)
-    a.D = _opt(D, "D", (d,), torch.float32, dev)
-    a.dt_bias = _opt(dt_bias, "dt_bias", (d,), torch.float32, dev)
-    a.initial_state = _opt(initial_state, "initial_state", (b, d, n), torch.float32, dev)
-    a.lengths = _opt(lengths, "lengths", (b,), torch.int32, dev)
-    a.batch, a.length, a.channels = b, 1 if step else shape[1], d
-    a.states, a.groups = n, B.shape[-2]
+    groups = B.shape[-2]
+    rows = shape[:-1] + (groups, n)
     if step:
-        a.x_stride[0], a.dt_stride[0] = x.stride(0), dt.stride(0)
-        a.B_stride[:] = (B.stride(0), 0, B.stride(1))
-        a.C_stride[:] = (C.stride(0), 0, C.stride(1))
+        def lead(t):
+            return t.stride(0), 0
+
+        def lead3(t):
+            return t.stride(0), 0, t.stride(1)
     else:
-        a.x_stride[:], a.dt_stride[:] = x.stride()[:2], dt.stride()[:2]
-        a.B_stride[:], a.C_stride[:] = B.stride()[:3], C.stride()[:3]
-    if z is not None:
-        a.z = _rows(z, "z", shape, ty, dev)
-        a.z_stride[:] = (z.stride(0), 0) if step else z.stride()[:2]
-    a.softplus, a.dtype = int(bool(softplus)), code
-    return a
+        def lead(t):
+            return t.stride()[:2]
+
+        def lead3(t):
+            return t.stride()[:3]
+    f32 = torch.float32
+    return ScanArgs(
+        _rows(x, "x", shape, ty, dev), _rows(dt, "dt", shape, ty, dev),
+        _rows(B, "B", rows, ty, dev), _rows(C, "C", rows, ty, dev),
+        None if z is None else _rows(z, "z", shape, ty, dev),
+        _like(A, "A", (d, n), f32, dev), _opt(D, "D", (d,), f32, dev),
+        _opt(dt_bias, "dt_bias", (d,), f32, dev),
+        _opt(initial_state, "initial_state", (b, d, n), f32, dev),
+        _opt(lengths, "lengths", (b,), torch.int32, dev),
+        b, 1 if step else shape[1], d, n, groups,
+        lead(x), lead(dt), (0, 0) if z is None else lead(z), lead3(B), lead3(C),
+        1 if softplus else 0, code)
 
 
 def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=False,
@@ -196,14 +206,14 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=False,
     ``keep_starts`` also what ``selective_scan_grad`` needs of this call.
     """
     a = _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, lengths, False)
-    y = _out(out, "out", tuple(x.shape), x.dtype, x.device)
-    fs = _out(final_state, "final_state", (a.batch, a.channels, a.states), torch.float32, x.device)
+    y = _out(out, "out", x.shape, x.dtype, x.device, stream)
+    fs = _out(final_state, "final_state", (a.batch, a.channels, a.states), torch.float32, x.device,
+              stream)
     L = lib()
     if not keep_starts:
         check(L.selective_scan(a, y.data_ptr(), fs.data_ptr(), None, _stream(stream)))
         return y, fs
-    starts = torch.empty(L.selective_scan_starts_bytes(a) // 4, dtype=torch.float32,
-                         device=x.device)
+    starts = _new(L.selective_scan_starts_bytes(a) // 4, torch.float32, x.device, stream)
     check(L.selective_scan(a, y.data_ptr(), fs.data_ptr(), starts.data_ptr(), _stream(stream)))
     return y, fs, starts
 
@@ -218,27 +228,21 @@ def selective_scan_grad(dy, x, dt, A, B, C, starts, D=None, z=None, dt_bias=None
     dev, ty, f32 = x.device, x.dtype, torch.float32
     state = (a.batch, a.channels, a.states)
     L = lib()
-    g = ScanGrads()
-    g.dy = _rows(dy, "dy", tuple(x.shape), ty, dev)
-    g.dy_stride[:] = dy.stride()[:2]
-    g.dfinal = _opt(dfinal, "dfinal", state, f32, dev)
-    g.starts = _like(starts, "starts", (L.selective_scan_starts_bytes(a) // 4,), f32, dev)
-    out = {"dx": torch.empty(x.shape, dtype=ty, device=dev),
-           "ddt": torch.empty(x.shape, dtype=ty, device=dev),
-           "dA": torch.empty(A.shape, dtype=f32, device=dev),
-           "dB": torch.empty(B.shape, dtype=ty, device=dev),
-           "dC": torch.empty(B.shape, dtype=ty, device=dev),
-           "dD": None if D is None else torch.empty(D.shape, dtype=f32, device=dev),
-           "dz": None if z is None else torch.empty(x.shape, dtype=ty, device=dev),
-           "ddt_bias": None if dt_bias is None else torch.empty(dt_bias.shape, dtype=f32,
-                                                                device=dev),
-           "dstate": torch.empty(state, dtype=f32, device=dev)}
-    g.dx, g.ddt, g.dA = out["dx"].data_ptr(), out["ddt"].data_ptr(), out["dA"].data_ptr()
-    g.dB, g.dC, g.dinitial = out["dB"].data_ptr(), out["dC"].data_ptr(), out["dstate"].data_ptr()
-    for name in ("dD", "dz", "ddt_bias"):
-        if out[name] is not None:
-            setattr(g, name, out[name].data_ptr())
-    scratch = _scratch(scratch, L.selective_scan_grad_scratch_bytes(a), dev)
+    dyp = _rows(dy, "dy", x.shape, ty, dev)
+    df = _opt(dfinal, "dfinal", state, f32, dev)
+    sp = _like(starts, "starts", (L.selective_scan_starts_bytes(a) // 4,), f32, dev)
+    rows = B.shape
+    out = {"dx": _new(x.shape, ty, dev, stream), "ddt": _new(x.shape, ty, dev, stream),
+           "dA": _new(A.shape, f32, dev, stream), "dB": _new(rows, ty, dev, stream),
+           "dC": _new(rows, ty, dev, stream),
+           "dD": None if D is None else _new(D.shape, f32, dev, stream),
+           "dz": None if z is None else _new(x.shape, ty, dev, stream),
+           "ddt_bias": None if dt_bias is None else _new(dt_bias.shape, f32, dev, stream),
+           "dstate": _new(state, f32, dev, stream)}
+    p = {k: None if v is None else v.data_ptr() for k, v in out.items()}
+    g = ScanGrads(dyp, dy.stride()[:2], df, sp, p["dx"], p["ddt"], p["dB"], p["dC"], p["dz"],
+                  p["dA"], p["dD"], p["ddt_bias"], p["dstate"])
+    scratch = _scratch(scratch, L.selective_scan_grad_scratch_bytes(a), dev, stream)
     check(L.selective_scan_grad(a, g, scratch.data_ptr(), scratch.numel(), _stream(stream)))
     return out
 
@@ -252,7 +256,7 @@ def selective_scan_step(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, sof
     shape = (a.batch, a.channels, a.states)
     sp = _like(state, "state", shape, torch.float32, x.device)
     np_ = sp if new_state is None else _like(new_state, "new_state", shape, torch.float32, x.device)
-    y = _out(out, "out", tuple(x.shape), x.dtype, x.device)
+    y = _out(out, "out", x.shape, x.dtype, x.device, stream)
     check(lib().selective_scan_step(a, sp, np_, y.data_ptr(), _stream(stream)))
     return y
 
@@ -279,7 +283,7 @@ def embedding(weight, ids, scale=1.0, out=None, stream=None):
     code, stride = _table(weight, "weight")
     idc = _id_code(ids, weight.device)
     rows, d = weight.shape
-    out = _out(out, "out", tuple(ids.shape) + (d,), weight.dtype, weight.device)
+    out = _out(out, "out", ids.shape + (d,), weight.dtype, weight.device, stream)
     check(lib().embedding(weight.data_ptr(), ids.data_ptr(), out.data_ptr(), ids.numel(), rows, d,
                           stride, code, idc, float(scale), _stream(stream)))
     return out
@@ -298,10 +302,11 @@ def embedding_grad(dout, ids, rows, scale=1.0, dtype=None, out=None, scratch=Non
     dtype = dtype or (out.dtype if out is not None else dout.dtype)
     if dtype not in (dout.dtype, torch.float32):
         raise NotImplementedError("the gradient is of dout's type or float32")
-    out = _out(out, "out", (int(rows), d), dtype, dout.device)
+    out = _out(out, "out", (int(rows), d), dtype, dout.device, stream)
     L = lib()
     n = ids.numel()
-    scratch = _scratch(scratch, L.embedding_grad_scratch_bytes(n, rows, d), dout.device)
+    scratch = _scratch(scratch, L.embedding_grad_scratch_bytes(n, rows, d), dout.device,
+                       stream)
     check(L.embedding_grad(flat.data_ptr(), ids.data_ptr(), out.data_ptr(), n, rows, d, stride,
                            code, idc, _ACT[dtype], float(scale), scratch.data_ptr(),
                            scratch.numel(), _stream(stream)))
