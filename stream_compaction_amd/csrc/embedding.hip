@@ -73,7 +73,8 @@ __global__ __launch_bounds__(256) void embedding_zero_kernel(uint4* out, int64_t
 // counts its rows per wave (a wave owns consecutive tokens) and places its
 // tokens in token order.  It also writes zeros to its rows: the segments'
 // kernel overwrites those that have a token, which costs less than waiting for
-// the counts before the first store.  Every id is read by every workgroup, from
+// the counts before the first store (the barriers between wait
+// for LDS alone).  Every id is read by every workgroup, from
 // L2: 64 MB for 16384 ids and 512 workgroups, against the four passes over the
 // list and the seven launches of the general path.
 constexpr int kBucketRows = 256;
@@ -122,11 +123,15 @@ __global__ __launch_bounds__(64 * kBucketWaves) void embedding_bucket_kernel(
     const int i = first + k * 64;
     row[k] = k < its && i < tokens ? (uint32_t)token_row(ids, i, rows) : kNone;
   }
-  {
+  // half of the workgroups write their zeros before the sort, half after it, so
+  // that some always keep the memory busy
+  auto clear = [&]() {
     const int64_t left = rows - lo, mine = left < bucket ? left : bucket;
     const uintptr_t a = (uintptr_t)dweight + (uintptr_t)(lo * row_bytes);
     zero_span(a, a + (uintptr_t)(mine * row_bytes), unit);
-  }
+  };
+  const bool late = blockIdx.x / 8 % 2 != 0;
+  if (!late) clear();
 #pragma unroll
   for (int k = 0; k < kBucketIds; ++k) {
     below += (uint32_t)__popcll(__ballot(row[k] < lo));
@@ -134,7 +139,7 @@ __global__ __launch_bounds__(64 * kBucketWaves) void embedding_bucket_kernel(
     if (rel[k] != kNone) atomicAdd(&s_off[wave][rel[k]], 1u);
   }
   if (lane == 0) s_below[wave] = below;
-  __syncthreads();
+  lds_barrier();
   uint32_t count = 0, incl = 0;
   if (threadIdx.x < kBucketRows) {
     // per row: where each wave's tokens begin among the row's, and their number
@@ -147,7 +152,7 @@ __global__ __launch_bounds__(64 * kBucketWaves) void embedding_bucket_kernel(
     incl = wave_scan_incl<Op::Add>(count);
     if (lane == kWave - 1) s_sum[wave] = incl;
   }
-  __syncthreads();
+  lds_barrier();
   uint32_t base = 0, all = 0;
 #pragma unroll
   for (int w = 0; w < kBucketWaves; ++w) base += s_below[w];
@@ -157,7 +162,7 @@ __global__ __launch_bounds__(64 * kBucketWaves) void embedding_bucket_kernel(
     all += s_sum[w];
   }
   if (threadIdx.x < kBucketRows) s_start[threadIdx.x] = base + incl - count;
-  __syncthreads();
+  lds_barrier();
 
 #pragma unroll
   for (int k = 0; k < kBucketIds; ++k) {
@@ -192,6 +197,7 @@ __global__ __launch_bounds__(64 * kBucketWaves) void embedding_bucket_kernel(
       keys[i] = (uint32_t)rows;
       pos[i] = 0;
     }
+  if (late) clear();
 }
 
 constexpr int kSegAhead = 8;      // gradient rows loaded together
@@ -301,28 +307,38 @@ __global__ __launch_bounds__(256) void embedding_border_kernel(const uint32_t* _
     if (k >= (uint32_t)rows || keys[end] != k) continue;  // no run continues past this segment
     if (s0 > 0 && keys[s0 - 1] == k) continue;            // it began in an earlier one
     const int64_t ch = (col * 256 + threadIdx.x) * E;
+    // pieces after the first: up to the first segment that does not go on
+    int64_t pieces = 0;
+    for (bool more = true; more;) {
+      const int64_t e = (seg + 2 + pieces + lane_id()) * seg_tokens;
+      const bool on = e < tokens && keys[e < tokens ? e - 1 : 0] == k && keys[e < tokens ? e : 0] == k;
+      const uint64_t stop = __ballot(!on);
+      more = stop == 0;
+      pieces += more ? kWave : __ffsll((unsigned long long)stop);
+    }
     if (ch >= channels) continue;
     float sum[E];
     IO::unpack(IO::load(part + (seg * 2 + 1) * channels + ch, E, E > 1), sum);
-    bool more = true;
-    for (int64_t s = seg + 1; more; s += kAhead) {
-      typename IO::Raw v[kAhead];
-      bool on[kAhead];                                    // the run goes on past segment s + j
+    const float* from = part + (seg + 1) * 2 * channels + ch;
+    typename IO::Raw next[kAhead];
+    auto fetch = [&](int64_t p0) {
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        // past the list's end the last entries are read again, without use
-        const int64_t e = (s + j + 1) * seg_tokens, r = s + j < segs ? s + j : segs - 1;
-        v[j] = IO::load(part + r * 2 * channels + ch, E, E > 1);
-        const int64_t i = e < tokens ? e : tokens - 1;
-        on[j] = (keys[i - 1] == k) & (keys[i] == k) & (e < tokens);
-      }
+      for (int j = 0; j < kAhead; ++j)
+        next[j] = p0 + j < pieces ? IO::load(from + (p0 + j) * 2 * channels, E, E > 1)
+                                  : typename IO::Raw{};
+    };
+    fetch(0);
+    for (int64_t p0 = 0; p0 < pieces; p0 += kAhead) {
+      typename IO::Raw v[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) v[j] = next[j];
+      fetch(p0 + kAhead);
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         float x[E];
         IO::unpack(v[j], x);
 #pragma unroll
-        for (int c = 0; c < E; ++c) sum[c] = more ? sum[c] + x[c] : sum[c];
-        more = more && on[j];
+        for (int c = 0; c < E; ++c) sum[c] += x[c];       // past the pieces: + 0
       }
     }
 #pragma unroll

@@ -144,6 +144,12 @@ __device__ __forceinline__ float wave_sum(float v) {
   return readlane(wave_scan_incl<Op::Add>(v), kWave - 1);
 }
 
+// A barrier for data that waves exchange through LDS: unlike __syncthreads() it
+// does not wait for the wave's global loads and stores.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 // Logical workgroup index: hardware deals consecutive workgroups to the 8
 // XCDs in turn, each with its own L2.  Runs of 4 logical neighbours (which share
 // the 128-byte lines of the activations) are put on one XCD and the runs dealt
