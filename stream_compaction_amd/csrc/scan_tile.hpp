@@ -17,6 +17,7 @@
 
 namespace sca {
 
+constexpr int kRowRor1 = 0x121;                // DPP: rotate each row of 16 lanes right by one
 constexpr int kScanWaves = 8;
 constexpr int kScanThreads = 64 * kScanWaves;
 constexpr int kScanTile = 2 * kScanWaves;      // channels per workgroup
@@ -93,6 +94,25 @@ __device__ __forceinline__ void affine_scan2(float& H0, float& H1, float& P0, fl
 }
 #undef SCA_AFFINE_STEP
 
+// The same within each row of 16 lanes, one sequence per row.  P is left
+// undefined.  An instruction and a wait state lie between a write and the DPP
+// read of the same register.
+#define SCA_ROW_STEP(SHIFT)                                                    \
+  "v_fmac_f32_dpp %0, %0, %1 row_shr:" SHIFT " row_mask:0xf bank_mask:0xf\n\t"  \
+  "v_mul_f32_dpp %1, %1, %1 row_shr:" SHIFT " row_mask:0xf bank_mask:0xf\n\t"   \
+  "s_nop 0\n\t"
+__device__ __forceinline__ void row_affine_scan(float& H, float& P) {
+  asm volatile(
+      "s_nop 1\n\t"
+      SCA_ROW_STEP("1")
+      SCA_ROW_STEP("2")
+      SCA_ROW_STEP("4")
+      "v_fmac_f32_dpp %0, %0, %1 row_shr:8 row_mask:0xf bank_mask:0xf\n\t"
+      "s_nop 1"
+      : "+v"(H), "+v"(P));
+}
+#undef SCA_ROW_STEP
+
 // One array of activations [batch, length, channels] as a workgroup sees it:
 // its sequence and first channel.
 template <class F> struct TileSrc {
@@ -108,6 +128,32 @@ __device__ __forceinline__ TileSrc<F> tile_src(const void* base, int64_t batch_s
   s.p = (const S*)base + b * batch_stride + ch;
   s.token = token_stride;
   s.vec = ((uintptr_t)s.p % 16 == 0) && ((token_stride * (int64_t)sizeof(S)) % 16 == 0);
+  return s;
+}
+
+// The same by pairs of neighbours: a thread's pair (thread % 8) of its token
+// (thread / 8) of the block, moving on by blocks.
+template <class F> struct PairSrc {
+  using IO = RowIO<F, 2>;
+  const typename F::S* p;
+  int64_t step;
+  bool vec;
+  // of the pair (and `off` elements on) those below n exist
+  __device__ __forceinline__ typename IO::Raw load(int n, int off = 0) const {
+    return IO::load(p + off, n - off - (int)(threadIdx.x % 8) * 2, vec);
+  }
+  __device__ __forceinline__ void next() { p += step; }
+};
+template <class F>
+__device__ __forceinline__ PairSrc<F> pair_src(const void* base, int64_t batch_stride,
+                                               int64_t token_stride, int64_t b, int64_t off,
+                                               int block) {
+  using S = typename F::S;
+  PairSrc<F> s;
+  const S* at = (const S*)base + b * batch_stride + off;
+  s.vec = ((uintptr_t)at % (2 * sizeof(S)) == 0) && token_stride % 2 == 0;
+  s.p = at + (int64_t)(threadIdx.x / 8) * token_stride + threadIdx.x % 8 * 2;
+  s.step = block * token_stride;
   return s;
 }
 

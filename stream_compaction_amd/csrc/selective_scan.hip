@@ -4,175 +4,280 @@
 // per channel, with `states` states each.  See scan_tile.hpp for the mapping.
 #include "scan_tile.hpp"
 
+#include <utility>
+
 namespace sca {
 
-template <class F, int K, int NG>
-__global__ __launch_bounds__(kScanThreads) void selective_scan_kernel(ScanProblem p, void* yv,
-                                                                     float* final_state,
-                                                                     float* starts, int64_t b0,
-                                                                     int64_t tiles,
-                                                                     uint32_t count) {
-  using S = typename F::S;
-  using Tile = TileStage<F, K>;
-  using Rows = RowStage<F, K, NG>;
-  constexpr int TB = 64 * K;
-  __shared__ alignas(16) float s_B[NG * TB], s_C[NG * TB];
-  __shared__ alignas(16) uint32_t s_x[Tile::WORDS], s_dt[Tile::WORDS], s_z[Tile::WORDS];
+namespace {
 
-  const int lane = lane_id(), wave = wave_id();
+// Forward.  A lane owns one channel and NS of its states and walks the tokens in
+// order: per token and state a product and an exponential for the decay, a
+// product for the input, a multiply-add for the state and a product with C,
+// which is what the definition asks for and no more, so the kernel is bound by
+// these vector instructions.  Lanes 16 r .. 16 r + 15 of wave w hold 16
+// channels' state w 4 + r (+ 16, ...): B and C are the same for a row of 16
+// lanes, so a lane holds them for one of 16 tokens and the products take them by
+// DPP row broadcast, without an instruction or an LDS read per token.
+//
+// A workgroup (4 waves) owns 16 channels of one sequence, in blocks of T tokens.
+// Its threads turn dt into steps and products with x, once per element, and
+// stage them and B and C in LDS as float32 planes of one value per token; the
+// sums over a wave's states are left there too, and the block's outputs are put
+// together from them.  Everything is buffered twice: one barrier per block.
+constexpr int kT = 32;                  // tokens per block
+constexpr int kPS = kT + 4;             // plane stride: 16 channels' 16-byte reads, and the
+                                        // pairs' stores, fall on different banks
+constexpr int kPlane = kScanTile * kPS;
+constexpr int kFwdThreads = 256;        // T tokens of 8 channel pairs
+
+// v = the row's lane T of `from`, for all its lanes (folds into the product)
+template <int T> __device__ __forceinline__ float row_bcast(float from) {
+  return dpp<0x150 + T, 0xf>(from, 0.0f);
+}
+
+// Sums over the four rows of 16 lanes of 16 values: row r gets values 4 r .. 4 r
+// + 3.  The swaps exchange halves (then rows) of a pair of registers, so that one
+// addition serves two values.
+__device__ __forceinline__ float swapped_sum32(float a, float b) {
+  const auto q = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, a),
+                                                  __builtin_bit_cast(uint32_t, b), false, false);
+  const uint32_t x = q[0], y = q[1];
+  return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+__device__ __forceinline__ float swapped_sum16(float a, float b) {
+  const auto q = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, a),
+                                                  __builtin_bit_cast(uint32_t, b), false, false);
+  const uint32_t x = q[0], y = q[1];
+  return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+__device__ __forceinline__ void rows_sum(const float (&v)[16], float (&out)[4]) {
+  float s[8];
+#pragma unroll
+  for (int t = 0; t < 8; ++t) s[t] = swapped_sum32(v[t], v[t + 8]);
+#pragma unroll
+  for (int t = 0; t < 4; ++t) out[t] = swapped_sum16(s[t], s[t + 4]);
+}
+
+template <class Fn, int... T>
+__device__ __forceinline__ void for_tokens(Fn&& fn, std::integer_sequence<int, T...>) {
+  (fn(std::integral_constant<int, T>{}), ...);
+}
+
+}  // namespace
+
+template <class F, int NS>
+__global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
+    ScanProblem p, void* yv, float* final_state, float* starts, int64_t start_tokens, int64_t b0,
+    int64_t tiles, uint32_t count) {
+  using S = typename F::S;
+  using IO = RowIO<F, 2>;
+  using Raw = typename IO::Raw;
+  typedef float vec4 __attribute__((ext_vector_type(4)));
+  __shared__ alignas(16) float s_x[2][2 * kPlane];           // steps, steps times x
+  __shared__ alignas(16) float s_bc[2][2 * NS * kPlane];     // B, C
+  __shared__ alignas(16) float s_part[2][4 * kPlane];        // per wave
+
   const uint32_t id = xcd_order(blockIdx.x);
   if (id >= count) return;
   const ScanPlace at = scan_place(p, b0, tiles, id);
   const int64_t len = scan_length(p, at.b);
-  const int N = (int)p.states;
+  const int N = (int)p.states, nch = (int)at.nch;
   const bool gate = p.z != nullptr;
-  const auto xs = tile_src<F>(p.x, p.x_batch, p.x_token, at.b, at.ch);
-  const auto dts = tile_src<F>(p.dt, p.dt_batch, p.dt_token, at.b, at.ch);
-  const auto zs = tile_src<F>(p.z, p.z_batch, p.z_token, at.b, at.ch);
-  const auto Bs = tile_src<F>(p.B, p.B_batch, p.B_token, at.b, at.g * p.B_group);
-  const auto Cs = tile_src<F>(p.C, p.C_batch, p.C_token, at.b, at.g * p.C_group);
+  const int tid = (int)threadIdx.x, lane = lane_id(), wave = wave_id();
+  const int row = lane / 16, cl = lane % 16;
+  const int n0 = wave * 4 + row;                // this lane's states: n0, n0 + 16, ...
+  const int64_t ch = at.ch + cl;
+
+  // staging: this thread's token and two channels (and two states of each 16)
+  const int tok = tid / 8, pair = tid % 8;
+  const bool stager = pair * 2 < nch;
+  auto xs = pair_src<F>(p.x, p.x_batch, p.x_token, at.b, at.ch, kT);
+  auto dts = pair_src<F>(p.dt, p.dt_batch, p.dt_token, at.b, at.ch, kT);
+  auto zs = pair_src<F>(p.z, p.z_batch, p.z_token, at.b, at.ch, kT);
+  auto Bs = pair_src<F>(p.B, p.B_batch, p.B_token, at.b, at.g * p.B_group, kT);
+  auto Cs = pair_src<F>(p.C, p.C_batch, p.C_token, at.b, at.g * p.C_group, kT);
   S* y = (S*)yv + at.b * p.length * p.channels + at.ch;
-  const bool yvec = (uintptr_t)y % 16 == 0 && (p.channels * (int64_t)sizeof(S)) % 16 == 0;
-
-  // lane n of these registers holds state n of the wave's two channels
-  float A2[2], carry[2], Dc[2], bias[2];
-  bool live[2];
-  int64_t row[2];
+  const bool vy = (uintptr_t)y % (2 * sizeof(S)) == 0 && p.channels % 2 == 0;
+  float Dc[2], bias[2];
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    live[c] = 2 * wave + c < at.nch;
-    const int64_t ch = at.ch + 2 * wave + c;
-    row[c] = (at.b * p.channels + ch) * N + lane;
-    const bool on = live[c] && lane < N;
-    A2[c] = on ? p.A[ch * N + lane] * kLog2e : 0.0f;
-    carry[c] = on && p.initial_state != nullptr ? p.initial_state[row[c]] : 0.0f;
-    Dc[c] = live[c] && p.D != nullptr ? p.D[ch] : 0.0f;
-    bias[c] = live[c] && p.dt_bias != nullptr ? p.dt_bias[ch] : 0.0f;
+  for (int i = 0; i < 2; ++i) {
+    const bool on = pair * 2 + i < nch;
+    Dc[i] = on && p.D != nullptr ? p.D[at.ch + pair * 2 + i] : 0.0f;
+    bias[i] = on && p.dt_bias != nullptr ? p.dt_bias[at.ch + pair * 2 + i] : 0.0f;
+  }
+  float A2[NS], h[NS];
+  bool mine[NS];
+  const int64_t srow = (at.b * p.channels + ch) * N;
+#pragma unroll
+  for (int s = 0; s < NS; ++s) {
+    const int n = n0 + s * 16;
+    mine[s] = cl < nch && n < N;
+    A2[s] = mine[s] ? p.A[ch * N + n] * kLog2e : 0.0f;
+    h[s] = mine[s] && p.initial_state != nullptr ? p.initial_state[srow + n] : 0.0f;
   }
 
-  Tile rx, rdt, rz;
-  Rows rB, rC;
-  auto fetch = [&](int64_t t0) {
-    rx.load(xs, t0, len, at.nch);
-    rdt.load(dts, t0, len, at.nch);
-    if (gate) rz.load(zs, t0, len, at.nch);
+  // two blocks are in flight: fetched[i] holds one of them, then the block's x and
+  // z until its outputs are due
+  struct Fetched { Raw x, dt, z, B[NS], C[NS]; };
+  auto fetch = [&](Fetched& f, int64_t t0) {
+    const bool exists = t0 + tok < len;
+    f.x = f.dt = f.z = Raw{};
+    if (stager && exists) {
+      f.x = xs.load(nch);
+      f.dt = dts.load(nch);
+      if (gate) f.z = zs.load(nch);
+    }
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      f.B[s] = f.C[s] = Raw{};
+      if (exists && s * 16 + pair * 2 < N) {
+        f.B[s] = Bs.load(N, s * 16);
+        f.C[s] = Cs.load(N, s * 16);
+      }
+    }
+    xs.next();
+    dts.next();
+    zs.next();
+    Bs.next();
+    Cs.next();
   };
-  const int64_t blocks = (len + TB - 1) / TB;
-  if (blocks > 0) {
-    fetch(0);
-    rB.load(Bs, 0, len, 0, N);
-    rC.load(Cs, 0, len, 0, N);
-  }
-  for (int64_t blk = 0; blk < blocks; ++blk) {
-    const int64_t t0 = blk * TB;
-    __syncthreads();                       // the last block's LDS is free
-    rx.put(s_x);
-    rdt.put(s_dt);
-    if (gate) rz.put(s_z);
+  // the fetched block into buffer `buf`; tokens past the end get step 0 (a = 1, b = 0)
+  auto stage = [&](const Fetched& f, int64_t t0, int buf) {
+    float x[2], dt[2], v[2];
+    IO::unpack(f.x, x);
+    IO::unpack(f.dt, dt);
+    const bool exists = t0 + tok < len;
+    float* to = s_x[buf] + pair * 2 * kPS + tok;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float raw = dt[i] + bias[i];
+      float d = p.softplus ? softplus(raw) : raw;
+      d = exists ? d : 0.0f;
+      to[i * kPS] = d;
+      to[kPlane + i * kPS] = d * x[i];
+    }
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      float* bc = s_bc[buf] + (s * 16 + pair * 2) * kPS + tok;
+      IO::unpack(f.B[s], v);
+      bc[0] = v[0];
+      bc[kPS] = v[1];
+      IO::unpack(f.C[s], v);
+      bc[NS * kPlane] = v[0];
+      bc[NS * kPlane + kPS] = v[1];
+    }
+  };
+  const bool busy = wave * 4 < N;               // waves whose states do not exist only stage
+  auto walk = [&](int buf) {
+#pragma unroll
+    for (int sub = 0; sub < kT; sub += 16) {
+      const float* xp = s_x[buf] + cl * kPS + sub;
+      float dt[16], u[16], v[16], sums[4];
+#pragma unroll
+      for (int t = 0; t < 16; t += 4) {
+        const vec4 d = *(const vec4*)(xp + t), w = *(const vec4*)(xp + kPlane + t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          dt[t + i] = d[i];
+          u[t + i] = w[i];
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        const float* bc = s_bc[buf] + (s * 16 + n0) * kPS + sub + cl;
+        const float B = bc[0], C = bc[NS * kPlane];
+        for_tokens([&](auto tc) {
+          constexpr int t = decltype(tc)::value;
+          const float a = exp2_hw(dt[t] * A2[s]);
+          h[s] = __builtin_fmaf(a, h[s], row_bcast<t>(B) * u[t]);
+          if (s == 0) {
+            v[t] = row_bcast<t>(C) * h[s];
+          } else {
+            v[t] = __builtin_fmaf(row_bcast<t>(C), h[s], v[t]);
+          }
+        }, std::make_integer_sequence<int, 16>{});
+      }
+      rows_sum(v, sums);
+      *(vec4*)(s_part[buf] + (wave * 16 + cl) * kPS + sub + row * 4) =
+          vec4{sums[0], sums[1], sums[2], sums[3]};
+    }
+  };
+  auto finish = [&](Raw fx, Raw fz, int64_t t0, int buf) {
+    if (!stager || t0 + tok >= len) return;
+    float x[2], z[2], out[2];
+    IO::unpack(fx, x);
+    IO::unpack(fz, z);
+    const float* from = s_part[buf] + pair * 2 * kPS + tok;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float v = Dc[i] * x[i];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) v += from[w * kPlane + i * kPS];
+      out[i] = gate ? v * silu(z[i]) : v;
+    }
+    IO::store(y + (t0 + tok) * p.channels + pair * 2, IO::pack(out), nch - pair * 2, vy);
+  };
+
+  const int64_t blocks = (len + kT - 1) / kT;
+  const int64_t nkeep = starts != nullptr ? (p.length + start_tokens - 1) / start_tokens : 0;
+  float* keep = starts + ((at.b * nkeep) * p.channels + ch) * N + n0;
+  int64_t until = 0;                            // tokens until the next state kept
+  Fetched f[2];
+  // block t0 is staged in buffer `buf` and its x and z are in nx and nz; `next`
+  // holds the block after it and gets the third one from here
+  Raw nx, nz;
+  auto step = [&](Fetched& next, int64_t t0, int buf) {
+    const Raw fx = nx, fz = nz;
+    nx = next.x;
+    nz = next.z;
+    stage(next, t0 + kT, buf ^ 1);
+    fetch(next, t0 + 3 * kT);
     if (starts != nullptr) {
+      if (until == 0) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        if (live[c] && lane < N) {
-          const int64_t nblk = (p.length + TB - 1) / TB;
-          const int64_t ch = at.ch + 2 * wave + c;
-          starts[((at.b * nblk + blk) * p.channels + ch) * N + lane] = carry[c];
-        }
-    }
-    rB.put(s_B);
-    rC.put(s_C);
-    __syncthreads();
-    float dt[K][2], u[K][2], acc[K][2], span[2];
-    Tile::get(s_x, wave, lane, u);
-    Tile::get(s_dt, wave, lane, dt);
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      float total = 0.0f;
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const float raw = dt[k][c] + bias[c];
-        const float d = p.softplus ? softplus(raw) : raw;
-        dt[k][c] = t0 + lane * K + k < len ? d : 0.0f;   // past the end: a = 1, b = 0
-        total += dt[k][c];
-        acc[k][c] = Dc[c] * u[k][c];
-        u[k][c] *= dt[k][c];
+        for (int s = 0; s < NS; ++s)
+          if (mine[s]) keep[s * 16] = h[s];
+        keep += p.channels * N;
+        until = start_tokens;
       }
-      span[c] = total;
+      until -= kT;
     }
-    for (int n0 = 0; n0 < N; n0 += NG) {
-      if (n0 > 0) {
-        __syncthreads();
-        rB.put(s_B);
-        rC.put(s_C);
-        __syncthreads();
-      }
-      // the next rows (of this block or the next) travel while these are used
-      if (n0 + NG < N) {
-        rB.load(Bs, t0, len, n0 + NG, N);
-        rC.load(Cs, t0, len, n0 + NG, N);
-      } else if (blk + 1 < blocks) {
-        fetch(t0 + TB);
-        rB.load(Bs, t0 + TB, len, 0, N);
-        rC.load(Cs, t0 + TB, len, 0, N);
-      }
-      const int nn = N - n0 < NG ? N - n0 : NG;
-      for (int i = 0; i < nn; ++i) {
-        const int n = n0 + i;
-        float Bk[K], Ck[K];
-        plane_read<K>(s_B + i * TB, lane, Bk);
-        plane_read<K>(s_C + i * TB, lane, Ck);
-        float a[2][K], b[2][K], P[2], H[2], h0[2];
+    if (busy) walk(buf);
+    lds_barrier();
+    finish(fx, fz, t0, buf);
+  };
+  if (blocks > 0) {
+    fetch(f[0], 0);
+    fetch(f[1], kT);
+    nx = f[0].x;
+    nz = f[0].z;
+    stage(f[0], 0, 0);
+    fetch(f[0], 2 * kT);
+    if (!busy && row == 0) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float An = readlane(A2[c], n);
-          float h = 0.0f;
+      for (int t = 0; t < kT; t += 4)
 #pragma unroll
-          for (int k = 0; k < K; ++k) {
-            a[c][k] = exp2_hw(dt[k][c] * An);
-            b[c][k] = u[k][c] * Bk[k];
-            h = __builtin_fmaf(a[c][k], h, b[c][k]);
-          }
-          P[c] = exp2_hw(span[c] * An);
-          h0[c] = readlane(carry[c], n);
-          // the block's start enters through the first lane
-          H[c] = __builtin_fmaf(P[c], lane == 0 ? h0[c] : 0.0f, h);
-        }
-        affine_scan2(H[0], H[1], P[0], P[1]);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          carry[c] = lane == n ? readlane(H[c], kWave - 1) : carry[c];
-          float h = dpp<kWaveShr1, 0xf>(H[c], h0[c]);
-#pragma unroll
-          for (int k = 0; k < K; ++k) {
-            h = __builtin_fmaf(a[c][k], h, b[c][k]);
-            acc[k][c] = __builtin_fmaf(Ck[k], h, acc[k][c]);
-          }
-        }
-      }
+        for (int q = 0; q < 2; ++q)
+          *(vec4*)(s_part[q] + (wave * 16 + cl) * kPS + t) = vec4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    if (gate) {
-      float zv[K][2];
-      Tile::get(s_z, wave, lane, zv);
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int k = 0; k < K; ++k) acc[k][c] *= silu(zv[k][c]);
+    lds_barrier();
+    for (int64_t blk = 0; blk < blocks; blk += 2) {
+      step(f[1], blk * kT, 0);
+      if (blk + 1 < blocks) step(f[0], (blk + 1) * kT, 1);
     }
-    Tile::set(s_x, wave, lane, acc);       // the wave's own planes, read above by itself alone
-    __syncthreads();
-    Tile::store(s_x, y, p.channels, yvec, t0, len, at.nch);
   }
   // tokens past the sequence's end
-  for (int64_t i = len * kScanTile + threadIdx.x; i < p.length * kScanTile; i += kScanThreads)
-    if (i % kScanTile < at.nch) y[(i / kScanTile) * p.channels + i % kScanTile] = S(0);
+  for (int64_t i = len * kScanTile + tid; i < p.length * kScanTile; i += kFwdThreads)
+    if (i % kScanTile < nch) y[(i / kScanTile) * p.channels + i % kScanTile] = S(0);
+  if (final_state == nullptr) return;
 #pragma unroll
-  for (int c = 0; c < 2; ++c)
-    if (live[c] && lane < N && final_state != nullptr) final_state[row[c]] = carry[c];
+  for (int s = 0; s < NS; ++s)
+    if (mine[s]) final_state[srow + n0 + s * 16] = h[s];
 }
 
-// Tokens per lane by length: the smallest block that holds the sequence, up
-// to 512 tokens (256 in float32, whose planes are twice as large).  A lane that
-// owns more tokens pays the cross-lane scan (about 20 instructions per channel
-// and state) fewer times; a block longer than the sequence leaves lanes idle.
+// Tokens between the states that the forward keeps for the gradient, which
+// works in blocks of as many: 64 tokens by the power of two that holds a short
+// sequence, up to 512 (256 in float32, whose planes are twice as large).
 static int scan_k(int64_t length, Fmt fmt) {
   if (length <= 64) return 1;
   if (length <= 128) return 2;
@@ -182,44 +287,39 @@ int64_t scan_block_tokens(int64_t length, Fmt fmt) { return 64 * scan_k(length, 
 
 // Workgroups of a launch: grid sizes count work-items in 32 bits, so batches
 // beyond that go out as several launches.
-constexpr int64_t kMaxGroups = 1ll << 22;
+constexpr int64_t kMaxGroups = 1ll << 21;
 
-template <class F, int K>
+template <class F>
 static hipError_t launch_fwd(const ScanProblem& p, void* y, float* final_state, float* starts,
-                             hipStream_t stream) {
+                             int64_t start_tokens, hipStream_t stream) {
   const int64_t tiles = (p.channels / p.groups + kScanTile - 1) / kScanTile;
   const int64_t per = tiles * p.groups;
   const int64_t step = kMaxGroups / per < 1 ? 1 : kMaxGroups / per;
   for (int64_t b0 = 0; b0 < p.batch; b0 += step) {
     const int64_t nb = p.batch - b0 < step ? p.batch - b0 : step;
-    selective_scan_kernel<F, K, sizeof(typename F::S) == 2 ? 16 : 8>
-        <<<dim3(xcd_grid(nb * per)), dim3(kScanThreads), 0, stream>>>(
-            p, y, final_state, starts, b0, tiles, (uint32_t)(nb * per));
+    auto go = [&](auto ns) {
+      selective_scan_kernel<F, decltype(ns)::value>
+          <<<dim3(xcd_grid(nb * per)), dim3(kFwdThreads), 0, stream>>>(
+              p, y, final_state, starts, start_tokens, b0, tiles, (uint32_t)(nb * per));
+    };
+    if (p.states <= 16) {
+      go(std::integral_constant<int, 1>{});
+    } else if (p.states <= 32) {
+      go(std::integral_constant<int, 2>{});
+    } else {
+      go(std::integral_constant<int, 4>{});
+    }
   }
   return hipGetLastError();
 }
 
-template <class F>
-static hipError_t launch_fwd_f(const ScanProblem& p, Fmt fmt, void* y, float* final_state,
-                               float* starts, hipStream_t stream) {
-  switch (scan_k(p.length, fmt)) {
-    case 1: return launch_fwd<F, 1>(p, y, final_state, starts, stream);
-    case 2: return launch_fwd<F, 2>(p, y, final_state, starts, stream);
-    case 4: return launch_fwd<F, 4>(p, y, final_state, starts, stream);
-    default:
-      if constexpr (sizeof(typename F::S) == 2) {
-        return launch_fwd<F, 8>(p, y, final_state, starts, stream);
-      }
-      return hipErrorInvalidValue;
-  }
-}
-
 hipError_t launch_selective_scan(const ScanProblem& p, Fmt fmt, void* y, float* final_state,
                                  float* starts, hipStream_t stream) {
+  const int64_t keep = scan_block_tokens(p.length, fmt);
   switch (fmt) {
-    case Fmt::F32: return launch_fwd_f<FmtF32>(p, fmt, y, final_state, starts, stream);
-    case Fmt::F16: return launch_fwd_f<FmtF16>(p, fmt, y, final_state, starts, stream);
-    case Fmt::BF16: return launch_fwd_f<FmtBF16>(p, fmt, y, final_state, starts, stream);
+    case Fmt::F32: return launch_fwd<FmtF32>(p, y, final_state, starts, keep, stream);
+    case Fmt::F16: return launch_fwd<FmtF16>(p, y, final_state, starts, keep, stream);
+    case Fmt::BF16: return launch_fwd<FmtBF16>(p, y, final_state, starts, keep, stream);
     default: return hipErrorInvalidValue;
   }
 }

@@ -147,7 +147,9 @@ __device__ __forceinline__ float wave_sum(float v) {
 // A barrier for data that waves exchange through LDS: unlike __syncthreads() it
 // does not wait for the wave's global loads and stores.
 __device__ __forceinline__ void lds_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 // Logical workgroup index: hardware deals consecutive workgroups to the 8
