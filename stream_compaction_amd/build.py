@@ -35,11 +35,15 @@ CFLAGS = [
     "-Wall", "-Wno-unused-command-line-argument",
     "-I", os.path.join(ROOT, "include"),
 ]
+# Pairing float operations into vectors gains nothing without packed instructions, and
+# keeps broadcasts across lanes from folding into the products that use them.
+FILE_FLAGS = {"selective_scan.hip": ["-fno-slp-vectorize"],
+              "selective_scan_grad.hip": ["-fno-slp-vectorize"]}
 
 
 def compile_cmd(src, obj, defines=()):
     lang = ["-x", "hip"] if src.endswith(".cpp") else []
-    return [HIPCC, *CFLAGS, *defines, *lang, "-c", os.path.join(CSRC, src), "-o", obj]
+    return [HIPCC, *CFLAGS, *FILE_FLAGS.get(src, ()), *defines, *lang, "-c", os.path.join(CSRC, src), "-o", obj]
 
 
 def build(verbose=False):

@@ -132,30 +132,56 @@ __device__ __forceinline__ TileSrc<F> tile_src(const void* base, int64_t batch_s
 }
 
 // The same by pairs of neighbours: a thread's pair (thread % 8) of its token
-// (thread / 8) of the block, moving on by blocks.
-template <class F> struct PairSrc {
-  using IO = RowIO<F, 2>;
-  const typename F::S* p;
-  int64_t step;
-  bool vec;
-  // of the pair (and `off` elements on) those below n exist
-  __device__ __forceinline__ typename IO::Raw load(int n, int off = 0) const {
-    return IO::load(p + off, n - off - (int)(threadIdx.x % 8) * 2, vec);
-  }
-  __device__ __forceinline__ void next() { p += step; }
-};
-template <class F>
-__device__ __forceinline__ PairSrc<F> pair_src(const void* base, int64_t batch_stride,
-                                               int64_t token_stride, int64_t b, int64_t off,
-                                               int block) {
+// (thread / 8) of a block, block after block.  Loads are never skipped: a
+// thread whose token or pair does not exist reads one that does (the caller
+// drops it), because behind a load that may not have happened the compiler can
+// only wait for all of them.  VEC: the pair is loaded as one.
+template <class F, bool VEC> struct Pair {
   using S = typename F::S;
-  PairSrc<F> s;
-  const S* at = (const S*)base + b * batch_stride + off;
-  s.vec = ((uintptr_t)at % (2 * sizeof(S)) == 0) && token_stride % 2 == 0;
-  s.p = at + (int64_t)(threadIdx.x / 8) * token_stride + threadIdx.x % 8 * 2;
-  s.step = block * token_stride;
-  return s;
-}
+  using Raw = std::conditional_t<VEC, typename RowIO<F, 2>::Raw, S>;
+  Raw r[VEC ? 1 : 2];
+  __device__ __forceinline__ void unpack(float (&v)[2]) const {
+    if constexpr (VEC) {
+      RowIO<F, 2>::unpack(r[0], v);
+    } else {
+      v[0] = widen<F>(r[0]);
+      v[1] = widen<F>(r[1]);
+    }
+  }
+};
+template <class F, bool VEC> struct PairSrc {
+  using S = typename F::S;
+  const S *base, *p;         // of the workgroup; of this thread
+  int64_t token;             // stride
+  int first, second;         // this thread's elements (the second relative to the first)
+  // `n` elements of a row exist, n > 0
+  PairSrc() = default;
+  __device__ __forceinline__ PairSrc(const void* at, int64_t batch_stride, int64_t token_stride,
+                                     int64_t b, int64_t off, int n) {
+    base = (const S*)at + b * batch_stride + off;
+    token = token_stride;
+    const int e = (int)(threadIdx.x % 8) * 2;
+    first = e < n ? e : 0;
+    second = first + 1 < n ? 1 : 0;
+    p = base;
+  }
+  // to the thread's token of block t0, the last that exists at the latest
+  __device__ __forceinline__ void seek(int64_t t0, int64_t len) {
+    const int64_t t = t0 + (int)(threadIdx.x / 8);
+    p = base + (t < len ? t : len - 1) * token + first;
+  }
+  __device__ __forceinline__ void advance(int tokens) { p += tokens * token; }
+  __device__ __forceinline__ Pair<F, VEC> load() const {
+    Pair<F, VEC> v;
+    if constexpr (VEC) {
+      v.r[0] = *gptr<const typename Pair<F, VEC>::Raw>((uintptr_t)p);
+    } else {
+      v.r[0] = *gptr<const S>((uintptr_t)p);
+      v.r[1] = *gptr<const S>((uintptr_t)(p + second));
+    }
+    return v;
+  }
+};
 
 // Global -> registers -> LDS staging of one activation array's block
 // ([TB tokens, 16 channels]).  Planes: 16-bit types hold one channel pair per
@@ -286,6 +312,17 @@ template <class F, int K, int NG> struct RowStage {
     }
   }
 };
+
+// Whether every pair of channels and of states lies on its size's alignment.
+template <class F> bool scan_pairs(const ScanProblem& p, const void* y) {
+  auto even = [](const void* a, int64_t s0, int64_t s1, int64_t s2) {
+    return (uintptr_t)a % (2 * sizeof(typename F::S)) == 0 && ((s0 | s1 | s2) & 1) == 0;
+  };
+  return even(y, 0, 0, 0) && (p.channels / p.groups) % 2 == 0 && p.states % 2 == 0 && even(p.x, p.x_batch, p.x_token, 0) &&
+         even(p.dt, p.dt_batch, p.dt_token, 0) &&
+         (p.z == nullptr || even(p.z, p.z_batch, p.z_token, 0)) &&
+         even(p.B, p.B_batch, p.B_token, p.B_group) && even(p.C, p.C_batch, p.C_token, p.C_group);
+}
 
 // Where a workgroup stands in the problem: sequence, group of B and C, first
 // channel, and how many of its 16 channels exist.

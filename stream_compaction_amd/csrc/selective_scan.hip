@@ -32,7 +32,8 @@ constexpr int kFwdThreads = 256;        // T tokens of 8 channel pairs
 
 // v = the row's lane T of `from`, for all its lanes (folds into the product)
 template <int T> __device__ __forceinline__ float row_bcast(float from) {
-  return dpp<0x150 + T, 0xf>(from, 0.0f);
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, from), 0x150 + T,
+                                                            0xf, 0xf, true));
 }
 
 // Sums over the four rows of 16 lanes of 16 values: row r gets values 4 r .. 4 r
@@ -65,13 +66,12 @@ __device__ __forceinline__ void for_tokens(Fn&& fn, std::integer_sequence<int, T
 
 }  // namespace
 
-template <class F, int NS>
+template <class F, int NS, bool VEC>
 __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
     ScanProblem p, void* yv, float* final_state, float* starts, int64_t start_tokens, int64_t b0,
     int64_t tiles, uint32_t count) {
   using S = typename F::S;
   using IO = RowIO<F, 2>;
-  using Raw = typename IO::Raw;
   typedef float vec4 __attribute__((ext_vector_type(4)));
   __shared__ alignas(16) float s_x[2][2 * kPlane];           // steps, steps times x
   __shared__ alignas(16) float s_bc[2][2 * NS * kPlane];     // B, C
@@ -91,13 +91,21 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
   // staging: this thread's token and two channels (and two states of each 16)
   const int tok = tid / 8, pair = tid % 8;
   const bool stager = pair * 2 < nch;
-  auto xs = pair_src<F>(p.x, p.x_batch, p.x_token, at.b, at.ch, kT);
-  auto dts = pair_src<F>(p.dt, p.dt_batch, p.dt_token, at.b, at.ch, kT);
-  auto zs = pair_src<F>(p.z, p.z_batch, p.z_token, at.b, at.ch, kT);
-  auto Bs = pair_src<F>(p.B, p.B_batch, p.B_token, at.b, at.g * p.B_group, kT);
-  auto Cs = pair_src<F>(p.C, p.C_batch, p.C_token, at.b, at.g * p.C_group, kT);
+  using Src = PairSrc<F, VEC>;
+  using Raw = Pair<F, VEC>;
+  Src xs(p.x, p.x_batch, p.x_token, at.b, at.ch, nch);
+  Src dts(p.dt, p.dt_batch, p.dt_token, at.b, at.ch, nch);
+  // without a gate x stands in, unused
+  Src zs(gate ? p.z : p.x, gate ? p.z_batch : p.x_batch, gate ? p.z_token : p.x_token, at.b, at.ch, nch);
+  Src Bs[NS], Cs[NS];
+#pragma unroll
+  for (int s = 0; s < NS; ++s) {
+    // the states past the last 16 that exist read the first ones, unused
+    const int n = s * 16 < N ? s * 16 : 0;
+    Bs[s] = Src(p.B, p.B_batch, p.B_token, at.b, at.g * p.B_group + n, N - n);
+    Cs[s] = Src(p.C, p.C_batch, p.C_token, at.b, at.g * p.C_group + n, N - n);
+  }
   S* y = (S*)yv + at.b * p.length * p.channels + at.ch;
-  const bool vy = (uintptr_t)y % (2 * sizeof(S)) == 0 && p.channels % 2 == 0;
   float Dc[2], bias[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -116,55 +124,66 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
     h[s] = mine[s] && p.initial_state != nullptr ? p.initial_state[srow + n] : 0.0f;
   }
 
-  // two blocks are in flight: fetched[i] holds one of them, then the block's x and
-  // z until its outputs are due
+  // the next block travels while one is worked on
   struct Fetched { Raw x, dt, z, B[NS], C[NS]; };
   auto fetch = [&](Fetched& f, int64_t t0) {
-    const bool exists = t0 + tok < len;
-    f.x = f.dt = f.z = Raw{};
-    if (stager && exists) {
-      f.x = xs.load(nch);
-      f.dt = dts.load(nch);
-      if (gate) f.z = zs.load(nch);
-    }
+    if (t0 + kT > len) {
+      xs.seek(t0, len);
+      dts.seek(t0, len);
+      zs.seek(t0, len);
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      f.B[s] = f.C[s] = Raw{};
-      if (exists && s * 16 + pair * 2 < N) {
-        f.B[s] = Bs.load(N, s * 16);
-        f.C[s] = Cs.load(N, s * 16);
+      for (int s = 0; s < NS; ++s) {
+        Bs[s].seek(t0, len);
+        Cs[s].seek(t0, len);
       }
     }
-    xs.next();
-    dts.next();
-    zs.next();
-    Bs.next();
-    Cs.next();
+    f.x = xs.load();
+    f.dt = dts.load();
+    f.z = zs.load();
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      f.B[s] = Bs[s].load();
+      f.C[s] = Cs[s].load();
+    }
+    xs.advance(kT);
+    dts.advance(kT);
+    zs.advance(kT);
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      Bs[s].advance(kT);
+      Cs[s].advance(kT);
+    }
   };
+  // what a block's outputs need beside the sums: D x and the gate's factor
+  struct Rest { float skip[2], factor[2]; };
   // the fetched block into buffer `buf`; tokens past the end get step 0 (a = 1, b = 0)
-  auto stage = [&](const Fetched& f, int64_t t0, int buf) {
+  auto stage = [&](const Fetched& f, int64_t t0, int buf, Rest& rest) {
     float x[2], dt[2], v[2];
-    IO::unpack(f.x, x);
-    IO::unpack(f.dt, dt);
+    f.x.unpack(x);
+    f.dt.unpack(dt);
     const bool exists = t0 + tok < len;
     float* to = s_x[buf] + pair * 2 * kPS + tok;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float raw = dt[i] + bias[i];
-      float d = p.softplus ? softplus(raw) : raw;
-      d = exists ? d : 0.0f;
-      to[i * kPS] = d;
-      to[kPlane + i * kPS] = d * x[i];
+      const float d = p.softplus ? softplus(raw) : raw;
+      to[i * kPS] = exists ? d : 0.0f;
+      to[kPlane + i * kPS] = exists ? d * x[i] : 0.0f;
+      rest.skip[i] = Dc[i] * x[i];
     }
+    f.z.unpack(v);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) rest.factor[i] = gate ? silu(v[i]) : 1.0f;
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       float* bc = s_bc[buf] + (s * 16 + pair * 2) * kPS + tok;
-      IO::unpack(f.B[s], v);
-      bc[0] = v[0];
-      bc[kPS] = v[1];
-      IO::unpack(f.C[s], v);
-      bc[NS * kPlane] = v[0];
-      bc[NS * kPlane + kPS] = v[1];
+      const int n = s * 16 + pair * 2;
+      f.B[s].unpack(v);
+      bc[0] = exists && n < N ? v[0] : 0.0f;
+      bc[kPS] = exists && n + 1 < N ? v[1] : 0.0f;
+      f.C[s].unpack(v);
+      bc[NS * kPlane] = exists && n < N ? v[0] : 0.0f;
+      bc[NS * kPlane + kPS] = exists && n + 1 < N ? v[1] : 0.0f;
     }
   };
   const bool busy = wave * 4 < N;               // waves whose states do not exist only stage
@@ -195,6 +214,8 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
           } else {
             v[t] = __builtin_fmaf(row_bcast<t>(C), h[s], v[t]);
           }
+          // the product stays beside its broadcast, which else does not fold into it
+          asm volatile("" : "+v"(v[t]));
         }, std::make_integer_sequence<int, 16>{});
       }
       rows_sum(v, sums);
@@ -202,36 +223,30 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
           vec4{sums[0], sums[1], sums[2], sums[3]};
     }
   };
-  auto finish = [&](Raw fx, Raw fz, int64_t t0, int buf) {
+  auto finish = [&](const Rest& rest, int64_t t0, int buf) {
     if (!stager || t0 + tok >= len) return;
-    float x[2], z[2], out[2];
-    IO::unpack(fx, x);
-    IO::unpack(fz, z);
+    float out[2];
     const float* from = s_part[buf] + pair * 2 * kPS + tok;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      float v = Dc[i] * x[i];
+      float v = rest.skip[i];
 #pragma unroll
       for (int w = 0; w < 4; ++w) v += from[w * kPlane + i * kPS];
-      out[i] = gate ? v * silu(z[i]) : v;
+      out[i] = v * rest.factor[i];
     }
-    IO::store(y + (t0 + tok) * p.channels + pair * 2, IO::pack(out), nch - pair * 2, vy);
+    IO::store(y + (t0 + tok) * p.channels + pair * 2, IO::pack(out), nch - pair * 2, VEC);
   };
 
   const int64_t blocks = (len + kT - 1) / kT;
   const int64_t nkeep = starts != nullptr ? (p.length + start_tokens - 1) / start_tokens : 0;
   float* keep = starts + ((at.b * nkeep) * p.channels + ch) * N + n0;
   int64_t until = 0;                            // tokens until the next state kept
-  Fetched f[2];
-  // block t0 is staged in buffer `buf` and its x and z are in nx and nz; `next`
-  // holds the block after it and gets the third one from here
-  Raw nx, nz;
-  auto step = [&](Fetched& next, int64_t t0, int buf) {
-    const Raw fx = nx, fz = nz;
-    nx = next.x;
-    nz = next.z;
-    stage(next, t0 + kT, buf ^ 1);
-    fetch(next, t0 + 3 * kT);
+  Fetched f;
+  // block t0 is staged in buffer `buf`, the block after it in f
+  Rest rest[2];
+  auto step = [&](int64_t t0, int buf) {
+    stage(f, t0 + kT, buf ^ 1, rest[buf ^ 1]);
+    fetch(f, t0 + 2 * kT);
     if (starts != nullptr) {
       if (until == 0) {
 #pragma unroll
@@ -244,15 +259,20 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
     }
     if (busy) walk(buf);
     lds_barrier();
-    finish(fx, fz, t0, buf);
+    finish(rest[buf], t0, buf);
   };
   if (blocks > 0) {
-    fetch(f[0], 0);
-    fetch(f[1], kT);
-    nx = f[0].x;
-    nz = f[0].z;
-    stage(f[0], 0, 0);
-    fetch(f[0], 2 * kT);
+    xs.seek(0, len);
+    dts.seek(0, len);
+    zs.seek(0, len);
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      Bs[s].seek(0, len);
+      Cs[s].seek(0, len);
+    }
+    fetch(f, 0);
+    stage(f, 0, 0, rest[0]);
+    fetch(f, kT);
     if (!busy && row == 0) {
 #pragma unroll
       for (int t = 0; t < kT; t += 4)
@@ -262,8 +282,9 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
     }
     lds_barrier();
     for (int64_t blk = 0; blk < blocks; blk += 2) {
-      step(f[1], blk * kT, 0);
-      if (blk + 1 < blocks) step(f[0], (blk + 1) * kT, 1);
+      step(blk * kT, 0);
+      if (blk + 1 >= blocks) break;
+      step((blk + 1) * kT, 1);
     }
   }
   // tokens past the sequence's end
@@ -295,19 +316,27 @@ static hipError_t launch_fwd(const ScanProblem& p, void* y, float* final_state, 
   const int64_t tiles = (p.channels / p.groups + kScanTile - 1) / kScanTile;
   const int64_t per = tiles * p.groups;
   const int64_t step = kMaxGroups / per < 1 ? 1 : kMaxGroups / per;
+  const bool pairs = scan_pairs<F>(p, y);
   for (int64_t b0 = 0; b0 < p.batch; b0 += step) {
     const int64_t nb = p.batch - b0 < step ? p.batch - b0 : step;
-    auto go = [&](auto ns) {
-      selective_scan_kernel<F, decltype(ns)::value>
+    auto go = [&](auto ns, auto vec) {
+      selective_scan_kernel<F, decltype(ns)::value, decltype(vec)::value>
           <<<dim3(xcd_grid(nb * per)), dim3(kFwdThreads), 0, stream>>>(
               p, y, final_state, starts, start_tokens, b0, tiles, (uint32_t)(nb * per));
     };
-    if (p.states <= 16) {
-      go(std::integral_constant<int, 1>{});
-    } else if (p.states <= 32) {
-      go(std::integral_constant<int, 2>{});
+    auto by_states = [&](auto vec) {
+      if (p.states <= 16) {
+        go(std::integral_constant<int, 1>{}, vec);
+      } else if (p.states <= 32) {
+        go(std::integral_constant<int, 2>{}, vec);
+      } else {
+        go(std::integral_constant<int, 4>{}, vec);
+      }
+    };
+    if (pairs) {
+      by_states(std::true_type{});
     } else {
-      go(std::integral_constant<int, 4>{});
+      by_states(std::false_type{});
     }
   }
   return hipGetLastError();

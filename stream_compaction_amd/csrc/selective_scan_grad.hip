@@ -16,9 +16,6 @@
 
 namespace sca {
 
-// 1 / log2(e), for sums taken with A log2(e)
-constexpr float kLn2 = 0.69314718055994530942f;
-
 template <class F, int K> struct GradShape {
   static constexpr int NG = 8;            // states of B and C staged at a time
   static constexpr int TB = 64 * K;

@@ -13,6 +13,7 @@ namespace sca {
 template <class F> constexpr int kVecElems = 16 / (int)sizeof(typename F::S);
 
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
 
 // 2^v with the hardware instruction (1 ulp; results below 2^-126 flush to 0,
 // which a decay factor that small may do).
@@ -32,24 +33,14 @@ __device__ __forceinline__ float silu_slope(float v) {
 }
 
 // softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|) in (0, 1].  The steps of
-// a state space layer are small (1e-3 to 1e-1), where log(1 + e) rounded
-// through 1 + e would keep few digits, so it is taken as 2 atanh(s) with
-// s = e / (2 + e) <= 1/3: of the odd series (1 + q/3 + q^2/5 + ..., q = s^2)
-// the terms past q^7/15 add less than 2e-9, well under float32's half step.
+// a state space layer are small (1e-3 to 1e-1), where rounding 1 + e to w loses
+// digits of e; c = e - (w - 1) is exactly what was lost (w - 1 is exact), and
+// log(1 + e) = log(w) + c / w up to c^2, where c / w is c to within float32's
+// half step (c is at most 2^-24, and w is 1 to within e where it matters).
 __device__ __forceinline__ float softplus(float v) {
   const float e = exp2_hw(-__builtin_fabsf(v) * kLog2e);
-  const float s = e * rcp_hw(2.0f + e);
-  const float q = s * s;
-  float p = 1.0f / 15.0f;
-  p = __builtin_fmaf(p, q, 1.0f / 13.0f);
-  p = __builtin_fmaf(p, q, 1.0f / 11.0f);
-  p = __builtin_fmaf(p, q, 1.0f / 9.0f);
-  p = __builtin_fmaf(p, q, 1.0f / 7.0f);
-  p = __builtin_fmaf(p, q, 1.0f / 5.0f);
-  p = __builtin_fmaf(p, q, 1.0f / 3.0f);
-  p = __builtin_fmaf(p, q, 1.0f);
-  const float r = __builtin_fmaf(2.0f * s, p, v > 0.0f ? v : 0.0f);
-  return v != v ? v : r;
+  const float w = 1.0f + e, c = e - (w - 1.0f);
+  return __builtin_fmaxf(v, 0.0f) + __builtin_fmaf(__builtin_amdgcn_logf(w), kLn2, c);
 }
 
 // The E = 16 / sizeof(S) elements at `p` whose count `n` (may exceed E) exist;
