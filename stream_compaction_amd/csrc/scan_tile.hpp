@@ -148,6 +148,13 @@ template <class F, bool VEC> struct Pair {
       v[1] = widen<F>(r[1]);
     }
   }
+  // zero for an element that is not `on`, without a branch
+  __device__ __forceinline__ void unpack_if(bool on0, bool on1, float (&v)[2]) const {
+    unpack(v);
+    v[0] = on0 ? v[0] : 0.0f;
+    v[1] = on1 ? v[1] : 0.0f;
+    asm volatile("" : "+v"(v[0]), "+v"(v[1]));
+  }
 };
 template <class F, bool VEC> struct PairSrc {
   using S = typename F::S;

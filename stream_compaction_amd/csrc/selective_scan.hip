@@ -126,17 +126,17 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
 
   // the next block travels while one is worked on
   struct Fetched { Raw x, dt, z, B[NS], C[NS]; };
-  auto fetch = [&](Fetched& f, int64_t t0) {
-    if (t0 + kT > len) {
-      xs.seek(t0, len);
-      dts.seek(t0, len);
-      zs.seek(t0, len);
+  auto seek = [&](int64_t t0) {
+    xs.seek(t0, len);
+    dts.seek(t0, len);
+    zs.seek(t0, len);
 #pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        Bs[s].seek(t0, len);
-        Cs[s].seek(t0, len);
-      }
+    for (int s = 0; s < NS; ++s) {
+      Bs[s].seek(t0, len);
+      Cs[s].seek(t0, len);
     }
+  };
+  auto fetch = [&](Fetched& f) {
     f.x = xs.load();
     f.dt = dts.load();
     f.z = zs.load();
@@ -156,37 +156,38 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
   };
   // what a block's outputs need beside the sums: D x and the gate's factor
   struct Rest { float skip[2], factor[2]; };
-  // the fetched block into buffer `buf`; tokens past the end get step 0 (a = 1, b = 0)
-  auto stage = [&](const Fetched& f, int64_t t0, int buf, Rest& rest) {
+  // The fetched block into buffer `buf`; tokens past the end get step 0 (a = 1,
+  // b = 0).  Without branches, so that it is scheduled into the walk's waits.
+  auto stage = [&](const Fetched& f, bool exists, int buf, Rest& rest) {
     float x[2], dt[2], v[2];
     f.x.unpack(x);
     f.dt.unpack(dt);
-    const bool exists = t0 + tok < len;
+    f.z.unpack(v);
     float* to = s_x[buf] + pair * 2 * kPS + tok;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float raw = dt[i] + bias[i];
-      const float d = p.softplus ? softplus(raw) : raw;
+      const float soft = softplus(raw);
+      const float d = p.softplus ? soft : raw;
       to[i * kPS] = exists ? d : 0.0f;
       to[kPlane + i * kPS] = exists ? d * x[i] : 0.0f;
       rest.skip[i] = Dc[i] * x[i];
+      const float factor = silu(v[i]);
+      rest.factor[i] = gate ? factor : 1.0f;
     }
-    f.z.unpack(v);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) rest.factor[i] = gate ? silu(v[i]) : 1.0f;
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       float* bc = s_bc[buf] + (s * 16 + pair * 2) * kPS + tok;
       const int n = s * 16 + pair * 2;
-      f.B[s].unpack(v);
-      bc[0] = exists && n < N ? v[0] : 0.0f;
-      bc[kPS] = exists && n + 1 < N ? v[1] : 0.0f;
-      f.C[s].unpack(v);
-      bc[NS * kPlane] = exists && n < N ? v[0] : 0.0f;
-      bc[NS * kPlane + kPS] = exists && n + 1 < N ? v[1] : 0.0f;
+      const bool on0 = exists && n < N, on1 = exists && n + 1 < N;
+      f.B[s].unpack_if(on0, on1, v);
+      bc[0] = v[0];
+      bc[kPS] = v[1];
+      f.C[s].unpack_if(on0, on1, v);
+      bc[NS * kPlane] = v[0];
+      bc[NS * kPlane + kPS] = v[1];
     }
   };
-  const bool busy = wave * 4 < N;               // waves whose states do not exist only stage
   auto walk = [&](int buf) {
 #pragma unroll
     for (int sub = 0; sub < kT; sub += 16) {
@@ -224,7 +225,6 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
     }
   };
   auto finish = [&](const Rest& rest, int64_t t0, int buf) {
-    if (!stager || t0 + tok >= len) return;
     float out[2];
     const float* from = s_part[buf] + pair * 2 * kPS + tok;
 #pragma unroll
@@ -234,7 +234,8 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
       for (int w = 0; w < 4; ++w) v += from[w * kPlane + i * kPS];
       out[i] = v * rest.factor[i];
     }
-    IO::store(y + (t0 + tok) * p.channels + pair * 2, IO::pack(out), nch - pair * 2, VEC);
+    if (stager && t0 + tok < len)
+      IO::store(y + (t0 + tok) * p.channels + pair * 2, IO::pack(out), nch - pair * 2, VEC);
   };
 
   const int64_t blocks = (len + kT - 1) / kT;
@@ -245,8 +246,6 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
   // block t0 is staged in buffer `buf`, the block after it in f
   Rest rest[2];
   auto step = [&](int64_t t0, int buf) {
-    stage(f, t0 + kT, buf ^ 1, rest[buf ^ 1]);
-    fetch(f, t0 + 2 * kT);
     if (starts != nullptr) {
       if (until == 0) {
 #pragma unroll
@@ -257,29 +256,19 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
       }
       until -= kT;
     }
-    if (busy) walk(buf);
+    if (t0 + 3 * kT > len) seek(t0 + 2 * kT);
+    stage(f, t0 + kT + tok < len, buf ^ 1, rest[buf ^ 1]);
+    fetch(f);
+    walk(buf);
     lds_barrier();
     finish(rest[buf], t0, buf);
   };
   if (blocks > 0) {
-    xs.seek(0, len);
-    dts.seek(0, len);
-    zs.seek(0, len);
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      Bs[s].seek(0, len);
-      Cs[s].seek(0, len);
-    }
-    fetch(f, 0);
-    stage(f, 0, 0, rest[0]);
-    fetch(f, kT);
-    if (!busy && row == 0) {
-#pragma unroll
-      for (int t = 0; t < kT; t += 4)
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          *(vec4*)(s_part[q] + (wave * 16 + cl) * kPS + t) = vec4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
+    seek(0);
+    fetch(f);
+    stage(f, tok < len, 0, rest[0]);
+    if (2 * kT > len) seek(kT);
+    fetch(f);
     lds_barrier();
     for (int64_t blk = 0; blk < blocks; blk += 2) {
       step(blk * kT, 0);
