@@ -245,8 +245,7 @@ size_t selective_scan_starts_bytes(const selective_scan_args* args) {
   sca::Fmt fmt;
   size_t eb;
   if (scan_problem(args, false, &p, &fmt, &eb) != SCAN_OK) return 0;
-  const int64_t tb = sca::scan_block_tokens(p.length, fmt);
-  const int64_t blocks = (p.length + tb - 1) / tb;
+  const int64_t blocks = (p.length + sca::kScanKeepTokens - 1) / sca::kScanKeepTokens;
   return bytes_or_zero((unsigned __int128)(p.batch * blocks) *
                        (unsigned __int128)(p.channels * p.states) * 4);
 }
@@ -274,7 +273,7 @@ size_t selective_scan_grad_scratch_bytes(const selective_scan_args* args) {
   sca::Fmt fmt;
   size_t eb;
   if (scan_problem(args, false, &p, &fmt, &eb) != SCAN_OK) return 0;
-  return sca::selective_scan_grad_scratch(p, fmt);
+  return sca::selective_scan_grad_scratch(p);
 }
 
 scan_status selective_scan_grad(const selective_scan_args* args, const selective_scan_grads* grads,
@@ -286,7 +285,7 @@ scan_status selective_scan_grad(const selective_scan_args* args, const selective
   if (st != SCAN_OK) return st;
   if (grads == nullptr) return SCAN_EINVAL;
   if ((p.z != nullptr) != (grads->dz != nullptr) && p.batch > 0 && p.length > 0) return SCAN_EINVAL;
-  const size_t need = sca::selective_scan_grad_scratch(p, fmt);
+  const size_t need = sca::selective_scan_grad_scratch(p);
   const uint64_t tokens = (uint64_t)p.batch * (uint64_t)p.length;
   const uint64_t state = (uint64_t)p.batch * (uint64_t)(p.channels * p.states);
   const int64_t dims[2] = {p.batch, p.length};

@@ -87,9 +87,8 @@ struct ScanProblem {
   int64_t B_batch, B_token, B_group, C_batch, C_token, C_group;
   bool softplus;
 };
-// Tokens per block: the forward keeps the states at the start of every block
-// for the gradient.
-int64_t scan_block_tokens(int64_t length, Fmt fmt);
+// The forward keeps the state before every so many tokens for the gradient.
+constexpr int kScanKeepTokens = 16;
 hipError_t launch_selective_scan(const ScanProblem& p, Fmt fmt, void* y, float* final_state,
                                  float* starts, hipStream_t stream);
 struct ScanGrads {
@@ -100,7 +99,7 @@ struct ScanGrads {
   void *dx, *ddt, *dB, *dC, *dz;    // dz null without z
   float *dA, *dD, *ddt_bias, *dinitial;   // any of the last three may be null
 };
-size_t selective_scan_grad_scratch(const ScanProblem& p, Fmt fmt);
+size_t selective_scan_grad_scratch(const ScanProblem& p);
 hipError_t launch_selective_scan_grad(const ScanProblem& p, Fmt fmt, const ScanGrads& g,
                                       void* scratch, hipStream_t stream);
 hipError_t launch_selective_scan_step(const ScanProblem& p, Fmt fmt, const float* state,

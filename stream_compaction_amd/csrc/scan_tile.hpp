@@ -1,138 +1,57 @@
-// Building blocks of the selective scan's forward and gradient kernels.
-//
-// Mapping shared by both: the recurrence h[t] = a[t] h[t-1] + b[t] is an
-// affine map per token, and affine maps compose, so it is scanned like a sum:
-// each lane of a wave64 owns K consecutive tokens, folds them into one map
-// (P, H), the 64 maps are scanned across the wave with DPP, and the lane then
-// walks its K tokens from the state it got.  Lanes along time (instead of
-// along channels) keep every sum over states and, in the gradient, every sum
-// over channels inside a lane, and a sequence of one batch needs no split of
-// its length to fill the chip: a wave owns one pair of channels.
-//
-// A workgroup of 8 waves owns 16 channels of one sequence and walks it in
-// blocks of TB = 64 K tokens, whose activations and B, C rows it stages in LDS.
+// Building blocks of the selective scan's forward and gradient kernels, which
+// share their mapping: a lane owns one channel and one state (or NS of them, 16
+// apart) and walks the tokens in order.  Lanes 16 r .. 16 r + 15 of wave w hold
+// 16 channels' state 4 w + r, so that B and C are the same for a row of 16
+// lanes: a lane holds them for one of 16 tokens, and products take them by DPP
+// row broadcast.  Sums over states go over the rows of a wave by register swaps
+// and over the four waves through LDS.
 #pragma once
+
+#include <utility>
 
 #include "sequence.hpp"
 
 namespace sca {
 
-constexpr int kRowRor1 = 0x121;                // DPP: rotate each row of 16 lanes right by one
-constexpr int kScanWaves = 8;
-constexpr int kScanThreads = 64 * kScanWaves;
-constexpr int kScanTile = 2 * kScanWaves;      // channels per workgroup
+constexpr int kScanTile = 16;                  // channels per row of lanes
+constexpr int kKeep = kScanKeepTokens;         // tokens between kept states
 
-// LDS planes hold one value (or one pair of 16-bit channels) per token of the
-// block, ordered so that each lane's K tokens are read 16 bytes at a time with
-// consecutive lanes 16 bytes apart (no bank conflicts).
-template <int K> __device__ __forceinline__ int plane_index(int t) {
-  constexpr int V = K < 4 ? K : 4;
-  const int lane = t / K, k = t % K;
-  return (k / V) * (64 * V) + lane * V + k % V;
-}
-template <int K> __device__ __forceinline__ int plane_token(int i) {
-  constexpr int V = K < 4 ? K : 4;
-  return ((i / V) % 64) * K + (i / (64 * V)) * V + i % V;
+// v = the row's lane T of `from`, for all its lanes (folds into the product)
+template <int T> __device__ __forceinline__ float row_bcast(float from) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, from), 0x150 + T,
+                                                            0xf, 0xf, true));
 }
 
-// This lane's K words of a plane.
-template <int K, class T>
-__device__ __forceinline__ void plane_read(const T* plane, int lane, T (&v)[K]) {
-  static_assert(sizeof(T) == 4, "a plane holds 32-bit words");
-  constexpr int V = K < 4 ? K : 4;
-  typedef T vec __attribute__((ext_vector_type(V)));
+// Sums over the four rows of 16 lanes of 16 values: row r gets values 4 r .. 4 r
+// + 3.  The swaps exchange halves (then rows) of a pair of registers, so that one
+// addition serves two values.
+__device__ __forceinline__ float swapped_sum32(float a, float b) {
+  const auto q = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, a),
+                                                  __builtin_bit_cast(uint32_t, b), false, false);
+  const uint32_t x = q[0], y = q[1];
+  return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+__device__ __forceinline__ float swapped_sum16(float a, float b) {
+  const auto q = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, a),
+                                                  __builtin_bit_cast(uint32_t, b), false, false);
+  const uint32_t x = q[0], y = q[1];
+  return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+__device__ __forceinline__ void rows_sum(const float (&v)[16], float (&out)[4]) {
+  float s[8];
 #pragma unroll
-  for (int j = 0; j < K / V; ++j) {
-    if constexpr (V == 1) {
-      v[j] = plane[lane];
-    } else {
-      const vec w = *(const vec*)(plane + j * 64 * V + lane * V);
+  for (int t = 0; t < 8; ++t) s[t] = swapped_sum32(v[t], v[t + 8]);
 #pragma unroll
-      for (int k = 0; k < V; ++k) v[j * V + k] = w[k];
-    }
-  }
-}
-template <int K, class T>
-__device__ __forceinline__ void plane_write(T* plane, int lane, const T (&v)[K]) {
-  constexpr int V = K < 4 ? K : 4;
-  typedef T vec __attribute__((ext_vector_type(V)));
-#pragma unroll
-  for (int j = 0; j < K / V; ++j) {
-    if constexpr (V == 1) {
-      plane[lane] = v[j];
-    } else {
-      vec w;
-#pragma unroll
-      for (int k = 0; k < V; ++k) w[k] = v[j * V + k];
-      *(vec*)(plane + j * 64 * V + lane * V) = w;
-    }
-  }
+  for (int t = 0; t < 4; ++t) out[t] = swapped_sum16(s[t], s[t + 4]);
 }
 
-// Inclusive scan across the 64 lanes of two independent sequences of affine
-// maps h -> P h + H (an earlier lane's map applies first).  Written in asm so
-// that each step is one instruction per register: lanes whose DPP source does
-// not exist keep their value (their writes are disabled), which is the
-// identity.  The leading s_nop and the order of the four instructions keep at
-// least two issue slots between a write and the DPP read of the same register.
-#define SCA_AFFINE_STEP(MODE)                                  \
-  "v_fmac_f32_dpp %0, %0, %2 " MODE "\n\t"                     \
-  "v_fmac_f32_dpp %1, %1, %3 " MODE "\n\t"                     \
-  "v_mul_f32_dpp %2, %2, %2 " MODE "\n\t"                      \
-  "v_mul_f32_dpp %3, %3, %3 " MODE "\n\t"
-__device__ __forceinline__ void affine_scan2(float& H0, float& H1, float& P0, float& P1) {
-  asm volatile(
-      "s_nop 1\n\t"
-      SCA_AFFINE_STEP("row_shr:1 row_mask:0xf bank_mask:0xf")
-      SCA_AFFINE_STEP("row_shr:2 row_mask:0xf bank_mask:0xf")
-      SCA_AFFINE_STEP("row_shr:4 row_mask:0xf bank_mask:0xf")
-      SCA_AFFINE_STEP("row_shr:8 row_mask:0xf bank_mask:0xf")
-      SCA_AFFINE_STEP("row_bcast:15 row_mask:0xa bank_mask:0xf")
-      SCA_AFFINE_STEP("row_bcast:31 row_mask:0xc bank_mask:0xf")
-      "s_nop 1"
-      : "+v"(H0), "+v"(H1), "+v"(P0), "+v"(P1));
-}
-#undef SCA_AFFINE_STEP
-
-// The same within each row of 16 lanes, one sequence per row.  P is left
-// undefined.  An instruction and a wait state lie between a write and the DPP
-// read of the same register.
-#define SCA_ROW_STEP(SHIFT)                                                    \
-  "v_fmac_f32_dpp %0, %0, %1 row_shr:" SHIFT " row_mask:0xf bank_mask:0xf\n\t"  \
-  "v_mul_f32_dpp %1, %1, %1 row_shr:" SHIFT " row_mask:0xf bank_mask:0xf\n\t"   \
-  "s_nop 0\n\t"
-__device__ __forceinline__ void row_affine_scan(float& H, float& P) {
-  asm volatile(
-      "s_nop 1\n\t"
-      SCA_ROW_STEP("1")
-      SCA_ROW_STEP("2")
-      SCA_ROW_STEP("4")
-      "v_fmac_f32_dpp %0, %0, %1 row_shr:8 row_mask:0xf bank_mask:0xf\n\t"
-      "s_nop 1"
-      : "+v"(H), "+v"(P));
-}
-#undef SCA_ROW_STEP
-
-// One array of activations [batch, length, channels] as a workgroup sees it:
-// its sequence and first channel.
-template <class F> struct TileSrc {
-  const typename F::S* p;
-  int64_t token;        // stride between tokens
-  bool vec;             // every vector of the tile is 16-byte aligned
-};
-template <class F>
-__device__ __forceinline__ TileSrc<F> tile_src(const void* base, int64_t batch_stride,
-                                               int64_t token_stride, int64_t b, int64_t ch) {
-  using S = typename F::S;
-  TileSrc<F> s;
-  s.p = (const S*)base + b * batch_stride + ch;
-  s.token = token_stride;
-  s.vec = ((uintptr_t)s.p % 16 == 0) && ((token_stride * (int64_t)sizeof(S)) % 16 == 0);
-  return s;
+template <class Fn, int... T>
+__device__ __forceinline__ void for_tokens(Fn&& fn, std::integer_sequence<int, T...>) {
+  (fn(std::integral_constant<int, T>{}), ...);
 }
 
-// The same by pairs of neighbours: a thread's pair (thread % 8) of its token
-// (thread / 8) of a block, block after block.  Loads are never skipped: a
+// An array of activations [.., token, channels] as a workgroup reads it: a
+// thread's pair (thread % 8) of its token (thread / 8) of a block, block after block.  Loads are never skipped: a
 // thread whose token or pair does not exist reads one that does (the caller
 // drops it), because behind a load that may not have happened the compiler can
 // only wait for all of them.  VEC: the pair is loaded as one.
@@ -190,136 +109,6 @@ template <class F, bool VEC> struct PairSrc {
   }
 };
 
-// Global -> registers -> LDS staging of one activation array's block
-// ([TB tokens, 16 channels]).  Planes: 16-bit types hold one channel pair per
-// word (8 planes), float32 one channel (16 planes).
-template <class F, int K> struct TileStage {
-  using S = typename F::S;
-  static constexpr int E = kVecElems<F>;
-  static constexpr int TB = 64 * K;
-  static constexpr int VT = kScanTile / E;                    // vectors per token
-  static constexpr int NV = (TB * VT + kScanThreads - 1) / kScanThreads;
-  static constexpr int PLANES = kScanTile * (int)sizeof(S) / 4;
-  static constexpr int WORDS = PLANES * TB;
-  uint4 r[NV];
-
-  // tokens [t0, t0 + TB) of which those before `len` exist; nch channels exist
-  __device__ __forceinline__ void load(const TileSrc<F>& s, int64_t t0, int64_t len, int64_t nch) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int v = (int)threadIdx.x + j * kScanThreads;
-      const int64_t t = t0 + v / VT;
-      const int c = (v % VT) * E;
-      r[j] = uint4{0, 0, 0, 0};
-      if (v < TB * VT && t < len && c < nch) r[j] = load_vec<F>(s.p + t * s.token + c, nch - c, s.vec);
-    }
-  }
-  __device__ __forceinline__ void put(uint32_t* lds) const {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int v = (int)threadIdx.x + j * kScanThreads;
-      if (TB * VT % kScanThreads == 0 || v < TB * VT) {
-        uint32_t* p = lds + (v % VT) * 4 * TB + plane_index<K>(v / VT);
-        p[0] = r[j].x;
-        p[TB] = r[j].y;
-        p[2 * TB] = r[j].z;
-        p[3 * TB] = r[j].w;
-      }
-    }
-  }
-  // LDS -> global (contiguous [.., channels] output at `out`, row stride `token`)
-  static __device__ __forceinline__ void store(const uint32_t* lds, S* out, int64_t token, bool vec,
-                                               int64_t t0, int64_t end, int64_t nch) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int v = (int)threadIdx.x + j * kScanThreads;
-      const int64_t t = t0 + v / VT;
-      const int c = (v % VT) * E;
-      if (v < TB * VT && t < end && c < nch) {
-        const uint32_t* p = lds + (v % VT) * 4 * TB + plane_index<K>(v / VT);
-        store_vec<F>(out + t * token + c, uint4{p[0], p[TB], p[2 * TB], p[3 * TB]}, nch - c, vec);
-      }
-    }
-  }
-  // this lane's K tokens of the two channels of `wave` (channel innermost, as
-  // the 16-bit formats pack them)
-  static __device__ __forceinline__ void get(const uint32_t* lds, int wave, int lane,
-                                             float (&v)[K][2]) {
-    if constexpr (sizeof(S) == 2) {
-      uint32_t w[K];
-      plane_read<K>(lds + wave * TB, lane, w);
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        v[k][0] = widen<F>((S)(w[k] & 0xffffu));
-        v[k][1] = widen<F>((S)(w[k] >> 16));
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t w[K];
-        plane_read<K>(lds + (2 * wave + c) * TB, lane, w);
-#pragma unroll
-        for (int k = 0; k < K; ++k) v[k][c] = __builtin_bit_cast(float, w[k]);
-      }
-    }
-  }
-  static __device__ __forceinline__ void set(uint32_t* lds, int wave, int lane,
-                                             const float (&v)[K][2]) {
-    if constexpr (sizeof(S) == 2) {
-      uint32_t w[K];
-#pragma unroll
-      for (int k = 0; k < K; ++k) w[k] = narrow2<F>(v[k][0], v[k][1]);
-      plane_write<K>(lds + wave * TB, lane, w);
-    } else {
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t w[K];
-#pragma unroll
-        for (int k = 0; k < K; ++k) w[k] = __builtin_bit_cast(uint32_t, v[k][c]);
-        plane_write<K>(lds + (2 * wave + c) * TB, lane, w);
-      }
-    }
-  }
-};
-
-// Staging of a block's rows of B or C: NG states per token, widened to float
-// planes [NG][TB].
-template <class F, int K, int NG> struct RowStage {
-  using S = typename F::S;
-  static constexpr int E = kVecElems<F>;
-  static constexpr int TB = 64 * K;
-  static constexpr int VT = NG / E;
-  static constexpr int NV = (TB * VT + kScanThreads - 1) / kScanThreads;
-  uint4 r[NV];
-
-  // states [n0, n0 + NG) of which those below `states` exist
-  __device__ __forceinline__ void load(const TileSrc<F>& s, int64_t t0, int64_t len, int n0,
-                                       int states) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int v = (int)threadIdx.x + j * kScanThreads;
-      const int64_t t = t0 + v / VT;
-      const int n = n0 + (v % VT) * E;
-      r[j] = uint4{0, 0, 0, 0};
-      if (v < TB * VT && t < len && n < states)
-        r[j] = load_vec<F>(s.p + t * s.token + n, states - n, s.vec);
-    }
-  }
-  __device__ __forceinline__ void put(float* lds) const {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int v = (int)threadIdx.x + j * kScanThreads;
-      if (TB * VT % kScanThreads == 0 || v < TB * VT) {
-        float x[E];
-        VecIO<S, E>::template unpack<F>(r[j], x);
-        float* p = lds + (v % VT) * E * TB + plane_index<K>(v / VT);
-#pragma unroll
-        for (int e = 0; e < E; ++e) p[e * TB] = x[e];
-      }
-    }
-  }
-};
-
 // Whether every pair of channels and of states lies on its size's alignment.
 template <class F> bool scan_pairs(const ScanProblem& p, const void* y) {
   auto even = [](const void* a, int64_t s0, int64_t s1, int64_t s2) {
@@ -336,17 +125,18 @@ template <class F> bool scan_pairs(const ScanProblem& p, const void* y) {
 struct ScanPlace {
   int64_t b, g, ch, nch, tile;
 };
+// `width` channels per workgroup, `tiles` workgroups per group.
 __device__ __forceinline__ ScanPlace scan_place(const ScanProblem& p, int64_t b0, int64_t tiles,
-                                                uint32_t id) {
+                                                uint32_t id, int width) {
   ScanPlace s;
   const int64_t per = p.channels / p.groups;
   const int64_t w = id / (uint32_t)tiles;
   s.tile = id % (uint32_t)tiles;
   s.g = w % p.groups;
   s.b = b0 + w / p.groups;
-  s.ch = s.g * per + s.tile * kScanTile;
-  const int64_t left = per - s.tile * kScanTile;
-  s.nch = left < kScanTile ? left : kScanTile;
+  s.ch = s.g * per + s.tile * width;
+  const int64_t left = per - s.tile * width;
+  s.nch = left < width ? left : width;
   return s;
 }
 __device__ __forceinline__ int64_t scan_length(const ScanProblem& p, int64_t b) {

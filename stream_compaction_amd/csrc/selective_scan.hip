@@ -4,8 +4,6 @@
 // per channel, with `states` states each.  See scan_tile.hpp for the mapping.
 #include "scan_tile.hpp"
 
-#include <utility>
-
 namespace sca {
 
 namespace {
@@ -30,46 +28,12 @@ constexpr int kPS = kT + 4;             // plane stride: 16 channels' 16-byte re
 constexpr int kPlane = kScanTile * kPS;
 constexpr int kFwdThreads = 256;        // T tokens of 8 channel pairs
 
-// v = the row's lane T of `from`, for all its lanes (folds into the product)
-template <int T> __device__ __forceinline__ float row_bcast(float from) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, from), 0x150 + T,
-                                                            0xf, 0xf, true));
-}
-
-// Sums over the four rows of 16 lanes of 16 values: row r gets values 4 r .. 4 r
-// + 3.  The swaps exchange halves (then rows) of a pair of registers, so that one
-// addition serves two values.
-__device__ __forceinline__ float swapped_sum32(float a, float b) {
-  const auto q = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, a),
-                                                  __builtin_bit_cast(uint32_t, b), false, false);
-  const uint32_t x = q[0], y = q[1];
-  return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
-}
-__device__ __forceinline__ float swapped_sum16(float a, float b) {
-  const auto q = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, a),
-                                                  __builtin_bit_cast(uint32_t, b), false, false);
-  const uint32_t x = q[0], y = q[1];
-  return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
-}
-__device__ __forceinline__ void rows_sum(const float (&v)[16], float (&out)[4]) {
-  float s[8];
-#pragma unroll
-  for (int t = 0; t < 8; ++t) s[t] = swapped_sum32(v[t], v[t + 8]);
-#pragma unroll
-  for (int t = 0; t < 4; ++t) out[t] = swapped_sum16(s[t], s[t + 4]);
-}
-
-template <class Fn, int... T>
-__device__ __forceinline__ void for_tokens(Fn&& fn, std::integer_sequence<int, T...>) {
-  (fn(std::integral_constant<int, T>{}), ...);
-}
-
 }  // namespace
 
-template <class F, int NS, bool VEC>
+// KEEP: write the state before every kKeep tokens to `starts`, for the gradient.
+template <class F, int NS, bool VEC, bool KEEP>
 __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
-    ScanProblem p, void* yv, float* final_state, float* starts, int64_t start_tokens, int64_t b0,
-    int64_t tiles, uint32_t count) {
+    ScanProblem p, void* yv, float* final_state, float* starts, int64_t b0, int64_t tiles, uint32_t count) {
   using S = typename F::S;
   using IO = RowIO<F, 2>;
   typedef float vec4 __attribute__((ext_vector_type(4)));
@@ -79,7 +43,7 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
 
   const uint32_t id = xcd_order(blockIdx.x);
   if (id >= count) return;
-  const ScanPlace at = scan_place(p, b0, tiles, id);
+  const ScanPlace at = scan_place(p, b0, tiles, id, kScanTile);
   const int64_t len = scan_length(p, at.b);
   const int N = (int)p.states, nch = (int)at.nch;
   const bool gate = p.z != nullptr;
@@ -91,6 +55,8 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
   // staging: this thread's token and two channels (and two states of each 16)
   const int tok = tid / 8, pair = tid % 8;
   const bool stager = pair * 2 < nch;
+  float* keep = KEEP ? starts + (at.b * ((p.length + kKeep - 1) / kKeep) * p.channels + ch) * N + n0
+                     : nullptr;
   using Src = PairSrc<F, VEC>;
   using Raw = Pair<F, VEC>;
   Src xs(p.x, p.x_batch, p.x_token, at.b, at.ch, nch);
@@ -188,7 +154,7 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
       bc[NS * kPlane + kPS] = v[1];
     }
   };
-  auto walk = [&](int buf) {
+  auto walk = [&](int64_t t0, int buf) {
 #pragma unroll
     for (int sub = 0; sub < kT; sub += 16) {
       const float* xp = s_x[buf] + cl * kPS + sub;
@@ -204,6 +170,7 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
       }
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
+        if (KEEP && mine[s] && t0 + sub < len) keep[s * 16] = h[s];
         const float* bc = s_bc[buf] + (s * 16 + n0) * kPS + sub + cl;
         const float B = bc[0], C = bc[NS * kPlane];
         for_tokens([&](auto tc) {
@@ -222,6 +189,7 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
       rows_sum(v, sums);
       *(vec4*)(s_part[buf] + (wave * 16 + cl) * kPS + sub + row * 4) =
           vec4{sums[0], sums[1], sums[2], sums[3]};
+      if (KEEP) keep += p.channels * N;
     }
   };
   auto finish = [&](const Rest& rest, int64_t t0, int buf) {
@@ -239,27 +207,14 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
   };
 
   const int64_t blocks = (len + kT - 1) / kT;
-  const int64_t nkeep = starts != nullptr ? (p.length + start_tokens - 1) / start_tokens : 0;
-  float* keep = starts + ((at.b * nkeep) * p.channels + ch) * N + n0;
-  int64_t until = 0;                            // tokens until the next state kept
   Fetched f;
   // block t0 is staged in buffer `buf`, the block after it in f
   Rest rest[2];
   auto step = [&](int64_t t0, int buf) {
-    if (starts != nullptr) {
-      if (until == 0) {
-#pragma unroll
-        for (int s = 0; s < NS; ++s)
-          if (mine[s]) keep[s * 16] = h[s];
-        keep += p.channels * N;
-        until = start_tokens;
-      }
-      until -= kT;
-    }
     if (t0 + 3 * kT > len) seek(t0 + 2 * kT);
     stage(f, t0 + kT + tok < len, buf ^ 1, rest[buf ^ 1]);
     fetch(f);
-    walk(buf);
+    walk(t0, buf);
     lds_barrier();
     finish(rest[buf], t0, buf);
   };
@@ -285,23 +240,13 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
     if (mine[s]) final_state[srow + n0 + s * 16] = h[s];
 }
 
-// Tokens between the states that the forward keeps for the gradient, which
-// works in blocks of as many: 64 tokens by the power of two that holds a short
-// sequence, up to 512 (256 in float32, whose planes are twice as large).
-static int scan_k(int64_t length, Fmt fmt) {
-  if (length <= 64) return 1;
-  if (length <= 128) return 2;
-  return length <= 256 || fmt == Fmt::F32 ? 4 : 8;
-}
-int64_t scan_block_tokens(int64_t length, Fmt fmt) { return 64 * scan_k(length, fmt); }
-
 // Workgroups of a launch: grid sizes count work-items in 32 bits, so batches
 // beyond that go out as several launches.
 constexpr int64_t kMaxGroups = 1ll << 21;
 
 template <class F>
 static hipError_t launch_fwd(const ScanProblem& p, void* y, float* final_state, float* starts,
-                             int64_t start_tokens, hipStream_t stream) {
+                             hipStream_t stream) {
   const int64_t tiles = (p.channels / p.groups + kScanTile - 1) / kScanTile;
   const int64_t per = tiles * p.groups;
   const int64_t step = kMaxGroups / per < 1 ? 1 : kMaxGroups / per;
@@ -309,9 +254,16 @@ static hipError_t launch_fwd(const ScanProblem& p, void* y, float* final_state, 
   for (int64_t b0 = 0; b0 < p.batch; b0 += step) {
     const int64_t nb = p.batch - b0 < step ? p.batch - b0 : step;
     auto go = [&](auto ns, auto vec) {
-      selective_scan_kernel<F, decltype(ns)::value, decltype(vec)::value>
-          <<<dim3(xcd_grid(nb * per)), dim3(kFwdThreads), 0, stream>>>(
-              p, y, final_state, starts, start_tokens, b0, tiles, (uint32_t)(nb * per));
+      auto keep = [&](auto k) {
+        selective_scan_kernel<F, decltype(ns)::value, decltype(vec)::value, decltype(k)::value>
+            <<<dim3(xcd_grid(nb * per)), dim3(kFwdThreads), 0, stream>>>(
+                p, y, final_state, starts, b0, tiles, (uint32_t)(nb * per));
+      };
+      if (starts != nullptr) {
+        keep(std::true_type{});
+      } else {
+        keep(std::false_type{});
+      }
     };
     auto by_states = [&](auto vec) {
       if (p.states <= 16) {
@@ -333,11 +285,10 @@ static hipError_t launch_fwd(const ScanProblem& p, void* y, float* final_state, 
 
 hipError_t launch_selective_scan(const ScanProblem& p, Fmt fmt, void* y, float* final_state,
                                  float* starts, hipStream_t stream) {
-  const int64_t keep = scan_block_tokens(p.length, fmt);
   switch (fmt) {
-    case Fmt::F32: return launch_fwd<FmtF32>(p, y, final_state, starts, keep, stream);
-    case Fmt::F16: return launch_fwd<FmtF16>(p, y, final_state, starts, keep, stream);
-    case Fmt::BF16: return launch_fwd<FmtBF16>(p, y, final_state, starts, keep, stream);
+    case Fmt::F32: return launch_fwd<FmtF32>(p, y, final_state, starts, stream);
+    case Fmt::F16: return launch_fwd<FmtF16>(p, y, final_state, starts, stream);
+    case Fmt::BF16: return launch_fwd<FmtBF16>(p, y, final_state, starts, stream);
     default: return hipErrorInvalidValue;
   }
 }

@@ -1,327 +1,375 @@
 // Gradient of the selective scan (selective_scan.hip has the forward).  With
 // q = dy silu(z) and m[t] the gradient with respect to h[t - 1],
-//   G[t] = C[t] q[t] + m[t + 1],   m[t] = a[t] G[t]     (a scan from the end),
+//   G[t] = C[t] q[t] + m[t + 1],   m[t] = a[t] G[t]     (from the last token),
 //   dC[t] = sum_channels q h,      dB[t] = sum_channels G dt x,
 //   dx = dt sum_n G B + D q,       ddt = x sum_n G B + sum_n A m h[t - 1],
 //   dA = sum_t dt m h[t - 1],      dD = sum_t q x.
 //
-// A workgroup walks its sequence's blocks from the last to the first.  Each
-// block starts from the states the forward kept, recomputes h forward and runs
-// m backward, both as wave scans of affine maps (scan_tile.hpp).  Sums over
-// states stay in a lane; dB and dC of the workgroup's 16 channels are added
-// through LDS, one state at a time, and written as partial sums, which a second
-// kernel adds over the workgroups in a fixed order (no atomics: the same bits
-// every time).
+// A workgroup walks its sequence in blocks of 16 tokens from the last to the
+// first.  A block's states are computed again from the one that the forward
+// kept before it, and stay in registers with the decays (16 of each per lane);
+// then m goes backward over them.  Bound by vector instructions: 12 products and
+// sums per token and state, and 8 to 9 for the sums over 16 states (dx, ddt, dz)
+// and 16 channels (dB, dC).  dB and dC of the workgroup's channels go out as
+// partial sums, which a second kernel adds over the workgroups in a fixed order
+// (no atomics: the same bits every time).
 #include "scan_tile.hpp"
 
 namespace sca {
 
-template <class F, int K> struct GradShape {
-  static constexpr int NG = 8;            // states of B and C staged at a time
-  static constexpr int TB = 64 * K;
-};
+namespace {
 
-// lane l's value from lane `from` of the wave
-__device__ __forceinline__ float lane_from(float v, int from) {
-  return __builtin_bit_cast(float,
-                            __builtin_amdgcn_ds_bpermute(from * 4, __builtin_bit_cast(int, v)));
+constexpr int kT = kKeep;               // tokens per block
+constexpr int kPS = kT + 4;             // stride of planes of one value per token
+constexpr int kPlane = kScanTile * kPS;
+
+// Sums over the 16 lanes of a row of 16 values: lane l gets value l.  A lane adds
+// its partner's share of the values it keeps: 8, then 4 lanes apart by additions
+// that write one half of the lanes, closer by selects.  Instructions between a
+// write and the DPP read of the same register: at least two throughout.
+__device__ __forceinline__ float lanes_sum(float (&v)[16], int l) {
+#define SCA_FAR(A, B)                                                          \
+  "v_add_f32_dpp " A ", " A ", " A " row_ror:8 row_mask:0xf bank_mask:0x3\n\t"   \
+  "v_add_f32_dpp " A ", " B ", " B " row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+#define SCA_NEAR(A, B)                                                         \
+  "v_add_f32_dpp " A ", " A ", " A " row_ror:12 row_mask:0xf bank_mask:0x5\n\t"  \
+  "v_add_f32_dpp " A ", " B ", " B " row_ror:4 row_mask:0xf bank_mask:0xa\n\t"
+  asm("s_nop 1\n\t"
+      SCA_FAR("%0", "%8") SCA_FAR("%1", "%9") SCA_FAR("%2", "%10") SCA_FAR("%3", "%11")
+      SCA_FAR("%4", "%12") SCA_FAR("%5", "%13") SCA_FAR("%6", "%14") SCA_FAR("%7", "%15")
+      SCA_NEAR("%0", "%4") SCA_NEAR("%1", "%5") SCA_NEAR("%2", "%6") SCA_NEAR("%3", "%7")
+      "s_nop 1"
+      : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3]), "+v"(v[4]), "+v"(v[5]), "+v"(v[6]), "+v"(v[7])
+      : "v"(v[8]), "v"(v[9]), "v"(v[10]), "v"(v[11]), "v"(v[12]), "v"(v[13]), "v"(v[14]), "v"(v[15]));
+#undef SCA_FAR
+#undef SCA_NEAR
+  const bool b1 = (l & 2) != 0, b0 = (l & 1) != 0;
+  float s[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const float keep = b1 ? v[t + 2] : v[t], give = b1 ? v[t] : v[t + 2];
+    s[t] = keep + dpp<0x4e, 0xf>(give, 0.0f);          // quad_perm [2, 3, 0, 1]
+  }
+  const float keep = b0 ? s[1] : s[0], give = b0 ? s[0] : s[1];
+  return keep + dpp<0xb1, 0xf>(give, 0.0f);            // quad_perm [1, 0, 3, 2]
 }
 
-template <class F, int K>
-__global__ __launch_bounds__(kScanThreads) void selective_scan_grad_kernel(
+}  // namespace
+
+// TL tiles of 16 channels, four waves each.
+template <class F, int NS, bool GATE, int TL>
+__global__ __launch_bounds__(256 * TL) void selective_scan_grad_kernel(
     ScanProblem p, ScanGrads g, float* part, float* part_params, int64_t b0, int64_t tiles,
     uint32_t count) {
   using S = typename F::S;
-  using Tile = TileStage<F, K>;
-  constexpr int NG = GradShape<F, K>::NG, TB = GradShape<F, K>::TB;
-  using Rows = RowStage<F, K, NG>;
-  __shared__ alignas(16) float s_B[NG * TB], s_C[NG * TB], s_ex[kScanWaves * 2 * TB];
-  __shared__ alignas(16) uint32_t s_x[Tile::WORDS], s_dt[Tile::WORDS], s_z[Tile::WORDS], s_dy[Tile::WORDS];
+  typedef float vec4 __attribute__((ext_vector_type(4)));
+  constexpr int RL = 2 / TL;            // rows of B and C that a thread stages
+  constexpr int SUMS = GATE ? 3 : 2;
+  __shared__ alignas(16) float s_x[2][TL][3 * kPlane];            // steps, steps times x, q
+  __shared__ alignas(16) float s_bc[2][2][NS * kPlane];           // B, C
+  __shared__ alignas(16) float s_sum[2][TL][SUMS][4 * kPlane];    // over a wave's states
+  __shared__ alignas(16) float s_dbc[2][TL][2][NS * 16 * kT];     // over a tile's channels
 
-  const int lane = lane_id(), wave = wave_id();
   const uint32_t id = xcd_order(blockIdx.x);
   if (id >= count) return;
-  const ScanPlace at = scan_place(p, b0, tiles, id);
+  const ScanPlace at = scan_place(p, b0, tiles, id, kScanTile * TL);
   const int64_t len = scan_length(p, at.b);
   const int N = (int)p.states;
-  const bool gate = p.z != nullptr;
-  const auto xs = tile_src<F>(p.x, p.x_batch, p.x_token, at.b, at.ch);
-  const auto dts = tile_src<F>(p.dt, p.dt_batch, p.dt_token, at.b, at.ch);
-  const auto zs = tile_src<F>(p.z, p.z_batch, p.z_token, at.b, at.ch);
-  const auto dys = tile_src<F>(g.dy, g.dy_batch, g.dy_token, at.b, at.ch);
-  const auto Bs = tile_src<F>(p.B, p.B_batch, p.B_token, at.b, at.g * p.B_group);
-  const auto Cs = tile_src<F>(p.C, p.C_batch, p.C_token, at.b, at.g * p.C_group);
-  const int64_t out0 = at.b * p.length * p.channels + at.ch;
-  S* dx = (S*)g.dx + out0;
-  S* ddt = (S*)g.ddt + out0;
-  S* dz = gate ? (S*)g.dz + out0 : nullptr;
-  const bool whole = (p.channels * (int64_t)sizeof(S)) % 16 == 0;
-  const bool xvec = whole && (uintptr_t)dx % 16 == 0, dtvec = whole && (uintptr_t)ddt % 16 == 0;
-  const bool zvec = whole && (uintptr_t)dz % 16 == 0;
+  const int tid = (int)threadIdx.x, lane = lane_id(), wave = wave_id();
+  const int tl = wave / 4, row = lane / 16, cl = lane % 16;
+  const int n0 = wave % 4 * 4 + row;            // this lane's states: n0, n0 + 16, ...
+  // channels of this wave's tile (none for a tile past the group's last channel)
+  const int nch = (int)at.nch - tl * kScanTile < kScanTile ? (int)at.nch - tl * kScanTile : kScanTile;
+  const int64_t tch = at.ch + tl * kScanTile, ch = tch + cl;
 
-  // lane n of these registers holds state n of the wave's two channels
-  float A2[2], m_carry[2], dA[2] = {0.0f, 0.0f}, Dc[2], bias[2];
-  float dD[2] = {0.0f, 0.0f}, dbias[2] = {0.0f, 0.0f};
-  bool live[2];
-  int64_t row[2];
+  // staging: this thread's token and channel, and its token and state of each 16
+  const int tok = tid % 256 / 16, c = tid % 16;
+  const bool on = c < nch;
+  const int64_t cch = on ? tch + c : at.ch;     // a channel that exists
+  struct Src {
+    const S *base, *p;
+    int64_t token;
+  };
+  auto source = [&](const void* a, int64_t batch, int64_t token, int64_t off) {
+    Src s;
+    s.base = s.p = (const S*)a + at.b * batch + off;
+    s.token = token;
+    return s;
+  };
+  Src xs = source(p.x, p.x_batch, p.x_token, cch), dts = source(p.dt, p.dt_batch, p.dt_token, cch);
+  Src dys = source(g.dy, g.dy_batch, g.dy_token, cch);
+  Src zs = GATE ? source(p.z, p.z_batch, p.z_token, cch) : xs;
+  Src rows[RL][NS];
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    live[c] = 2 * wave + c < at.nch;
-    const int64_t ch = at.ch + 2 * wave + c;
-    row[c] = (at.b * p.channels + ch) * N + lane;
-    const bool on = live[c] && lane < N;
-    A2[c] = on ? p.A[ch * N + lane] * kLog2e : 0.0f;
-    m_carry[c] = on && g.dfinal != nullptr ? g.dfinal[row[c]] : 0.0f;
-    Dc[c] = live[c] && p.D != nullptr ? p.D[ch] : 0.0f;
-    bias[c] = live[c] && p.dt_bias != nullptr ? p.dt_bias[ch] : 0.0f;
+  for (int r = 0; r < RL; ++r)
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const int n = s * 16 + c < N ? s * 16 + c : 0;
+      rows[r][s] = r + tl == 0 ? source(p.B, p.B_batch, p.B_token, at.g * p.B_group + n)
+                               : source(p.C, p.C_batch, p.C_token, at.g * p.C_group + n);
+    }
+  const float Dc = on && p.D != nullptr ? p.D[cch] : 0.0f;
+  const float bias = on && p.dt_bias != nullptr ? p.dt_bias[cch] : 0.0f;
+  float dD = 0.0f, dbias = 0.0f;
+
+  float A2[NS], m[NS], dA[NS] = {};
+  bool mine[NS];
+  const int64_t srow = (at.b * p.channels + ch) * N;
+  const float* kept[NS];                        // of the block before the one last fetched
+  const int64_t nkeep = (p.length + kKeep - 1) / kKeep;
+#pragma unroll
+  for (int s = 0; s < NS; ++s) {
+    const int n = n0 + s * 16;
+    mine[s] = cl < nch && n < N;
+    A2[s] = mine[s] ? p.A[ch * N + n] * kLog2e : 0.0f;
+    m[s] = mine[s] && g.dfinal != nullptr ? g.dfinal[srow + n] : 0.0f;
+    kept[s] = g.starts + (at.b * nkeep * p.channels + (mine[s] ? ch : at.ch)) * N + (mine[s] ? n : 0);
   }
 
-  const int64_t nblk = (p.length + TB - 1) / TB;
-  const int64_t blocks = (len + TB - 1) / TB;
+  struct Fetched { S x, dt, dy, z, rows[RL][NS]; float h[NS]; } f;
+  auto each = [&](auto&& fn) {
+    fn(xs);
+    fn(dts);
+    fn(dys);
+    fn(zs);
+#pragma unroll
+    for (int r = 0; r < RL; ++r)
+#pragma unroll
+      for (int s = 0; s < NS; ++s) fn(rows[r][s]);
+  };
+  auto seek = [&](int64_t blk) {                // the last token that exists at the latest
+    const int64_t t = blk * kT + tok;
+    each([&](Src& s) { s.p = s.base + (t < len ? t : len - 1) * s.token; });
+  };
+  auto fetch = [&](int64_t blk) {
+    f.x = *gptr<const S>((uintptr_t)xs.p);
+    f.dt = *gptr<const S>((uintptr_t)dts.p);
+    f.dy = *gptr<const S>((uintptr_t)dys.p);
+    f.z = *gptr<const S>((uintptr_t)zs.p);
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+#pragma unroll
+      for (int r = 0; r < RL; ++r) f.rows[r][s] = *gptr<const S>((uintptr_t)rows[r][s].p);
+      f.h[s] = kept[s][blk * p.channels * N];
+    }
+  };
+
+  // what a block's outputs need beside the sums
+  struct Rest { float x, dt, skip, slope, gate; };
+  auto stage = [&](int64_t t, int buf, Rest& rest, float (&start)[NS]) {
+    // past either end of the sequence, and in channels past the last: a = 1, b = 0
+    const bool token = t >= 0 && t < len, exists = token && on;
+    const float x = widen<F>(f.x), raw = widen<F>(f.dt) + bias, dy = widen<F>(f.dy);
+    const float soft = softplus(raw), sig = sigmoid(raw);
+    float d = p.softplus ? soft : raw;
+    d = exists ? d : 0.0f;
+    float q = dy;
+    if constexpr (GATE) {
+      const float z = widen<F>(f.z);
+      q = dy * silu(z);
+      rest.gate = dy * silu_slope(z);
+    }
+    q = exists ? q : 0.0f;
+    const float u = exists ? d * x : 0.0f;
+    float* to = s_x[buf][tl] + c * kPS + tok;
+    to[0] = d;
+    to[kPlane] = u;
+    to[2 * kPlane] = q;
+    rest.x = x;
+    rest.dt = d;
+    rest.skip = Dc * q;
+    rest.slope = p.softplus ? sig : 1.0f;
+    dD += exists ? q * x : 0.0f;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const bool real = token && s * 16 + c < N;
+#pragma unroll
+      for (int r = 0; r < RL; ++r)
+        s_bc[buf][r + tl][(s * 16 + c) * kPS + tok] = real ? widen<F>(f.rows[r][s]) : 0.0f;
+      start[s] = mine[s] ? f.h[s] : 0.0f;
+    }
+  };
+
+  auto walk = [&](int buf, const float (&start)[NS]) {
+    const float* xp = s_x[buf][tl] + cl * kPS;
+    float dt[16], u[16], q[16], vG[16], vA[16], vY[16];
+#pragma unroll
+    for (int t = 0; t < 16; t += 4) {
+      const vec4 a = *(const vec4*)(xp + t), b = *(const vec4*)(xp + kPlane + t),
+                 e = *(const vec4*)(xp + 2 * kPlane + t);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        dt[t + i] = a[i];
+        u[t + i] = b[i];
+        q[t + i] = e[i];
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const int bc = (s * 16 + n0) * kPS + cl;
+      const float B = s_bc[buf][0][bc], C = s_bc[buf][1][bc];
+      float a[16], h[16], v[16], now = start[s];
+      for_tokens([&](auto tc) {
+        constexpr int t = decltype(tc)::value;
+        a[t] = exp2_hw(dt[t] * A2[s]);
+        now = __builtin_fmaf(a[t], now, row_bcast<t>(B) * u[t]);
+        h[t] = now;
+        v[t] = q[t] * now;
+        if constexpr (GATE) {
+          // (the asm keeps a product beside its broadcast, which else does not fold)
+          if (s == 0) {
+            vY[t] = row_bcast<t>(C) * now;
+          } else {
+            vY[t] = __builtin_fmaf(row_bcast<t>(C), now, vY[t]);
+          }
+          asm volatile("" : "+v"(vY[t]));
+        }
+      }, std::make_integer_sequence<int, 16>{});
+      float* out = s_dbc[buf][tl][0] + (s * 16 + n0) * kT + cl;
+      out[NS * 16 * kT] = lanes_sum(v, cl);
+      for_tokens([&](auto tc) {
+        constexpr int t = 15 - decltype(tc)::value;
+        float G = __builtin_fmaf(row_bcast<t>(C), q[t], m[s]);
+        asm volatile("" : "+v"(G));
+        v[t] = G * u[t];
+        if (s == 0) {
+          vG[t] = row_bcast<t>(B) * G;
+        } else {
+          vG[t] = __builtin_fmaf(row_bcast<t>(B), G, vG[t]);
+        }
+        asm volatile("" : "+v"(vG[t]));
+        m[s] = a[t] * G;
+        const float w = m[s] * (t > 0 ? h[t > 0 ? t - 1 : 0] : start[s]);
+        vA[t] = s == 0 ? w * A2[s] : __builtin_fmaf(w, A2[s], vA[t]);
+        dA[s] = __builtin_fmaf(w, dt[t], dA[s]);
+      }, std::make_integer_sequence<int, 16>{});
+      out[0] = lanes_sum(v, cl);
+    }
+    const int to = (wave % 4 * 16 + cl) * kPS + row * 4;
+    auto put = [&](int k, const float (&v)[16]) {
+      float sums[4];
+      rows_sum(v, sums);
+      *(vec4*)(s_sum[buf][tl][k] + to) = vec4{sums[0], sums[1], sums[2], sums[3]};
+    };
+    put(0, vG);
+    put(1, vA);
+    if constexpr (GATE) put(SUMS - 1, vY);
+  };
+
+  const int64_t out0 = at.b * p.length * p.channels + tch + c;
   const int64_t group = at.b * p.groups + at.g;
-  for (int64_t blk = blocks - 1; blk >= 0; --blk) {
-    const int64_t t0 = blk * TB;
-    Rows rB, rC;
-    {
-      Tile rx, rdt, rz, rdy;
-      rx.load(xs, t0, len, at.nch);
-      rdt.load(dts, t0, len, at.nch);
-      rdy.load(dys, t0, len, at.nch);
-      if (gate) rz.load(zs, t0, len, at.nch);
-      rB.load(Bs, t0, len, 0, N);
-      rC.load(Cs, t0, len, 0, N);
-      __syncthreads();                     // the last block's LDS is free
-      rx.put(s_x);
-      rdt.put(s_dt);
-      rdy.put(s_dy);
-      if (gate) rz.put(s_z);
-      rB.put(s_B);
-      rC.put(s_C);
-    }
-    float start[2];
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int64_t ch = at.ch + 2 * wave + c;
-      start[c] = live[c] && lane < N
-                     ? g.starts[((at.b * nblk + blk) * p.channels + ch) * N + lane]
-                     : 0.0f;
-    }
-    __syncthreads();
-    float dt[K][2], u[K][2], q[K][2], span[2];
-    float gb[K][2] = {}, da[K][2] = {}, ysum[K][2] = {};
-    Tile::get(s_dt, wave, lane, dt);
-    Tile::get(s_x, wave, lane, u);
-    Tile::get(s_dy, wave, lane, q);
-    if (gate) {
-      float zv[K][2];
-      Tile::get(s_z, wave, lane, zv);
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) q[k][c] *= silu(zv[k][c]);
-    }
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      float total = 0.0f;
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const float raw = dt[k][c] + bias[c];
-        const float d = p.softplus ? softplus(raw) : raw;
-        dt[k][c] = t0 + lane * K + k < len ? d : 0.0f;   // past the end: a = 1, b = 0
-        total += dt[k][c];
-        dD[c] = __builtin_fmaf(q[k][c], u[k][c], dD[c]);
-        u[k][c] *= dt[k][c];
-      }
-      span[c] = total;
-    }
-    for (int n0 = 0; n0 < N; n0 += NG) {
-      if (n0 > 0) {
-        rB.put(s_B);
-        rC.put(s_C);
-        __syncthreads();
-      }
-      if (n0 + NG < N) {
-        rB.load(Bs, t0, len, n0 + NG, N);
-        rC.load(Cs, t0, len, n0 + NG, N);
-      }
-      const int nn = N - n0 < NG ? N - n0 : NG;
-      for (int i = 0; i < nn; ++i) {
-        const int n = n0 + i;
-        float Bk[K], Ck[K], dBk[K], dCk[K];
-        plane_read<K>(s_B + i * TB, lane, Bk);
-        plane_read<K>(s_C + i * TB, lane, Ck);
-        float a[2][K], h[2][K], P[2], H[2], h0[2], M[2], m0[2], An[2];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          An[c] = readlane(A2[c], n);
-          float hl = 0.0f, ml = 0.0f;
-#pragma unroll
-          for (int k = 0; k < K; ++k) {
-            a[c][k] = exp2_hw(dt[k][c] * An[c]);
-            h[c][k] = u[k][c] * Bk[k];
-            hl = __builtin_fmaf(a[c][k], hl, h[c][k]);
-          }
-#pragma unroll
-          for (int k = K - 1; k >= 0; --k) ml = a[c][k] * __builtin_fmaf(Ck[k], q[k][c], ml);
-          P[c] = exp2_hw(span[c] * An[c]);
-          h0[c] = readlane(start[c], n);
-          m0[c] = readlane(m_carry[c], n);
-          H[c] = __builtin_fmaf(P[c], lane == 0 ? h0[c] : 0.0f, hl);
-          M[c] = __builtin_fmaf(P[c], lane == kWave - 1 ? m0[c] : 0.0f, ml);
-        }
-        // the backward scan runs over the lanes in reverse
-        float R[2];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          M[c] = lane_from(M[c], kWave - 1 - lane);
-          R[c] = lane_from(P[c], kWave - 1 - lane);
-        }
-        affine_scan2(H[0], H[1], P[0], P[1]);
-        affine_scan2(M[0], M[1], R[0], R[1]);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float hin = dpp<kWaveShr1, 0xf>(H[c], h0[c]);
-          const float last = readlane(M[c], kWave - 1);
-          m_carry[c] = lane == n ? last : m_carry[c];
-          const float back = lane_from(M[c], kWave - 2 - lane);
-          float m = lane == kWave - 1 ? m0[c] : back;
-          float hk = hin;
-#pragma unroll
-          for (int k = 0; k < K; ++k) {
-            hk = __builtin_fmaf(a[c][k], hk, h[c][k]);
-            h[c][k] = hk;
-            const float dC = q[k][c] * hk;
-            dCk[k] = c == 0 ? dC : dCk[k] + dC;
-            ysum[k][c] = __builtin_fmaf(Ck[k], hk, ysum[k][c]);
-          }
-          float dAl = 0.0f;
-#pragma unroll
-          for (int k = K - 1; k >= 0; --k) {
-            const float G = __builtin_fmaf(Ck[k], q[k][c], m);
-            m = a[c][k] * G;
-            const float dB = G * u[k][c];
-            dBk[k] = c == 0 ? dB : dBk[k] + dB;
-            gb[k][c] = __builtin_fmaf(G, Bk[k], gb[k][c]);
-            const float w = m * (k > 0 ? h[c][k > 0 ? k - 1 : 0] : hin);
-            da[k][c] = __builtin_fmaf(w, An[c], da[k][c]);
-            dAl = __builtin_fmaf(w, dt[k][c], dAl);
-          }
-          const float dAn = wave_sum(dAl);
-          dA[c] += lane == n ? dAn : 0.0f;
-        }
-        plane_write<K>(s_ex + (wave * 2 + 0) * TB, lane, dBk);
-        plane_write<K>(s_ex + (wave * 2 + 1) * TB, lane, dCk);
-        __syncthreads();
-        float* to = part + (((group * tiles + at.tile) * nblk + blk) * N + n) * (2 * TB);
-        for (int j = threadIdx.x; j < 2 * TB; j += kScanThreads) {
-          float v = s_ex[j];
-#pragma unroll
-          for (int w = 1; w < kScanWaves; ++w) v += s_ex[w * 2 * TB + j];
-          to[j] = v;
-        }
-        __syncthreads();
+  float* part0 = part + (group * tiles + at.tile) * p.length * (2 * N);
+  auto finish = [&](const Rest& rest, int64_t blk, int buf) {
+    const int64_t t = blk * kT + tok;
+    auto total = [&](int k) {
+      const float* from = s_sum[buf][tl][k] + c * kPS + tok;
+      return (from[0] + from[kPlane]) + (from[2 * kPlane] + from[3 * kPlane]);
+    };
+    const float gb = total(0), da = total(1);
+    const float ddt = __builtin_fmaf(gb, rest.x, da * kLn2) * rest.slope;
+    if (t < len) {
+      dbias += ddt;
+      const int64_t o = out0 + t * p.channels;
+      if (on) {
+        ((S*)g.dx)[o] = narrow<F>(__builtin_fmaf(gb, rest.dt, rest.skip));
+        ((S*)g.ddt)[o] = narrow<F>(ddt);
+        if constexpr (GATE)
+          ((S*)g.dz)[o] = narrow<F>(rest.gate * __builtin_fmaf(Dc, rest.x, total(SUMS - 1)));
       }
     }
-    // the block's outputs, through the waves' own planes
-    float xv[K][2], out[K][2];
-    Tile::get(s_x, wave, lane, xv);
+    // this workgroup's part of dB and dC, [token][2][states]
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int k = 0; k < 2 * NS; k += TL) {
+      const int j = k + tl, arr = j / NS, n = j % NS * 16 + c;
+      if (t >= len || n >= N) continue;
+      float v = 0.0f;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) out[k][c] = __builtin_fmaf(gb[k][c], dt[k][c], Dc[c] * q[k][c]);
-    Tile::set(s_x, wave, lane, out);
-    Tile::get(s_dt, wave, lane, out);
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const float raw = out[k][c] + bias[c];
-        float v = __builtin_fmaf(gb[k][c], xv[k][c], da[k][c] * kLn2);
-        if (p.softplus) v *= sigmoid(raw);
-        v = t0 + lane * K + k < len ? v : 0.0f;
-        dbias[c] += v;
-        out[k][c] = v;
-      }
-    Tile::set(s_dt, wave, lane, out);
-    if (gate) {
-      float zv[K][2];
-      Tile::get(s_z, wave, lane, zv);
-      Tile::get(s_dy, wave, lane, out);
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          out[k][c] *= __builtin_fmaf(Dc[c], xv[k][c], ysum[k][c]) * silu_slope(zv[k][c]);
-      Tile::set(s_z, wave, lane, out);
+      for (int i = 0; i < TL; ++i) v += s_dbc[buf][i][arr][n * kT + tok];
+      part0[t * (2 * N) + arr * N + n] = v;
     }
-    __syncthreads();
-    Tile::store(s_x, dx, p.channels, xvec, t0, len, at.nch);
-    Tile::store(s_dt, ddt, p.channels, dtvec, t0, len, at.nch);
-    if (gate) Tile::store(s_z, dz, p.channels, zvec, t0, len, at.nch);
+  };
+
+  const int64_t blocks = (len + kT - 1) / kT;
+  Rest rest[2];
+  float start[2][NS];
+  auto back = [&](int64_t blk) {                // from block blk to blk - 1, all of it exists
+    if (blk > 0) each([&](Src& s) { s.p -= kT * s.token; });
+  };
+  // block blk is staged in buffer `buf`, the block before it in f
+  auto step = [&](int64_t blk, int buf) {
+    stage((blk - 1) * kT + tok, buf ^ 1, rest[buf ^ 1], start[buf ^ 1]);
+    back(blk - 1);
+    fetch(blk > 2 ? blk - 2 : 0);
+    walk(buf, start[buf]);
+    lds_barrier();
+    finish(rest[buf], blk, buf);
+  };
+  if (blocks > 0) {
+    seek(blocks - 1);
+    fetch(blocks - 1);
+    stage((blocks - 1) * kT + tok, 0, rest[0], start[0]);
+    if (blocks > 1) seek(blocks - 2);
+    fetch(blocks > 1 ? blocks - 2 : 0);
+    lds_barrier();
+    for (int64_t blk = blocks - 1; blk >= 0; blk -= 2) {
+      step(blk, 0);
+      if (blk == 0) break;
+      step(blk - 1, 1);
+    }
   }
   // tokens past the sequence's end
-  for (int64_t i = len * kScanTile + threadIdx.x; i < p.length * kScanTile; i += kScanThreads)
-    if (i % kScanTile < at.nch) {
-      const int64_t o = (i / kScanTile) * p.channels + i % kScanTile;
-      dx[o] = S(0);
-      ddt[o] = S(0);
-      if (gate) dz[o] = S(0);
+  const int width = kScanTile * TL;
+  for (int64_t i = len * width + tid; i < p.length * width; i += 256 * TL)
+    if (i % width < at.nch) {
+      const int64_t o = (at.b * p.length + i / width) * p.channels + at.ch + i % width;
+      ((S*)g.dx)[o] = S(0);
+      ((S*)g.ddt)[o] = S(0);
+      if constexpr (GATE) ((S*)g.dz)[o] = S(0);
     }
   // sums over this sequence: [batch][channels * states | channels | channels]
   float* params = part_params + at.b * p.channels * (N + 2);
+  __syncthreads();
+  float* sums = &s_sum[0][0][0][0];
+  sums[tid] = dD;
+  sums[256 * TL + tid] = dbias;
+  __syncthreads();
+  if (tid < 2 * width) {
+    const int k = tid / width, j = tid % width;
+    float v = 0.0f;
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const int64_t ch = at.ch + 2 * wave + c;
-    const float sD = wave_sum(dD[c]), sb = wave_sum(dbias[c]);
-    if (!live[c]) continue;
-    if (lane < N) {
-      params[ch * N + lane] = dA[c];
-      if (g.dinitial != nullptr) g.dinitial[row[c]] = m_carry[c];
-    }
-    if (lane == 0) {
-      params[p.channels * N + ch] = sD;
-      params[p.channels * (N + 1) + ch] = sb;
-    }
+    for (int t = 0; t < kT; ++t) v += sums[k * 256 * TL + j / 16 * 256 + t * 16 + j % 16];
+    if (j < at.nch) params[p.channels * (N + k) + at.ch + j] = v;
   }
+#pragma unroll
+  for (int s = 0; s < NS; ++s)
+    if (mine[s]) {
+      params[ch * N + n0 + s * 16] = dA[s];
+      if (g.dinitial != nullptr) g.dinitial[srow + n0 + s * 16] = m[s];
+    }
 }
 
-// dB and dC: the sums over the workgroups of a group's channels, 64 tokens of
-// one array per workgroup, turned from one state per plane to one token per row.
-template <class F, int K>
+// dB and dC: the sums over the workgroups of a group's channels.
+template <class F>
 __global__ __launch_bounds__(256) void scan_rows_sum_kernel(ScanProblem p, const float* part,
                                                            void* dBv, void* dCv, int64_t tiles) {
   using S = typename F::S;
-  constexpr int TB = 64 * K;
-  __shared__ alignas(16) float s_v[64 * 65];
-  const int lane = lane_id(), wave = wave_id();
-  const int N = (int)p.states;
-  const int64_t nblk = (p.length + TB - 1) / TB;
-  const int64_t total = p.batch * p.groups * nblk * K * 2;
-  for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
-    const int arr = (int)(w % 2), seg = (int)(w / 2 % K);
-    const int64_t blk = w / (2 * K) % nblk, group = w / (2 * K) / nblk;
-    const int64_t b = group / p.groups, gi = group % p.groups;
-    const bool any = blk * TB < scan_length(p, b);
-    for (int n = wave; n < N; n += 4) {
-      float v = 0.0f;
-      if (any) {
-        const float* src = part + ((group * tiles * nblk + blk) * N + n) * (2 * TB) + arr * TB +
-                           seg * 64 + lane;
-        const int64_t step = nblk * N * (2 * TB);
-#pragma unroll 4
-        for (int64_t t = 0; t < tiles; ++t) v += src[t * step];
-      }
-      s_v[lane * 65 + n] = v;
+  const int64_t N = p.states, per = p.length * 2 * N, total = p.batch * p.groups * per;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    int64_t j, e, gi;
+    const int64_t group = divide(i, per, &j), t = divide(j, 2 * N, &e);
+    const int64_t b = divide(group, p.groups, &gi);
+    float v = 0.0f;
+    if (t < scan_length(p, b)) {
+      const float* src = part + group * tiles * per + j;
+#pragma unroll 8
+      for (int64_t k = 0; k < tiles; ++k) v += src[k * per];
     }
-    __syncthreads();
-    S* out = (S*)(arr == 0 ? dBv : dCv);
-    for (int i = threadIdx.x; i < 64 * N; i += 256) {
-      const int l = i / N, n = i % N;
-      const int64_t t = blk * TB + plane_token<K>(seg * 64 + l);
-      if (t < p.length)
-        out[((b * p.length + t) * p.groups + gi) * N + n] = narrow<F>(s_v[l * 65 + n]);
+    const int64_t o = ((b * p.length + t) * p.groups + gi) * N;
+    if (e < N) {
+      ((S*)dBv)[o + e] = narrow<F>(v);
+    } else {
+      ((S*)dCv)[o + e - N] = narrow<F>(v);
     }
-    __syncthreads();
   }
 }
 
@@ -343,66 +391,80 @@ __global__ __launch_bounds__(256) void scan_params_sum_kernel(const float* part,
 }
 
 namespace {
-int64_t grad_tiles(const ScanProblem& p) {
-  return (p.channels / p.groups + kScanTile - 1) / kScanTile;
+// Tiles per workgroup: two halve the partial sums of dB and dC, where a group
+// has two tiles, that leaves a workgroup for every CU, and the registers hold it.
+int grad_tiles_each(const ScanProblem& p) {
+  const int64_t tiles = (p.channels / p.groups + kScanTile - 1) / kScanTile;
+  return tiles > 1 && p.states <= 16 && p.batch * p.groups * ((tiles + 1) / 2) >= 256 ? 2 : 1;
 }
-size_t rows_part_floats(const ScanProblem& p, Fmt fmt) {
-  const int64_t tb = scan_block_tokens(p.length, fmt);
-  const int64_t nblk = (p.length + tb - 1) / tb;
-  return (size_t)(p.batch * p.groups * grad_tiles(p) * nblk * p.states * 2 * tb);
+int64_t grad_tiles(const ScanProblem& p) {
+  const int64_t width = kScanTile * grad_tiles_each(p);
+  return (p.channels / p.groups + width - 1) / width;
+}
+size_t rows_part_floats(const ScanProblem& p) {
+  return (size_t)(p.batch * p.groups * grad_tiles(p) * p.length * 2 * p.states);
 }
 }  // namespace
 
-size_t selective_scan_grad_scratch(const ScanProblem& p, Fmt fmt) {
-  return 4 * (rows_part_floats(p, fmt) + (size_t)(p.batch * p.channels * (p.states + 2)));
+size_t selective_scan_grad_scratch(const ScanProblem& p) {
+  return 4 * (rows_part_floats(p) + (size_t)(p.batch * p.channels * (p.states + 2)));
 }
 
 constexpr int64_t kMaxGroups = 1ll << 22;   // workgroups per launch
 
-template <class F, int K>
-static hipError_t launch_grad(const ScanProblem& p, Fmt fmt, const ScanGrads& g, void* scratch,
+template <class F>
+static hipError_t launch_grad(const ScanProblem& p, const ScanGrads& g, void* scratch,
                               hipStream_t stream) {
   const int64_t tiles = grad_tiles(p);
   const int64_t per = tiles * p.groups;
   const int64_t step = kMaxGroups / per < 1 ? 1 : kMaxGroups / per;
   float* part = (float*)scratch;
-  float* params = part + rows_part_floats(p, fmt);
+  float* params = part + rows_part_floats(p);
   for (int64_t b0 = 0; b0 < p.batch; b0 += step) {
     const int64_t nb = p.batch - b0 < step ? p.batch - b0 : step;
-    selective_scan_grad_kernel<F, K><<<dim3(xcd_grid(nb * per)), dim3(kScanThreads), 0, stream>>>(
-        p, g, part, params, b0, tiles, (uint32_t)(nb * per));
+    auto go = [&](auto ns, auto gate, auto tl) {
+      constexpr int TL = decltype(tl)::value;
+      selective_scan_grad_kernel<F, decltype(ns)::value, decltype(gate)::value, TL>
+          <<<dim3(xcd_grid(nb * per)), dim3(256 * TL), 0, stream>>>(p, g, part, params, b0, tiles,
+                                                                   (uint32_t)(nb * per));
+    };
+    auto by_tiles = [&](auto ns, auto gate) {
+      if constexpr (decltype(ns)::value == 1) {
+        if (grad_tiles_each(p) == 2) return go(ns, gate, std::integral_constant<int, 2>{});
+      }
+      go(ns, gate, std::integral_constant<int, 1>{});
+    };
+    auto by_gate = [&](auto ns) {
+      if (p.z != nullptr) {
+        by_tiles(ns, std::true_type{});
+      } else {
+        by_tiles(ns, std::false_type{});
+      }
+    };
+    if (p.states <= 16) {
+      by_gate(std::integral_constant<int, 1>{});
+    } else if (p.states <= 32) {
+      by_gate(std::integral_constant<int, 2>{});
+    } else {
+      by_gate(std::integral_constant<int, 4>{});
+    }
   }
-  constexpr int TB = 64 * K;
-  const int64_t nblk = (p.length + TB - 1) / TB;
-  const int64_t sums = p.batch * p.groups * nblk * K * 2;
+  const int64_t sums = (p.batch * p.groups * p.length * 2 * p.states + 255) / 256;
   if (sums > 0)
-    scan_rows_sum_kernel<F, K><<<dim3((unsigned)(sums < (1 << 20) ? sums : 1 << 20)), dim3(256), 0,
-                                 stream>>>(p, part, g.dB, g.dC, tiles);
+    scan_rows_sum_kernel<F><<<dim3((unsigned)(sums < (1 << 20) ? sums : 1 << 20)), dim3(256), 0,
+                              stream>>>(p, part, g.dB, g.dC, tiles);
   const int64_t count = p.channels * (p.states + 2);
   scan_params_sum_kernel<<<dim3((unsigned)((count + 255) / 256)), dim3(256), 0, stream>>>(
       params, p.batch, p.channels, p.states, g.dA, g.dD, g.ddt_bias);
   return hipGetLastError();
 }
 
-template <class F>
-static hipError_t launch_grad_f(const ScanProblem& p, Fmt fmt, const ScanGrads& g, void* scratch,
-                                hipStream_t stream) {
-  switch (scan_block_tokens(p.length, fmt) / 64) {
-    case 1: return launch_grad<F, 1>(p, fmt, g, scratch, stream);
-    case 2: return launch_grad<F, 2>(p, fmt, g, scratch, stream);
-    case 4: return launch_grad<F, 4>(p, fmt, g, scratch, stream);
-    case 8:
-      if constexpr (sizeof(typename F::S) == 2) return launch_grad<F, 8>(p, fmt, g, scratch, stream);
-  }
-  return hipErrorInvalidValue;
-}
-
 hipError_t launch_selective_scan_grad(const ScanProblem& p, Fmt fmt, const ScanGrads& g,
                                       void* scratch, hipStream_t stream) {
   switch (fmt) {
-    case Fmt::F32: return launch_grad_f<FmtF32>(p, fmt, g, scratch, stream);
-    case Fmt::F16: return launch_grad_f<FmtF16>(p, fmt, g, scratch, stream);
-    case Fmt::BF16: return launch_grad_f<FmtBF16>(p, fmt, g, scratch, stream);
+    case Fmt::F32: return launch_grad<FmtF32>(p, g, scratch, stream);
+    case Fmt::F16: return launch_grad<FmtF16>(p, g, scratch, stream);
+    case Fmt::BF16: return launch_grad<FmtBF16>(p, g, scratch, stream);
     default: return hipErrorInvalidValue;
   }
 }
