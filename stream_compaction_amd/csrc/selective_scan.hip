@@ -192,6 +192,7 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
       if (KEEP) keep += p.channels * N;
     }
   };
+  const uint32_t off = (uint32_t)((tok * p.channels + pair * 2) * (int64_t)sizeof(S));
   auto finish = [&](const Rest& rest, int64_t t0, int buf) {
     float out[2];
     const float* from = s_part[buf] + pair * 2 * kPS + tok;
@@ -202,21 +203,29 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
       for (int w = 0; w < 4; ++w) v += from[w * kPlane + i * kPS];
       out[i] = v * rest.factor[i];
     }
-    if (stager && t0 + tok < len)
-      IO::store(y + (t0 + tok) * p.channels + pair * 2, IO::pack(out), nch - pair * 2, VEC);
+    const bool live = t0 >= 0 && t0 + tok < len;
+    const S* to = y + t0 * p.channels;
+    if constexpr (VEC) {
+      store_if(to, off, live && stager, IO::pack(out));
+    } else {
+      store_if(to, off, live && pair * 2 < nch, narrow<F>(out[0]));
+      store_if(to, off + (uint32_t)sizeof(S), live && pair * 2 + 1 < nch, narrow<F>(out[1]));
+    }
   };
 
   const int64_t blocks = (len + kT - 1) / kT;
   Fetched f;
-  // block t0 is staged in buffer `buf`, the block after it in f
-  Rest rest[2];
+  // Block t0 is staged in buffer `buf`, the block after it in f; the outputs of the
+  // block before it (none for the first) are due.  No branch between the barriers
+  // but the last blocks' seek: all of it is scheduled together.
+  Rest rest[2] = {};
   auto step = [&](int64_t t0, int buf) {
     if (t0 + 3 * kT > len) seek(t0 + 2 * kT);
+    finish(rest[buf ^ 1], t0 - kT, buf ^ 1);
     stage(f, t0 + kT + tok < len, buf ^ 1, rest[buf ^ 1]);
     fetch(f);
     walk(t0, buf);
     lds_barrier();
-    finish(rest[buf], t0, buf);
   };
   if (blocks > 0) {
     seek(0);
@@ -225,10 +234,16 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
     if (2 * kT > len) seek(kT);
     fetch(f);
     lds_barrier();
-    for (int64_t blk = 0; blk < blocks; blk += 2) {
+    int64_t blk = 0;
+    for (; blk + 1 < blocks; blk += 2) {
       step(blk * kT, 0);
-      if (blk + 1 >= blocks) break;
       step((blk + 1) * kT, 1);
+    }
+    if (blk < blocks) step(blk * kT, 0);
+    if (blocks & 1) {
+      finish(rest[0], (blocks - 1) * kT, 0);
+    } else {
+      finish(rest[1], (blocks - 1) * kT, 1);
     }
   }
   // tokens past the sequence's end

@@ -227,15 +227,18 @@ __global__ __launch_bounds__(256 * TL) void selective_scan_grad_kernel(
       }, std::make_integer_sequence<int, 16>{});
       float* out = s_dbc[buf][tl][0] + (s * 16 + n0) * kT + cl;
       out[NS * 16 * kT] = lanes_sum(v, cl);
+      // other registers to the compiler: broadcasts shared by two products do not fold
+      float Bb = B, Cb = C;
+      asm volatile("" : "+v"(Bb), "+v"(Cb));
       for_tokens([&](auto tc) {
         constexpr int t = 15 - decltype(tc)::value;
-        float G = __builtin_fmaf(row_bcast<t>(C), q[t], m[s]);
+        float G = __builtin_fmaf(row_bcast<t>(Cb), q[t], m[s]);
         asm volatile("" : "+v"(G));
         v[t] = G * u[t];
         if (s == 0) {
-          vG[t] = row_bcast<t>(B) * G;
+          vG[t] = row_bcast<t>(Bb) * G;
         } else {
-          vG[t] = __builtin_fmaf(row_bcast<t>(B), G, vG[t]);
+          vG[t] = __builtin_fmaf(row_bcast<t>(Bb), G, vG[t]);
         }
         asm volatile("" : "+v"(vG[t]));
         m[s] = a[t] * G;

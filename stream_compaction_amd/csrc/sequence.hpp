@@ -118,6 +118,22 @@ template <class F, int E> struct RowIO {
   }
 };
 
+// Stores v at `off` bytes (below 2^31) past the wave-uniform base, if `on`: a
+// buffer store drops what lies outside the resource, so there is no branch.
+template <class T>
+__device__ __forceinline__ void store_if(const void* base, uint32_t off, bool on, T v) {
+  const Buf b((uintptr_t)base, 0x7fffffff);
+  const uint32_t at = on ? off : ~0u;
+  if constexpr (sizeof(T) == 2) {
+    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, v), b.r, at, 0, 0);
+  } else if constexpr (sizeof(T) == 4) {
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), b.r, at, 0, 0);
+  } else {
+    typedef uint32_t vec2 __attribute__((ext_vector_type(2)));
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(vec2, v), b.r, at, 0, 0);
+  }
+}
+
 // i = q d + r.  A 64-bit division costs some 150 instructions, a 32-bit one 25.
 __device__ __forceinline__ int64_t divide(int64_t i, int64_t d, int64_t* r) {
   int64_t q;
