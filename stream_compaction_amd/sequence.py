@@ -33,48 +33,57 @@ def _code(x, what):
     return _ACT[x.dtype]
 
 
-def _like(t, what, shape, dtype, device):
-    """Pointer of a contiguous tensor of this shape, type and device."""
-    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+# Devices are compared by index and new tensors made like existing ones where that serves:
+# a step for one token is bound by this side, and both cost half of the plain way.
+def _like(t, what, shape, dtype, dev):
+    """Pointer of a contiguous tensor of this shape, type and GPU."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                         f"cuda:{dev}")
     return t.data_ptr()
 
 
-def _opt(t, what, shape, dtype, device):
-    return None if t is None else _like(t, what, shape, dtype, device)
+def _opt(t, what, shape, dtype, dev):
+    return None if t is None else _like(t, what, shape, dtype, dev)
 
 
-def _new(shape, dtype, device, stream):
-    """A new tensor.  Memory for an explicit stream comes from that stream's pool, so that it
-    is not handed on while the stream still works on it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _out(t, what, shape, dtype, device, stream):
-    if t is None:
-        return _new(shape, dtype, device, stream)
-    _like(t, what, shape, dtype, device)
-    return t
-
-
-def _rows(t, what, shape, dtype, device):
-    """An activation tensor: shape, type, device, contiguous last axis."""
-    if t.shape != shape or t.dtype is not dtype or t.device != device:
-        raise ValueError(f"{what} must be a {dtype} tensor of shape {shape} on {device}")
+def _rows(t, what, shape, dtype, dev):
+    """An activation tensor: shape, type, GPU, contiguous last axis."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{what} must be a {dtype} tensor of shape {tuple(shape)} on cuda:{dev}")
     if shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{what} must have a contiguous last axis")
     return t.data_ptr()
 
 
-def _scratch(scratch, need, device, stream):
+def _new(shape, dtype, like, stream):
+    """A new tensor on ``like``'s GPU.  Memory for an explicit stream comes from that stream's
+    pool, so that it is not handed on while the stream still works on it."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=like.device)
+    if like.dtype is dtype:
+        if like.shape == shape and like.is_contiguous():
+            return torch.empty_like(like)
+        return like.new_empty(shape)
+    return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _out(t, what, shape, dtype, like, stream):
+    if t is None:
+        return _new(shape, dtype, like, stream)
+    _like(t, what, shape, dtype, like.get_device())
+    return t
+
+
+def _scratch(scratch, need, like, stream):
+    """Bytes of scratch memory; a float32 ``like`` makes them the cheapest."""
     if scratch is None:
-        return _new(max(need, 16), torch.uint8, device, stream)
-    if scratch.dtype != torch.uint8 or scratch.device != device or not scratch.is_contiguous():
+        return _new((max(need, 16) + 3) // 4, torch.float32, like, stream), need
+    if scratch.dtype != torch.uint8 or scratch.get_device() != like.get_device() or \
+            not scratch.is_contiguous():
         raise ValueError("scratch must be a contiguous uint8 tensor on the data's device")
-    return scratch
+    return scratch, scratch.numel()
 
 
 def _conv_args(x, weight, bias, initial_state, lengths, silu, step):
@@ -83,7 +92,7 @@ def _conv_args(x, weight, bias, initial_state, lengths, silu, step):
                          "x must be [batch, length, channels]")
     _require(x.is_cuda, "x must be a GPU tensor")
     code = _code(x, "x")
-    shape, dev, stride = x.shape, x.device, x.stride()
+    shape, dev, stride = x.shape, x.get_device(), x.stride()
     b, d = shape[0], shape[-1]
     _require(weight.dim() == 2, "weight must be [channels, width]")
     w = weight.shape[1]
@@ -107,9 +116,8 @@ def causal_conv(x, weight, bias=None, initial_state=None, lengths=None, silu=Tru
     ``(y, final_state)``: the second is the next call's initial state.
     """
     a = _conv_args(x, weight, bias, initial_state, lengths, silu, False)
-    y = _out(out, "out", x.shape, x.dtype, x.device, stream)
-    fs = _out(final_state, "final_state", (a.batch, a.width - 1, a.channels), x.dtype, x.device,
-              stream)
+    y = _out(out, "out", x.shape, x.dtype, x, stream)
+    fs = _out(final_state, "final_state", (a.batch, a.width - 1, a.channels), x.dtype, x, stream)
     check(lib().causal_conv(a, y.data_ptr(), fs.data_ptr(), _stream(stream)))
     return y, fs
 
@@ -120,19 +128,19 @@ def causal_conv_grad(dy, x, weight, bias=None, initial_state=None, lengths=None,
     with ``dx``, ``dweight``, ``dbias`` and ``dstate`` (of the initial state; both None when
     that input is)."""
     a = _conv_args(x, weight, bias, initial_state, lengths, silu, False)
-    dev, state = x.device, (a.batch, a.width - 1, a.channels)
+    dev, state = x.get_device(), (a.batch, a.width - 1, a.channels)
     dyp = _rows(dy, "dy", x.shape, x.dtype, dev)
     df = _opt(dfinal, "dfinal", state, x.dtype, dev)
-    dx = _new(x.shape, x.dtype, dev, stream)
-    dw = _new(weight.shape, torch.float32, dev, stream)
-    db = None if bias is None else _new(bias.shape, torch.float32, dev, stream)
-    ds = None if initial_state is None else _new(state, x.dtype, dev, stream)
+    dx = _new(x.shape, x.dtype, x, stream)
+    dw = _new(weight.shape, torch.float32, weight, stream)
+    db = None if bias is None else _new(bias.shape, torch.float32, bias, stream)
+    ds = None if initial_state is None else _new(state, x.dtype, initial_state, stream)
     L = lib()
-    scratch = _scratch(scratch, L.causal_conv_grad_scratch_bytes(a), dev, stream)
+    scratch, room = _scratch(scratch, L.causal_conv_grad_scratch_bytes(a), weight, stream)
     check(L.causal_conv_grad(a, dyp, (_i64 * 2)(*dy.stride()[:2]), df, dx.data_ptr(),
                              dw.data_ptr(), None if db is None else db.data_ptr(),
                              None if ds is None else ds.data_ptr(), scratch.data_ptr(),
-                             scratch.numel(), _stream(stream)))
+                             room, _stream(stream)))
     return {"dx": dx, "dweight": dw, "dbias": db, "dstate": ds}
 
 
@@ -143,9 +151,10 @@ def causal_conv_step(state, x, weight, bias=None, silu=True, new_state=None, out
     ``new_state``).  Returns ``y``."""
     a = _conv_args(x, weight, bias, None, None, silu, True)
     shape = (a.batch, a.width - 1, a.channels)
-    sp = _like(state, "state", shape, x.dtype, x.device)
-    np_ = sp if new_state is None else _like(new_state, "new_state", shape, x.dtype, x.device)
-    y = _out(out, "out", x.shape, x.dtype, x.device, stream)
+    dev = x.get_device()
+    sp = _like(state, "state", shape, x.dtype, dev)
+    np_ = sp if new_state is None else _like(new_state, "new_state", shape, x.dtype, dev)
+    y = _out(out, "out", x.shape, x.dtype, x, stream)
     check(lib().causal_conv_step(a, sp, np_, y.data_ptr(), _stream(stream)))
     return y
 
@@ -156,7 +165,7 @@ def _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, lengths, 
                          "x must be [batch, length, channels]")
     _require(x.is_cuda, "x must be a GPU tensor")
     code = _code(x, "x")
-    dev, ty = x.device, x.dtype
+    dev, ty = x.get_device(), x.dtype
     shape = x.shape
     b, d = shape[0], shape[-1]
     _require(A.dim() == 2, "A must be [channels, states]")
@@ -206,14 +215,14 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=False,
     ``keep_starts`` also what ``selective_scan_grad`` needs of this call.
     """
     a = _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, lengths, False)
-    y = _out(out, "out", x.shape, x.dtype, x.device, stream)
-    fs = _out(final_state, "final_state", (a.batch, a.channels, a.states), torch.float32, x.device,
-              stream)
+    y = _out(out, "out", x.shape, x.dtype, x, stream)
+    fs = _out(final_state, "final_state", (a.batch, a.channels, a.states), torch.float32,
+              A if initial_state is None else initial_state, stream)
     L = lib()
     if not keep_starts:
         check(L.selective_scan(a, y.data_ptr(), fs.data_ptr(), None, _stream(stream)))
         return y, fs
-    starts = _new(L.selective_scan_starts_bytes(a) // 4, torch.float32, x.device, stream)
+    starts = _new((L.selective_scan_starts_bytes(a) // 4,), torch.float32, A, stream)
     check(L.selective_scan(a, y.data_ptr(), fs.data_ptr(), starts.data_ptr(), _stream(stream)))
     return y, fs, starts
 
@@ -225,25 +234,24 @@ def selective_scan_grad(dy, x, dt, A, B, C, starts, D=None, z=None, dt_bias=None
     ``dB``, ``dC``, ``dD``, ``dz``, ``ddt_bias`` (None where that input is) and ``dstate``
     (of the initial state)."""
     a = _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, None, lengths, False)
-    dev, ty, f32 = x.device, x.dtype, torch.float32
+    dev, ty, f32 = x.get_device(), x.dtype, torch.float32
     state = (a.batch, a.channels, a.states)
     L = lib()
     dyp = _rows(dy, "dy", x.shape, ty, dev)
     df = _opt(dfinal, "dfinal", state, f32, dev)
     sp = _like(starts, "starts", (L.selective_scan_starts_bytes(a) // 4,), f32, dev)
-    rows = B.shape
-    out = {"dx": _new(x.shape, ty, dev, stream), "ddt": _new(x.shape, ty, dev, stream),
-           "dA": _new(A.shape, f32, dev, stream), "dB": _new(rows, ty, dev, stream),
-           "dC": _new(rows, ty, dev, stream),
-           "dD": None if D is None else _new(D.shape, f32, dev, stream),
-           "dz": None if z is None else _new(x.shape, ty, dev, stream),
-           "ddt_bias": None if dt_bias is None else _new(dt_bias.shape, f32, dev, stream),
-           "dstate": _new(state, f32, dev, stream)}
+    out = {"dx": _new(x.shape, ty, x, stream), "ddt": _new(x.shape, ty, x, stream),
+           "dA": _new(A.shape, f32, A, stream), "dB": _new(B.shape, ty, B, stream),
+           "dC": _new(B.shape, ty, B, stream),
+           "dD": None if D is None else _new(D.shape, f32, D, stream),
+           "dz": None if z is None else _new(x.shape, ty, x, stream),
+           "ddt_bias": None if dt_bias is None else _new(dt_bias.shape, f32, dt_bias, stream),
+           "dstate": _new(state, f32, A, stream)}
     p = {k: None if v is None else v.data_ptr() for k, v in out.items()}
     g = ScanGrads(dyp, dy.stride()[:2], df, sp, p["dx"], p["ddt"], p["dB"], p["dC"], p["dz"],
                   p["dA"], p["dD"], p["ddt_bias"], p["dstate"])
-    scratch = _scratch(scratch, L.selective_scan_grad_scratch_bytes(a), dev, stream)
-    check(L.selective_scan_grad(a, g, scratch.data_ptr(), scratch.numel(), _stream(stream)))
+    scratch, room = _scratch(scratch, L.selective_scan_grad_scratch_bytes(a), A, stream)
+    check(L.selective_scan_grad(a, g, scratch.data_ptr(), room, _stream(stream)))
     return out
 
 
@@ -254,9 +262,10 @@ def selective_scan_step(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, sof
     moves on in place, or into ``new_state``.  Returns ``y``."""
     a = _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, None, None, True)
     shape = (a.batch, a.channels, a.states)
-    sp = _like(state, "state", shape, torch.float32, x.device)
-    np_ = sp if new_state is None else _like(new_state, "new_state", shape, torch.float32, x.device)
-    y = _out(out, "out", x.shape, x.dtype, x.device, stream)
+    dev = x.get_device()
+    sp = _like(state, "state", shape, torch.float32, dev)
+    np_ = sp if new_state is None else _like(new_state, "new_state", shape, torch.float32, dev)
+    y = _out(out, "out", x.shape, x.dtype, x, stream)
     check(lib().selective_scan_step(a, sp, np_, y.data_ptr(), _stream(stream)))
     return y
 
@@ -269,11 +278,11 @@ def _table(t, what):
     return _code(t, what), t.stride(0)
 
 
-def _id_code(ids, device):
+def _id_code(ids, dev):
     if ids.dtype not in _IDS:
         raise NotImplementedError(f"ids: dtype {ids.dtype} is not supported")
-    if ids.device != device or not ids.is_contiguous():
-        raise ValueError(f"ids must be a contiguous tensor on {device}")
+    if ids.get_device() != dev or not ids.is_contiguous():
+        raise ValueError(f"ids must be a contiguous tensor on cuda:{dev}")
     return _IDS[ids.dtype]
 
 
@@ -281,9 +290,9 @@ def embedding(weight, ids, scale=1.0, out=None, stream=None):
     """``scale * weight[ids]`` for int32 or int64 ``ids`` of any shape; ids outside the table
     are masked tokens and give zeros.  Returns ``[*ids.shape, channels]`` in weight's type."""
     code, stride = _table(weight, "weight")
-    idc = _id_code(ids, weight.device)
+    idc = _id_code(ids, weight.get_device())
     rows, d = weight.shape
-    out = _out(out, "out", ids.shape + (d,), weight.dtype, weight.device, stream)
+    out = _out(out, "out", ids.shape + (d,), weight.dtype, weight, stream)
     check(lib().embedding(weight.data_ptr(), ids.data_ptr(), out.data_ptr(), ids.numel(), rows, d,
                           stride, code, idc, float(scale), _stream(stream)))
     return out
@@ -298,16 +307,15 @@ def embedding_grad(dout, ids, rows, scale=1.0, dtype=None, out=None, scratch=Non
         raise ValueError("dout must be [*ids.shape, channels]")
     flat = dout.view(-1, d) if dout.dim() != 2 else dout
     code, stride = _table(flat, "dout")
-    idc = _id_code(ids, dout.device)
+    idc = _id_code(ids, dout.get_device())
     dtype = dtype or (out.dtype if out is not None else dout.dtype)
     if dtype not in (dout.dtype, torch.float32):
         raise NotImplementedError("the gradient is of dout's type or float32")
-    out = _out(out, "out", (int(rows), d), dtype, dout.device, stream)
+    out = _out(out, "out", (int(rows), d), dtype, dout, stream)
     L = lib()
     n = ids.numel()
-    scratch = _scratch(scratch, L.embedding_grad_scratch_bytes(n, rows, d), dout.device,
-                       stream)
+    scratch, room = _scratch(scratch, L.embedding_grad_scratch_bytes(n, rows, d), dout, stream)
     check(L.embedding_grad(flat.data_ptr(), ids.data_ptr(), out.data_ptr(), n, rows, d, stride,
                            code, idc, _ACT[dtype], float(scale), scratch.data_ptr(),
-                           scratch.numel(), _stream(stream)))
+                           room, _stream(stream)))
     return out
