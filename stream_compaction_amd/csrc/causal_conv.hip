@@ -56,8 +56,7 @@ __device__ __forceinline__ void load_filters(const ConvProblem& p, int64_t ch, f
 // Input token t of sequence b: the initial state before 0, zero past `len`.
 template <class F, int E, int W>
 __device__ __forceinline__ typename RowIO<F, E>::Raw conv_input(const ConvProblem& p, int64_t b,
-                                                               int64_t t, int64_t len, int64_t ch,
-                                                               int64_t n, bool vec) {
+                                                               int64_t t, int64_t len, int64_t ch) {
   using S = typename F::S;
   const S* src = nullptr;
   if (t >= 0) {
@@ -66,7 +65,7 @@ __device__ __forceinline__ typename RowIO<F, E>::Raw conv_input(const ConvProble
     src = (const S*)p.initial_state + (b * (W - 1) + t + W - 1) * p.channels + ch;
   }
   if (src == nullptr) return typename RowIO<F, E>::Raw{};
-  return RowIO<F, E>::load(src, n, vec);
+  return RowIO<F, E>::load(src);
 }
 
 }  // namespace
@@ -78,7 +77,6 @@ __global__ __launch_bounds__(256) void causal_conv_kernel(ConvProblem p, void* y
                                                          void* final_state, int run_tokens) {
   using S = typename F::S;
   using IO = RowIO<F, E>;
-  constexpr bool vec = E > 1;
   const int64_t vecs = (p.channels + E - 1) / E;
   const int64_t runs = p.length > 0 ? (p.length + run_tokens - 1) / run_tokens : 1;
   const int64_t total = p.batch * runs * vecs;
@@ -87,7 +85,6 @@ __global__ __launch_bounds__(256) void causal_conv_kernel(ConvProblem p, void* y
     int64_t ch, run;
     const int64_t b = divide(divide(i, vecs, &ch), runs, &run);
     ch *= E;
-    const int64_t n = p.channels - ch;
     const int64_t len = conv_length(p, b);
     const int64_t t0 = run * run_tokens;
     const int64_t end = t0 + run_tokens < p.length ? t0 + run_tokens : p.length;
@@ -97,7 +94,7 @@ __global__ __launch_bounds__(256) void causal_conv_kernel(ConvProblem p, void* y
     int64_t t = t0;
     if (t < last) {
       auto row = [&](int64_t at) {
-        return at < last ? IO::load(x + at * p.x_token, n, vec) : typename IO::Raw{};
+        return at < last ? IO::load(x + at * p.x_token) : typename IO::Raw{};
       };
       typename IO::Raw next[kConvAhead];
 #pragma unroll
@@ -106,7 +103,7 @@ __global__ __launch_bounds__(256) void causal_conv_kernel(ConvProblem p, void* y
       load_filters<E, W>(p, ch, w, bias);
 #pragma unroll
       for (int k = 0; k + 1 < W; ++k)
-        IO::unpack(conv_input<F, E, W>(p, b, t0 - W + 1 + k, len, ch, n, vec), win[k + 1]);
+        IO::unpack(conv_input<F, E, W>(p, b, t0 - W + 1 + k, len, ch), win[k + 1]);
       for (; t < last; t += kConvAhead) {
         typename IO::Raw raw[kConvAhead];
 #pragma unroll
@@ -128,18 +125,18 @@ __global__ __launch_bounds__(256) void causal_conv_kernel(ConvProblem p, void* y
             for (int k = 0; k < W; ++k) a = __builtin_fmaf(w[k][c], win[k][c], a);
             out[c] = p.silu ? silu(a) : a;
           }
-          if (t + j < last) IO::store(y + (t + j) * p.channels, IO::pack(out), n, vec);
+          if (t + j < last) IO::store(y + (t + j) * p.channels, IO::pack(out));
         }
       }
       t = last;
     }
-    for (; t < end; ++t) IO::store(y + t * p.channels, typename IO::Raw{}, n, vec);
+    for (; t < end; ++t) IO::store(y + t * p.channels, typename IO::Raw{});
     if (run == 0 && final_state != nullptr) {
       S* fs = (S*)final_state + b * (W - 1) * p.channels + ch;
 #pragma unroll
       for (int k = 0; k + 1 < W; ++k)
         IO::store(fs + k * p.channels,
-                  conv_input<F, E, W>(p, b, len - W + 1 + k, len, ch, n, vec), n, vec);
+                  conv_input<F, E, W>(p, b, len - W + 1 + k, len, ch));
     }
   }
 }
@@ -155,14 +152,13 @@ constexpr int kConvGradWaves = 4;
 // the initial state for t < 0) when t is among the last W - 1 before len.
 template <class F, int E, int W>
 __device__ __forceinline__ void add_final(const ConvProblem& p, const void* dfinal, int64_t b,
-                                          int64_t t, int64_t len, int64_t ch, int64_t n, bool vec,
-                                          float (&d)[E]) {
+                                          int64_t t, int64_t len, int64_t ch, float (&d)[E]) {
   using S = typename F::S;
   const int64_t j = t - len + W - 1;
   if (dfinal == nullptr || j < 0 || j >= W - 1) return;
   float v[E];
   RowIO<F, E>::unpack(
-      RowIO<F, E>::load((const S*)dfinal + (b * (W - 1) + j) * p.channels + ch, n, vec), v);
+      RowIO<F, E>::load((const S*)dfinal + (b * (W - 1) + j) * p.channels + ch), v);
 #pragma unroll
   for (int c = 0; c < E; ++c) d[c] += v[c];
 }
@@ -173,7 +169,6 @@ __global__ __launch_bounds__(64 * kConvGradWaves) void causal_conv_grad_kernel(
     void* dxv, void* dinitial, float* part, int run_tokens) {
   using S = typename F::S;
   using IO = RowIO<F, E>;
-  constexpr bool vec = E > 1;
   constexpr int M = W + 1;                          // sums per channel
   __shared__ float s_sum[kConvGradWaves][E * M][64];
   const int lane = lane_id(), wave = wave_id();
@@ -183,11 +178,11 @@ __global__ __launch_bounds__(64 * kConvGradWaves) void causal_conv_grad_kernel(
   const int64_t col = blockIdx.x % cols, set = blockIdx.x / cols;
   const int64_t sets = gridDim.x / cols;
   const int64_t ch = (col * 64 + lane) * E;
-  const int64_t n = p.channels - ch;                // may be <= 0: a lane past the last channel
+  const bool live = ch < p.channels;
   float w[W][E], bias[E], dw[W][E] = {}, db[E] = {};
-  if (n > 0) load_filters<E, W>(p, ch, w, bias);
+  if (live) load_filters<E, W>(p, ch, w, bias);
   for (int64_t r = set * kConvGradWaves + wave; r < total; r += sets * kConvGradWaves) {
-    if (n <= 0) break;
+    if (!live) break;
     int64_t t0;
     const int64_t b = divide(r, runs, &t0);
     t0 *= run_tokens;
@@ -198,15 +193,15 @@ __global__ __launch_bounds__(64 * kConvGradWaves) void causal_conv_grad_kernel(
     float win[W][E], g[W][E] = {};                  // inputs and gradients, newest last
 #pragma unroll
     for (int k = 0; k + 1 < W; ++k)
-      IO::unpack(conv_input<F, E, W>(p, b, t0 - W + 1 + k, len, ch, n, vec), win[k + 1]);
+      IO::unpack(conv_input<F, E, W>(p, b, t0 - W + 1 + k, len, ch), win[k + 1]);
     const int steps = run_tokens + W - 1;
     for (int s0 = 0; s0 < steps; s0 += kConvAhead) {
       typename IO::Raw rx[kConvAhead], rdy[kConvAhead];
 #pragma unroll
       for (int j = 0; j < kConvAhead; ++j) {
         const int64_t t = t0 + s0 + j;
-        rx[j] = conv_input<F, E, W>(p, b, t, len, ch, n, vec);
-        rdy[j] = t < len ? IO::load(dy + t * dy_token, n, vec) : typename IO::Raw{};
+        rx[j] = conv_input<F, E, W>(p, b, t, len, ch);
+        rdy[j] = t < len ? IO::load(dy + t * dy_token) : typename IO::Raw{};
       }
 #pragma unroll
       for (int j = 0; j < kConvAhead; ++j) {
@@ -247,13 +242,13 @@ __global__ __launch_bounds__(64 * kConvGradWaves) void causal_conv_grad_kernel(
 #pragma unroll
             for (int k = 0; k < W; ++k) d[c] = __builtin_fmaf(w[k][c], g[W - 1 - k][c], d[c]);
           }
-          add_final<F, E, W>(p, dfinal, b, u, len, ch, n, vec, d);
+          add_final<F, E, W>(p, dfinal, b, u, len, ch, d);
           S* to = u >= 0 ? dx + u * p.channels
                          : (S*)dinitial + (b * (W - 1) + u + W - 1) * p.channels + ch;
           if (u < len) {
-            IO::store(to, IO::pack(d), n, vec);
+            IO::store(to, IO::pack(d));
           } else {
-            IO::store(to, typename IO::Raw{}, n, vec);
+            IO::store(to, typename IO::Raw{});
           }
         }
       }
@@ -311,20 +306,18 @@ __global__ __launch_bounds__(256) void causal_conv_step_kernel(ConvProblem p, co
                                                               void* new_state, void* yv) {
   using S = typename F::S;
   using IO = RowIO<F, E>;
-  constexpr bool vec = E > 1;
   const int64_t vecs = (p.channels + E - 1) / E;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= p.batch * vecs) return;
   int64_t ch;
   const int64_t b = divide(i, vecs, &ch);
   ch *= E;
-  const int64_t n = p.channels - ch;
   float w[W][E], bias[E], a[E];
   typename IO::Raw row[W];
 #pragma unroll
   for (int k = 0; k + 1 < W; ++k)
-    row[k] = IO::load((const S*)state + (b * (W - 1) + k) * p.channels + ch, n, vec);
-  row[W - 1] = IO::load((const S*)p.x + b * p.x_batch + ch, n, vec);
+    row[k] = IO::load((const S*)state + (b * (W - 1) + k) * p.channels + ch);
+  row[W - 1] = IO::load((const S*)p.x + b * p.x_batch + ch);
   load_filters<E, W>(p, ch, w, bias);
 #pragma unroll
   for (int c = 0; c < E; ++c) a[c] = bias[c];
@@ -339,10 +332,10 @@ __global__ __launch_bounds__(256) void causal_conv_step_kernel(ConvProblem p, co
 #pragma unroll
     for (int c = 0; c < E; ++c) a[c] = silu(a[c]);
   }
-  IO::store((S*)yv + b * p.channels + ch, IO::pack(a), n, vec);
+  IO::store((S*)yv + b * p.channels + ch, IO::pack(a));
 #pragma unroll
   for (int k = 0; k + 1 < W; ++k)
-    IO::store((S*)new_state + (b * (W - 1) + k) * p.channels + ch, row[k + 1], n, vec);
+    IO::store((S*)new_state + (b * (W - 1) + k) * p.channels + ch, row[k + 1]);
 }
 
 // Vectors of E channels can be used when every row starts on E elements.

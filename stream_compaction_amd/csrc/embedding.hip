@@ -38,12 +38,12 @@ __global__ __launch_bounds__(256) void embedding_kernel(const void* weight, cons
     typename IO::Raw r{};
     if (row >= 0) {
       float v[E];
-      IO::unpack(IO::load((const S*)weight + row * row_stride + ch, channels - ch, E > 1), v);
+      IO::unpack(IO::load((const S*)weight + row * row_stride + ch), v);
 #pragma unroll
       for (int c = 0; c < E; ++c) v[c] *= scale;
       r = IO::pack(v);
     }
-    IO::store((S*)out + t * channels + ch, r, channels - ch, E > 1);
+    IO::store((S*)out + t * channels + ch, r);
   }
 }
 
@@ -243,7 +243,7 @@ __global__ __launch_bounds__(256) void embedding_segment_kernel(
       for (int j = 0; j < kSegAhead; ++j) {
         raw[j] = typename IO::Raw{};
         const int64_t i = (uint32_t)__builtin_amdgcn_readlane((int)at, j0 + j);
-        if (j0 + j < cnt && n > 0) raw[j] = IO::load((const S*)dout + i * row_stride + ch, n, E > 1);
+        if (j0 + j < cnt && n > 0) raw[j] = IO::load((const S*)dout + i * row_stride + ch);
       }
 #pragma unroll
       for (int j = 0; j < kSegAhead; ++j) {
@@ -267,13 +267,12 @@ __global__ __launch_bounds__(256) void embedding_segment_kernel(
               float o[OE];
 #pragma unroll
               for (int c = 0; c < OE; ++c) o[c] = sum[h + c] * scale;
-              OIO::store(to + h, OIO::pack(o), n - h, E > 1);
+              OIO::store(to + h, OIO::pack(o));
             }
           } else {
             float* to = out_part + (whole ? channels : 0);
 #pragma unroll
-            for (int c = 0; c < E; ++c)
-              if (c < n) to[c] = sum[c];
+            for (int c = 0; c < E; ++c) to[c] = sum[c];
           }
         }
 #pragma unroll
@@ -318,13 +317,13 @@ __global__ __launch_bounds__(256) void embedding_border_kernel(const uint32_t* _
     }
     if (ch >= channels) continue;
     float sum[E];
-    IO::unpack(IO::load(part + (seg * 2 + 1) * channels + ch, E, E > 1), sum);
+    IO::unpack(IO::load(part + (seg * 2 + 1) * channels + ch), sum);
     const float* from = part + (seg + 1) * 2 * channels + ch;
     typename IO::Raw next[kAhead];
     auto fetch = [&](int64_t p0) {
 #pragma unroll
       for (int j = 0; j < kAhead; ++j)
-        next[j] = p0 + j < pieces ? IO::load(from + (p0 + j) * 2 * channels, E, E > 1)
+        next[j] = p0 + j < pieces ? IO::load(from + (p0 + j) * 2 * channels)
                                   : typename IO::Raw{};
     };
     fetch(0);

@@ -351,7 +351,7 @@ __global__ __launch_bounds__(256) void selective_scan_step_kernel(ScanProblem p,
   }
   for (int n = q * V; n < N; n += G * V) {
     float A[V];
-    IO::unpack(IO::load(p.A + ch * N + n, V, V > 1), A);
+    IO::unpack(IO::load(p.A + ch * N + n), A);
     typename IO::Raw h0[R];
     typename BIO::Raw Bn[R], Cn[R];
 #pragma unroll
@@ -360,9 +360,9 @@ __global__ __launch_bounds__(256) void selective_scan_step_kernel(ScanProblem p,
       h0[r] = typename IO::Raw{};
       Bn[r] = Cn[r] = typename BIO::Raw{};
       if (!on[r]) continue;
-      h0[r] = IO::load(state + (b * p.channels + ch) * N + n, V, V > 1);
-      Bn[r] = BIO::load((const S*)p.B + b * p.B_batch + g * p.B_group + n, V, V > 1);
-      Cn[r] = BIO::load((const S*)p.C + b * p.C_batch + g * p.C_group + n, V, V > 1);
+      h0[r] = IO::load(state + (b * p.channels + ch) * N + n);
+      Bn[r] = BIO::load((const S*)p.B + b * p.B_batch + g * p.B_group + n);
+      Cn[r] = BIO::load((const S*)p.C + b * p.C_batch + g * p.C_group + n);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) A[v] *= kLog2e;
@@ -379,7 +379,7 @@ __global__ __launch_bounds__(256) void selective_scan_step_kernel(ScanProblem p,
         acc[r] = __builtin_fmaf(h[v], Cv[v], acc[r]);
       }
       if (on[r])
-        IO::store(new_state + ((b0 + r) * p.channels + ch) * N + n, IO::pack(h), V, V > 1);
+        IO::store(new_state + ((b0 + r) * p.channels + ch) * N + n, IO::pack(h));
     }
   }
   const float D = p.D != nullptr ? p.D[ch] : 0.0f;

@@ -22,14 +22,19 @@ __device__ __forceinline__ float rcp_hw(float v) { return __builtin_amdgcn_rcpf(
 
 // sigmoid(v); v -> -inf gives rcp(inf) = 0, v -> inf gives 1.
 __device__ __forceinline__ float sigmoid(float v) { return rcp_hw(1.0f + exp2_hw(-v * kLog2e)); }
-// silu(v) = v sigmoid(v).  Below -104 the sigmoid underflows (v = -inf would
-// give -inf * 0): there the limit, a signed zero, is returned.
-__device__ __forceinline__ float silu(float v) { return v < -104.0f ? -0.0f : v * sigmoid(v); }
-// d silu / dv = s (1 + v (1 - s)), with the same limits at the two ends.
+// The greater and the lesser of two, a NaN if either is one.
+__device__ __forceinline__ float at_least(float v, float low) { return __builtin_elementwise_maximum(v, low); }
+__device__ __forceinline__ float at_most(float v, float high) { return __builtin_elementwise_minimum(v, high); }
+// silu(v) = v sigmoid(v); v is kept finite, as -inf * 0 would be no number.
+__device__ __forceinline__ float silu(float v) {
+  v = at_least(v, -1e30f);
+  return v * sigmoid(v);
+}
+// d silu / dv = s (1 + v (1 - s)), with 0 and 1 at the two ends.
 __device__ __forceinline__ float silu_slope(float v) {
+  v = at_most(at_least(v, -1e30f), 1e30f);
   const float s = sigmoid(v);
-  const float r = s * (1.0f + v * (1.0f - s));
-  return v < -104.0f ? 0.0f : (v > 104.0f ? 1.0f : r);
+  return s * __builtin_fmaf(v, 1.0f - s, 1.0f);
 }
 
 // softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|) in (0, 1].  The steps of
@@ -80,6 +85,9 @@ template <class F, int E> struct RowIO {
   using Raw = std::conditional_t<sizeof(Elems) == 16, u32x4,
               std::conditional_t<sizeof(Elems) == 8, vec2,
               std::conditional_t<sizeof(Elems) == 4, uint32_t, uint16_t>>>;
+  // all of them, aligned
+  static __device__ __forceinline__ Raw load(const S* p) { return *gptr<const Raw>((uintptr_t)p); }
+  static __device__ __forceinline__ void store(S* p, Raw r) { *gptr<Raw>((uintptr_t)p) = r; }
   static __device__ __forceinline__ Raw load(const S* p, int64_t n, bool vec) {
     if (vec && n >= E) return *gptr<const Raw>((uintptr_t)p);
     Elems s = {};
