@@ -76,9 +76,17 @@ def _out(t, what, shape, dtype, like, stream):
     return t
 
 
+_unused = {}        # per GPU, 16 bytes that no kernel touches, for calls that work without scratch
+
+
 def _scratch(scratch, need, like, stream):
-    """Bytes of scratch memory; a float32 ``like`` makes them the cheapest."""
+    """Scratch memory and its bytes; a float32 ``like`` makes it the cheapest."""
     if scratch is None:
+        if need <= 16:
+            dev = like.get_device()
+            if dev not in _unused:
+                _unused[dev] = torch.empty(4, dtype=torch.float32, device=like.device)
+            return _unused[dev], 16
         return _new((max(need, 16) + 3) // 4, torch.float32, like, stream), need
     if scratch.dtype != torch.uint8 or scratch.get_device() != like.get_device() or \
             not scratch.is_contiguous():
