@@ -399,7 +399,7 @@ static hipError_t launch_step_g(const ScanProblem& p, const float* state, float*
                                 void* y, hipStream_t stream) {
   const int64_t cols = (p.channels * G + 255) / 256;
   // several sequences a lane once that still leaves 2048 workgroups, 8 waves a SIMD
-  constexpr int R = 4;
+  constexpr int R = 2;
   const bool many = p.batch * cols >= 2048 * R;
   const int64_t step = kMaxGroups / cols < 1 ? 1 : kMaxGroups / cols;
   for (int64_t b0 = 0; b0 < p.batch; b0 += step) {

@@ -57,7 +57,7 @@ def test_conv_long_runs():
 
 
 def test_scan_step_many_sequences():
-    # four sequences a lane, and the one or three left over; fewer take another path
+    # two sequences a lane, and the one left over; fewer take another path
     d, n = 4096, 16
     for b in (128, 131):
         r = gen(220 + b)
