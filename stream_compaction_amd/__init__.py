@@ -58,7 +58,8 @@ EXPORTS = ("scan_rows", "scan_device", "scan_device_inclusive", "scan_device_scr
            "scan_device_inclusive_devn", "reduce_device_devn", "reduce_by_key_devn",
            "radix_sort_devn", "select_compact_devn", "scan_device_noalloc", "causal_conv",
            "causal_conv_grad", "causal_conv_grad_scratch_bytes", "causal_conv_step",
-           "selective_scan", "selective_scan_starts_bytes", "selective_scan_grad",
+           "selective_scan", "selective_scan_starts_bytes", "selective_scan_split",
+           "selective_scan_split_scratch_bytes", "selective_scan_grad",
            "selective_scan_grad_scratch_bytes", "selective_scan_step", "embedding",
            "embedding_grad", "embedding_grad_scratch_bytes", "scan_status_str",
            "scan_last_hip_error")

@@ -35,6 +35,7 @@ def declare(L):
                                   sz, _vp]),
             ("causal_conv_step", [conv, _vp, _vp, _vp, _vp]),
             ("selective_scan", [scan, _vp, _vp, _vp, _vp]),
+            ("selective_scan_split", [scan, _vp, _vp, _vp, _vp, sz, _vp]),
             ("selective_scan_grad", [scan, ctypes.POINTER(ScanGrads), _vp, sz, _vp]),
             ("selective_scan_step", [scan, _vp, _vp, _vp, _vp]),
             ("embedding", [_vp, _vp, _vp, _i64, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int, f32,
@@ -45,6 +46,7 @@ def declare(L):
         getattr(L, name).restype = ctypes.c_int
     for name, args in (("causal_conv_grad_scratch_bytes", [conv]),
                        ("selective_scan_starts_bytes", [scan]),
+                       ("selective_scan_split_scratch_bytes", [scan]),
                        ("selective_scan_grad_scratch_bytes", [scan]),
                        ("embedding_grad_scratch_bytes", [_i64, _i64, _i64])):
         getattr(L, name).argtypes = args

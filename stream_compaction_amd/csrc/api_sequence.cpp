@@ -250,22 +250,45 @@ size_t selective_scan_starts_bytes(const selective_scan_args* args) {
                        (unsigned __int128)(p.channels * p.states) * 4);
 }
 
-scan_status selective_scan(const selective_scan_args* args, void* y, float* final_state,
-                           float* starts, void* stream) {
+static scan_status scan_call(const selective_scan_args* args, void* y, float* final_state,
+                             float* starts, bool split, void* scratch, size_t scratch_bytes,
+                             void* stream) {
   sca::ScanProblem p;
   sca::Fmt fmt;
   size_t eb;
   const scan_status st = scan_problem(args, false, &p, &fmt, &eb);
   if (st != SCAN_OK) return st;
   if (p.batch == 0) return SCAN_OK;
+  const size_t need = split ? sca::selective_scan_scratch(p) : 0;
   Ranges r;
   scan_inputs(p, eb, &r);
   r.add(y, (uint64_t)p.batch * (uint64_t)p.length * (uint64_t)p.channels, eb, true, true);
   r.add(final_state, (uint64_t)p.batch * (uint64_t)(p.channels * p.states), 4, true, false);
   if (starts != nullptr) r.add(starts, selective_scan_starts_bytes(args) / 4, 4, true, false);
+  r.add(scratch, need, 1, true, true);
+  if (need > 0 && !aligned(scratch, 16)) return SCAN_EINVAL;
+  if (scratch_bytes < need) return SCAN_ESCRATCH;
   if (r.status() != SCAN_OK) return r.status();
-  return hip_status(
-      sca::launch_selective_scan(p, fmt, y, final_state, starts, (hipStream_t)stream));
+  return hip_status(sca::launch_selective_scan(p, fmt, y, final_state, starts,
+                                               need > 0 ? scratch : nullptr, (hipStream_t)stream));
+}
+
+scan_status selective_scan(const selective_scan_args* args, void* y, float* final_state,
+                           float* starts, void* stream) {
+  return scan_call(args, y, final_state, starts, false, nullptr, 0, stream);
+}
+
+size_t selective_scan_split_scratch_bytes(const selective_scan_args* args) {
+  sca::ScanProblem p;
+  sca::Fmt fmt;
+  size_t eb;
+  if (scan_problem(args, false, &p, &fmt, &eb) != SCAN_OK) return 0;
+  return sca::selective_scan_scratch(p);
+}
+
+scan_status selective_scan_split(const selective_scan_args* args, void* y, float* final_state,
+                                 float* starts, void* scratch, size_t scratch_bytes, void* stream) {
+  return scan_call(args, y, final_state, starts, true, scratch, scratch_bytes, stream);
 }
 
 size_t selective_scan_grad_scratch_bytes(const selective_scan_args* args) {

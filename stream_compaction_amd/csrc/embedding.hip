@@ -490,9 +490,7 @@ GradScratch grad_scratch(int64_t tokens, int64_t rows, int64_t channels) {
 }
 }  // namespace
 size_t embedding_grad_scratch(int64_t tokens, int64_t rows, int64_t channels) {
-  if (tokens == 0) return 0;
-  // (one rule for callers: a list of tokens comes with scratch, though a short one uses none)
-  return embedding_few(tokens) ? 16 : grad_scratch(tokens, rows, channels).bytes;
+  return tokens == 0 ? 0 : grad_scratch(tokens, rows, channels).bytes;
 }
 
 static hipError_t few_go(const void* dout, const void* ids, bool wide_ids, void* dweight,

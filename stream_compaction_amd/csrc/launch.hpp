@@ -89,8 +89,11 @@ struct ScanProblem {
 };
 // The forward keeps the state before every so many tokens for the gradient.
 constexpr int kScanKeepTokens = 16;
+// Chunks that a scan of few channels is split into when it is given scratch.
+int64_t scan_chunks(const ScanProblem& p, int64_t* tokens);
+size_t selective_scan_scratch(const ScanProblem& p);     // 0: not split
 hipError_t launch_selective_scan(const ScanProblem& p, Fmt fmt, void* y, float* final_state,
-                                 float* starts, hipStream_t stream);
+                                 float* starts, void* scratch, hipStream_t stream);
 struct ScanGrads {
   const void* dy;
   int64_t dy_batch, dy_token;

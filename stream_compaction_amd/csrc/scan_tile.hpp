@@ -120,6 +120,18 @@ template <class F> bool scan_pairs(const ScanProblem& p, const void* y) {
          even(p.B, p.B_batch, p.B_token, p.B_group) && even(p.C, p.C_batch, p.C_token, p.C_group);
 }
 
+// A scan with too few workgroups is split over its length: `chunks` of `tokens`
+// tokens each.  A first kernel finds every chunk's state from a zero start
+// (`ends`) and the sum of its steps (`spans`): a chunk's start is then exp(A sum)
+// of the chunk before's times that one's start, plus that one's end.  One chunk:
+// not split.
+struct ScanSplit {
+  int64_t tokens;
+  uint32_t chunks;
+  float* ends;          // [batch][chunks][channels][states]
+  float* spans;         // [batch][chunks][channels]
+};
+
 // Where a workgroup stands in the problem: sequence, group of B and C, first
 // channel, and how many of its 16 channels exist.
 struct ScanPlace {

@@ -40,21 +40,32 @@ constexpr int kFwdThreads = 256;        // T tokens of 8 channel pairs
 
 }  // namespace
 
-// KEEP: write the state before every kKeep tokens to `starts`, for the gradient.
-template <class F, int NS, bool VEC, bool KEEP>
+// What a launch does: all; also keep the state before every kKeep tokens in
+// `starts`, for the gradient; or find the chunks' ends of a split scan alone.
+enum class Pass { Run, Keep, Ends };
+
+template <class F, int NS, bool VEC, Pass PASS>
 __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
-    ScanProblem p, void* yv, float* final_state, float* starts, int64_t b0, int64_t tiles, uint32_t count) {
+    ScanProblem p, void* yv, float* final_state, float* starts, ScanSplit split, int64_t b0,
+    int64_t tiles, uint32_t count) {
+  constexpr bool KEEP = PASS == Pass::Keep, ENDS = PASS == Pass::Ends;
   using S = typename F::S;
   using IO = RowIO<F, 2>;
   typedef float vec4 __attribute__((ext_vector_type(4)));
   __shared__ alignas(16) float s_x[2][2 * kPlane];           // steps, steps times x
   __shared__ alignas(16) float s_bc[2][2 * NS * kPlane];     // B, C
-  __shared__ alignas(16) float s_part[2][4 * kPlane];        // per wave
+  __shared__ alignas(16) float s_part[2][ENDS ? 1 : 4 * kPlane];   // per wave
 
   const uint32_t id = xcd_order(blockIdx.x);
   if (id >= count) return;
-  const ScanPlace at = scan_place(p, b0, tiles, id, kScanTile);
-  const int64_t len = scan_length(p, at.b);
+  // chunk by chunk; a chunk is worked on like a sequence that begins at `first`
+  const uint32_t per = ENDS ? count / (split.chunks - 1) : count / split.chunks;
+  const int64_t chunk = id / per, first = chunk * split.tokens;
+  const ScanPlace at = scan_place(p, b0, tiles, id % per, kScanTile);
+  auto within = [&](int64_t n) {
+    return n <= first ? 0 : (n - first < split.tokens ? n - first : split.tokens);
+  };
+  const int64_t whole = scan_length(p, at.b), len = within(whole), padded = within(p.length);
   const int N = (int)p.states, nch = (int)at.nch;
   const bool gate = p.z != nullptr;
   const int tid = (int)threadIdx.x, lane = lane_id(), wave = wave_id();
@@ -65,23 +76,27 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
   // staging: this thread's token and two channels (and two states of each 16)
   const int tok = tid / 8, pair = tid % 8;
   const bool stager = pair * 2 < nch;
-  float* keep = KEEP ? starts + (at.b * ((p.length + kKeep - 1) / kKeep) * p.channels + ch) * N + n0
+  float* keep = KEEP ? starts + ((at.b * ((p.length + kKeep - 1) / kKeep) + first / kKeep) * p.channels +
+                                 ch) * N + n0
                      : nullptr;
   using Src = PairSrc<F, VEC>;
   using Raw = Pair<F, VEC>;
-  Src xs(p.x, p.x_batch, p.x_token, at.b, at.ch, nch);
-  Src dts(p.dt, p.dt_batch, p.dt_token, at.b, at.ch, nch);
+  Src xs(p.x, p.x_batch, p.x_token, at.b, at.ch + first * p.x_token, nch);
+  Src dts(p.dt, p.dt_batch, p.dt_token, at.b, at.ch + first * p.dt_token, nch);
   // without a gate x stands in, unused
-  Src zs(gate ? p.z : p.x, gate ? p.z_batch : p.x_batch, gate ? p.z_token : p.x_token, at.b, at.ch, nch);
+  const int64_t z_token = gate ? p.z_token : p.x_token;
+  Src zs(gate ? p.z : p.x, gate ? p.z_batch : p.x_batch, z_token, at.b, at.ch + first * z_token, nch);
   Src Bs[NS], Cs[NS];
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
     // the states past the last 16 that exist read the first ones, unused
     const int n = s * 16 < N ? s * 16 : 0;
-    Bs[s] = Src(p.B, p.B_batch, p.B_token, at.b, at.g * p.B_group + n, N - n);
-    Cs[s] = Src(p.C, p.C_batch, p.C_token, at.b, at.g * p.C_group + n, N - n);
+    Bs[s] = Src(p.B, p.B_batch, p.B_token, at.b,
+                at.g * p.B_group + n + first * p.B_token, N - n);
+    Cs[s] = Src(p.C, p.C_batch, p.C_token, at.b,
+                at.g * p.C_group + n + first * p.C_token, N - n);
   }
-  S* y = (S*)yv + at.b * p.length * p.channels + at.ch;
+  S* y = (S*)yv + (at.b * p.length + first) * p.channels + at.ch;
   float Dc[2], bias[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -97,9 +112,22 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
     const int n = n0 + s * 16;
     mine[s] = cl < nch && n < N;
     A2[s] = mine[s] ? p.A[ch * N + n] * kLog2e : 0.0f;
-    h[s] = mine[s] && p.initial_state != nullptr ? p.initial_state[srow + n] : 0.0f;
+    h[s] = !ENDS && mine[s] && p.initial_state != nullptr ? p.initial_state[srow + n] : 0.0f;
   }
 
+  float span = 0.0f;                            // ENDS: sum of the channel's steps
+  if constexpr (!ENDS) {
+    // the chunk's start, from the chunks before (eight loads at a time)
+#pragma unroll 8
+    for (int64_t c = 0; c < chunk; ++c) {
+      const int64_t r = (at.b * split.chunks + c) * p.channels + (cl < nch ? ch : at.ch);
+      const float passed = split.spans[r];
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+        h[s] = __builtin_fmaf(exp2_hw(passed * A2[s]), h[s],
+                              mine[s] ? split.ends[r * N + n0 + s * 16] : 0.0f);
+    }
+  }
   // the next block travels while one is worked on
   struct Fetched { Raw x, dt, z, B[NS], C[NS]; };
   auto seek = [&](int64_t t0) {
@@ -115,11 +143,11 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
   auto fetch = [&](Fetched& f) {
     f.x = xs.load();
     f.dt = dts.load();
-    f.z = zs.load();
+    if constexpr (!ENDS) f.z = zs.load();
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       f.B[s] = Bs[s].load();
-      f.C[s] = Cs[s].load();
+      if constexpr (!ENDS) f.C[s] = Cs[s].load();
     }
     xs.advance(kT);
     dts.advance(kT);
@@ -138,7 +166,7 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
     float x[2], dt[2], v[2];
     f.x.unpack(x);
     f.dt.unpack(dt);
-    f.z.unpack(v);
+    if constexpr (!ENDS) f.z.unpack(v);
     float* to = s_x[buf] + pair * 2 * kPS + tok;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -147,9 +175,11 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
       const float d = p.softplus ? soft : raw;
       to[i * kPS] = exists ? d : 0.0f;
       to[kPlane + i * kPS] = exists ? d * x[i] : 0.0f;
-      rest.skip[i] = Dc[i] * x[i];
-      const float factor = silu(v[i]);
-      rest.factor[i] = gate ? factor : 1.0f;
+      if constexpr (!ENDS) {
+        rest.skip[i] = Dc[i] * x[i];
+        const float factor = silu(v[i]);
+        rest.factor[i] = gate ? factor : 1.0f;
+      }
     }
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
@@ -159,9 +189,11 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
       f.B[s].unpack_if(on0, on1, v);
       bc[0] = v[0];
       bc[kPS] = v[1];
-      f.C[s].unpack_if(on0, on1, v);
-      bc[NS * kPlane] = v[0];
-      bc[NS * kPlane + kPS] = v[1];
+      if constexpr (!ENDS) {
+        f.C[s].unpack_if(on0, on1, v);
+        bc[NS * kPlane] = v[0];
+        bc[NS * kPlane + kPS] = v[1];
+      }
     }
   };
   auto walk = [&](int64_t t0, int buf) {
@@ -182,11 +214,12 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
       for (int s = 0; s < NS; ++s) {
         if (KEEP && mine[s] && t0 + sub < len) keep[s * 16] = h[s];
         const float* bc = s_bc[buf] + (s * 16 + n0) * kPS + sub + cl;
-        const float B = bc[0], C = bc[NS * kPlane];
+        const float B = bc[0], C = ENDS ? 0.0f : bc[NS * kPlane];
         for_tokens([&](auto tc) {
           constexpr int t = decltype(tc)::value;
           const float a = exp2_hw(dt[t] * A2[s]);
           h[s] = __builtin_fmaf(a, h[s], row_bcast<t>(B) * u[t]);
+          if constexpr (ENDS) return;
           if (s == 0) {
             v[t] = row_bcast<t>(C) * h[s];
           } else {
@@ -195,6 +228,13 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
           // the product stays beside its broadcast, which else does not fold into it
           asm volatile("" : "+v"(v[t]));
         }, std::make_integer_sequence<int, 16>{});
+      }
+      if constexpr (ENDS) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int t = 0; t < 16; ++t) sum += dt[t];
+        span += sum;
+        continue;
       }
       rows_sum(v, sums);
       *(vec4*)(s_part[buf] + (wave * 16 + cl) * kPS + sub + row * 4) =
@@ -231,7 +271,7 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
   Rest rest[2] = {};
   auto step = [&](int64_t t0, int buf) {
     if (t0 + 3 * kT > len) seek(t0 + 2 * kT);
-    finish(rest[buf ^ 1], t0 - kT, buf ^ 1);
+    if constexpr (!ENDS) finish(rest[buf ^ 1], t0 - kT, buf ^ 1);
     stage(f, t0 + kT + tok < len, buf ^ 1, rest[buf ^ 1]);
     fetch(f);
     walk(t0, buf);
@@ -250,16 +290,28 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
       step((blk + 1) * kT, 1);
     }
     if (blk < blocks) step(blk * kT, 0);
-    if (blocks & 1) {
-      finish(rest[0], (blocks - 1) * kT, 0);
-    } else {
-      finish(rest[1], (blocks - 1) * kT, 1);
+    if constexpr (!ENDS) {
+      if (blocks & 1) {
+        finish(rest[0], (blocks - 1) * kT, 0);
+      } else {
+        finish(rest[1], (blocks - 1) * kT, 1);
+      }
     }
   }
+  if constexpr (ENDS) {
+    const int64_t r = (at.b * split.chunks + chunk) * p.channels + ch;
+    if (wave == 0 && row == 0 && cl < nch) split.spans[r] = span;
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+      if (mine[s]) split.ends[r * N + n0 + s * 16] = h[s];
+    return;
+  }
   // tokens past the sequence's end
-  for (int64_t i = len * kScanTile + tid; i < p.length * kScanTile; i += kFwdThreads)
+  for (int64_t i = len * kScanTile + tid; i < padded * kScanTile; i += kFwdThreads)
     if (i % kScanTile < nch) y[(i / kScanTile) * p.channels + i % kScanTile] = S(0);
-  if (final_state == nullptr) return;
+  // the final state is the chunk's in which the sequence ends
+  const bool ends_here = whole > first ? whole - first <= split.tokens : chunk == 0 && whole == 0;
+  if (final_state == nullptr || !ends_here) return;
 #pragma unroll
   for (int s = 0; s < NS; ++s)
     if (mine[s]) final_state[srow + n0 + s * 16] = h[s];
@@ -269,51 +321,96 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
 // beyond that go out as several launches.
 constexpr int64_t kMaxGroups = 1ll << 21;
 
-template <class F>
-static hipError_t launch_fwd(const ScanProblem& p, void* y, float* final_state, float* starts,
-                             hipStream_t stream) {
+// Chunks by an estimate in tokens' time.  With w waves per SIMD (256 workgroups
+// are one) a token takes 1 + 0.5 (w - 1) times as long as with up to one; the
+// first pass costs 0.6 of the second and leaves out one chunk; its launch and the
+// chunks' starts stand for 150 + 8 n tokens.  The split must win a fifth.  Forward
+// / gradient, split against whole, 16 states in bf16: 8192 x 64 channels 28 / 57 us
+// against 263 / 717, 2048 x 512 24 / 53 against 69 / 192, 2 x 4096 x 768 74 / 169
+// against 134 / 377, 8192 x 2048 162 / 403 against 262 / 748, 7 x 1024 x 300 37 / 80
+// against 38 / 105.  From 256 workgroups on (8192 x 4096) the estimate gains
+// nothing.
+int64_t scan_chunks(const ScanProblem& p, int64_t* tokens) {
+  const int64_t groups = (p.channels / p.groups + kScanTile - 1) / kScanTile * p.groups * p.batch;
+  *tokens = p.length > 0 ? p.length : 1;
+  if (groups == 0 || groups >= 256 || p.length < 512) return 1;
+  int64_t best = p.length * 8 / 10, chunks = 1;
+  for (int64_t n = 2; n <= 32 && n * 128 <= p.length; ++n) {
+    const int64_t over = groups * n > 256 ? groups * n - 256 : 0;
+    const int64_t time = p.length / n * (10 * n + 6 * (n - 1)) / (10 * n) * (256 * 100 + 50 * over) / (256 * 100) + 150 + 8 * n;
+    if (time < best) {
+      best = time;
+      chunks = n;
+    }
+  }
+  if (chunks == 1) return 1;
+  *tokens = ((p.length + chunks - 1) / chunks + kT - 1) / kT * kT;
+  return (p.length + *tokens - 1) / *tokens;
+}
+size_t selective_scan_scratch(const ScanProblem& p) {
+  int64_t tokens;
+  const int64_t chunks = scan_chunks(p, &tokens);
+  return chunks == 1 ? 0 : (size_t)(p.batch * chunks * p.channels * (p.states + 1)) * 4;
+}
+
+template <class F, int NS, bool VEC>
+static void fwd_go(const ScanProblem& p, void* y, float* final_state, float* starts,
+                   const ScanSplit& split, hipStream_t stream) {
   const int64_t tiles = (p.channels / p.groups + kScanTile - 1) / kScanTile;
   const int64_t per = tiles * p.groups;
   const int64_t step = kMaxGroups / per < 1 ? 1 : kMaxGroups / per;
-  const bool pairs = scan_pairs<F>(p, y);
   for (int64_t b0 = 0; b0 < p.batch; b0 += step) {
     const int64_t nb = p.batch - b0 < step ? p.batch - b0 : step;
-    auto go = [&](auto ns, auto vec) {
-      auto keep = [&](auto k) {
-        selective_scan_kernel<F, decltype(ns)::value, decltype(vec)::value, decltype(k)::value>
-            <<<dim3(xcd_grid(nb * per)), dim3(kFwdThreads), 0, stream>>>(
-                p, y, final_state, starts, b0, tiles, (uint32_t)(nb * per));
-      };
-      if (starts != nullptr) {
-        keep(std::true_type{});
-      } else {
-        keep(std::false_type{});
-      }
+    auto go = [&](auto pass, int64_t chunks) {
+      const int64_t count = nb * per * chunks;
+      selective_scan_kernel<F, NS, VEC, decltype(pass)::value>
+          <<<dim3(xcd_grid(count)), dim3(kFwdThreads), 0, stream>>>(
+              p, y, final_state, starts, split, b0, tiles, (uint32_t)count);
     };
-    auto by_states = [&](auto vec) {
-      if (p.states <= 16) {
-        go(std::integral_constant<int, 1>{}, vec);
-      } else if (p.states <= 32) {
-        go(std::integral_constant<int, 2>{}, vec);
-      } else {
-        go(std::integral_constant<int, 4>{}, vec);
-      }
-    };
-    if (pairs) {
-      by_states(std::true_type{});
+    if (split.chunks > 1) go(std::integral_constant<Pass, Pass::Ends>{}, split.chunks - 1);
+    if (starts != nullptr) {
+      go(std::integral_constant<Pass, Pass::Keep>{}, split.chunks);
     } else {
-      by_states(std::false_type{});
+      go(std::integral_constant<Pass, Pass::Run>{}, split.chunks);
     }
+  }
+}
+
+template <class F>
+static hipError_t launch_fwd(const ScanProblem& p, void* y, float* final_state, float* starts,
+                             void* scratch, hipStream_t stream) {
+  ScanSplit split{};
+  split.chunks = 1;
+  split.tokens = p.length > 0 ? p.length : 1;
+  if (scratch != nullptr) {
+    split.chunks = (uint32_t)scan_chunks(p, &split.tokens);
+    split.ends = (float*)scratch;
+    split.spans = split.ends + p.batch * split.chunks * p.channels * p.states;
+  }
+  auto by_states = [&](auto vec) {
+    constexpr bool VEC = decltype(vec)::value;
+    if (p.states <= 16) {
+      fwd_go<F, 1, VEC>(p, y, final_state, starts, split, stream);
+    } else if (p.states <= 32) {
+      fwd_go<F, 2, VEC>(p, y, final_state, starts, split, stream);
+    } else {
+      fwd_go<F, 4, VEC>(p, y, final_state, starts, split, stream);
+    }
+  };
+  if (scan_pairs<F>(p, y)) {
+    by_states(std::true_type{});
+  } else {
+    by_states(std::false_type{});
   }
   return hipGetLastError();
 }
 
 hipError_t launch_selective_scan(const ScanProblem& p, Fmt fmt, void* y, float* final_state,
-                                 float* starts, hipStream_t stream) {
+                                 float* starts, void* scratch, hipStream_t stream) {
   switch (fmt) {
-    case Fmt::F32: return launch_fwd<FmtF32>(p, y, final_state, starts, stream);
-    case Fmt::F16: return launch_fwd<FmtF16>(p, y, final_state, starts, stream);
-    case Fmt::BF16: return launch_fwd<FmtBF16>(p, y, final_state, starts, stream);
+    case Fmt::F32: return launch_fwd<FmtF32>(p, y, final_state, starts, scratch, stream);
+    case Fmt::F16: return launch_fwd<FmtF16>(p, y, final_state, starts, scratch, stream);
+    case Fmt::BF16: return launch_fwd<FmtBF16>(p, y, final_state, starts, scratch, stream);
     default: return hipErrorInvalidValue;
   }
 }

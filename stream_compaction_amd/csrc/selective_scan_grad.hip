@@ -61,11 +61,12 @@ __device__ __forceinline__ float lanes_sum(float (&v)[16], int l) {
 
 }  // namespace
 
-// TL tiles of 16 channels, four waves each.
-template <class F, int NS, bool GATE, int TL>
+// TL tiles of 16 channels, four waves each.  ENDS: only find m before each chunk
+// of a split scan (but the first) from zero after it, and the sum of its steps.
+template <class F, int NS, bool GATE, int TL, bool ENDS>
 __global__ __launch_bounds__(256 * TL) void selective_scan_grad_kernel(
-    ScanProblem p, ScanGrads g, float* part, float* part_params, int64_t b0, int64_t tiles,
-    uint32_t count) {
+    ScanProblem p, ScanGrads g, float* part, float* part_params, ScanSplit split, int64_t b0,
+    int64_t tiles, uint32_t count) {
   using S = typename F::S;
   typedef float vec4 __attribute__((ext_vector_type(4)));
   constexpr int RL = 2 / TL;            // rows of B and C that a thread stages
@@ -77,8 +78,14 @@ __global__ __launch_bounds__(256 * TL) void selective_scan_grad_kernel(
 
   const uint32_t id = xcd_order(blockIdx.x);
   if (id >= count) return;
-  const ScanPlace at = scan_place(p, b0, tiles, id, kScanTile * TL);
-  const int64_t len = scan_length(p, at.b);
+  // chunk by chunk; a chunk is worked on like a sequence that begins at `first`
+  const uint32_t per = ENDS ? count / (split.chunks - 1) : count / split.chunks;
+  const int64_t chunk = id / per + (ENDS ? 1 : 0), first = chunk * split.tokens;
+  const ScanPlace at = scan_place(p, b0, tiles, id % per, kScanTile * TL);
+  auto within = [&](int64_t n) {
+    return n <= first ? 0 : (n - first < split.tokens ? n - first : split.tokens);
+  };
+  const int64_t len = within(scan_length(p, at.b)), padded = within(p.length);
   const int N = (int)p.states;
   const int tid = (int)threadIdx.x, lane = lane_id(), wave = wave_id();
   const int tl = wave / 4, row = lane / 16, cl = lane % 16;
@@ -97,7 +104,7 @@ __global__ __launch_bounds__(256 * TL) void selective_scan_grad_kernel(
   };
   auto source = [&](const void* a, int64_t batch, int64_t token, int64_t off) {
     Src s;
-    s.base = s.p = (const S*)a + at.b * batch + off;
+    s.base = s.p = (const S*)a + at.b * batch + first * token + off;
     s.token = token;
     return s;
   };
@@ -127,8 +134,22 @@ __global__ __launch_bounds__(256 * TL) void selective_scan_grad_kernel(
     const int n = n0 + s * 16;
     mine[s] = cl < nch && n < N;
     A2[s] = mine[s] ? p.A[ch * N + n] * kLog2e : 0.0f;
-    m[s] = mine[s] && g.dfinal != nullptr ? g.dfinal[srow + n] : 0.0f;
-    kept[s] = g.starts + (at.b * nkeep * p.channels + (mine[s] ? ch : at.ch)) * N + (mine[s] ? n : 0);
+    m[s] = !ENDS && mine[s] && g.dfinal != nullptr ? g.dfinal[srow + n] : 0.0f;
+    kept[s] = g.starts + ((at.b * nkeep + first / kKeep) * p.channels + (mine[s] ? ch : at.ch)) * N + (mine[s] ? n : 0);
+  }
+
+  float span = 0.0f;                            // ENDS: sum of the channel's steps
+  if constexpr (!ENDS) {
+    // m after the chunk, from the chunks after it (eight loads at a time)
+#pragma unroll 8
+    for (int64_t c = split.chunks - 1; c > chunk; --c) {
+      const int64_t r = (at.b * split.chunks + c) * p.channels + (cl < nch ? ch : at.ch);
+      const float passed = split.spans[r];
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+        m[s] = __builtin_fmaf(exp2_hw(passed * A2[s]), m[s],
+                              mine[s] ? split.ends[r * N + n0 + s * 16] : 0.0f);
+    }
   }
 
   struct Fetched { S x, dt, dy, z, rows[RL][NS]; float h[NS]; } f;
@@ -155,7 +176,7 @@ __global__ __launch_bounds__(256 * TL) void selective_scan_grad_kernel(
     for (int s = 0; s < NS; ++s) {
 #pragma unroll
       for (int r = 0; r < RL; ++r) f.rows[r][s] = *gptr<const S>((uintptr_t)rows[r][s].p);
-      f.h[s] = kept[s][blk * p.channels * N];
+      if constexpr (!ENDS) f.h[s] = kept[s][blk * p.channels * N];
     }
   };
 
@@ -191,7 +212,7 @@ __global__ __launch_bounds__(256 * TL) void selective_scan_grad_kernel(
 #pragma unroll
       for (int r = 0; r < RL; ++r)
         s_bc[buf][r + tl][(s * 16 + c) * kPS + tok] = real ? widen<F>(f.rows[r][s]) : 0.0f;
-      start[s] = mine[s] ? f.h[s] : 0.0f;
+      if constexpr (!ENDS) start[s] = mine[s] ? f.h[s] : 0.0f;
     }
   };
 
@@ -208,6 +229,21 @@ __global__ __launch_bounds__(256 * TL) void selective_scan_grad_kernel(
         u[t + i] = b[i];
         q[t + i] = e[i];
       }
+    }
+    if constexpr (ENDS) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int t = 0; t < 16; ++t) sum += dt[t];
+      span += sum;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        const float C = s_bc[buf][1][(s * 16 + n0) * kPS + cl];
+        for_tokens([&](auto tc) {
+          constexpr int t = 15 - decltype(tc)::value;
+          m[s] = exp2_hw(dt[t] * A2[s]) * __builtin_fmaf(row_bcast<t>(C), q[t], m[s]);
+        }, std::make_integer_sequence<int, 16>{});
+      }
+      return;
     }
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
@@ -235,6 +271,7 @@ __global__ __launch_bounds__(256 * TL) void selective_scan_grad_kernel(
       // other registers to the compiler: broadcasts shared by two products do not fold
       float Bb = B, Cb = C;
       asm volatile("" : "+v"(Bb), "+v"(Cb));
+      float dAb = 0.0f;                         // of the block: shorter chains of additions
       for_tokens([&](auto tc) {
         constexpr int t = 15 - decltype(tc)::value;
         float G = __builtin_fmaf(row_bcast<t>(Cb), q[t], m[s]);
@@ -249,8 +286,9 @@ __global__ __launch_bounds__(256 * TL) void selective_scan_grad_kernel(
         m[s] = a[t] * G;
         const float w = m[s] * (t > 0 ? h[t > 0 ? t - 1 : 0] : start[s]);
         vA[t] = s == 0 ? w * A2[s] : __builtin_fmaf(w, A2[s], vA[t]);
-        dA[s] = __builtin_fmaf(w, dt[t], dA[s]);
+        dAb = __builtin_fmaf(w, dt[t], dAb);
       }, std::make_integer_sequence<int, 16>{});
+      dA[s] += dAb;
       out[0] = lanes_sum(v, cl);
     }
     const int to = (wave % 4 * 16 + cl) * kPS + row * 4;
@@ -264,9 +302,9 @@ __global__ __launch_bounds__(256 * TL) void selective_scan_grad_kernel(
     if constexpr (GATE) put(SUMS - 1, vY);
   };
 
-  const int64_t out0 = at.b * p.length * p.channels + tch + c;
+  const int64_t out0 = (at.b * p.length + first) * p.channels + tch + c;
   const int64_t group = at.b * p.groups + at.g;
-  float* part0 = part + (group * tiles + at.tile) * p.length * (2 * N);
+  float* part0 = part + ((group * tiles + at.tile) * p.length + first) * (2 * N);
   auto finish = [&](const Rest& rest, int64_t blk, int buf) {
     const int64_t t = blk * kT + tok;
     auto total = [&](int k) {
@@ -310,7 +348,7 @@ __global__ __launch_bounds__(256 * TL) void selective_scan_grad_kernel(
     fetch(blk > 2 ? blk - 2 : 0);
     walk(buf, start[buf]);
     lds_barrier();
-    finish(rest[buf], blk, buf);
+    if constexpr (!ENDS) finish(rest[buf], blk, buf);
   };
   if (blocks > 0) {
     seek(blocks - 1);
@@ -325,17 +363,25 @@ __global__ __launch_bounds__(256 * TL) void selective_scan_grad_kernel(
       step(blk - 1, 1);
     }
   }
+  if constexpr (ENDS) {
+    const int64_t r = (at.b * split.chunks + chunk) * p.channels + ch;
+    if (wave == 0 && row == 0 && cl < nch) split.spans[r] = span;
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+      if (mine[s]) split.ends[r * N + n0 + s * 16] = m[s];
+    return;
+  }
   // tokens past the sequence's end
   const int width = kScanTile * TL;
-  for (int64_t i = len * width + tid; i < p.length * width; i += 256 * TL)
+  for (int64_t i = len * width + tid; i < padded * width; i += 256 * TL)
     if (i % width < at.nch) {
-      const int64_t o = (at.b * p.length + i / width) * p.channels + at.ch + i % width;
+      const int64_t o = (at.b * p.length + first + i / width) * p.channels + at.ch + i % width;
       ((S*)g.dx)[o] = S(0);
       ((S*)g.ddt)[o] = S(0);
       if constexpr (GATE) ((S*)g.dz)[o] = S(0);
     }
-  // sums over this sequence: [batch][channels * states | channels | channels]
-  float* params = part_params + at.b * p.channels * (N + 2);
+  // sums over this chunk: [batch][chunks][channels * states | channels | channels]
+  float* params = part_params + (at.b * split.chunks + chunk) * p.channels * (N + 2);
   __syncthreads();
   float* sums = &s_sum[0][0][0][0];
   sums[tid] = dD;
@@ -352,7 +398,7 @@ __global__ __launch_bounds__(256 * TL) void selective_scan_grad_kernel(
   for (int s = 0; s < NS; ++s)
     if (mine[s]) {
       params[ch * N + n0 + s * 16] = dA[s];
-      if (g.dinitial != nullptr) g.dinitial[srow + n0 + s * 16] = m[s];
+      if (g.dinitial != nullptr && chunk == 0) g.dinitial[srow + n0 + s * 16] = m[s];
     }
 }
 
@@ -381,13 +427,14 @@ __global__ __launch_bounds__(256) void scan_rows_sum_kernel(ScanProblem p, const
   }
 }
 
-// dA, dD and ddt_bias: sums over the batch, in order.
+// dA, dD and ddt_bias: sums over the batch and its chunks, in order.
 __global__ __launch_bounds__(256) void scan_params_sum_kernel(const float* part, int64_t batch,
                                                              int64_t channels, int64_t states,
                                                              float* dA, float* dD, float* dbias) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, count = channels * (states + 2);
   if (i >= count) return;
   float v = 0.0f;
+#pragma unroll 8
   for (int64_t b = 0; b < batch; ++b) v += part[b * count + i];
   if (i < channels * states) {
     dA[i] = v;
@@ -415,7 +462,10 @@ size_t rows_part_floats(const ScanProblem& p) {
 }  // namespace
 
 size_t selective_scan_grad_scratch(const ScanProblem& p) {
-  return 4 * (rows_part_floats(p) + (size_t)(p.batch * p.channels * (p.states + 2)));
+  int64_t tokens;
+  const int64_t chunks = scan_chunks(p, &tokens);
+  return 4 * (rows_part_floats(p) + (size_t)(p.batch * chunks * p.channels * (p.states + 2))) +
+         selective_scan_scratch(p);
 }
 
 constexpr int64_t kMaxGroups = 1ll << 22;   // workgroups per launch
@@ -428,13 +478,25 @@ static hipError_t launch_grad(const ScanProblem& p, const ScanGrads& g, void* sc
   const int64_t step = kMaxGroups / per < 1 ? 1 : kMaxGroups / per;
   float* part = (float*)scratch;
   float* params = part + rows_part_floats(p);
+  ScanSplit split{};
+  split.chunks = (uint32_t)scan_chunks(p, &split.tokens);
+  split.ends = params + p.batch * split.chunks * p.channels * (p.states + 2);
+  split.spans = split.ends + p.batch * split.chunks * p.channels * p.states;
   for (int64_t b0 = 0; b0 < p.batch; b0 += step) {
     const int64_t nb = p.batch - b0 < step ? p.batch - b0 : step;
     auto go = [&](auto ns, auto gate, auto tl) {
-      constexpr int TL = decltype(tl)::value;
-      selective_scan_grad_kernel<F, decltype(ns)::value, decltype(gate)::value, TL>
-          <<<dim3(xcd_grid(nb * per)), dim3(256 * TL), 0, stream>>>(p, g, part, params, b0, tiles,
-                                                                   (uint32_t)(nb * per));
+      constexpr int TL = decltype(tl)::value, NS = decltype(ns)::value;
+      constexpr bool GATE = decltype(gate)::value;
+      if constexpr (TL == 1) {
+        if (split.chunks > 1) {
+          const int64_t count = nb * per * (split.chunks - 1);
+          selective_scan_grad_kernel<F, NS, GATE, TL, true><<<dim3(xcd_grid(count)), dim3(256), 0, stream>>>(
+              p, g, part, params, split, b0, tiles, (uint32_t)count);
+        }
+      }
+      const int64_t count = nb * per * split.chunks;
+      selective_scan_grad_kernel<F, NS, GATE, TL, false><<<dim3(xcd_grid(count)), dim3(256 * TL), 0, stream>>>(
+          p, g, part, params, split, b0, tiles, (uint32_t)count);
     };
     auto by_tiles = [&](auto ns, auto gate) {
       if constexpr (decltype(ns)::value == 1) {
@@ -463,7 +525,7 @@ static hipError_t launch_grad(const ScanProblem& p, const ScanGrads& g, void* sc
                               stream>>>(p, part, g.dB, g.dC, tiles);
   const int64_t count = p.channels * (p.states + 2);
   scan_params_sum_kernel<<<dim3((unsigned)((count + 255) / 256)), dim3(256), 0, stream>>>(
-      params, p.batch, p.channels, p.states, g.dA, g.dD, g.ddt_bias);
+      params, p.batch * split.chunks, p.channels, p.states, g.dA, g.dD, g.ddt_bias);
   return hipGetLastError();
 }
 

@@ -76,17 +76,9 @@ def _out(t, what, shape, dtype, like, stream):
     return t
 
 
-_unused = {}        # per GPU, 16 bytes that no kernel touches, for calls that work without scratch
-
-
 def _scratch(scratch, need, like, stream):
     """Scratch memory and its bytes; a float32 ``like`` makes it the cheapest."""
     if scratch is None:
-        if need <= 16:
-            dev = like.get_device()
-            if dev not in _unused:
-                _unused[dev] = torch.empty(4, dtype=torch.float32, device=like.device)
-            return _unused[dev], 16
         return _new((max(need, 16) + 3) // 4, torch.float32, like, stream), need
     if scratch.dtype != torch.uint8 or scratch.get_device() != like.get_device() or \
             not scratch.is_contiguous():
@@ -227,12 +219,18 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=False,
     fs = _out(final_state, "final_state", (a.batch, a.channels, a.states), torch.float32,
               A if initial_state is None else initial_state, stream)
     L = lib()
-    if not keep_starts:
-        check(L.selective_scan(a, y.data_ptr(), fs.data_ptr(), None, _stream(stream)))
-        return y, fs
-    starts = _new((L.selective_scan_starts_bytes(a) // 4,), torch.float32, A, stream)
-    check(L.selective_scan(a, y.data_ptr(), fs.data_ptr(), starts.data_ptr(), _stream(stream)))
-    return y, fs, starts
+    starts = None
+    if keep_starts:
+        starts = _new((L.selective_scan_starts_bytes(a) // 4,), torch.float32, A, stream)
+    sp = None if starts is None else starts.data_ptr()
+    need = L.selective_scan_split_scratch_bytes(a)
+    if need == 0:
+        check(L.selective_scan(a, y.data_ptr(), fs.data_ptr(), sp, _stream(stream)))
+    else:
+        scratch, room = _scratch(None, need, A, stream)
+        check(L.selective_scan_split(a, y.data_ptr(), fs.data_ptr(), sp, scratch.data_ptr(), room,
+                                     _stream(stream)))
+    return (y, fs, starts) if keep_starts else (y, fs)
 
 
 def selective_scan_grad(dy, x, dt, A, B, C, starts, D=None, z=None, dt_bias=None, softplus=False,

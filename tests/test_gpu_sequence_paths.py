@@ -39,6 +39,43 @@ def test_scan_grad_two_tiles(case):
             assert torch.equal(v, again[name])
 
 
+# few channels over a length that is cut into chunks: sequences that end inside a chunk, at its
+# border, before it, and nowhere
+@pytest.mark.parametrize("case", [
+    (1, 1500, 20, 16, 1, "bf16", None, "gate soft bias D init"),
+    (3, 1300, 18, 13, 1, "f32", [1300, 417, 0], "soft bias D init"),
+    (2, 1024, 34, 16, 2, "f16", [512, 1], "gate soft bias D"),
+    (1, 700, 6, 33, 1, "bf16", None, "gate soft bias D init"),
+    (2, 4099, 5, 4, 1, "f32", [4099, 2049], "gate D init"),
+], ids=["whole", "ragged", "border", "states", "long"])
+def test_scan_in_chunks(case):
+    k, w, dy, dfinal = scan_inputs(case, 290, grads=True)
+    y, state, starts = sc.selective_scan(keep_starts=True, **k)
+    y2, state2 = sc.selective_scan(**k)
+    init = k.pop("initial_state", None)
+    got = sc.selective_scan_grad(dy, starts=starts, dfinal=dfinal, **k)
+    again = sc.selective_scan_grad(dy, starts=starts, dfinal=dfinal, **k)
+    want = ref.scan(**w)
+    assert torch.equal(y, y2) and torch.equal(state, state2)
+    agree(y, want["y"], case[5], "y")
+    agree(state, want["state"], "f32", "state")
+    for name, v in got.items():
+        if v is not None:
+            agree(v, want[name], case[5] if v.dtype != torch.float32 else "f32", name)
+            assert torch.equal(v, again[name])
+    # the whole scan in one piece gives the same but for rounding, and so do two halves in turn
+    half = case[1] // 2
+    if case[6] is None:
+        part = {n: k[n][:, :half] for n in ("x", "dt", "B", "C") + (("z",) if "z" in k else ())}
+        rest = {n: k[n][:, half:] for n in part}
+        a, mid = sc.selective_scan(**{**k, **part}, initial_state=init)
+        b, end = sc.selective_scan(**{**k, **rest}, initial_state=mid)
+        cut = lambda v, s: ref.V(v.val[:, s], v.mag[:, s], v.err[:, s])  # noqa: E731
+        agree(a, cut(want["y"], slice(None, half)), case[5], "first half")
+        agree(b, cut(want["y"], slice(half, None)), case[5], "second half")
+        agree(end, want["state"], "f32", "state after both")
+
+
 def test_conv_long_runs():
     # enough lanes for the longest runs; in two parts the runs are shorter, the sums the same
     x = torch.randn(1, 16391, 4096, generator=gen(210)).bfloat16().cuda()
