@@ -383,9 +383,10 @@ scan_status selective_scan(const selective_scan_args* args, void* y, float* fina
                            float* starts, void* stream);
 
 /* The same, with scratch by which a long scan of few channels is split over its
- * length (selective_scan_split_scratch_bytes, 0 where it is not worth it: then
- * scratch may be NULL and the result is selective_scan's to the bit; a split one
- * differs by the rounding of the chunks' starts). */
+ * length (selective_scan_split_scratch_bytes; 0 where that is not worth it, and
+ * always below 512 tokens: then scratch may be NULL and the result is
+ * selective_scan's to the bit; a split one differs by the rounding of the chunks'
+ * starts). */
 size_t selective_scan_split_scratch_bytes(const selective_scan_args* args);
 scan_status selective_scan_split(const selective_scan_args* args, void* y, float* final_state,
                                  float* starts, void* scratch, size_t scratch_bytes, void* stream);

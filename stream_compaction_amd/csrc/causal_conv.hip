@@ -23,12 +23,14 @@ __device__ __forceinline__ int64_t conv_length(const ConvProblem& p, int64_t b) 
 }
 
 // The filters of E channels, channel c's tap k in w[k][c].  E W consecutive
-// floats (the lane's channels all exist when E > 1), 16 bytes at a time where
-// the arrays are aligned: one by one they cost more than a run's input.
+// floats, 16 bytes at a time where the arrays are aligned and the lane's channels
+// all exist: one by one they cost more than a run's input.
 template <int E, int W>
 __device__ __forceinline__ void load_filters(const ConvProblem& p, int64_t ch, float (&w)[W][E],
                                              float (&bias)[E]) {
-  const bool wide = E > 1 && (((uintptr_t)p.weight | (uintptr_t)p.bias) % 16 == 0);
+  const int64_t n = p.channels - ch;
+  const bool wide = E > 1 && p.channels % E == 0 &&
+                    (((uintptr_t)p.weight | (uintptr_t)p.bias) % 16 == 0);
   typedef float vec4 __attribute__((ext_vector_type(4)));
   if (wide) {
 #pragma unroll
@@ -50,13 +52,13 @@ __device__ __forceinline__ void load_filters(const ConvProblem& p, int64_t ch, f
 #pragma unroll
   for (int c = 0; c < E; ++c) {
 #pragma unroll
-    for (int k = 0; k < W; ++k) w[k][c] = p.weight[(ch + c) * W + k];
-    bias[c] = p.bias != nullptr ? p.bias[ch + c] : 0.0f;
+    for (int k = 0; k < W; ++k) w[k][c] = c < n ? p.weight[(ch + c) * W + k] : 0.0f;
+    bias[c] = c < n && p.bias != nullptr ? p.bias[ch + c] : 0.0f;
   }
 }
 
 // Input token t of sequence b: the initial state before 0, zero past `len`.
-template <class F, int E, int W>
+template <class F, int E, int W, bool ALIGNED = true>
 __device__ __forceinline__ typename RowIO<F, E>::Raw conv_input(const ConvProblem& p, int64_t b,
                                                                int64_t t, int64_t len, int64_t ch) {
   using S = typename F::S;
@@ -67,7 +69,7 @@ __device__ __forceinline__ typename RowIO<F, E>::Raw conv_input(const ConvProble
     src = (const S*)p.initial_state + (b * (W - 1) + t + W - 1) * p.channels + ch;
   }
   if (src == nullptr) return typename RowIO<F, E>::Raw{};
-  return RowIO<F, E>::load(src);
+  return RowIO<F, E>::template get<ALIGNED>(src, p.channels - ch);
 }
 
 }  // namespace
@@ -156,7 +158,7 @@ constexpr int kConvGradWaves = 4;
 
 // Gradients with respect to the final state reach line token t (x for t >= 0,
 // the initial state for t < 0) when t is among the last W - 1 before len.
-template <class F, int E, int W>
+template <class F, int E, int W, bool ALIGNED>
 __device__ __forceinline__ void add_final(const ConvProblem& p, const void* dfinal, int64_t b,
                                           int64_t t, int64_t len, int64_t ch, float (&d)[E]) {
   using S = typename F::S;
@@ -164,12 +166,14 @@ __device__ __forceinline__ void add_final(const ConvProblem& p, const void* dfin
   if (dfinal == nullptr || j < 0 || j >= W - 1) return;
   float v[E];
   RowIO<F, E>::unpack(
-      RowIO<F, E>::load((const S*)dfinal + (b * (W - 1) + j) * p.channels + ch), v);
+      RowIO<F, E>::template get<ALIGNED>((const S*)dfinal + (b * (W - 1) + j) * p.channels + ch,
+                                         p.channels - ch),
+      v);
 #pragma unroll
   for (int c = 0; c < E; ++c) d[c] += v[c];
 }
 
-template <class F, int E, int W>
+template <class F, int E, int W, bool ALIGNED>
 __global__ __launch_bounds__(64 * kConvGradWaves) void causal_conv_grad_kernel(
     ConvProblem p, const void* dyv, int64_t dy_batch, int64_t dy_token, const void* dfinal,
     void* dxv, void* dinitial, float* part, int run_tokens) {
@@ -184,7 +188,8 @@ __global__ __launch_bounds__(64 * kConvGradWaves) void causal_conv_grad_kernel(
   const int64_t col = blockIdx.x % cols, set = blockIdx.x / cols;
   const int64_t sets = gridDim.x / cols;
   const int64_t ch = (col * 64 + lane) * E;
-  const bool live = ch < p.channels;
+  const int64_t n = p.channels - ch;
+  const bool live = n > 0;
   float w[W][E], bias[E], dw[W][E] = {}, db[E] = {};
   if (live) load_filters<E, W>(p, ch, w, bias);
   for (int64_t r = set * kConvGradWaves + wave; r < total; r += sets * kConvGradWaves) {
@@ -199,15 +204,15 @@ __global__ __launch_bounds__(64 * kConvGradWaves) void causal_conv_grad_kernel(
     float win[W][E], g[W][E] = {};                  // inputs and gradients, newest last
 #pragma unroll
     for (int k = 0; k + 1 < W; ++k)
-      IO::unpack(conv_input<F, E, W>(p, b, t0 - W + 1 + k, len, ch), win[k + 1]);
+      IO::unpack(conv_input<F, E, W, ALIGNED>(p, b, t0 - W + 1 + k, len, ch), win[k + 1]);
     const int steps = run_tokens + W - 1;
     for (int s0 = 0; s0 < steps; s0 += kConvAhead) {
       typename IO::Raw rx[kConvAhead], rdy[kConvAhead];
 #pragma unroll
       for (int j = 0; j < kConvAhead; ++j) {
         const int64_t t = t0 + s0 + j;
-        rx[j] = conv_input<F, E, W>(p, b, t, len, ch);
-        rdy[j] = t < len ? IO::load(dy + t * dy_token) : typename IO::Raw{};
+        rx[j] = conv_input<F, E, W, ALIGNED>(p, b, t, len, ch);
+        rdy[j] = t < len ? IO::template get<ALIGNED>(dy + t * dy_token, n) : typename IO::Raw{};
       }
 #pragma unroll
       for (int j = 0; j < kConvAhead; ++j) {
@@ -248,13 +253,13 @@ __global__ __launch_bounds__(64 * kConvGradWaves) void causal_conv_grad_kernel(
 #pragma unroll
             for (int k = 0; k < W; ++k) d[c] = __builtin_fmaf(w[k][c], g[W - 1 - k][c], d[c]);
           }
-          add_final<F, E, W>(p, dfinal, b, u, len, ch, d);
+          add_final<F, E, W, ALIGNED>(p, dfinal, b, u, len, ch, d);
           S* to = u >= 0 ? dx + u * p.channels
                          : (S*)dinitial + (b * (W - 1) + u + W - 1) * p.channels + ch;
           if (u < len) {
-            IO::store(to, IO::pack(d));
+            IO::template put<ALIGNED>(to, IO::pack(d), n);
           } else {
-            IO::store(to, typename IO::Raw{});
+            IO::template put<ALIGNED>(to, typename IO::Raw{}, n);
           }
         }
       }
@@ -414,11 +419,11 @@ static hipError_t grad_w(const ConvProblem& p, const void* dy, int64_t dy_batch,
       rows_aligned<F>(E, p.channels, dy, dy_batch, dy_token) &&
       rows_aligned<F>(E, p.channels, dx) && rows_aligned<F>(E, p.channels, dinitial) &&
       rows_aligned<F>(E, p.channels, dfinal) && rows_aligned<F>(E, p.channels, p.initial_state)) {
-    causal_conv_grad_kernel<F, E, W><<<dim3((unsigned)(sets * cols(E))), dim3(64 * kConvGradWaves),
+    causal_conv_grad_kernel<F, E, W, true><<<dim3((unsigned)(sets * cols(E))), dim3(64 * kConvGradWaves),
                                        0, stream>>>(p, dy, dy_batch, dy_token, dfinal, dx, dinitial,
                                                     part, run);
   } else {
-    causal_conv_grad_kernel<F, 1, W><<<dim3((unsigned)(sets * cols(1))), dim3(64 * kConvGradWaves),
+    causal_conv_grad_kernel<F, E, W, false><<<dim3((unsigned)(sets * cols(E))), dim3(64 * kConvGradWaves),
                                        0, stream>>>(p, dy, dy_batch, dy_token, dfinal, dx, dinitial,
                                                     part, run);
   }

@@ -28,7 +28,7 @@ __device__ __forceinline__ int64_t token_row(const I* ids, int64_t i, int64_t ro
 
 }  // namespace
 
-template <class F, int E, class I>
+template <class F, int E, bool ALIGNED, class I>
 __global__ __launch_bounds__(256) void embedding_kernel(const void* weight, const I* ids,
                                                        void* out, int64_t tokens, int64_t rows,
                                                        int64_t channels, int64_t row_stride,
@@ -43,12 +43,12 @@ __global__ __launch_bounds__(256) void embedding_kernel(const void* weight, cons
     typename IO::Raw r{};
     if (row >= 0) {
       float v[E];
-      IO::unpack(IO::load((const S*)weight + row * row_stride + ch), v);
+      IO::unpack(IO::template get<ALIGNED>((const S*)weight + row * row_stride + ch, channels - ch), v);
 #pragma unroll
       for (int c = 0; c < E; ++c) v[c] *= scale;
       r = IO::pack(v);
     }
-    IO::store((S*)out + t * channels + ch, r);
+    IO::template put<ALIGNED>((S*)out + t * channels + ch, r, channels - ch);
   }
 }
 
@@ -84,7 +84,7 @@ __global__ __launch_bounds__(256) void embedding_zero_kernel(uint4* out, int64_t
 constexpr int kFewIds = 4;
 constexpr int64_t kFewTokens = 64 * kFewIds;
 
-template <class F, class G, int E, class I>
+template <class F, class G, int E, bool ALIGNED, class I>
 __global__ __launch_bounds__(256) void embedding_few_kernel(const void* dout, const I* ids,
                                                            void* dweight, int tokens, int64_t rows,
                                                            int64_t channels, int64_t row_stride,
@@ -116,7 +116,7 @@ __global__ __launch_bounds__(256) void embedding_few_kernel(const void* dout, co
           if (left == 0) continue;
           const int64_t i = k * 64 + __builtin_ctzll(left);
           left &= left - 1;
-          if (live) raw[j] = IO::load((const S*)dout + i * row_stride + ch);
+          if (live) raw[j] = IO::template get<ALIGNED>((const S*)dout + i * row_stride + ch, channels - ch);
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
@@ -134,7 +134,7 @@ __global__ __launch_bounds__(256) void embedding_few_kernel(const void* dout, co
       float o[OE];
 #pragma unroll
       for (int c = 0; c < OE; ++c) o[c] = sum[h + c] * scale;
-      OIO::store(to + h, OIO::pack(o));
+      if (ALIGNED || h < channels - ch) OIO::template put<ALIGNED>(to + h, OIO::pack(o), channels - ch - h);
     }
   }
 }
@@ -278,7 +278,7 @@ constexpr int kSegAhead = 8;      // gradient rows loaded together
 // channels.  part[seg][0] gets the sum of the run that began before the
 // segment, part[seg][1] that of the run that continues past it (both float32);
 // a run that covers the whole segment and goes on at both ends is in [0].
-template <class F, class G, int E>
+template <class F, class G, int E, bool ALIGNED>
 __global__ __launch_bounds__(256) void embedding_segment_kernel(
     const void* dout, const uint32_t* keys, const uint32_t* pos, void* dweight, float* part,
     int64_t tokens, int64_t rows, int64_t channels, int64_t row_stride, float scale, int seg_tokens) {
@@ -315,7 +315,7 @@ __global__ __launch_bounds__(256) void embedding_segment_kernel(
       for (int j = 0; j < kSegAhead; ++j) {
         raw[j] = typename IO::Raw{};
         const int64_t i = (uint32_t)__builtin_amdgcn_readlane((int)at, j0 + j);
-        if (j0 + j < cnt && n > 0) raw[j] = IO::load((const S*)dout + i * row_stride + ch);
+        if (j0 + j < cnt && n > 0) raw[j] = IO::template get<ALIGNED>((const S*)dout + i * row_stride + ch, n);
       }
 #pragma unroll
       for (int j = 0; j < kSegAhead; ++j) {
@@ -339,12 +339,13 @@ __global__ __launch_bounds__(256) void embedding_segment_kernel(
               float o[OE];
 #pragma unroll
               for (int c = 0; c < OE; ++c) o[c] = sum[h + c] * scale;
-              OIO::store(to + h, OIO::pack(o));
+              if (ALIGNED || h < n) OIO::template put<ALIGNED>(to + h, OIO::pack(o), n - h);
             }
           } else {
             float* to = out_part + (whole ? channels : 0);
 #pragma unroll
-            for (int c = 0; c < E; ++c) to[c] = sum[c];
+            for (int c = 0; c < E; ++c)
+              if (ALIGNED || c < n) to[c] = sum[c];
           }
         }
 #pragma unroll
@@ -359,7 +360,7 @@ __global__ __launch_bounds__(256) void embedding_segment_kernel(
 // begins adds its pieces in order and writes the row (256 E channels of it).  A
 // frequent token's run crosses many segments: kAhead of them are looked at
 // together.
-template <class G, int E>
+template <class G, int E, bool ALIGNED>
 __global__ __launch_bounds__(256) void embedding_border_kernel(const uint32_t* __restrict__ keys,
                                                               void* __restrict__ dweight,
                                                               const float* __restrict__ part,
@@ -389,13 +390,13 @@ __global__ __launch_bounds__(256) void embedding_border_kernel(const uint32_t* _
     }
     if (ch >= channels) continue;
     float sum[E];
-    IO::unpack(IO::load(part + (seg * 2 + 1) * channels + ch), sum);
+    IO::unpack(IO::template get<ALIGNED>(part + (seg * 2 + 1) * channels + ch, channels - ch), sum);
     const float* from = part + (seg + 1) * 2 * channels + ch;
     typename IO::Raw next[kAhead];
     auto fetch = [&](int64_t p0) {
 #pragma unroll
       for (int j = 0; j < kAhead; ++j)
-        next[j] = p0 + j < pieces ? IO::load(from + (p0 + j) * 2 * channels)
+        next[j] = p0 + j < pieces ? IO::template get<ALIGNED>(from + (p0 + j) * 2 * channels, channels - ch)
                                   : typename IO::Raw{};
     };
     fetch(0);
@@ -414,7 +415,8 @@ __global__ __launch_bounds__(256) void embedding_border_kernel(const uint32_t* _
     }
 #pragma unroll
     for (int c = 0; c < E; ++c)
-      ((typename G::S*)dweight)[(int64_t)k * channels + ch + c] = narrow<G>(sum[c] * scale);
+      if (ALIGNED || c < channels - ch)
+        ((typename G::S*)dweight)[(int64_t)k * channels + ch + c] = narrow<G>(sum[c] * scale);
   }
 }
 
@@ -437,14 +439,14 @@ hipError_t launch_embedding(const void* weight, const void* ids, bool wide_ids, 
     constexpr int E = kVecElems<F>;
     const bool vec = channels % E == 0 && row_stride % E == 0 && (uintptr_t)weight % 16 == 0 &&
                      (uintptr_t)out % 16 == 0;
-    const int64_t blocks = (tokens * (vec ? channels / E : channels) + 255) / 256;
+    const int64_t blocks = (tokens * ((channels + E - 1) / E) + 255) / 256;
     const dim3 grid((unsigned)(blocks < kGridMost ? blocks : kGridMost));
     auto go = [&](auto* id) {
       if (vec) {
-        embedding_kernel<F, E><<<grid, dim3(256), 0, stream>>>(weight, id, out, tokens, rows,
+        embedding_kernel<F, E, true><<<grid, dim3(256), 0, stream>>>(weight, id, out, tokens, rows,
                                                                channels, row_stride, scale);
       } else {
-        embedding_kernel<F, 1><<<grid, dim3(256), 0, stream>>>(weight, id, out, tokens, rows,
+        embedding_kernel<F, E, false><<<grid, dim3(256), 0, stream>>>(weight, id, out, tokens, rows,
                                                                channels, row_stride, scale);
       }
     };
@@ -498,13 +500,13 @@ static hipError_t few_go(const void* dout, const void* ids, bool wide_ids, void*
                          Fmt out_fmt, float scale, hipStream_t stream) {
   return by_format(fmt, [&](auto f) {
     using F = decltype(f);
-    auto go = [&](auto o, auto e, auto* id) {
+    auto go = [&](auto o, auto aligned, auto* id) {
       using G = decltype(o);
-      constexpr int E = decltype(e)::value;
+      constexpr int E = kVecElems<F>;
       const int64_t cols = (channels + 64 * E - 1) / (64 * E);
       // 16 waves a CU, or every row and column block its own
       const int64_t most = 4096 / cols < 1 ? 1 : 4096 / cols, step = rows < most ? rows : most;
-      embedding_few_kernel<F, G, E><<<dim3((unsigned)((step * cols + 3) / 4)), dim3(256), 0, stream>>>(
+      embedding_few_kernel<F, G, E, decltype(aligned)::value><<<dim3((unsigned)((step * cols + 3) / 4)), dim3(256), 0, stream>>>(
           dout, id, dweight, (int)tokens, rows, channels, row_stride, scale, (uint32_t)cols,
           (uint32_t)step);
     };
@@ -519,9 +521,9 @@ static hipError_t few_go(const void* dout, const void* ids, bool wide_ids, void*
       constexpr int E = kVecElems<F>;
       if (channels % E == 0 && row_stride % E == 0 && (uintptr_t)dout % 16 == 0 &&
           (uintptr_t)dweight % 16 == 0) {
-        by_ids(o, std::integral_constant<int, E>{});
+        by_ids(o, std::true_type{});
       } else {
-        by_ids(o, std::integral_constant<int, 1>{});
+        by_ids(o, std::false_type{});
       }
     };
     if (out_fmt == Fmt::F32) {
@@ -596,30 +598,36 @@ hipError_t launch_embedding_grad(const void* dout, const void* ids, bool wide_id
       constexpr int E = kVecElems<F>;
       const bool vec = channels % E == 0 && row_stride % E == 0 && (uintptr_t)dout % 16 == 0 &&
                        (uintptr_t)dweight % 16 == 0;
-      const int64_t waves = segs * ((channels + 64 * (vec ? E : 1) - 1) / (64 * (vec ? E : 1)));
-      auto grid_of = [](int64_t w) {
-        const int64_t b = (w + 3) / 4;
-        return dim3((unsigned)(b < kGridMost ? b : kGridMost));
+      auto segment = [&](auto e, auto aligned) {
+        constexpr int SE = decltype(e)::value;
+        const int64_t b = (segs * ((channels + 64 * SE - 1) / (64 * SE)) + 3) / 4;
+        embedding_segment_kernel<F, G, SE, decltype(aligned)::value>
+            <<<dim3((unsigned)(b < kGridMost ? b : kGridMost)), dim3(256), 0, stream>>>(
+                dout, keys, pos, dweight, part, tokens, rows, channels, row_stride, scale, seg);
       };
-      const dim3 grid = grid_of(waves);
+      // rows off alignment: wide loose accesses, or one channel per lane where that
+      // is what fills the card (1531 tokens x 333: 4.3 us against 6.4)
+      const bool wide = segs * ((channels + 64 * E - 1) / (64 * E)) >= 1024;
       if (vec) {
-        embedding_segment_kernel<F, G, E><<<grid, dim3(256), 0, stream>>>(
-            dout, keys, pos, dweight, part, tokens, rows, channels, row_stride, scale, seg);
+        segment(std::integral_constant<int, E>{}, std::true_type{});
+      } else if (wide) {
+        segment(std::integral_constant<int, E>{}, std::false_type{});
       } else {
-        embedding_segment_kernel<F, G, 1><<<grid, dim3(256), 0, stream>>>(
-            dout, keys, pos, dweight, part, tokens, rows, channels, row_stride, scale, seg);
+        segment(std::integral_constant<int, 1>{}, std::true_type{});
       }
-      auto border = [&](auto e) {
+      auto border = [&](auto e, auto aligned) {
         constexpr int BE = decltype(e)::value;
         const int64_t b = segs * ((channels + 256 * BE - 1) / (256 * BE));
-        embedding_border_kernel<G, BE><<<dim3((unsigned)(b < kGridMost ? b : kGridMost)), dim3(256), 0,
-                                         stream>>>(keys, dweight, part, tokens, rows, channels,
-                                                   scale, seg);
+        embedding_border_kernel<G, BE, decltype(aligned)::value>
+            <<<dim3((unsigned)(b < kGridMost ? b : kGridMost)), dim3(256), 0, stream>>>(
+                keys, dweight, part, tokens, rows, channels, scale, seg);
       };
       if (channels % 4 == 0) {
-        border(std::integral_constant<int, 4>{});
+        border(std::integral_constant<int, 4>{}, std::true_type{});
+      } else if (wide) {
+        border(std::integral_constant<int, 4>{}, std::false_type{});
       } else {
-        border(std::integral_constant<int, 1>{});
+        border(std::integral_constant<int, 1>{}, std::true_type{});
       }
       return hipGetLastError();
     };

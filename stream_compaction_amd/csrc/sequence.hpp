@@ -85,6 +85,40 @@ template <class F, int E> struct RowIO {
   using Raw = std::conditional_t<sizeof(Elems) == 16, u32x4,
               std::conditional_t<sizeof(Elems) == 8, vec2,
               std::conditional_t<sizeof(Elems) == 4, uint32_t, uint16_t>>>;
+  // at any element, n > 0 of them exist: one access for a whole vector (the
+  // hardware takes any alignment), one by one at a row's end
+  static __device__ __forceinline__ Raw load_any(const S* p, int64_t n) {
+    typedef Raw Loose __attribute__((aligned(sizeof(S))));
+    if (n >= E) return *gptr<const Loose>((uintptr_t)p);
+    Elems s = {};
+#pragma unroll
+    for (int k = 0; k < E; ++k)
+      if (k < n) s.e[k] = *gptr<const S>((uintptr_t)(p + k));
+    return __builtin_bit_cast(Raw, s);
+  }
+  static __device__ __forceinline__ void store_any(S* p, Raw r, int64_t n) {
+    typedef Raw Loose __attribute__((aligned(sizeof(S))));
+    if (n >= E) {
+      *gptr<Loose>((uintptr_t)p) = r;
+      return;
+    }
+    const Elems s = __builtin_bit_cast(Elems, r);
+#pragma unroll
+    for (int k = 0; k < E; ++k)
+      if (k < n) *gptr<S>((uintptr_t)(p + k)) = s.e[k];
+  }
+  // aligned and whole (ALIGNED), or any
+  template <bool ALIGNED> static __device__ __forceinline__ Raw get(const S* p, int64_t n) {
+    if constexpr (ALIGNED) return load(p);
+    return load_any(p, n);
+  }
+  template <bool ALIGNED> static __device__ __forceinline__ void put(S* p, Raw r, int64_t n) {
+    if constexpr (ALIGNED) {
+      store(p, r);
+    } else {
+      store_any(p, r, n);
+    }
+  }
   // all of them, aligned
   static __device__ __forceinline__ Raw load(const S* p) { return *gptr<const Raw>((uintptr_t)p); }
   static __device__ __forceinline__ void store(S* p, Raw r) { *gptr<Raw>((uintptr_t)p) = r; }

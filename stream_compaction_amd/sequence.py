@@ -174,30 +174,28 @@ def _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, lengths, 
                                      "[batch, groups, states])")
     groups = B.shape[-2]
     rows = shape[:-1] + (groups, n)
+    length, zs = 1, (0, 0)
     if step:
-        def lead(t):
-            return t.stride(0), 0
-
-        def lead3(t):
-            return t.stride(0), 0, t.stride(1)
+        xs, ds = (x.stride(0), 0), (dt.stride(0), 0)
+        Bs, Cs = (B.stride(0), 0, B.stride(1)), (C.stride(0), 0, C.stride(1))
+        if z is not None:
+            zs = (z.stride(0), 0)
     else:
-        def lead(t):
-            return t.stride()[:2]
-
-        def lead3(t):
-            return t.stride()[:3]
+        length = shape[1]
+        xs, ds, Bs, Cs = x.stride()[:2], dt.stride()[:2], B.stride()[:3], C.stride()[:3]
+        if z is not None:
+            zs = z.stride()[:2]
     f32 = torch.float32
     return ScanArgs(
         _rows(x, "x", shape, ty, dev), _rows(dt, "dt", shape, ty, dev),
         _rows(B, "B", rows, ty, dev), _rows(C, "C", rows, ty, dev),
         None if z is None else _rows(z, "z", shape, ty, dev),
-        _like(A, "A", (d, n), f32, dev), _opt(D, "D", (d,), f32, dev),
-        _opt(dt_bias, "dt_bias", (d,), f32, dev),
-        _opt(initial_state, "initial_state", (b, d, n), f32, dev),
-        _opt(lengths, "lengths", (b,), torch.int32, dev),
-        b, 1 if step else shape[1], d, n, groups,
-        lead(x), lead(dt), (0, 0) if z is None else lead(z), lead3(B), lead3(C),
-        1 if softplus else 0, code)
+        _like(A, "A", (d, n), f32, dev), None if D is None else _like(D, "D", (d,), f32, dev),
+        None if dt_bias is None else _like(dt_bias, "dt_bias", (d,), f32, dev),
+        None if initial_state is None else
+        _like(initial_state, "initial_state", (b, d, n), f32, dev),
+        None if lengths is None else _like(lengths, "lengths", (b,), torch.int32, dev),
+        b, length, d, n, groups, xs, ds, zs, Bs, Cs, 1 if softplus else 0, code)
 
 
 def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=False,
@@ -223,7 +221,8 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=False,
     if keep_starts:
         starts = _new((L.selective_scan_starts_bytes(a) // 4,), torch.float32, A, stream)
     sp = None if starts is None else starts.data_ptr()
-    need = L.selective_scan_split_scratch_bytes(a)
+    # (short scans are never split)
+    need = L.selective_scan_split_scratch_bytes(a) if x.shape[1] >= 512 else 0
     if need == 0:
         check(L.selective_scan(a, y.data_ptr(), fs.data_ptr(), sp, _stream(stream)))
     else:

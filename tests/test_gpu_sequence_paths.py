@@ -112,7 +112,7 @@ def test_scan_step_many_sequences():
             assert torch.equal(v, y[s]) and torch.equal(one, new[s])
 
 
-@pytest.mark.parametrize("tokens,rows,d", [(16384, 700, 8), (16385, 700, 8), (300, 131072, 8),
+@pytest.mark.parametrize("tokens,rows,d", [(16384, 700, 8), (16385, 700, 8), (16384, 700, 133), (300, 131072, 8),
                                            (300, 131073, 8), (1024, 65537, 16), (2, 1 << 24, 2)])
 def test_embedding_grad_paths(tokens, rows, d):
     r = gen(230)
