@@ -116,7 +116,8 @@ __global__ __launch_bounds__(256) void embedding_few_kernel(const void* dout, co
           if (left == 0) continue;
           const int64_t i = k * 64 + __builtin_ctzll(left);
           left &= left - 1;
-          if (live) raw[j] = IO::template get<ALIGNED>((const S*)dout + i * row_stride + ch, channels - ch);
+          if (live)
+            raw[j] = IO::template get<ALIGNED>((const S*)dout + i * row_stride + ch, channels - ch);
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
@@ -134,7 +135,8 @@ __global__ __launch_bounds__(256) void embedding_few_kernel(const void* dout, co
       float o[OE];
 #pragma unroll
       for (int c = 0; c < OE; ++c) o[c] = sum[h + c] * scale;
-      if (ALIGNED || h < channels - ch) OIO::template put<ALIGNED>(to + h, OIO::pack(o), channels - ch - h);
+      if (ALIGNED || h < channels - ch)
+        OIO::template put<ALIGNED>(to + h, OIO::pack(o), channels - ch - h);
     }
   }
 }
@@ -396,7 +398,8 @@ __global__ __launch_bounds__(256) void embedding_border_kernel(const uint32_t* _
     auto fetch = [&](int64_t p0) {
 #pragma unroll
       for (int j = 0; j < kAhead; ++j)
-        next[j] = p0 + j < pieces ? IO::template get<ALIGNED>(from + (p0 + j) * 2 * channels, channels - ch)
+        next[j] = p0 + j < pieces ? IO::template get<ALIGNED>(from + (p0 + j) * 2 * channels,
+                                                              channels - ch)
                                   : typename IO::Raw{};
     };
     fetch(0);
@@ -506,7 +509,8 @@ static hipError_t few_go(const void* dout, const void* ids, bool wide_ids, void*
       const int64_t cols = (channels + 64 * E - 1) / (64 * E);
       // 16 waves a CU, or every row and column block its own
       const int64_t most = 4096 / cols < 1 ? 1 : 4096 / cols, step = rows < most ? rows : most;
-      embedding_few_kernel<F, G, E, decltype(aligned)::value><<<dim3((unsigned)((step * cols + 3) / 4)), dim3(256), 0, stream>>>(
+      embedding_few_kernel<F, G, E, decltype(aligned)::value>
+          <<<dim3((unsigned)((step * cols + 3) / 4)), dim3(256), 0, stream>>>(
           dout, id, dweight, (int)tokens, rows, channels, row_stride, scale, (uint32_t)cols,
           (uint32_t)step);
     };

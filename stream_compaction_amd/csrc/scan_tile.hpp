@@ -51,10 +51,11 @@ __device__ __forceinline__ void for_tokens(Fn&& fn, std::integer_sequence<int, T
 }
 
 // An array of activations [.., token, channels] as a workgroup reads it: a
-// thread's pair (thread % 8) of its token (thread / 8) of a block, block after block.  Loads are never skipped: a
-// thread whose token or pair does not exist reads one that does (the caller
-// drops it), because behind a load that may not have happened the compiler can
-// only wait for all of them.  VEC: the pair is loaded as one.
+// thread's pair (thread % 8) of its token (thread / 8) of a block, block after
+// block.  Loads are never skipped: a thread whose token or pair does not exist
+// reads one that does (the caller drops it), because behind a load that may not
+// have happened the compiler can only wait for all of them.  VEC: the pair is
+// loaded as one.
 template <class F, bool VEC> struct Pair {
   using S = typename F::S;
   using Raw = std::conditional_t<VEC, typename RowIO<F, 2>::Raw, S>;
@@ -114,8 +115,8 @@ template <class F> bool scan_pairs(const ScanProblem& p, const void* y) {
   auto even = [](const void* a, int64_t s0, int64_t s1, int64_t s2) {
     return (uintptr_t)a % (2 * sizeof(typename F::S)) == 0 && ((s0 | s1 | s2) & 1) == 0;
   };
-  return even(y, 0, 0, 0) && (p.channels / p.groups) % 2 == 0 && p.states % 2 == 0 && even(p.x, p.x_batch, p.x_token, 0) &&
-         even(p.dt, p.dt_batch, p.dt_token, 0) &&
+  return even(y, 0, 0, 0) && (p.channels / p.groups) % 2 == 0 && p.states % 2 == 0 &&
+         even(p.x, p.x_batch, p.x_token, 0) && even(p.dt, p.dt_batch, p.dt_token, 0) &&
          (p.z == nullptr || even(p.z, p.z_batch, p.z_token, 0)) &&
          even(p.B, p.B_batch, p.B_token, p.B_group) && even(p.C, p.C_batch, p.C_token, p.C_group);
 }
@@ -133,7 +134,7 @@ struct ScanSplit {
 };
 
 // Where a workgroup stands in the problem: sequence, group of B and C, first
-// channel, and how many of its 16 channels exist.
+// channel, and how many of its channels exist.
 struct ScanPlace {
   int64_t b, g, ch, nch, tile;
 };

@@ -85,7 +85,8 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
   Src dts(p.dt, p.dt_batch, p.dt_token, at.b, at.ch + first * p.dt_token, nch);
   // without a gate x stands in, unused
   const int64_t z_token = gate ? p.z_token : p.x_token;
-  Src zs(gate ? p.z : p.x, gate ? p.z_batch : p.x_batch, z_token, at.b, at.ch + first * z_token, nch);
+  Src zs(gate ? p.z : p.x, gate ? p.z_batch : p.x_batch, z_token, at.b, at.ch + first * z_token,
+         nch);
   Src Bs[NS], Cs[NS];
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
@@ -337,7 +338,8 @@ int64_t scan_chunks(const ScanProblem& p, int64_t* tokens) {
   int64_t best = p.length * 8 / 10, chunks = 1;
   for (int64_t n = 2; n <= 32 && n * 128 <= p.length; ++n) {
     const int64_t over = groups * n > 256 ? groups * n - 256 : 0;
-    const int64_t time = p.length / n * (10 * n + 6 * (n - 1)) / (10 * n) * (256 * 100 + 50 * over) / (256 * 100) + 150 + 8 * n;
+    const int64_t each = p.length / n * (10 * n + 6 * (n - 1)) / (10 * n);
+    const int64_t time = each * (25600 + 50 * over) / 25600 + 150 + 8 * n;
     if (time < best) {
       best = time;
       chunks = n;

@@ -135,7 +135,8 @@ __global__ __launch_bounds__(256 * TL) void selective_scan_grad_kernel(
     mine[s] = cl < nch && n < N;
     A2[s] = mine[s] ? p.A[ch * N + n] * kLog2e : 0.0f;
     m[s] = !ENDS && mine[s] && g.dfinal != nullptr ? g.dfinal[srow + n] : 0.0f;
-    kept[s] = g.starts + ((at.b * nkeep + first / kKeep) * p.channels + (mine[s] ? ch : at.ch)) * N + (mine[s] ? n : 0);
+    const int64_t from = (at.b * nkeep + first / kKeep) * p.channels + (mine[s] ? ch : at.ch);
+    kept[s] = g.starts + from * N + (mine[s] ? n : 0);
   }
 
   float span = 0.0f;                            // ENDS: sum of the channel's steps
@@ -490,12 +491,14 @@ static hipError_t launch_grad(const ScanProblem& p, const ScanGrads& g, void* sc
       if constexpr (TL == 1) {
         if (split.chunks > 1) {
           const int64_t count = nb * per * (split.chunks - 1);
-          selective_scan_grad_kernel<F, NS, GATE, TL, true><<<dim3(xcd_grid(count)), dim3(256), 0, stream>>>(
+          selective_scan_grad_kernel<F, NS, GATE, TL, true>
+              <<<dim3(xcd_grid(count)), dim3(256), 0, stream>>>(
               p, g, part, params, split, b0, tiles, (uint32_t)count);
         }
       }
       const int64_t count = nb * per * split.chunks;
-      selective_scan_grad_kernel<F, NS, GATE, TL, false><<<dim3(xcd_grid(count)), dim3(256 * TL), 0, stream>>>(
+      selective_scan_grad_kernel<F, NS, GATE, TL, false>
+          <<<dim3(xcd_grid(count)), dim3(256 * TL), 0, stream>>>(
           p, g, part, params, split, b0, tiles, (uint32_t)count);
     };
     auto by_tiles = [&](auto ns, auto gate) {

@@ -1,6 +1,6 @@
 // Shared by the sequence kernels (causal convolution, selective scan,
-// embedding): problem descriptions as the kernels take them, strided loads of
-// 16-byte vectors, and the elementwise functions of a gated state space layer.
+// embedding): vector loads and stores of activations, and the elementwise
+// functions of a gated state space layer.
 #pragma once
 
 #include "device.hpp"
@@ -23,8 +23,12 @@ __device__ __forceinline__ float rcp_hw(float v) { return __builtin_amdgcn_rcpf(
 // sigmoid(v); v -> -inf gives rcp(inf) = 0, v -> inf gives 1.
 __device__ __forceinline__ float sigmoid(float v) { return rcp_hw(1.0f + exp2_hw(-v * kLog2e)); }
 // The greater and the lesser of two, a NaN if either is one.
-__device__ __forceinline__ float at_least(float v, float low) { return __builtin_elementwise_maximum(v, low); }
-__device__ __forceinline__ float at_most(float v, float high) { return __builtin_elementwise_minimum(v, high); }
+__device__ __forceinline__ float at_least(float v, float low) {
+  return __builtin_elementwise_maximum(v, low);
+}
+__device__ __forceinline__ float at_most(float v, float high) {
+  return __builtin_elementwise_minimum(v, high);
+}
 // silu(v) = v sigmoid(v); v is kept finite, as -inf * 0 would be no number.
 __device__ __forceinline__ float silu(float v) {
   v = at_least(v, -1e30f);
@@ -48,36 +52,7 @@ __device__ __forceinline__ float softplus(float v) {
   return __builtin_fmaxf(v, 0.0f) + __builtin_fmaf(__builtin_amdgcn_logf(w), kLn2, c);
 }
 
-// The E = 16 / sizeof(S) elements at `p` whose count `n` (may exceed E) exist;
-// the others read as zero bits.  vec: p is 16-byte aligned.
-template <class F>
-__device__ __forceinline__ uint4 load_vec(const typename F::S* p, int64_t n, bool vec) {
-  constexpr int E = kVecElems<F>;
-  if (vec && n >= E) return __builtin_bit_cast(uint4, *gptr<const u32x4>((uintptr_t)p));
-  typename F::S e[E] = {};
-#pragma unroll
-  for (int k = 0; k < E; ++k)
-    if (k < n) e[k] = *gptr<const typename F::S>((uintptr_t)(p + k));
-  return __builtin_bit_cast(uint4, e);
-}
-
-// Stores the first n elements of r.
-template <class F>
-__device__ __forceinline__ void store_vec(typename F::S* p, uint4 r, int64_t n, bool vec) {
-  constexpr int E = kVecElems<F>;
-  if (vec && n >= E) {
-    *gptr<u32x4>((uintptr_t)p) = __builtin_bit_cast(u32x4, r);
-    return;
-  }
-  struct Elems { typename F::S e[E]; };
-  const Elems s = __builtin_bit_cast(Elems, r);
-#pragma unroll
-  for (int k = 0; k < E; ++k)
-    if (k < n) *gptr<typename F::S>((uintptr_t)(p + k)) = s.e[k];
-}
-
-// E consecutive elements as one load or store of 2 to 16 bytes (`vec`: p is
-// aligned to that), or one by one.  `n` of them exist: others read as zero.
+// E consecutive elements of a row as one load or store of 2 to 16 bytes.
 template <class F, int E> struct RowIO {
   using S = typename F::S;
   struct Elems { S e[E]; };
@@ -85,8 +60,9 @@ template <class F, int E> struct RowIO {
   using Raw = std::conditional_t<sizeof(Elems) == 16, u32x4,
               std::conditional_t<sizeof(Elems) == 8, vec2,
               std::conditional_t<sizeof(Elems) == 4, uint32_t, uint16_t>>>;
-  // at any element, n > 0 of them exist: one access for a whole vector (the
-  // hardware takes any alignment), one by one at a row's end
+  // At any element, n > 0 of them exist: one access for a whole vector (global
+  // accesses need no alignment), one by one at a row's end, where elements that do
+  // not exist read as zero.
   static __device__ __forceinline__ Raw load_any(const S* p, int64_t n) {
     typedef Raw Loose __attribute__((aligned(sizeof(S))));
     if (n >= E) return *gptr<const Loose>((uintptr_t)p);
@@ -122,14 +98,6 @@ template <class F, int E> struct RowIO {
   // all of them, aligned
   static __device__ __forceinline__ Raw load(const S* p) { return *gptr<const Raw>((uintptr_t)p); }
   static __device__ __forceinline__ void store(S* p, Raw r) { *gptr<Raw>((uintptr_t)p) = r; }
-  static __device__ __forceinline__ Raw load(const S* p, int64_t n, bool vec) {
-    if (vec && n >= E) return *gptr<const Raw>((uintptr_t)p);
-    Elems s = {};
-#pragma unroll
-    for (int k = 0; k < E; ++k)
-      if (k < n) s.e[k] = *gptr<const S>((uintptr_t)(p + k));
-    return __builtin_bit_cast(Raw, s);
-  }
   static __device__ __forceinline__ void unpack(Raw r, float (&x)[E]) {
     const Elems s = __builtin_bit_cast(Elems, r);
 #pragma unroll
@@ -147,16 +115,6 @@ template <class F, int E> struct RowIO {
       for (int k = 0; k < E; ++k) s.e[k] = narrow<F>(x[k]);
       return __builtin_bit_cast(Raw, s);
     }
-  }
-  static __device__ __forceinline__ void store(S* p, Raw r, int64_t n, bool vec) {
-    if (vec && n >= E) {
-      *gptr<Raw>((uintptr_t)p) = r;
-      return;
-    }
-    const Elems s = __builtin_bit_cast(Elems, r);
-#pragma unroll
-    for (int k = 0; k < E; ++k)
-      if (k < n) *gptr<S>((uintptr_t)(p + k)) = s.e[k];
   }
 };
 
@@ -186,11 +144,6 @@ __device__ __forceinline__ int64_t divide(int64_t i, int64_t d, int64_t* r) {
   }
   *r = i - q * d;
   return q;
-}
-
-// Sum over the 64 lanes, the same value in every lane of the wave.
-__device__ __forceinline__ float wave_sum(float v) {
-  return readlane(wave_scan_incl<Op::Add>(v), kWave - 1);
 }
 
 // A barrier for data that waves exchange through LDS: unlike __syncthreads() it
