@@ -9,7 +9,7 @@
 // bytes per token) and walks a run of tokens with the last W inputs in
 // registers, so each input is read once but for the W - 1 tokens before a run.
 // Measured, bf16, W = 4: forward 4 x 4096 x 4096 with half of it padding (202 MB)
-// 40 us, 5.0 TB/s; step 128 x 4096 (8.5 MB) 4.6 us, most of it latency.
+// 34 us, 6.0 TB/s; step 128 x 4096 (8.5 MB) 4.6 us, most of it latency.
 #include "sequence.hpp"
 
 namespace sca {
@@ -76,7 +76,7 @@ __device__ __forceinline__ typename RowIO<F, E>::Raw conv_input(const ConvProble
 
 constexpr int kConvAhead = 4;     // token rows loaded together
 
-template <class F, int E, int W>
+template <class F, int E, int W, bool PAST>
 __global__ __launch_bounds__(256) void causal_conv_kernel(ConvProblem p, void* yv,
                                                          void* final_state, int run_tokens) {
   using S = typename F::S;
@@ -129,12 +129,14 @@ __global__ __launch_bounds__(256) void causal_conv_kernel(ConvProblem p, void* y
             for (int k = 0; k < W; ++k) a = __builtin_fmaf(w[k][c], win[k][c], a);
             out[c] = p.silu ? silu(a) : a;
           }
-          if (t + j < last) IO::store(y + (t + j) * p.channels, IO::pack(out));
+          if (t + j < last)
+            IO::template store_past<PAST>(y + (t + j) * p.channels, IO::pack(out));
         }
       }
       t = last;
     }
-    for (; t < end; ++t) IO::store(y + t * p.channels, typename IO::Raw{});
+    for (; t < end; ++t)
+      IO::template store_past<PAST>(y + t * p.channels, typename IO::Raw{});
     if (run == 0 && final_state != nullptr) {
       S* fs = (S*)final_state + b * (W - 1) * p.channels + ch;
 #pragma unroll
@@ -373,8 +375,14 @@ static void fwd_go(const ConvProblem& p, void* y, void* final_state, hipStream_t
   const int run = conv_run(p, E, 32, 1024);
   const int64_t runs = p.length > 0 ? (p.length + run - 1) / run : 1;
   const int64_t blocks = (p.batch * runs * ((p.channels + E - 1) / E) + 255) / 256;
-  causal_conv_kernel<F, E, W><<<dim3((unsigned)(blocks < kGridMost ? blocks : kGridMost)),
-                                dim3(256), 0, stream>>>(p, y, final_state, run);
+  const dim3 grid((unsigned)(blocks < kGridMost ? blocks : kGridMost));
+  if constexpr (E > 1) {
+    if (past_caches(p.batch * p.length * p.channels * (int64_t)sizeof(typename F::S))) {
+      causal_conv_kernel<F, E, W, true><<<grid, dim3(256), 0, stream>>>(p, y, final_state, run);
+      return;
+    }
+  }
+  causal_conv_kernel<F, E, W, false><<<grid, dim3(256), 0, stream>>>(p, y, final_state, run);
 }
 template <class F, int W>
 static hipError_t fwd_w(const ConvProblem& p, void* y, void* fs, hipStream_t stream) {

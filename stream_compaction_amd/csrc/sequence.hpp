@@ -12,6 +12,12 @@ namespace sca {
 // parameters and states are float32, and each output is rounded once.
 template <class F> constexpr int kVecElems = 16 / (int)sizeof(typename F::S);
 
+// Outputs that the L2 caches (8 of 4 MB) cannot hold are stored past them where
+// that gains (PAST below): a convolution of 134 MB takes 34 us against 49, a
+// lookup of 67 MB 16 against 18.5, with inputs that no cache holds.  Smaller
+// outputs stay for their reader.
+inline bool past_caches(int64_t bytes) { return bytes >= (32ll << 20); }
+
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -98,6 +104,13 @@ template <class F, int E> struct RowIO {
   // all of them, aligned
   static __device__ __forceinline__ Raw load(const S* p) { return *gptr<const Raw>((uintptr_t)p); }
   static __device__ __forceinline__ void store(S* p, Raw r) { *gptr<Raw>((uintptr_t)p) = r; }
+  template <bool PAST> static __device__ __forceinline__ void store_past(S* p, Raw r) {
+    if constexpr (PAST) {
+      __builtin_nontemporal_store(r, gptr<Raw>((uintptr_t)p));
+    } else {
+      store(p, r);
+    }
+  }
   static __device__ __forceinline__ void unpack(Raw r, float (&x)[E]) {
     const Elems s = __builtin_bit_cast(Elems, r);
 #pragma unroll

@@ -130,6 +130,17 @@ def test_embedding_grad_paths(tokens, rows, d):
     assert not bool(got.any())
 
 
+def test_embedding_past_the_caches():
+    # an output that is stored past the caches: with scale 1 a copy of the rows
+    r = gen(235)
+    table = torch.randn(300, 2048, generator=r).bfloat16().cuda()
+    ids = torch.randint(-1, 301, (8200,), generator=r).cuda()
+    live = (ids >= 0) & (ids < 300)
+    want = torch.where(live[:, None], table[ids.clamp(0, 299)], torch.zeros((), dtype=torch.bfloat16,
+                                                                           device="cuda"))
+    assert torch.equal(sc.embedding(table, ids), want)
+
+
 def test_explicit_stream():
     case = (2, 90, 48, 16, 1, "bf16", None, "gate soft bias D init")
     k, _, dy, dfinal = scan_inputs(case, 240, grads=True)
