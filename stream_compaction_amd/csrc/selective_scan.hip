@@ -424,13 +424,15 @@ hipError_t launch_selective_scan(const ScanProblem& p, Fmt fmt, void* y, float* 
 // stores 16 bytes wide and a wave's contiguous.  A lane takes R sequences of
 // its channel at once: A, D and the bias are read once for them and R loads of
 // the state are in flight.  128 x 4096 x 16 in bf16 (72 MB): R = 2 16.4 us (4.4
-// TB/s), R = 4 20.2 us, whose registers leave fewer waves.
+// TB/s), R = 4 20.2 us, whose registers leave fewer waves.  A launch owns the
+// sequences [first, end): what a lane's R reach past `end` is the next launch's,
+// and to be moved once only.
 // ---------------------------------------------------------------------------
 template <class F, int V, int G, int R>
 __global__ __launch_bounds__(256) void selective_scan_step_kernel(ScanProblem p,
                                                                  const float* state,
                                                                  float* new_state, void* yv,
-                                                                 int64_t first) {
+                                                                 int64_t first, int64_t end) {
   using S = typename F::S;
   using IO = RowIO<FmtF32, V>;
   using BIO = RowIO<F, V>;
@@ -448,7 +450,7 @@ __global__ __launch_bounds__(256) void selective_scan_step_kernel(ScanProblem p,
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int64_t b = b0 + r;
-    on[r] = b < p.batch;
+    on[r] = b < end;
     x[r] = on[r] ? widen<F>(((const S*)p.x)[b * p.x_batch + ch]) : 0.0f;
     dt[r] = on[r] ? widen<F>(((const S*)p.dt)[b * p.dt_batch + ch]) : 0.0f;
     z[r] = on[r] && p.z != nullptr ? widen<F>(((const S*)p.z)[b * p.z_batch + ch]) : 0.0f;
@@ -516,10 +518,10 @@ static hipError_t launch_step_g(const ScanProblem& p, const float* state, float*
     const int64_t nb = p.batch - b0 < step ? p.batch - b0 : step;
     if (many) {
       selective_scan_step_kernel<F, V, G, R><<<dim3((unsigned)((nb + R - 1) / R * cols)), dim3(256), 0,
-                                               stream>>>(p, state, new_state, y, b0);
+                                               stream>>>(p, state, new_state, y, b0, b0 + nb);
     } else {
       selective_scan_step_kernel<F, V, G, 1><<<dim3((unsigned)(nb * cols)), dim3(256), 0, stream>>>(
-          p, state, new_state, y, b0);
+          p, state, new_state, y, b0, b0 + nb);
     }
   }
   return hipGetLastError();
