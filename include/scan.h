@@ -386,7 +386,9 @@ scan_status selective_scan(const selective_scan_args* args, void* y, float* fina
  * length (selective_scan_split_scratch_bytes; 0 where that is not worth it, and
  * always below 512 tokens: then scratch may be NULL and the result is
  * selective_scan's to the bit; a split one differs by the rounding of the chunks'
- * starts). */
+ * starts, and where a state of its own leaves float32's range inside a chunk and
+ * comes back: split, it may be the finite value where the whole scan has infinity
+ * or 0). */
 size_t selective_scan_split_scratch_bytes(const selective_scan_args* args);
 scan_status selective_scan_split(const selective_scan_args* args, void* y, float* final_state,
                                  float* starts, void* scratch, size_t scratch_bytes, void* stream);

@@ -132,6 +132,15 @@ struct ScanSplit {
   float* ends;          // [batch][chunks][channels][states]
   float* spans;         // [batch][chunks][channels]
 };
+// What becomes of h over a chunk: 2^p h, p = A log2(e) times the chunk's steps.
+// The factor may leave float32's range where the product does not, so it is
+// applied in two halves; and 0 and infinity stay what they are, as they do token by
+// token, where a half that is infinite or 0 would make them no number.
+__device__ __forceinline__ float carried(float p, float h) {
+  const float half = exp2_hw(0.5f * p), v = h * half * half;
+  const bool stays = h == 0.0f || __builtin_isinf(h);
+  return stays && __builtin_isfinite(p) ? h : v;
+}
 
 // Where a workgroup stands in the problem: sequence, group of B and C, first
 // channel, and how many of its channels exist.

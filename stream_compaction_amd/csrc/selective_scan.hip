@@ -125,8 +125,7 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
       const float passed = split.spans[r];
 #pragma unroll
       for (int s = 0; s < NS; ++s)
-        h[s] = __builtin_fmaf(exp2_hw(passed * A2[s]), h[s],
-                              mine[s] ? split.ends[r * N + n0 + s * 16] : 0.0f);
+        h[s] = carried(passed * A2[s], h[s]) + (mine[s] ? split.ends[r * N + n0 + s * 16] : 0.0f);
     }
   }
   // the next block travels while one is worked on

@@ -148,8 +148,7 @@ __global__ __launch_bounds__(256 * TL) void selective_scan_grad_kernel(
       const float passed = split.spans[r];
 #pragma unroll
       for (int s = 0; s < NS; ++s)
-        m[s] = __builtin_fmaf(exp2_hw(passed * A2[s]), m[s],
-                              mine[s] ? split.ends[r * N + n0 + s * 16] : 0.0f);
+        m[s] = carried(passed * A2[s], m[s]) + (mine[s] ? split.ends[r * N + n0 + s * 16] : 0.0f);
     }
   }
 

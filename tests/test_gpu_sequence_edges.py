@@ -1,8 +1,11 @@
-"""The sequence operators at their edges on the GPU: batches that go out as several launches."""
+"""The sequence operators at their edges on the GPU: batches that go out as several launches,
+and states whose decay over a chunk leaves float32's range."""
 import pytest
 import torch
 
 import stream_compaction_amd as sc
+from stream_compaction_amd.sequence import _scan_args
+from test_gpu_sequence import act, gen
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +38,72 @@ def test_scan_step_over_several_launches(n):
         assert torch.equal(v, y[s]) and torch.equal(new[0], state[i]), f"sequence {i}"
     del state, fresh
     torch.cuda.empty_cache()
+
+
+def whole(x, dt, A, B, C, **more):
+    """``selective_scan`` in one piece, whatever its length."""
+    k = {"D": None, "z": None, "dt_bias": None, "softplus": False, "initial_state": None,
+         "lengths": None, **more}
+    a = _scan_args(x, dt, A, B, C, k["D"], k["z"], k["dt_bias"], k["softplus"], k["initial_state"],
+                   k["lengths"], False)
+    y, state = torch.empty_like(x), torch.empty((a.batch, a.channels, a.states), device="cuda")
+    sc.check(sc.lib().selective_scan(a, y.data_ptr(), state.data_ptr(), None,
+                                     torch.cuda.current_stream().cuda_stream))
+    return y, state
+
+
+@pytest.mark.parametrize("n,signs", [(16, "A"), (13, "dt"), (40, "A")])
+def test_growing_system_in_chunks(n, signs):
+    # the decay over a chunk overflows, no state does: they are zero until the last tokens.  The
+    # gradient likewise, from the other end
+    b, l, d = 1, 1024, 20
+    r = gen(300 + n)
+    x, B, C = (act(r, s, "f32")[0] for s in ((b, l, d), (b, l, 1, n), (b, l, 1, n)))
+    A = torch.rand((d, n), generator=r).cuda() + 0.5
+    dt = torch.rand((b, l, d), generator=r).cuda() + 0.5
+    if signs == "dt":
+        A, dt = -A, -dt
+    late = x.clone()
+    late[:, :l - 20] = 0
+    assert sc.lib().selective_scan_split_scratch_bytes(
+        _scan_args(x, dt, A, B, C, None, None, None, False, None, None, False)) > 0
+    y, state, starts = sc.selective_scan(late, dt, A, B, C, keep_starts=True)
+    y1, state1 = whole(late, dt, A, B, C)
+    assert bool(torch.isfinite(y1).all()) and bool(torch.isfinite(state1).all())
+    # nothing is carried from chunk to chunk
+    assert torch.equal(y, y1) and torch.equal(state, state1)
+    # dy in the first 20 tokens alone: nothing is carried to them
+    dy = act(r, (b, l, d), "f32")[0]
+    dy[:, 20:] = 0
+    zero = torch.zeros_like(x)
+    _, _, starts = sc.selective_scan(zero, dt, A, B, C, keep_starts=True)
+    g = sc.selective_scan_grad(dy, zero, dt, A, B, C, starts)
+    # the same 64 tokens alone
+    cut = lambda t: t[:, :64].contiguous()  # noqa: E731
+    k = [cut(t) for t in (zero, dt)] + [A] + [cut(t) for t in (B, C)]
+    _, _, s1 = sc.selective_scan(*k, keep_starts=True)
+    g1 = sc.selective_scan_grad(cut(dy), *k, s1)
+    for name in ("dx", "ddt", "dB", "dC"):
+        assert torch.equal(cut(g[name]), g1[name]), name
+        assert not bool(g[name][:, 64:].any()), name
+    assert torch.equal(g["dstate"], g1["dstate"]) and bool(torch.isfinite(g["dA"]).all())
+
+
+def test_carried_state_past_the_factors_range():
+    # a chunk's decay is below float32's least (2^-126) or above its greatest, the product with
+    # the state is not; and an infinite state stays infinite
+    b, l, d, n = 1, 1024, 16, 16
+    A = torch.full((d, n), -1.0, device="cuda")
+    zero = torch.zeros((b, l, d), device="cuda")
+    B = torch.ones((b, l, 1, n), device="cuda")
+    for per, start in ((0.6875, 2.0 ** 125), (-0.6875, 2.0 ** -125), (0.6875, float("inf"))):
+        dt = torch.full((b, l, d), per, device="cuda")
+        init = torch.full((b, d, n), start, device="cuda")
+        y, state = sc.selective_scan(zero, dt, A, B, B, initial_state=init)
+        y1, state1 = whole(zero, dt, A, B, B, initial_state=init)
+        assert torch.equal(torch.isinf(y), torch.isinf(y1)) and not bool(torch.isnan(y).any())
+        # token by token and in chunks: one rounding a token at most, and those of the exponents
+        ok = torch.isfinite(y1) & (y1.abs() > 2.0 ** -110)
+        assert int(ok.sum()) > 100 * d or start == float("inf")
+        rel = ((y - y1).abs() / y1.abs())[ok]
+        assert ok.sum() == 0 or float(rel.max()) <= 4 * l * 2.0 ** -24 + 2 * 140 * 2.0 ** -23
