@@ -44,7 +44,7 @@ constexpr int kFwdThreads = 256;        // T tokens of 8 channel pairs
 // `starts`, for the gradient; or find the chunks' ends of a split scan alone.
 enum class Pass { Run, Keep, Ends };
 
-template <class F, int NS, bool VEC, Pass PASS>
+template <class F, int NS, bool VEC, bool ALL, Pass PASS>
 __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
     ScanProblem p, void* yv, float* final_state, float* starts, ScanSplit split, int64_t b0,
     int64_t tiles, uint32_t count) {
@@ -55,6 +55,7 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
   __shared__ alignas(16) float s_x[2][2 * kPlane];           // steps, steps times x
   __shared__ alignas(16) float s_bc[2][2 * NS * kPlane];     // B, C
   __shared__ alignas(16) float s_part[2][ENDS ? 1 : 4 * kPlane];   // per wave
+  __shared__ alignas(16) float s_none[ALL ? 1 : kT];         // products of states that do not exist
 
   const uint32_t id = xcd_order(blockIdx.x);
   if (id >= count) return;
@@ -112,9 +113,11 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
   for (int s = 0; s < NS; ++s) {
     const int n = n0 + s * 16;
     mine[s] = cl < nch && n < N;
-    A2[s] = mine[s] ? p.A[ch * N + n] * kLog2e : 0.0f;
+    A2[s] = mine[s] ? p.A[ch * N + n] * kLog2e : kNoState;
     h[s] = !ENDS && mine[s] && p.initial_state != nullptr ? p.initial_state[srow + n] : 0.0f;
   }
+
+  if (!ALL && tid < kT) s_none[tid] = 0.0f;
 
   float span = 0.0f;                            // ENDS: sum of the channel's steps
   if constexpr (!ENDS) {
@@ -197,13 +200,16 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
     }
   };
   auto walk = [&](int64_t t0, int buf) {
+    auto products = [&](int s) {
+      return ALL || mine[s] ? s_x[buf] + kPlane + cl * kPS : s_none;
+    };
 #pragma unroll
     for (int sub = 0; sub < kT; sub += 16) {
       const float* xp = s_x[buf] + cl * kPS + sub;
       float dt[16], u[16], v[16], sums[4];
 #pragma unroll
       for (int t = 0; t < 16; t += 4) {
-        const vec4 d = *(const vec4*)(xp + t), w = *(const vec4*)(xp + kPlane + t);
+        const vec4 d = *(const vec4*)(xp + t), w = *(const vec4*)(products(0) + sub + t);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           dt[t + i] = d[i];
@@ -212,6 +218,14 @@ __global__ __launch_bounds__(kFwdThreads) void selective_scan_kernel(
       }
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
+        if (!ALL && s > 0) {
+#pragma unroll
+          for (int t = 0; t < 16; t += 4) {
+            const vec4 w = *(const vec4*)(products(s) + sub + t);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[t + i] = w[i];
+          }
+        }
         if (KEEP && mine[s] && t0 + sub < len) keep[s * 16] = h[s];
         const float* bc = s_bc[buf] + (s * 16 + n0) * kPS + sub + cl;
         const float B = bc[0], C = ENDS ? 0.0f : bc[NS * kPlane];
@@ -354,8 +368,8 @@ size_t selective_scan_scratch(const ScanProblem& p) {
   return chunks == 1 ? 0 : (size_t)(p.batch * chunks * p.channels * (p.states + 1)) * 4;
 }
 
-template <class F, int NS, bool VEC>
-static void fwd_go(const ScanProblem& p, void* y, float* final_state, float* starts,
+template <class F, int NS, bool VEC, bool ALL>
+static void fwd_launch(const ScanProblem& p, void* y, float* final_state, float* starts,
                    const ScanSplit& split, hipStream_t stream) {
   const int64_t tiles = (p.channels / p.groups + kScanTile - 1) / kScanTile;
   const int64_t per = tiles * p.groups;
@@ -364,7 +378,7 @@ static void fwd_go(const ScanProblem& p, void* y, float* final_state, float* sta
     const int64_t nb = p.batch - b0 < step ? p.batch - b0 : step;
     auto go = [&](auto pass, int64_t chunks) {
       const int64_t count = nb * per * chunks;
-      selective_scan_kernel<F, NS, VEC, decltype(pass)::value>
+      selective_scan_kernel<F, NS, VEC, ALL, decltype(pass)::value>
           <<<dim3(xcd_grid(count)), dim3(kFwdThreads), 0, stream>>>(
               p, y, final_state, starts, split, b0, tiles, (uint32_t)count);
     };
@@ -375,6 +389,16 @@ static void fwd_go(const ScanProblem& p, void* y, float* final_state, float* sta
       go(std::integral_constant<Pass, Pass::Run>{}, split.chunks);
     }
   }
+}
+
+template <class F, int NS, bool VEC>
+static void fwd_go(const ScanProblem& p, void* y, float* final_state, float* starts,
+                   const ScanSplit& split, hipStream_t stream) {
+  if constexpr (NS > 1) {
+    if (scan_all_states<NS>(p))
+      return fwd_launch<F, NS, VEC, true>(p, y, final_state, starts, split, stream);
+  }
+  fwd_launch<F, NS, VEC, false>(p, y, final_state, starts, split, stream);
 }
 
 template <class F>

@@ -63,7 +63,7 @@ __device__ __forceinline__ float lanes_sum(float (&v)[16], int l) {
 
 // TL tiles of 16 channels, four waves each.  ENDS: only find m before each chunk
 // of a split scan (but the first) from zero after it, and the sum of its steps.
-template <class F, int NS, bool GATE, int TL, bool ENDS>
+template <class F, int NS, bool GATE, int TL, bool ALL, bool ENDS>
 __global__ __launch_bounds__(256 * TL) void selective_scan_grad_kernel(
     ScanProblem p, ScanGrads g, float* part, float* part_params, ScanSplit split, int64_t b0,
     int64_t tiles, uint32_t count) {
@@ -75,6 +75,7 @@ __global__ __launch_bounds__(256 * TL) void selective_scan_grad_kernel(
   __shared__ alignas(16) float s_bc[2][2][NS * kPlane];           // B, C
   __shared__ alignas(16) float s_sum[2][TL][SUMS][4 * kPlane];    // over a wave's states
   __shared__ alignas(16) float s_dbc[2][TL][2][NS * 16 * kT];     // over a tile's channels
+  __shared__ alignas(16) float s_none[ALL ? 1 : kT];     // u and q of states that do not exist
 
   const uint32_t id = xcd_order(blockIdx.x);
   if (id >= count) return;
@@ -133,11 +134,13 @@ __global__ __launch_bounds__(256 * TL) void selective_scan_grad_kernel(
   for (int s = 0; s < NS; ++s) {
     const int n = n0 + s * 16;
     mine[s] = cl < nch && n < N;
-    A2[s] = mine[s] ? p.A[ch * N + n] * kLog2e : 0.0f;
+    A2[s] = mine[s] ? p.A[ch * N + n] * kLog2e : kNoState;
     m[s] = !ENDS && mine[s] && g.dfinal != nullptr ? g.dfinal[srow + n] : 0.0f;
     const int64_t from = (at.b * nkeep + first / kKeep) * p.channels + (mine[s] ? ch : at.ch);
     kept[s] = g.starts + from * N + (mine[s] ? n : 0);
   }
+
+  if (!ALL && tid < kT) s_none[tid] = 0.0f;
 
   float span = 0.0f;                            // ENDS: sum of the channel's steps
   if constexpr (!ENDS) {
@@ -221,15 +224,25 @@ __global__ __launch_bounds__(256 * TL) void selective_scan_grad_kernel(
     float dt[16], u[16], q[16], vG[16], vA[16], vY[16];
 #pragma unroll
     for (int t = 0; t < 16; t += 4) {
-      const vec4 a = *(const vec4*)(xp + t), b = *(const vec4*)(xp + kPlane + t),
-                 e = *(const vec4*)(xp + 2 * kPlane + t);
+      const vec4 a = *(const vec4*)(xp + t);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        dt[t + i] = a[i];
-        u[t + i] = b[i];
-        q[t + i] = e[i];
-      }
+      for (int i = 0; i < 4; ++i) dt[t + i] = a[i];
     }
+    // u and q as state s of this lane takes them
+    auto take = [&](int s) {
+      if (s > 0 && ALL) return;
+      const float* up = ALL || mine[s] ? xp + kPlane : s_none;
+      const float* qp = ALL || mine[s] ? xp + 2 * kPlane : s_none;
+#pragma unroll
+      for (int t = 0; t < 16; t += 4) {
+        const vec4 b = *(const vec4*)(up + t), e = *(const vec4*)(qp + t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          u[t + i] = b[i];
+          q[t + i] = e[i];
+        }
+      }
+    };
     if constexpr (ENDS) {
       float sum = 0.0f;
 #pragma unroll
@@ -238,6 +251,7 @@ __global__ __launch_bounds__(256 * TL) void selective_scan_grad_kernel(
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
         const float C = s_bc[buf][1][(s * 16 + n0) * kPS + cl];
+        take(s);
         for_tokens([&](auto tc) {
           constexpr int t = 15 - decltype(tc)::value;
           m[s] = exp2_hw(dt[t] * A2[s]) * __builtin_fmaf(row_bcast<t>(C), q[t], m[s]);
@@ -249,6 +263,7 @@ __global__ __launch_bounds__(256 * TL) void selective_scan_grad_kernel(
     for (int s = 0; s < NS; ++s) {
       const int bc = (s * 16 + n0) * kPS + cl;
       const float B = s_bc[buf][0][bc], C = s_bc[buf][1][bc];
+      take(s);
       float a[16], h[16], v[16], now = start[s];
       for_tokens([&](auto tc) {
         constexpr int t = decltype(tc)::value;
@@ -484,21 +499,28 @@ static hipError_t launch_grad(const ScanProblem& p, const ScanGrads& g, void* sc
   split.spans = split.ends + p.batch * split.chunks * p.channels * p.states;
   for (int64_t b0 = 0; b0 < p.batch; b0 += step) {
     const int64_t nb = p.batch - b0 < step ? p.batch - b0 : step;
-    auto go = [&](auto ns, auto gate, auto tl) {
+    auto launch = [&](auto ns, auto gate, auto tl, auto all) {
       constexpr int TL = decltype(tl)::value, NS = decltype(ns)::value;
-      constexpr bool GATE = decltype(gate)::value;
+      constexpr bool GATE = decltype(gate)::value, ALL = decltype(all)::value;
       if constexpr (TL == 1) {
         if (split.chunks > 1) {
           const int64_t count = nb * per * (split.chunks - 1);
-          selective_scan_grad_kernel<F, NS, GATE, TL, true>
+          selective_scan_grad_kernel<F, NS, GATE, TL, ALL, true>
               <<<dim3(xcd_grid(count)), dim3(256), 0, stream>>>(
               p, g, part, params, split, b0, tiles, (uint32_t)count);
         }
       }
       const int64_t count = nb * per * split.chunks;
-      selective_scan_grad_kernel<F, NS, GATE, TL, false>
+      selective_scan_grad_kernel<F, NS, GATE, TL, ALL, false>
           <<<dim3(xcd_grid(count)), dim3(256 * TL), 0, stream>>>(
           p, g, part, params, split, b0, tiles, (uint32_t)count);
+    };
+    auto go = [&](auto ns, auto gate, auto tl) {
+      constexpr int NS = decltype(ns)::value;
+      if constexpr (NS > 1) {
+        if (scan_all_states<NS>(p)) return launch(ns, gate, tl, std::true_type{});
+      }
+      launch(ns, gate, tl, std::false_type{});
     };
     auto by_tiles = [&](auto ns, auto gate) {
       if constexpr (decltype(ns)::value == 1) {

@@ -1,5 +1,5 @@
 """The sequence operators at their edges on the GPU: batches that go out as several launches,
-and states whose decay over a chunk leaves float32's range."""
+states whose decay over a chunk leaves float32's range, and infinities among the inputs."""
 import pytest
 import torch
 
@@ -107,3 +107,53 @@ def test_carried_state_past_the_factors_range():
         assert int(ok.sum()) > 100 * d or start == float("inf")
         rel = ((y - y1).abs() / y1.abs())[ok]
         assert ok.sum() == 0 or float(rel.max()) <= 4 * l * 2.0 ** -24 + 2 * 140 * 2.0 ** -23
+
+
+@pytest.mark.parametrize("n", [1, 13, 16, 20, 33])
+@pytest.mark.parametrize("what", ["x", "dt"])
+@pytest.mark.parametrize("l", [70, 600])
+def test_infinite_input(n, what, l):
+    # an infinite input makes its channel's state and outputs infinite from there on, and nothing
+    # else: with positive B, C and D there is no difference of infinities
+    b, d = 1, 19
+    r = gen(320 + n)
+    x, dt = (torch.rand((b, l, d), generator=r).cuda() + 0.1 for _ in range(2))
+    B, C = (torch.rand((b, l, 1, n), generator=r).cuda() + 0.1 for _ in range(2))
+    A, D = -torch.rand((d, n), generator=r).cuda() * 0.1 - 0.01, torch.ones(d, device="cuda")
+    y0, state0 = sc.selective_scan(x, dt, A, B, C, D)
+    t, c = 37, 17
+    {"x": x, "dt": dt}[what][0, t, c] = float("inf")
+    y, state = sc.selective_scan(x, dt, A, B, C, D)
+    hit = torch.zeros_like(y, dtype=torch.bool)
+    hit[0, t:, c] = True
+    assert bool((y[hit] == float("inf")).all()) and torch.equal(y[~hit], y0[~hit])
+    assert bool((state[0, c] == float("inf")).all())
+    keep = torch.arange(d) != c
+    assert torch.equal(state[:, keep], state0[:, keep])
+
+
+@pytest.mark.parametrize("n", [1, 13, 16, 20, 33])
+@pytest.mark.parametrize("l", [70, 600])
+def test_infinite_step_in_the_gradient(n, l):
+    # behind an infinite step nothing of the tokens before it is left: their gradients are those
+    # of a zero gradient from there on, and finite; so are all other channels'
+    b, d, t, c = 1, 19, 37, 17
+    r = gen(340 + n)
+    x, dt, dy = (torch.rand((b, l, d), generator=r).cuda() + 0.1 for _ in range(3))
+    B, C = (torch.rand((b, l, 1, n), generator=r).cuda() + 0.1 for _ in range(2))
+    A = -torch.rand((d, n), generator=r).cuda() * 0.1 - 0.01
+    dt[0, t, c] = float("inf")
+    _, _, starts = sc.selective_scan(x, dt, A, B, C, keep_starts=True)
+    g = sc.selective_scan_grad(dy, x, dt, A, B, C, starts)
+    dt[0, t, c] = 1.0
+    dy[0, t:, c] = 0
+    cut = lambda v: v[:, :t].contiguous()  # noqa: E731
+    k = [cut(x), cut(dt), A, cut(B), cut(C)]
+    _, _, s0 = sc.selective_scan(*k, keep_starts=True)
+    g0 = sc.selective_scan_grad(cut(dy), *k, s0)
+    for name in ("dx", "ddt"):
+        # sums over a state's own tokens: the same but for where a block of 16 begins
+        assert torch.allclose(g[name][0, :t, c], g0[name][0, :, c], rtol=1e-5, atol=0), name
+    keep = torch.arange(d) != c
+    assert bool(torch.isfinite(g["dx"][..., keep]).all() & torch.isfinite(g["ddt"][..., keep]).all())
+    assert bool((g["dx"][0, t, c] == float("inf")).all())
