@@ -293,9 +293,10 @@ scan_status select_compact_devn(const void* in, const uint8_t* flags, void* out,
  *  - lengths: NULL, or device pointer to `batch` int32, read by the kernels and
  *    clamped to [0, length].  Tokens at and past lengths[b] do not exist: they
  *    are not read, their outputs and gradients are 0 and states do not move.
- *  - 0 <= batch, length <= INT32_MAX and 1 <= channels <= 2^22.  batch == 0 is
- *    a no-op, except that a gradient's sums over the batch are then 0;
- *    length == 0 copies the initial state to the final one.
+ *  - 0 <= batch, length <= INT32_MAX and 1 <= channels <= 2^22, and no array of
+ *    2^47 bytes or more (SCAN_EINVAL).  batch == 0 is a no-op, except that a
+ *    gradient's sums over the batch are then 0; length == 0 copies the initial
+ *    state to the final one.
  *  - Results do not depend on timing: no floating atomics, the same bits for
  *    the same arguments.
  * ------------------------------------------------------------------------- */

@@ -84,6 +84,15 @@ class Ranges {
   scan_status status_ = SCAN_OK;
 };
 
+// Whether [batch, length, channels] has a size below kMaxBytes.  (Its factors'
+// product can pass 64 bits; below kMaxBytes, no product of sizes in this file
+// does: a scan's rows of B and C and its kept states are at most 2^6 times as much,
+// its state is at most 2^31 2^22 2^6 elements.)
+bool activations_fit(int64_t batch, int64_t length, int64_t channels, size_t eb) {
+  return (unsigned __int128)batch * (unsigned __int128)length * (unsigned __int128)channels * eb <
+         kMaxBytes;
+}
+
 // Sizes and types of a convolution; with `step`, of one token.
 scan_status conv_problem(const causal_conv_args* a, bool step, sca::ConvProblem* p, sca::Fmt* fmt,
                          size_t* eb) {
@@ -94,6 +103,7 @@ scan_status conv_problem(const causal_conv_args* a, bool step, sca::ConvProblem*
   const int64_t length = step ? 1 : a->length;
   if (a->batch < 0 || a->batch > kMaxN || length < 0 || length > kMaxN) return SCAN_EINVAL;
   if (a->channels < 1 || a->channels > kMaxChannels) return SCAN_EINVAL;
+  if (!activations_fit(a->batch, length, a->channels, *eb)) return SCAN_EINVAL;
   p->x = a->x;
   p->weight = a->weight;
   p->bias = a->bias;
@@ -130,6 +140,7 @@ scan_status scan_problem(const selective_scan_args* a, bool step, sca::ScanProbl
   if (a->batch < 0 || a->batch > kMaxN || length < 0 || length > kMaxN) return SCAN_EINVAL;
   if (a->channels < 1 || a->channels > kMaxChannels) return SCAN_EINVAL;
   if (a->groups < 1 || a->channels % a->groups != 0) return SCAN_EINVAL;
+  if (!activations_fit(a->batch, length, a->channels, *eb)) return SCAN_EINVAL;
   *p = sca::ScanProblem{
       a->x, a->dt, a->B, a->C, a->z, a->A, a->D, a->dt_bias,
       step ? nullptr : a->initial_state, step ? nullptr : a->lengths,
@@ -161,8 +172,11 @@ void scan_inputs(const sca::ScanProblem& p, size_t eb, Ranges* r) {
   r->add(p.lengths, (uint64_t)p.batch, 4, false, false);
 }
 
-// Bytes of a product of sizes, 0 where it is no size.
-size_t bytes_or_zero(unsigned __int128 b) { return b >= kMaxBytes ? 0 : (size_t)b; }
+// Float32 values of the states that a scan keeps for its gradient.
+uint64_t starts_count(const sca::ScanProblem& p) {
+  const int64_t blocks = (p.length + sca::kScanKeepTokens - 1) / sca::kScanKeepTokens;
+  return (uint64_t)(p.batch * blocks) * (uint64_t)(p.channels * p.states);
+}
 
 }  // namespace
 
@@ -245,9 +259,8 @@ size_t selective_scan_starts_bytes(const selective_scan_args* args) {
   sca::Fmt fmt;
   size_t eb;
   if (scan_problem(args, false, &p, &fmt, &eb) != SCAN_OK) return 0;
-  const int64_t blocks = (p.length + sca::kScanKeepTokens - 1) / sca::kScanKeepTokens;
-  return bytes_or_zero((unsigned __int128)(p.batch * blocks) *
-                       (unsigned __int128)(p.channels * p.states) * 4);
+  const uint64_t bytes = starts_count(p) * 4;
+  return bytes < kMaxBytes ? bytes : 0;
 }
 
 static scan_status scan_call(const selective_scan_args* args, void* y, float* final_state,
@@ -264,7 +277,7 @@ static scan_status scan_call(const selective_scan_args* args, void* y, float* fi
   scan_inputs(p, eb, &r);
   r.add(y, (uint64_t)p.batch * (uint64_t)p.length * (uint64_t)p.channels, eb, true, true);
   r.add(final_state, (uint64_t)p.batch * (uint64_t)(p.channels * p.states), 4, true, false);
-  if (starts != nullptr) r.add(starts, selective_scan_starts_bytes(args) / 4, 4, true, false);
+  if (starts != nullptr) r.add(starts, starts_count(p), 4, true, false);
   r.add(scratch, need, 1, true, true);
   if (need > 0 && !aligned(scratch, 16)) return SCAN_EINVAL;
   if (scratch_bytes < need) return SCAN_ESCRATCH;
@@ -316,7 +329,7 @@ scan_status selective_scan_grad(const selective_scan_args* args, const selective
   scan_inputs(p, eb, &r);
   r.add_strided(grads->dy, dims, grads->dy_stride, 2, p.channels, eb, true);
   r.add(grads->dfinal, state, 4, false, false);
-  r.add(grads->starts, selective_scan_starts_bytes(args) / 4, 4, false, true);
+  r.add(grads->starts, starts_count(p), 4, false, true);
   r.add(grads->dx, tokens * (uint64_t)p.channels, eb, true, true);
   r.add(grads->ddt, tokens * (uint64_t)p.channels, eb, true, true);
   r.add(grads->dz, tokens * (uint64_t)p.channels, eb, true, false);
