@@ -41,10 +41,11 @@ class _CausalConv(torch.autograd.Function):
 
 class _SelectiveScan(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, dt, A, B, C, D, z, dt_bias, initial_state, lengths, softplus):
+    def forward(ctx, x, dt, A, B, C, D, z, dt_bias, initial_state, lengths, softplus, recording):
         ctx.set_materialize_grads(False)
         more = {"D": D, "z": z, "dt_bias": dt_bias, "softplus": softplus, "lengths": lengths}
-        if not any(ctx.needs_input_grad):
+        # (an input that requires a gradient is said to need one under no_grad, too)
+        if not (recording and any(ctx.needs_input_grad)):
             return _ops.selective_scan(x, dt, A, B, C, initial_state=initial_state, **more)
         y, state, starts = _ops.selective_scan(x, dt, A, B, C, initial_state=initial_state,
                                                keep_starts=True, **more)
@@ -60,7 +61,7 @@ class _SelectiveScan(torch.autograd.Function):
                                      dt_bias=dt_bias, softplus=ctx.softplus, lengths=lengths,
                                      dfinal=_dense(dfinal))
         return (g["dx"], g["ddt"], g["dA"], g["dB"], g["dC"], g["dD"], g["dz"], g["ddt_bias"],
-                g["dstate"] if ctx.has_state else None, None, None)
+                g["dstate"] if ctx.has_state else None, None, None, None)
 
 
 class _Embedding(torch.autograd.Function):
@@ -86,7 +87,7 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=False,
                    initial_state=None, lengths=None):
     """Differentiable ``sequence.selective_scan``: ``(y, final_state)``."""
     return _SelectiveScan.apply(x, dt, A, B, C, D, z, dt_bias, initial_state, lengths,
-                                bool(softplus))
+                                bool(softplus), torch.is_grad_enabled())
 
 
 def embedding(weight, ids, scale=1.0):
