@@ -31,7 +31,8 @@ constexpr int kPlane = kScanTile * kPS;
 // Sums over the 16 lanes of a row of 16 values: lane l gets value l.  A lane adds
 // its partner's share of the values it keeps: 8, then 4 lanes apart by additions
 // that write one half of the lanes, closer by selects.  Instructions between a
-// write and the DPP read of the same register: at least two throughout.
+// write and the DPP read of the same register: at least two throughout.  The
+// first eight values are written before the others are read: early clobbers.
 __device__ __forceinline__ float lanes_sum(float (&v)[16], int l) {
 #define SCA_FAR(A, B)                                                          \
   "v_add_f32_dpp " A ", " A ", " A " row_ror:8 row_mask:0xf bank_mask:0x3\n\t"   \
@@ -44,7 +45,8 @@ __device__ __forceinline__ float lanes_sum(float (&v)[16], int l) {
       SCA_FAR("%4", "%12") SCA_FAR("%5", "%13") SCA_FAR("%6", "%14") SCA_FAR("%7", "%15")
       SCA_NEAR("%0", "%4") SCA_NEAR("%1", "%5") SCA_NEAR("%2", "%6") SCA_NEAR("%3", "%7")
       "s_nop 1"
-      : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3]), "+v"(v[4]), "+v"(v[5]), "+v"(v[6]), "+v"(v[7])
+      : "+&v"(v[0]), "+&v"(v[1]), "+&v"(v[2]), "+&v"(v[3]), "+&v"(v[4]), "+&v"(v[5]),
+        "+&v"(v[6]), "+&v"(v[7])
       : "v"(v[8]), "v"(v[9]), "v"(v[10]), "v"(v[11]), "v"(v[12]), "v"(v[13]), "v"(v[14]), "v"(v[15]));
 #undef SCA_FAR
 #undef SCA_NEAR
