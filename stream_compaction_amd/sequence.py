@@ -174,6 +174,10 @@ def _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, lengths, 
                                      "[batch, groups, states])")
     groups = B.shape[-2]
     rows = shape[:-1] + (groups, n)
+    # (shapes before strides: an argument of another rank has not as many)
+    xp, dtp = _rows(x, "x", shape, ty, dev), _rows(dt, "dt", shape, ty, dev)
+    Bp, Cp = _rows(B, "B", rows, ty, dev), _rows(C, "C", rows, ty, dev)
+    zp = None if z is None else _rows(z, "z", shape, ty, dev)
     length, zs = 1, (0, 0)
     if step:
         xs, ds = (x.stride(0), 0), (dt.stride(0), 0)
@@ -187,9 +191,7 @@ def _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, lengths, 
             zs = z.stride()[:2]
     f32 = torch.float32
     return ScanArgs(
-        _rows(x, "x", shape, ty, dev), _rows(dt, "dt", shape, ty, dev),
-        _rows(B, "B", rows, ty, dev), _rows(C, "C", rows, ty, dev),
-        None if z is None else _rows(z, "z", shape, ty, dev),
+        xp, dtp, Bp, Cp, zp,
         _like(A, "A", (d, n), f32, dev), None if D is None else _like(D, "D", (d,), f32, dev),
         None if dt_bias is None else _like(dt_bias, "dt_bias", (d,), f32, dev),
         None if initial_state is None else
@@ -307,10 +309,15 @@ def embedding_grad(dout, ids, rows, scale=1.0, dtype=None, out=None, scratch=Non
     """Gradient of ``embedding``'s table: ``[rows, channels]`` in ``dtype`` (dout's, or
     float32), row ``v`` being ``scale`` times the sum of ``dout`` over the tokens with id
     ``v``; masked tokens add nothing.  The same bits every time."""
-    d = dout.shape[-1]
-    if dout.shape[:-1] != ids.shape:
+    if dout.dim() == 0 or dout.shape[:-1] != ids.shape:
         raise ValueError("dout must be [*ids.shape, channels]")
-    flat = dout.view(-1, d) if dout.dim() != 2 else dout
+    d = dout.shape[-1]
+    flat = dout
+    if dout.dim() != 2:
+        try:
+            flat = dout.view(ids.numel(), d)
+        except RuntimeError:
+            raise ValueError("dout's rows must lie at one stride") from None
     code, stride = _table(flat, "dout")
     idc = _id_code(ids, dout.get_device())
     dtype = dtype or (out.dtype if out is not None else dout.dtype)
