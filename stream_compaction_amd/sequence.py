@@ -12,7 +12,7 @@ import ctypes
 
 import torch
 
-from . import DTYPE_CODES, _stream, check, lib
+from . import DTYPE_CODES, check, lib
 from ._sequence_abi import ConvArgs, ScanArgs, ScanGrads
 
 _ACT = {torch.float32: DTYPE_CODES["f32"], torch.float16: DTYPE_CODES["f16"],
@@ -54,6 +54,19 @@ def _rows(t, what, shape, dtype, dev):
     if shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{what} must have a contiguous last axis")
     return t.data_ptr()
+
+
+def _queue(stream, dev):
+    """The stream a call goes to, as a raw handle: one of the data's GPU, which a kernel of
+    another GPU could not read."""
+    if stream is not None:
+        at = stream.device_index
+    else:
+        at = torch._C._cuda_getDevice()
+    if at != dev:
+        raise ValueError(f"the data is on cuda:{dev}, the stream on cuda:{at}")
+    # (the raw handle: a Stream object costs more than the rest of a small call)
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _new(shape, dtype, like, stream):
@@ -118,7 +131,7 @@ def causal_conv(x, weight, bias=None, initial_state=None, lengths=None, silu=Tru
     a = _conv_args(x, weight, bias, initial_state, lengths, silu, False)
     y = _out(out, "out", x.shape, x.dtype, x, stream)
     fs = _out(final_state, "final_state", (a.batch, a.width - 1, a.channels), x.dtype, x, stream)
-    check(lib().causal_conv(a, y.data_ptr(), fs.data_ptr(), _stream(stream)))
+    check(lib().causal_conv(a, y.data_ptr(), fs.data_ptr(), _queue(stream, x.get_device())))
     return y, fs
 
 
@@ -140,7 +153,7 @@ def causal_conv_grad(dy, x, weight, bias=None, initial_state=None, lengths=None,
     check(L.causal_conv_grad(a, dyp, (_i64 * 2)(*dy.stride()[:2]), df, dx.data_ptr(),
                              dw.data_ptr(), None if db is None else db.data_ptr(),
                              None if ds is None else ds.data_ptr(), scratch.data_ptr(),
-                             room, _stream(stream)))
+                             room, _queue(stream, dev)))
     return {"dx": dx, "dweight": dw, "dbias": db, "dstate": ds}
 
 
@@ -155,7 +168,7 @@ def causal_conv_step(state, x, weight, bias=None, silu=True, new_state=None, out
     sp = _like(state, "state", shape, x.dtype, dev)
     np_ = sp if new_state is None else _like(new_state, "new_state", shape, x.dtype, dev)
     y = _out(out, "out", x.shape, x.dtype, x, stream)
-    check(lib().causal_conv_step(a, sp, np_, y.data_ptr(), _stream(stream)))
+    check(lib().causal_conv_step(a, sp, np_, y.data_ptr(), _queue(stream, dev)))
     return y
 
 
@@ -226,11 +239,11 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=False,
     # (short scans are never split)
     need = L.selective_scan_split_scratch_bytes(a) if x.shape[1] >= 512 else 0
     if need == 0:
-        check(L.selective_scan(a, y.data_ptr(), fs.data_ptr(), sp, _stream(stream)))
+        check(L.selective_scan(a, y.data_ptr(), fs.data_ptr(), sp, _queue(stream, x.get_device())))
     else:
         scratch, room = _scratch(None, need, A, stream)
         check(L.selective_scan_split(a, y.data_ptr(), fs.data_ptr(), sp, scratch.data_ptr(), room,
-                                     _stream(stream)))
+                                     _queue(stream, x.get_device())))
     return (y, fs, starts) if keep_starts else (y, fs)
 
 
@@ -258,7 +271,7 @@ def selective_scan_grad(dy, x, dt, A, B, C, starts, D=None, z=None, dt_bias=None
     g = ScanGrads(dyp, dy.stride()[:2], df, sp, p["dx"], p["ddt"], p["dB"], p["dC"], p["dz"],
                   p["dA"], p["dD"], p["ddt_bias"], p["dstate"])
     scratch, room = _scratch(scratch, L.selective_scan_grad_scratch_bytes(a), A, stream)
-    check(L.selective_scan_grad(a, g, scratch.data_ptr(), room, _stream(stream)))
+    check(L.selective_scan_grad(a, g, scratch.data_ptr(), room, _queue(stream, dev)))
     return out
 
 
@@ -273,7 +286,7 @@ def selective_scan_step(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, sof
     sp = _like(state, "state", shape, torch.float32, dev)
     np_ = sp if new_state is None else _like(new_state, "new_state", shape, torch.float32, dev)
     y = _out(out, "out", x.shape, x.dtype, x, stream)
-    check(lib().selective_scan_step(a, sp, np_, y.data_ptr(), _stream(stream)))
+    check(lib().selective_scan_step(a, sp, np_, y.data_ptr(), _queue(stream, dev)))
     return y
 
 
@@ -301,7 +314,7 @@ def embedding(weight, ids, scale=1.0, out=None, stream=None):
     rows, d = weight.shape
     out = _out(out, "out", ids.shape + (d,), weight.dtype, weight, stream)
     check(lib().embedding(weight.data_ptr(), ids.data_ptr(), out.data_ptr(), ids.numel(), rows, d,
-                          stride, code, idc, float(scale), _stream(stream)))
+                          stride, code, idc, float(scale), _queue(stream, weight.get_device())))
     return out
 
 
@@ -329,5 +342,5 @@ def embedding_grad(dout, ids, rows, scale=1.0, dtype=None, out=None, scratch=Non
     scratch, room = _scratch(scratch, L.embedding_grad_scratch_bytes(n, rows, d), dout, stream)
     check(L.embedding_grad(flat.data_ptr(), ids.data_ptr(), out.data_ptr(), n, rows, d, stride,
                            code, idc, _ACT[dtype], float(scale), scratch.data_ptr(),
-                           room, _stream(stream)))
+                           room, _queue(stream, dout.get_device())))
     return out

@@ -95,3 +95,38 @@ def test_rows_of_an_embedding():
     for table in (OnGpu(), OnGpu(8), OnGpu(4, 8, 2), OnGpu(4, 16)[:, ::2]):
         with pytest.raises(ValueError):
             seq.embedding(table, ids)
+
+
+def calls(stream=None):
+    """One call of every operator on data of GPU 0."""
+    x, one = OnGpu(2, 8, 16), OnGpu(2, 16)
+    w, A = OnGpu(16, 4), OnGpu(16, 4)
+    rows, row, ids = OnGpu(2, 8, 1, 4), OnGpu(2, 1, 4), OnGpu(2, 8, dtype=torch.int64)
+    return (lambda: seq.causal_conv(x, w, out=OnGpu(2, 8, 16), final_state=OnGpu(2, 3, 16), stream=stream),
+            lambda: seq.causal_conv_grad(x, x, w, stream=stream),
+            lambda: seq.causal_conv_step(OnGpu(2, 3, 16), one, w, stream=stream),
+            lambda: seq.selective_scan(x, x, A, rows, rows, stream=stream),
+            lambda: seq.selective_scan_grad(x, x, x, A, rows, rows, OnGpu(16), stream=stream),
+            lambda: seq.selective_scan_step(OnGpu(2, 16, 4), one, one, A, row, row, stream=stream),
+            lambda: seq.embedding(w, ids, stream=stream),
+            lambda: seq.embedding_grad(x, ids, 9, stream=stream))
+
+
+@pytest.mark.parametrize("which", range(8))
+def test_data_of_another_gpu_than_the_stream(monkeypatch, which):
+    # the current stream of GPU 0 may take the work; of GPU 1, or a stream of GPU 1, not
+    with pytest.raises(AssertionError, match="reached the library"):
+        calls()[which]()
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    with pytest.raises(ValueError, match="cuda:1"):
+        calls()[which]()
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+
+    class Other:
+        cuda_stream, device_index = 64, 1
+
+    def new(shape, dtype, like, stream):
+        return OnGpu(*((shape,) if isinstance(shape, int) else shape), dtype=dtype)
+    monkeypatch.setattr(seq, "_new", new)
+    with pytest.raises(ValueError, match="cuda:1"):
+        calls(Other())[which]()
