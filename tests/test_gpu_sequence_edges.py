@@ -157,3 +157,17 @@ def test_infinite_step_in_the_gradient(n, l):
     keep = torch.arange(d) != c
     assert bool(torch.isfinite(g["dx"][..., keep]).all() & torch.isfinite(g["ddt"][..., keep]).all())
     assert bool((g["dx"][0, t, c] == float("inf")).all())
+
+
+def test_convolution_past_the_caches():
+    # a batch whose output is stored past the caches against its sequences, whose are not
+    b, l, d = 3, 2051, 4096
+    assert b * l * d * 2 >= 32 << 20 > l * d * 2
+    r = gen(360)
+    x = torch.randn(b, l, 2 * d, generator=r).bfloat16().cuda()[..., d:]
+    w, bias = torch.randn(d, 4, generator=r).cuda(), torch.randn(d, generator=r).cuda()
+    lengths = torch.tensor([l, 1000, 0], dtype=torch.int32).cuda()
+    y, state = sc.causal_conv(x, w, bias, lengths=lengths)
+    for i in range(b):
+        one, last = sc.causal_conv(x[i:i + 1], w, bias, lengths=lengths[i:i + 1])
+        assert torch.equal(one, y[i:i + 1]) and torch.equal(last, state[i:i + 1])
