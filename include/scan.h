@@ -340,7 +340,7 @@ scan_status causal_conv_grad(const causal_conv_args* args, const void* dy,
 /* One token per sequence: x is [batch, channels] (x_stride[0] between rows;
  * args->length, lengths and initial_state are not used).  state and new_state
  * are [batch, width - 1, channels] and either the same array or disjoint; y is
- * [batch, channels]. */
+ * [batch, channels].  batch * channels <= INT32_MAX, else SCAN_EINVAL. */
 scan_status causal_conv_step(const causal_conv_args* args, const void* state, void* new_state,
                              void* y, void* stream);
 
@@ -377,8 +377,8 @@ typedef struct {
 
 /* y: [batch, length, channels].  final_state: float32 [batch, channels, states]
  * (NULL: not written).  starts (NULL: not written): what the gradient needs,
- * selective_scan_starts_bytes(length, ...) bytes, the states before each block
- * of tokens. */
+ * selective_scan_starts_bytes(args) bytes, the states before each block of 16
+ * tokens. */
 size_t selective_scan_starts_bytes(const selective_scan_args* args);
 scan_status selective_scan(const selective_scan_args* args, void* y, float* final_state,
                            float* starts, void* stream);
@@ -422,7 +422,8 @@ scan_status selective_scan_grad(const selective_scan_args* args, const selective
 /* One token per sequence: x, dt, z are [batch, channels] and B, C [batch,
  * groups, states] (token strides, length, lengths and initial_state are not
  * used).  state and new_state are float32 [batch, channels, states] and either
- * the same array or disjoint; y is [batch, channels]. */
+ * the same array or disjoint; y is [batch, channels].  batch * channels <=
+ * INT32_MAX / 16, else SCAN_EINVAL. */
 scan_status selective_scan_step(const selective_scan_args* args, const float* state,
                                 float* new_state, void* y, void* stream);
 

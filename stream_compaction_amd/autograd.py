@@ -4,7 +4,9 @@
 these names in ``stream_compaction_amd.sequence`` and can be differentiated with respect to
 every floating input, through the output and the final state.  Both directions run in the
 library's kernels on the current stream; work space comes from torch's allocator, so a
-forward and backward pass can be captured into a HIP graph.
+forward and backward pass can be captured into a HIP graph.  Gradients are taken once, in
+reverse: there are no second derivatives, no forward mode and no ``torch.func`` transforms
+(``grad``, ``vmap``, ...), which torch refuses with an error of its own.
 """
 import torch
 

@@ -9,7 +9,9 @@
 // bytes per token) and walks a run of tokens with the last W inputs in
 // registers, so each input is read once but for the W - 1 tokens before a run.
 // Measured, bf16, W = 4: forward 4 x 4096 x 4096 with half of it padding (202 MB)
-// 34 us, 6.0 TB/s; step 128 x 4096 (8.5 MB) 4.6 us, most of it latency.
+// 47.5 us, 4.2 TB/s, with inputs that no cache holds and 34 us with inputs in the
+// last-level cache; step 128 x 4096 (8.5 MB) 4.6 us, most of it latency.  Rows off
+// alignment go one channel per lane: 4 x 4096 x 2047 40 us against 29 for 2048.
 #include "sequence.hpp"
 
 namespace sca {
@@ -152,8 +154,8 @@ __global__ __launch_bounds__(256) void causal_conv_kernel(ConvProblem p, void* y
 // over a run stay in registers; the four waves of a workgroup (four runs of
 // the same channels) add theirs in LDS, and a second kernel adds the
 // workgroups' sums in a fixed order, so results are the same every time.  Some
-// 40 instructions per element keep the vector units 76% busy beside 101 MB: 4 x
-// 2048 x 2048 takes 31 us and 4 us for the filter sums.  Four channels per lane:
+// 40 instructions per element keep the vector units 73% busy beside 101 MB: 4 x
+// 2048 x 2048 takes 32 us and 4 us for the filter sums.  Four channels per lane:
 // eight hold too many values in registers for four waves a SIMD, two read rows in
 // 4-byte pieces (37 us against 35).
 constexpr int kConvGradWaves = 4;

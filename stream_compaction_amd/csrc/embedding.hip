@@ -10,10 +10,12 @@
 // block), writes the rows whose run lies inside, and leaves the sums of runs
 // that cross a border to a second kernel.
 //
-// Both directions are bound by memory.  Measured, bf16, 16384 tokens, a table of
-// 50000 x 2048: lookup (134 MB with every row counted once; frequent rows come
-// from the caches) 16 us; gradient (272 MB) 69 us: 43 us for sort and zeros, 20
-// for the segments, 8 for the borders.
+// Both directions are bound by memory.  Measured, bf16, 16384 tokens with a
+// language's frequencies, a table of 50000 x 2048: lookup of the 5850 rows that
+// occur (91 MB) 17 us, 23 where no cache holds any of them; gradient (272 MB) 70
+// us: 44 us for sort and zeros, 19 for the segments, 9 for the borders.  Gradients
+// past the short sort's limit: 16385 tokens 134 us, 32768 149 (339 MB), 131072 265
+// (743 MB), 524288 703 (2.4 GB).
 #include "sequence.hpp"
 
 namespace sca {

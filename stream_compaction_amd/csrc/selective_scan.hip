@@ -24,12 +24,12 @@ namespace {
 // together from them during the next block's walk.  Everything is buffered twice:
 // one barrier per block.
 //
-// Measured, bf16, 16 states, softplus and gate: 8192 x 4096 284 us (1.9e12 updates
-// a second; one wave per SIMD, vector units 58% busy, the rest is latency), a
-// batch of 4 with 8192 of 16384 tokens 197 us (three waves, 85%).  The
-// definition's own instructions alone would take 93 us; a block's 297
+// Measured (traced), 16 states, softplus and gate: bf16 8192 x 4096 277 us (1.9e12
+// updates a second; one wave per SIMD, vector units 57% busy, the rest is latency),
+// f16, a batch of 4 with 8192 of 16384 tokens 204 us (three waves, 93%).  The
+// definition's own instructions alone would take 93 us; a block's 291
 // instructions per wave are 128 + 32 exponentials for them, 48 for the sums over
-// rows and some 90 for steps, gate and staging.  Tokens across lanes with wave
+// rows and some 83 for steps, gate and staging.  Tokens across lanes with wave
 // scans of affine maps, the arrangement before, took 302 and 342 us: its second
 // pass over every token and the scans cost more than the sums over rows here.
 constexpr int kT = 32;                  // tokens per block
@@ -339,9 +339,9 @@ constexpr int64_t kMaxGroups = 1ll << 21;
 // are one) a token takes 1 + 0.5 (w - 1) times as long as with up to one; the
 // first pass costs 0.6 of the second and leaves out one chunk; its launch and the
 // chunks' starts stand for 150 + 8 n tokens.  The split must win a fifth.  Forward
-// / gradient, split against whole, 16 states in bf16: 8192 x 64 channels 28 / 57 us
-// against 263 / 717, 2048 x 512 24 / 53 against 69 / 192, 2 x 4096 x 768 74 / 169
-// against 134 / 377, 8192 x 2048 162 / 403 against 262 / 748, 7 x 1024 x 300 37 / 80
+// / gradient, split against whole, 16 states in bf16: 8192 x 64 channels 28 / 53 us
+// against 263 / 717, 2048 x 512 24 / 49 against 69 / 192, 2 x 4096 x 768 71 / 154
+// against 134 / 377, 8192 x 2048 160 / 385 against 266 / 748, 7 x 1024 x 300 38 / 79
 // against 38 / 105.  From 256 workgroups on (8192 x 4096) the estimate gains
 // nothing.
 int64_t scan_chunks(const ScanProblem& p, int64_t* tokens) {
@@ -446,8 +446,9 @@ hipError_t launch_selective_scan(const ScanProblem& p, Fmt fmt, void* y, float* 
 // owning the V states at q V, (q + G) V, ...; V = 4 makes the state's loads and
 // stores 16 bytes wide and a wave's contiguous.  A lane takes R sequences of
 // its channel at once: A, D and the bias are read once for them and R loads of
-// the state are in flight.  128 x 4096 x 16 in bf16 (72 MB): R = 2 16.4 us (4.4
-// TB/s), R = 4 20.2 us, whose registers leave fewer waves.  A launch owns the
+// the state are in flight.  128 x 4096 x 16 in bf16 (72 MB), three states in turn,
+// which the last-level cache holds in part: R = 2 16.4 us (4.4 TB/s), R = 4 20.2 us,
+// whose registers leave fewer waves; six in turn: R = 2 20.5 us (3.5 TB/s).  A launch owns the
 // sequences [first, end): what a lane's R reach past `end` is the next launch's,
 // and to be moved once only.
 // ---------------------------------------------------------------------------

@@ -14,9 +14,9 @@
 // partial sums, which a second kernel adds over the workgroups in a fixed order
 // (no atomics: the same bits every time).
 //
-// Measured, bf16, 16 states, 4 x 2048 x 2048 with gate: 280 us, and 12 + 5 us for
-// the two kernels of partial sums (67 MB); two waves per SIMD, vector units 83%
-// busy, 27 instructions per token and state.  One tile of channels per workgroup
+// Measured (traced), bf16, 16 states, 4 x 2048 x 2048 with gate: 284 us, and 12 + 5
+// us for the two kernels of partial sums (67 MB); two waves per SIMD, vector units
+// 82% busy, 28 instructions per token and state.  One tile of channels per workgroup
 // instead of two takes 5% longer for twice the partial sums.
 #include "scan_tile.hpp"
 

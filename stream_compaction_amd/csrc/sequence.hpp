@@ -13,9 +13,14 @@ namespace sca {
 template <class F> constexpr int kVecElems = 16 / (int)sizeof(typename F::S);
 
 // Outputs that the L2 caches (8 of 4 MB) cannot hold are stored past them where
-// that gains (PAST below): a convolution of 134 MB takes 34 us against 49, a
-// lookup of 67 MB 16 against 18.5, with inputs that no cache holds.  Smaller
-// outputs stay for their reader.
+// that gains (PAST below).  With inputs that no cache holds a convolution with 134
+// MB of output, half of it padding, takes 47.5 us against 49.3, without padding 57.7
+// against 60.7, a lookup of 67 MB (4 outputs in turn) 16.6 against 25.  With inputs
+// in the 256 MB last-level cache, which such stores leave there, the convolution
+// takes 34 us against 49.  With a kernel that reads the output behind it the two
+// together take the same to within 4% either way, over 32 to 256 MB (a product
+// behind 128 MB 110 against 114 us, behind 256 MB 183 against 180).  The one loss:
+// an output that is written over and over unread (47.5 us against 39).
 inline bool past_caches(int64_t bytes) { return bytes >= (32ll << 20); }
 
 constexpr float kLog2e = 1.44269504088896340736f;

@@ -2,9 +2,10 @@
 embedding, each with its gradient, and the first two with their single-token step.
 
 Thin wrappers over the C ABI (``include/scan.h`` has every definition and rule): they
-check shapes and types, allocate what is not given, and pass pointers, strides and the
-current HIP stream.  Activations are ``[batch, length, channels]`` float32, float16 or
-bfloat16 tensors with contiguous channels; parameters and the scan's states are float32.
+check shapes, types and devices, allocate what is not given, and pass pointers, strides and
+the current HIP stream, which must be of the data's GPU (as must a ``stream`` that is
+given).  Activations are ``[batch, length, channels]`` float32, float16 or bfloat16 tensors
+with contiguous channels; parameters and the scan's states are float32.
 ``stream_compaction_amd.autograd`` has the same operators for torch's automatic
 differentiation.
 """
@@ -161,7 +162,7 @@ def causal_conv_step(state, x, weight, bias=None, silu=True, new_state=None, out
                      stream=None):
     """One token of ``causal_conv``: ``x`` is ``[batch, channels]`` and ``state`` the last
     ``width - 1`` inputs, replaced by those that include ``x`` (in place, or into
-    ``new_state``).  Returns ``y``."""
+    ``new_state``).  ``batch * channels`` is at most 2^31 - 1.  Returns ``y``."""
     a = _conv_args(x, weight, bias, None, None, silu, True)
     shape = (a.batch, a.width - 1, a.channels)
     dev = x.get_device()
@@ -279,7 +280,8 @@ def selective_scan_step(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, sof
                         new_state=None, out=None, stream=None):
     """One token of ``selective_scan``: ``x``, ``dt``, ``z`` are ``[batch, channels]``, ``B``
     and ``C`` ``[batch, groups, states]``; ``state`` (float32 ``[batch, channels, states]``)
-    moves on in place, or into ``new_state``.  Returns ``y``."""
+    moves on in place, or into ``new_state``.  ``batch * channels`` is at most 2^27 - 1.
+    Returns ``y``."""
     a = _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, None, None, True)
     shape = (a.batch, a.channels, a.states)
     dev = x.get_device()
