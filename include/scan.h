@@ -2,8 +2,8 @@
  * scan.h - C ABI of the stream_compaction_amd library (libscan_amd.so):
  * row-wise prefix scan, device-wide exclusive and inclusive scan, device-wide
  * reduction, reduce-by-key, radix sort and stream compaction, and the sequence
- * operators built on them (causal convolution, selective scan, token
- * embedding), on one AMD Instinct MI355X (gfx950).
+ * operators built on them (causal convolution, selective and gated scan, token
+ * embedding, beam search), on one AMD Instinct MI355X (gfx950).
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -278,15 +278,15 @@ scan_status select_compact_devn(const void* in, const uint8_t* flags, void* out,
                                 void* scratch, size_t scratch_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
- * Sequence operators: the scan whose combine is an affine map (the selective
- * state space scan), the short causal convolution that stands before it, and
- * the token embedding whose gradient is a sorted segmented sum.  They share
+ * Sequence operators: the scans whose combine is an affine map (the selective
+ * state space scan, the gated scan), the short causal convolution that stands
+ * before them, and the token embedding whose gradient is a sorted segmented sum.  They share
  * the conventions above, and:
  *  - Activations are [batch, length, channels] of one `dtype` (SCAN_F32,
  *    SCAN_F16 or SCAN_BF16, else SCAN_ENOTSUP) with contiguous channels;
  *    inputs may have any non-negative batch and token strides (in elements; 0
  *    repeats), the arrays a call writes are contiguous.  Parameters and states
- *    of the scan are contiguous float32.  All arithmetic and every sum is
+ *    of the scans are contiguous float32.  All arithmetic and every sum is
  *    float32; each output is rounded once, to nearest even.
  *  - Inputs may overlap one another; outputs and scratch overlap nothing
  *    (SCAN_EALIAS), but a step may update its state in place.
@@ -426,6 +426,71 @@ scan_status selective_scan_grad(const selective_scan_args* args, const selective
  * INT32_MAX / 16, else SCAN_EINVAL. */
 scan_status selective_scan_step(const selective_scan_args* args, const float* state,
                                 float* new_state, void* y, void* stream);
+
+/*
+ * Gated scan: one state per channel, moved by gates that depend on the token.
+ * With s = sigmoid(forget[b,t,c]) and v = sigmoid(input_gate[b,t,c]) (1 when
+ * input_gate is NULL):
+ *   rate NULL:  a = s,  w = 1 - s                           (a convex average)
+ *   rate:       a = exp(-rate[c] s),  w = sqrt(1 - a^2)     (a normalised one)
+ *   h = a h + w v x[b,t,c],   y[b,t,c] = h z sigmoid(z)  (y = h when z is NULL).
+ *   x, forget, input_gate, z   activations, each with its {batch, token} strides
+ *   rate           float32 [channels]; a rate below 0 counts as 0, which holds
+ *                  the state and takes no input
+ *   initial_state  float32 [batch, channels], h before t = 0 (NULL: zeros)
+ * The state is float32 throughout.
+ */
+typedef struct {
+    const void* x;
+    const void* forget;
+    const void* input_gate;
+    const void* z;
+    const float* rate;
+    const float* initial_state;
+    const int32_t* lengths;
+    int64_t batch, length, channels;
+    int64_t x_stride[2], forget_stride[2], input_gate_stride[2], z_stride[2];
+    scan_dtype dtype;
+} gated_scan_args;
+
+/* y: [batch, length, channels].  final_state: float32 [batch, channels] (NULL:
+ * not written).  starts (NULL: not written): what the gradient needs,
+ * gated_scan_starts_bytes(args) bytes, the states before each block of 64 tokens.
+ * Scratch carries the state between workgroups that share a sequence (0 bytes for
+ * short ones: then scratch may be NULL). */
+size_t gated_scan_starts_bytes(const gated_scan_args* args);
+size_t gated_scan_scratch_bytes(const gated_scan_args* args);
+scan_status gated_scan(const gated_scan_args* args, void* y, float* final_state, float* starts,
+                       void* scratch, size_t scratch_bytes, void* stream);
+
+/* Gradients of a forward call with the same args that wrote `starts`, from dy
+ * (strides {batch, token}) and dfinal (of final_state's shape; NULL: zeros).
+ * dx, dforget, dinput_gate and dz: [batch, length, channels] of dtype, the last
+ * two required exactly when their input is given; drate: float32 [channels],
+ * likewise (0 for a rate of 0 and below, where w has no derivative); dinitial:
+ * float32 [batch, channels], not written when NULL. */
+typedef struct {
+    const void* dy;
+    int64_t dy_stride[2];
+    const float* dfinal;
+    const float* starts;
+    void* dx;
+    void* dforget;
+    void* dinput_gate;
+    void* dz;
+    float* drate;
+    float* dinitial;
+} gated_scan_grads;
+size_t gated_scan_grad_scratch_bytes(const gated_scan_args* args);
+scan_status gated_scan_grad(const gated_scan_args* args, const gated_scan_grads* grads,
+                            void* scratch, size_t scratch_bytes, void* stream);
+
+/* One token per sequence: x, forget, input_gate and z are [batch, channels]
+ * (token strides, length, lengths and initial_state are not used).  state and
+ * new_state are float32 [batch, channels] and either the same array or disjoint;
+ * y is [batch, channels].  batch * channels <= INT32_MAX, else SCAN_EINVAL. */
+scan_status gated_scan_step(const gated_scan_args* args, const float* state, float* new_state,
+                            void* y, void* stream);
 
 /*
  * Token embedding: out[i,:] = scale * weight[ids[i],:]; an id outside [0, rows)

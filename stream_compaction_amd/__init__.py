@@ -37,8 +37,8 @@ Entry points (same names as the C ABI):
 
 Sequence operators (module ``sequence``, reached by the same names from here; each
 described there): ``causal_conv``, ``causal_conv_grad``, ``causal_conv_step``,
-``selective_scan``, ``selective_scan_grad``, ``selective_scan_step``, ``embedding``,
-``embedding_grad``; module ``autograd`` has the differentiable forms.
+``selective_scan``, ``selective_scan_grad``, ``selective_scan_step``, ``gated_scan``,
+``gated_scan_grad``, ``gated_scan_step``, ``embedding``, ``embedding_grad``; module ``autograd`` has the differentiable forms.
 """
 import ctypes
 import os
@@ -60,12 +60,15 @@ EXPORTS = ("scan_rows", "scan_device", "scan_device_inclusive", "scan_device_scr
            "causal_conv_grad", "causal_conv_grad_scratch_bytes", "causal_conv_step",
            "selective_scan", "selective_scan_starts_bytes", "selective_scan_split",
            "selective_scan_split_scratch_bytes", "selective_scan_grad",
-           "selective_scan_grad_scratch_bytes", "selective_scan_step", "embedding",
+           "selective_scan_grad_scratch_bytes", "selective_scan_step", "gated_scan",
+           "gated_scan_starts_bytes", "gated_scan_scratch_bytes", "gated_scan_grad",
+           "gated_scan_grad_scratch_bytes", "gated_scan_step", "embedding",
            "embedding_grad", "embedding_grad_scratch_bytes", "scan_status_str",
            "scan_last_hip_error")
 # entry points whose wrappers live in the module `sequence`, loaded on first use
 _SEQUENCE = ("causal_conv", "causal_conv_grad", "causal_conv_step", "selective_scan",
-             "selective_scan_grad", "selective_scan_step", "embedding", "embedding_grad")
+             "selective_scan_grad", "selective_scan_step", "gated_scan", "gated_scan_grad",
+             "gated_scan_step", "embedding", "embedding_grad")
 
 _lib = None
 

@@ -25,10 +25,24 @@ class ScanGrads(ctypes.Structure):
                 ("dD", _vp), ("ddt_bias", _vp), ("dinitial", _vp)]
 
 
+class GatedArgs(ctypes.Structure):
+    _fields_ = [("x", _vp), ("forget", _vp), ("input_gate", _vp), ("z", _vp), ("rate", _vp),
+                ("initial_state", _vp), ("lengths", _vp), ("batch", _i64), ("length", _i64),
+                ("channels", _i64), ("x_stride", _i64 * 2), ("forget_stride", _i64 * 2),
+                ("input_gate_stride", _i64 * 2), ("z_stride", _i64 * 2), ("dtype", _i32)]
+
+
+class GatedGrads(ctypes.Structure):
+    _fields_ = [("dy", _vp), ("dy_stride", _i64 * 2), ("dfinal", _vp), ("starts", _vp),
+                ("dx", _vp), ("dforget", _vp), ("dinput_gate", _vp), ("dz", _vp), ("drate", _vp),
+                ("dinitial", _vp)]
+
+
 def declare(L):
     """C signatures of the sequence entry points on a loaded library."""
     sz, f32 = ctypes.c_size_t, ctypes.c_float
     conv, scan = ctypes.POINTER(ConvArgs), ctypes.POINTER(ScanArgs)
+    gated = ctypes.POINTER(GatedArgs)
     for name, args in (
             ("causal_conv", [conv, _vp, _vp, _vp]),
             ("causal_conv_grad", [conv, _vp, ctypes.POINTER(_i64), _vp, _vp, _vp, _vp, _vp, _vp,
@@ -38,6 +52,9 @@ def declare(L):
             ("selective_scan_split", [scan, _vp, _vp, _vp, _vp, sz, _vp]),
             ("selective_scan_grad", [scan, ctypes.POINTER(ScanGrads), _vp, sz, _vp]),
             ("selective_scan_step", [scan, _vp, _vp, _vp, _vp]),
+            ("gated_scan", [gated, _vp, _vp, _vp, _vp, sz, _vp]),
+            ("gated_scan_grad", [gated, ctypes.POINTER(GatedGrads), _vp, sz, _vp]),
+            ("gated_scan_step", [gated, _vp, _vp, _vp, _vp]),
             ("embedding", [_vp, _vp, _vp, _i64, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int, f32,
                            _vp]),
             ("embedding_grad", [_vp, _vp, _vp, _i64, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int,
@@ -48,6 +65,9 @@ def declare(L):
                        ("selective_scan_starts_bytes", [scan]),
                        ("selective_scan_split_scratch_bytes", [scan]),
                        ("selective_scan_grad_scratch_bytes", [scan]),
+                       ("gated_scan_starts_bytes", [gated]),
+                       ("gated_scan_scratch_bytes", [gated]),
+                       ("gated_scan_grad_scratch_bytes", [gated]),
                        ("embedding_grad_scratch_bytes", [_i64, _i64, _i64])):
         getattr(L, name).argtypes = args
         getattr(L, name).restype = sz

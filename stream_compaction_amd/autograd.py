@@ -1,7 +1,7 @@
 """The sequence operators for torch's automatic differentiation.
 
-``causal_conv``, ``selective_scan`` and ``embedding`` take the arguments of the functions of
-these names in ``stream_compaction_amd.sequence`` and can be differentiated with respect to
+``causal_conv``, ``selective_scan``, ``gated_scan`` and ``embedding`` take the arguments of the
+functions of these names in ``stream_compaction_amd.sequence`` and can be differentiated with respect to
 every floating input, through the output and the final state.  Both directions run in the
 library's kernels on the current stream; work space comes from torch's allocator, so a
 forward and backward pass can be captured into a HIP graph.  Gradients are taken once, in
@@ -66,6 +66,31 @@ class _SelectiveScan(torch.autograd.Function):
                 g["dstate"] if ctx.has_state else None, None, None, None)
 
 
+class _GatedScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, forget, rate, input_gate, z, initial_state, lengths, recording):
+        ctx.set_materialize_grads(False)
+        more = {"rate": rate, "input_gate": input_gate, "z": z, "lengths": lengths}
+        # (an input that requires a gradient is said to need one under no_grad, too)
+        if not (recording and any(ctx.needs_input_grad)):
+            return _ops.gated_scan(x, forget, initial_state=initial_state, **more)
+        y, state, starts = _ops.gated_scan(x, forget, initial_state=initial_state,
+                                           keep_starts=True, **more)
+        ctx.save_for_backward(x, forget, rate, input_gate, z, lengths, starts)
+        ctx.has_state = initial_state is not None
+        return y, state
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dfinal):
+        x, forget, rate, input_gate, z, lengths, starts = ctx.saved_tensors
+        g = _ops.gated_scan_grad(_rows(dy, x), x, forget, starts, rate=rate,
+                                 input_gate=input_gate, z=z, lengths=lengths,
+                                 dfinal=_dense(dfinal))
+        return (g["dx"], g["dforget"], g["drate"], g["dinput_gate"], g["dz"],
+                g["dstate"] if ctx.has_state else None, None, None)
+
+
 class _Embedding(torch.autograd.Function):
     @staticmethod
     def forward(ctx, weight, ids, scale):
@@ -90,6 +115,12 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=False,
     """Differentiable ``sequence.selective_scan``: ``(y, final_state)``."""
     return _SelectiveScan.apply(x, dt, A, B, C, D, z, dt_bias, initial_state, lengths,
                                 bool(softplus), torch.is_grad_enabled())
+
+
+def gated_scan(x, forget, rate=None, input_gate=None, z=None, initial_state=None, lengths=None):
+    """Differentiable ``sequence.gated_scan``: ``(y, final_state)``."""
+    return _GatedScan.apply(x, forget, rate, input_gate, z, initial_state, lengths,
+                            torch.is_grad_enabled())
 
 
 def embedding(weight, ids, scale=1.0):

@@ -1,0 +1,58 @@
+// The gated scan's gates, shared by its forward, gradient and step.
+//
+// With s = sigmoid(forget) a token moves a channel's state by h = a h + w v x,
+// where v = sigmoid(input_gate) (1 without one) and
+//   without rates  a = s, w = 1 - s                        (a convex average),
+//   with a rate r  p = r s, a = exp(-p), w = sqrt(1 - a^2)  (a normalised one).
+// A rate below 0 counts as 0: the state is held and takes no input.
+#pragma once
+
+#include "sequence.hpp"
+
+namespace sca {
+
+// sigmoid(v) and sigmoid(-v), each to a few units in its last place: 1 minus a
+// rounded sigmoid would lose the digits of the smaller one.
+struct Sides { float up, down; };
+__device__ __forceinline__ Sides sides(float v) {
+  const float e = exp2_hw(-__builtin_fabsf(v) * kLog2e);   // in (0, 1]
+  const float r = rcp_hw(1.0f + e), er = e * r;
+  return v >= 0.0f ? Sides{r, er} : Sides{er, r};
+}
+
+// 1 - exp(-t) for t >= 0, exp(-t) = q being known.  Below 1/2, where the
+// difference loses digits, a polynomial of (1 - exp(-t)) / t that is within 8e-8
+// of it (least maximum of the relative error, fitted on [0, 1/2]).
+__device__ __forceinline__ float one_minus_exp(float t, float q) {
+  float s = __builtin_fmaf(t, 0.00677103782f, -0.0410012789f);
+  s = __builtin_fmaf(t, s, 0.166548148f);
+  s = __builtin_fmaf(t, s, -0.49999249f);
+  s = __builtin_fmaf(t, s, 0.99999994f);
+  return t < 0.5f ? t * s : 1.0f - q;
+}
+
+// What a token's gate does: decay a, log2 of it, the input's weight w.
+struct Gate { float a, log_a, w; };
+
+// nr: -log2(e) times the rate, at most 0 (unused without rates).
+template <bool RATE>
+__device__ __forceinline__ Gate gate(float forget, float nr) {
+  Gate g;
+  if constexpr (RATE) {
+    g.log_a = nr * sigmoid(forget);
+    g.a = exp2_hw(g.log_a);
+    g.w = __builtin_amdgcn_sqrtf(one_minus_exp(g.log_a * (-2.0f * kLn2), g.a * g.a));
+  } else {
+    const Sides s = sides(forget);
+    g.a = s.up;
+    g.w = s.down;
+    // log2 sigmoid(v) = min(v, 0) log2(e) - log2(1 + exp(-|v|))
+    g.log_a = __builtin_amdgcn_logf(s.up);
+  }
+  return g;
+}
+
+// -log2(e) r of a rate, a negative one counting as 0 (a NaN stays one).
+__device__ __forceinline__ float rate_log2(float r) { return at_least(r, 0.0f) * -kLog2e; }
+
+}  // namespace sca

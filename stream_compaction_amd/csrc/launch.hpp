@@ -117,6 +117,50 @@ hipError_t launch_embedding_grad(const void* dout, const void* ids, bool wide_id
                                  int64_t row_stride, Fmt fmt, Fmt out_fmt, float scale,
                                  void* scratch, hipStream_t stream);
 
+// The gated scan.
+struct GatedProblem {
+  const void *x, *forget, *input_gate, *z;   // the last two may be null
+  const float* rate;                // [channels] or null (a convex average)
+  const float* initial_state;       // [batch, channels] or null (zeros)
+  const int32_t* lengths;           // [batch] or null
+  int64_t batch, length, channels;
+  int64_t x_batch, x_token, forget_batch, forget_token, input_batch, input_token, z_batch, z_token;
+};
+// The forward keeps the state before every so many tokens for the gradient.
+constexpr int kGatedKeepTokens = 64;
+size_t gated_scan_scratch(const GatedProblem& p);        // 0: none needed
+hipError_t launch_gated_scan(const GatedProblem& p, Fmt fmt, void* y, float* final_state,
+                             float* starts, void* scratch, hipStream_t stream);
+struct GatedGrads {
+  const void* dy;
+  int64_t dy_batch, dy_token;
+  const float* dfinal;              // [batch, channels] or null
+  const float* starts;
+  void *dx, *dforget, *dinput_gate, *dz;   // the last two null without their input
+  float *drate, *dinitial;          // drate null without rates; dinitial may be null
+};
+size_t gated_scan_grad_scratch(const GatedProblem& p);
+hipError_t launch_gated_scan_grad(const GatedProblem& p, Fmt fmt, const GatedGrads& g,
+                                  void* scratch, hipStream_t stream);
+hipError_t launch_gated_scan_step(const GatedProblem& p, Fmt fmt, const float* state,
+                                  float* new_state, void* y, hipStream_t stream);
+
+// Beam search: the `count` best of batch x [beams, vocab] continuations, and the
+// states' rows moved to their new beams.
+struct BeamProblem {
+  const void* logits;
+  const float* scores;              // [batch, beams]
+  const uint8_t* finished;          // [batch, beams] or null
+  int64_t batch, beams, vocab, count, end_token;
+  int64_t logits_batch, logits_beam;
+};
+size_t beam_select_scratch(const BeamProblem& p, Fmt fmt);
+hipError_t launch_beam_select(const BeamProblem& p, Fmt fmt, float* scores, int32_t* parents,
+                              int32_t* tokens, void* scratch, hipStream_t stream);
+hipError_t launch_beam_reorder(const void* const* states, void* const* new_states,
+                               const int64_t* row_bytes, int64_t tensors, const int32_t* parents,
+                               int64_t batch, int64_t beams, hipStream_t stream);
+
 // Scratch of the look-back kernels holds only the tile descriptors, one per
 // 128-byte line (kDescBytes), whose used words are zeroed at the start of
 // every call by a small fill kernel (no hipMemsetAsync, so the call can sit

@@ -1,11 +1,11 @@
-"""Sequence operators of the library: causal convolution, selective scan and token
-embedding, each with its gradient, and the first two with their single-token step.
+"""Sequence operators of the library: causal convolution, selective scan, gated scan and token
+embedding, each with its gradient, and the first three with their single-token step.
 
 Thin wrappers over the C ABI (``include/scan.h`` has every definition and rule): they
 check shapes, types and devices, allocate what is not given, and pass pointers, strides and
 the current HIP stream, which must be of the data's GPU (as must a ``stream`` that is
 given).  Activations are ``[batch, length, channels]`` float32, float16 or bfloat16 tensors
-with contiguous channels; parameters and the scan's states are float32.
+with contiguous channels; parameters and the scans' states are float32.
 ``stream_compaction_amd.autograd`` has the same operators for torch's automatic
 differentiation.
 """
@@ -14,7 +14,7 @@ import ctypes
 import torch
 
 from . import DTYPE_CODES, check, lib
-from ._sequence_abi import ConvArgs, ScanArgs, ScanGrads
+from ._sequence_abi import ConvArgs, GatedArgs, GatedGrads, ScanArgs, ScanGrads
 
 _ACT = {torch.float32: DTYPE_CODES["f32"], torch.float16: DTYPE_CODES["f16"],
         torch.bfloat16: DTYPE_CODES["bf16"]}
@@ -289,6 +289,107 @@ def selective_scan_step(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, sof
     np_ = sp if new_state is None else _like(new_state, "new_state", shape, torch.float32, dev)
     y = _out(out, "out", x.shape, x.dtype, x, stream)
     check(lib().selective_scan_step(a, sp, np_, y.data_ptr(), _queue(stream, dev)))
+    return y
+
+
+def _gated_args(x, forget, rate, input_gate, z, initial_state, lengths, step):
+    if x.dim() != (2 if step else 3):
+        raise ValueError("x must be [batch, channels]" if step else
+                         "x must be [batch, length, channels]")
+    _require(x.is_cuda, "x must be a GPU tensor")
+    code = _code(x, "x")
+    dev, ty, shape, f32 = x.get_device(), x.dtype, x.shape, torch.float32
+    b, d = shape[0], shape[-1]
+    # (shapes before strides: an argument of another rank has not as many)
+    xp, fp = _rows(x, "x", shape, ty, dev), _rows(forget, "forget", shape, ty, dev)
+    ip = None if input_gate is None else _rows(input_gate, "input_gate", shape, ty, dev)
+    zp = None if z is None else _rows(z, "z", shape, ty, dev)
+
+    def strides(t):
+        if t is None:
+            return (0, 0)
+        return (t.stride(0), 0) if step else t.stride()[:2]
+
+    return GatedArgs(
+        xp, fp, ip, zp, None if rate is None else _like(rate, "rate", (d,), f32, dev),
+        None if initial_state is None else
+        _like(initial_state, "initial_state", (b, d), f32, dev),
+        None if lengths is None else _like(lengths, "lengths", (b,), torch.int32, dev),
+        b, 1 if step else shape[1], d, strides(x), strides(forget), strides(input_gate),
+        strides(z), code)
+
+
+def gated_scan(x, forget, rate=None, input_gate=None, z=None, initial_state=None, lengths=None,
+               keep_starts=False, out=None, final_state=None, scratch=None, stream=None):
+    """Gated scan: one state per channel, moved by gates that depend on the token.
+
+    ``x``, ``forget`` and, when given, ``input_gate`` and the output gate ``z`` are ``[batch,
+    length, channels]``.  With ``s = sigmoid(forget)`` and ``v = sigmoid(input_gate)`` (1
+    without one), the state moves by ``h = a h + w v x`` and ``y = h silu(z)``, where
+
+    * without ``rate``: ``a = s`` and ``w = 1 - s``, a convex average;
+    * with ``rate`` (float32 ``[channels]``, 0 or greater): ``a = exp(-rate s)`` and ``w =
+      sqrt(1 - a^2)``, which keeps the state's variance at the input's.
+
+    Returns ``(y, final_state)``, the state float32 ``[batch, channels]``; with
+    ``keep_starts`` also what ``gated_scan_grad`` needs of this call.
+    """
+    a = _gated_args(x, forget, rate, input_gate, z, initial_state, lengths, False)
+    y = _out(out, "out", x.shape, x.dtype, x, stream)
+    f32 = torch.float32
+    fs = _out(final_state, "final_state", (a.batch, a.channels), f32, x, stream)
+    L = lib()
+    starts = None
+    if keep_starts:
+        starts = _new((L.gated_scan_starts_bytes(a) // 4,), f32, fs, stream)
+    sp = None if starts is None else starts.data_ptr()
+    need = L.gated_scan_scratch_bytes(a)
+    scratch_p, room = None, 0
+    if need or scratch is not None:
+        scratch, room = _scratch(scratch, need, fs, stream)
+        scratch_p = scratch.data_ptr()
+    check(L.gated_scan(a, y.data_ptr(), fs.data_ptr(), sp, scratch_p, room,
+                       _queue(stream, x.get_device())))
+    return (y, fs, starts) if keep_starts else (y, fs)
+
+
+def gated_scan_grad(dy, x, forget, starts, rate=None, input_gate=None, z=None, lengths=None,
+                    dfinal=None, scratch=None, stream=None):
+    """Gradients of ``gated_scan`` called with the same arguments and ``keep_starts``, from
+    ``dy`` (and ``dfinal``, of the final state): a dict with ``dx``, ``dforget``, ``drate``,
+    ``dinput_gate``, ``dz`` (None where that input is) and ``dstate`` (of the initial state).
+    A rate of 0 or below, where the weight has no derivative, gets a gradient of 0."""
+    a = _gated_args(x, forget, rate, input_gate, z, None, lengths, False)
+    dev, ty, f32 = x.get_device(), x.dtype, torch.float32
+    L = lib()
+    dyp = _rows(dy, "dy", x.shape, ty, dev)
+    df = _opt(dfinal, "dfinal", (a.batch, a.channels), f32, dev)
+    sp = _like(starts, "starts", (L.gated_scan_starts_bytes(a) // 4,), f32, dev)
+    out = {"dx": _new(x.shape, ty, x, stream), "dforget": _new(x.shape, ty, x, stream),
+           "drate": None if rate is None else _new(rate.shape, f32, rate, stream),
+           "dinput_gate": None if input_gate is None else _new(x.shape, ty, x, stream),
+           "dz": None if z is None else _new(x.shape, ty, x, stream),
+           "dstate": _new((a.batch, a.channels), f32, starts, stream)}
+    p = {k: None if v is None else v.data_ptr() for k, v in out.items()}
+    g = GatedGrads(dyp, dy.stride()[:2], df, sp, p["dx"], p["dforget"], p["dinput_gate"], p["dz"],
+                   p["drate"], p["dstate"])
+    scratch, room = _scratch(scratch, L.gated_scan_grad_scratch_bytes(a), starts, stream)
+    check(L.gated_scan_grad(a, g, scratch.data_ptr(), room, _queue(stream, dev)))
+    return out
+
+
+def gated_scan_step(state, x, forget, rate=None, input_gate=None, z=None, new_state=None, out=None,
+                    stream=None):
+    """One token of ``gated_scan``: ``x``, ``forget``, ``input_gate`` and ``z`` are ``[batch,
+    channels]``; ``state`` (float32 ``[batch, channels]``) moves on in place, or into
+    ``new_state``.  ``batch * channels`` is at most 2^31 - 1.  Returns ``y``."""
+    a = _gated_args(x, forget, rate, input_gate, z, None, None, True)
+    shape = (a.batch, a.channels)
+    dev = x.get_device()
+    sp = _like(state, "state", shape, torch.float32, dev)
+    np_ = sp if new_state is None else _like(new_state, "new_state", shape, torch.float32, dev)
+    y = _out(out, "out", x.shape, x.dtype, x, stream)
+    check(lib().gated_scan_step(a, sp, np_, y.data_ptr(), _queue(stream, dev)))
     return y
 
 
