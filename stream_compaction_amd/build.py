@@ -39,7 +39,9 @@ CFLAGS = [
 # Pairing float operations into vectors gains nothing without packed instructions, and
 # keeps broadcasts across lanes from folding into the products that use them.
 FILE_FLAGS = {"selective_scan.hip": ["-fno-slp-vectorize"],
-              "selective_scan_grad.hip": ["-fno-slp-vectorize"]}
+              "selective_scan_grad.hip": ["-fno-slp-vectorize"],
+              "gated_scan.hip": ["-fno-slp-vectorize"],
+              "gated_scan_grad.hip": ["-fno-slp-vectorize"]}
 
 
 def compile_cmd(src, obj, defines=()):

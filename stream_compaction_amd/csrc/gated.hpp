@@ -28,7 +28,9 @@ __device__ __forceinline__ float one_minus_exp(float t, float q) {
   s = __builtin_fmaf(t, s, 0.166548148f);
   s = __builtin_fmaf(t, s, -0.49999249f);
   s = __builtin_fmaf(t, s, 0.99999994f);
-  return t < 0.5f ? t * s : 1.0f - q;
+  s *= t;
+  materialize(s);                            // a select, not a branch around the polynomial
+  return t < 0.5f ? s : 1.0f - q;
 }
 
 // What a token's gate does: decay a, log2 of it, the input's weight w.

@@ -2,12 +2,212 @@
 //
 //   h[t] = a[t] h[t-1] + w[t] v[t] x[t],  y = h silu(z)      (gates: gated.hpp)
 //
-// A thread per channel walks its sequence's tokens in order.
-#include "gated.hpp"
+// One pass: a workgroup reads its tile of 128 tokens by 128 channels once, finds the
+// state that enters it from the tiles before (gated_tile.hpp), and walks its tokens.
+#include "gated_tile.hpp"
 
 namespace sca {
 
-constexpr int64_t kMaxGroups = 1ll << 21;    // workgroups per launch
+constexpr int kFwdTokens = 16;                              // of a wave
+constexpr int kFwdTile = kFwdTokens * kTileWaves;           // of a workgroup
+static_assert(kGatedKeepTokens % kFwdTokens == 0, "a kept state is a wave's first");
+
+template <class F, bool RATE, bool IG, bool Z, bool ODD>
+__global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(4, 4)))
+void gated_scan_kernel(GatedProblem p, void* yv, float* final_state, float* starts, uint64_t* scratch,
+                       Tiles tiles) {
+  using S = typename F::S;
+  using PIO = PairIO<F, ODD>;
+  using Raw = typename PIO::Raw;
+  constexpr int T = kFwdTokens;
+  constexpr int eb = sizeof(S);
+  constexpr bool kLateZ = sizeof(S) == 4;    // four float32 inputs at once have no room in registers
+  __shared__ TileMaps sh;
+  const int wave = wave_id();
+  const int D = (int)p.channels;
+  const int64_t tile = tiles.chunks > 1 ? next_tile(scratch, &sh.tile) : blockIdx.x;
+  if (tile >= tiles.count()) return;
+  int64_t col, part;
+  const int64_t chunk = divide(tile, tiles.cols, &col);
+  const int64_t b = tiles.b0 + divide(col, tiles.parts, &part);
+  const int ch = (int)part * kTileChannels + 2 * lane_id();
+  const int have = D - ch >= 2 ? 2 : (D - ch == 1 ? 1 : 0);
+  // lanes past the last channel work on the last one (pair), unheard
+  const int c0 = ODD ? (ch < D ? ch : D - 1) : (ch < D ? ch : D - 2);
+  const int c1 = ch + 1 < D ? ch + 1 : D - 1;
+  const uint32_t o0 = (uint32_t)c0 * eb, o1 = (uint32_t)c1 * eb;
+  const int64_t n = p.lengths == nullptr ? p.length : live_count(p.length, p.lengths + b);
+  const int64_t t0 = chunk * kFwdTile + wave * T;          // this wave's first token
+  uintptr_t yrow = (uintptr_t)yv + ((b * p.length + t0) * D) * eb;
+  float h[2] = {0.0f, 0.0f};
+  if (p.initial_state != nullptr) {
+    h[0] = p.initial_state[b * D + c0];
+    h[1] = p.initial_state[b * D + c1];
+  }
+  const int room = (int)(p.length - t0 < T ? p.length - t0 : T);   // tokens of the output
+  if (chunk * kFwdTile >= n) {                             // no token of this tile exists
+    for (int k = 0; k < room; ++k, yrow += D * eb) PIO::store(yrow, o0, PIO::splat(0.0f), have);
+    if (chunk == 0 && wave == 0 && final_state != nullptr) {
+      if (have > 0) final_state[b * D + ch] = h[0];
+      if (have > 1) final_state[b * D + ch + 1] = h[1];
+    }
+    return;
+  }
+  const int count = (int)(n - t0 <= 0 ? 0 : (n - t0 < T ? n - t0 : T));
+  // (past the last token it is read again)
+  const int64_t first_token = count > 0 ? t0 : n - 1;
+  Rows ax((uintptr_t)p.x, p.x_batch, p.x_token, b, first_token, eb);
+  Rows af((uintptr_t)p.forget, p.forget_batch, p.forget_token, b, first_token, eb);
+  Rows ai((uintptr_t)p.input_gate, p.input_batch, p.input_token, b, first_token, eb);
+  Rows az((uintptr_t)p.z, p.z_batch, p.z_token, b, first_token, eb);
+  Raw rx[T], rf[T], ri[IG ? T : 1], rz[Z ? T : 1];
+#pragma unroll
+  for (int k = 0; k < T; ++k) {
+    rx[k] = PIO::load(ax.at, o0, o1);
+    rf[k] = PIO::load(af.at, o0, o1);
+    if constexpr (IG) ri[k] = PIO::load(ai.at, o0, o1);
+    if constexpr (Z && !kLateZ) rz[k] = PIO::load(az.at, o0, o1);
+    const bool more = k + 1 < count;
+    ax.next(more);
+    af.next(more);
+    ai.next(more);
+    if constexpr (!kLateZ) az.next(more);
+  }
+  float nr[2] = {0.0f, 0.0f};
+  if constexpr (RATE) {
+    nr[0] = rate_log2(p.rate[c0]);
+    nr[1] = rate_log2(p.rate[c1]);
+  }
+  if (count < T) {                                       // tokens that do not exist: a = 1, u = 0
+#pragma unroll
+    for (int k = 0; k < T; ++k) {
+      if (k < count) continue;
+      rx[k] = PIO::splat(0.0f);
+      rf[k] = PIO::splat(RATE ? -__builtin_huge_valf() : __builtin_huge_valf());
+      if constexpr (IG) ri[k] = PIO::splat(0.0f);
+    }
+  }
+  float a[T][2], u[T][2], l[2] = {0.0f, 0.0f}, least[2] = {1.0f, 1.0f}, last[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int k = 0; k < T; ++k) {
+    float x[2], f[2], v[2];
+    PIO::IO::unpack(rx[k], x);
+    PIO::IO::unpack(rf[k], f);
+    if constexpr (IG) PIO::IO::unpack(ri[k], v);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const Gate g = gate<RATE>(f[c], nr[c]);
+      a[k][c] = g.a;
+      u[k][c] = g.w * x[c];
+      if constexpr (IG) u[k][c] *= sigmoid(v[c]);
+      l[c] += g.log_a;
+      least[c] = __builtin_fminf(least[c], g.a);
+      last[c] = __builtin_fmaf(g.a, last[c], u[k][c]);
+    }
+    // token after token: left alone, the compiler starts many at once and runs out
+    // of registers
+    __builtin_amdgcn_sched_barrier(0);
+  }
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+    if (least[c] == 0.0f) l[c] = -__builtin_huge_valf();
+  if constexpr (Z && kLateZ) {
+#pragma unroll
+    for (int k = 0; k < T; ++k) {
+      rz[k] = PIO::load(az.at, o0, o1);
+      az.next(k + 1 < count);
+    }
+  }
+  put2(sh.l[wave], l[0], l[1]);
+  put2(sh.m[wave], half_decay(l[0]), half_decay(l[1]));
+  put2(sh.b[wave], last[0], last[1]);
+  lds_barrier();
+  if (tiles.chunks > 1) {
+    const float first[2] = {h[0], h[1]};
+    tile_entry(sh, wave, chunk, (n + kFwdTile - 1) / kFwdTile, col, tiles.cols, scratch,
+               tiles.chunks, first, h);
+  }
+  wave_entry(sh, wave, h);
+  if (starts != nullptr && t0 % kGatedKeepTokens == 0 && t0 < n) {
+    const int64_t blocks = (p.length + kGatedKeepTokens - 1) / kGatedKeepTokens;
+    float* at = starts + (b * blocks + t0 / kGatedKeepTokens) * D + ch;
+    if (have > 0) at[0] = h[0];
+    if (have > 1) at[1] = h[1];
+  }
+#pragma unroll
+  for (int k = 0; k < T; ++k) {
+    float y[2], z[2];
+    if constexpr (Z) PIO::IO::unpack(rz[k], z);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      h[c] = __builtin_fmaf(a[k][c], h[c], u[k][c]);
+      y[c] = h[c];
+      if constexpr (Z) y[c] *= silu(z[c]);
+      if (k >= count) y[c] = 0.0f;
+    }
+    if (k < room) PIO::store(yrow, o0, PIO::IO::pack(y), have);
+    yrow += D * eb;
+  }
+  if (final_state != nullptr && count > 0 && t0 + count == n) {
+    if (have > 0) final_state[b * D + ch] = h[0];
+    if (have > 1) final_state[b * D + ch + 1] = h[1];
+  }
+}
+
+__global__ __launch_bounds__(256) void tile_clear_kernel(uint64_t* scratch, int64_t words) {
+  typedef uint64_t two __attribute__((ext_vector_type(2)));
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < words / 2; i += (int64_t)gridDim.x * 256)
+    *gptr<two>((uintptr_t)(scratch + 2 * i)) = i == 0 ? two{0, 0} : two{~0ull, ~0ull};
+}
+
+hipError_t launch_tile_clear(uint64_t* scratch, int64_t words, hipStream_t stream) {
+  const int64_t blocks = (words / 2 + 255) / 256;
+  tile_clear_kernel<<<dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), 0, stream>>>(scratch, words);
+  return hipGetLastError();
+}
+
+size_t gated_scan_scratch(const GatedProblem& p) { return (size_t)gated_tiles(p, kFwdTile).words() * 8; }
+
+template <class F, bool RATE, bool IG, bool Z>
+static hipError_t launch_gated_z(const GatedProblem& p, void* y, float* final_state, float* starts,
+                                 uint64_t* scratch, hipStream_t stream) {
+  return launch_tiles(gated_tiles(p, kFwdTile), p.batch, scratch, stream, [&](dim3 grid, const Tiles& t) {
+    if (p.channels % 2 == 0)
+      gated_scan_kernel<F, RATE, IG, Z, false><<<grid, dim3(kTileThreads), 0, stream>>>(
+          p, y, final_state, starts, scratch, t);
+    else
+      gated_scan_kernel<F, RATE, IG, Z, true><<<grid, dim3(kTileThreads), 0, stream>>>(
+          p, y, final_state, starts, scratch, t);
+  });
+}
+
+template <class F, bool RATE>
+static hipError_t launch_gated_r(const GatedProblem& p, void* y, float* final_state, float* starts,
+                                 uint64_t* s, hipStream_t stream) {
+  if (p.input_gate != nullptr)
+    return p.z != nullptr ? launch_gated_z<F, RATE, true, true>(p, y, final_state, starts, s, stream)
+                          : launch_gated_z<F, RATE, true, false>(p, y, final_state, starts, s, stream);
+  return p.z != nullptr ? launch_gated_z<F, RATE, false, true>(p, y, final_state, starts, s, stream)
+                        : launch_gated_z<F, RATE, false, false>(p, y, final_state, starts, s, stream);
+}
+
+template <class F>
+static hipError_t launch_gated_f(const GatedProblem& p, void* y, float* final_state, float* starts,
+                                 void* scratch, hipStream_t stream) {
+  return p.rate != nullptr
+             ? launch_gated_r<F, true>(p, y, final_state, starts, (uint64_t*)scratch, stream)
+             : launch_gated_r<F, false>(p, y, final_state, starts, (uint64_t*)scratch, stream);
+}
+
+hipError_t launch_gated_scan(const GatedProblem& p, Fmt fmt, void* y, float* final_state,
+                             float* starts, void* scratch, hipStream_t stream) {
+  switch (fmt) {
+    case Fmt::F32: return launch_gated_f<FmtF32>(p, y, final_state, starts, scratch, stream);
+    case Fmt::F16: return launch_gated_f<FmtF16>(p, y, final_state, starts, scratch, stream);
+    case Fmt::BF16: return launch_gated_f<FmtBF16>(p, y, final_state, starts, scratch, stream);
+    default: return hipErrorInvalidValue;
+  }
+}
 
 template <class F, bool RATE>
 __device__ __forceinline__ float gated_token(float h, typename F::S x, typename F::S f,
@@ -16,67 +216,6 @@ __device__ __forceinline__ float gated_token(float h, typename F::S x, typename 
   float u = g.w * widen<F>(x);
   if (ig != nullptr) u *= sigmoid(widen<F>(*ig));
   return __builtin_fmaf(g.a, h, u);
-}
-
-template <class F, bool RATE>
-__global__ __launch_bounds__(64) void gated_scan_kernel(GatedProblem p, void* yv,
-                                                        float* final_state, float* starts,
-                                                        int64_t b0) {
-  using S = typename F::S;
-  int64_t part;
-  const int64_t parts = (p.channels + 63) / 64;
-  const int64_t b = b0 + divide((int64_t)blockIdx.x, parts, &part), c = part * 64 + threadIdx.x;
-  if (c >= p.channels) return;
-  const float nr = RATE ? rate_log2(p.rate[c]) : 0.0f;
-  const int64_t n = p.lengths == nullptr ? p.length : live_count(p.length, p.lengths + b);
-  float h = p.initial_state == nullptr ? 0.0f : p.initial_state[b * p.channels + c];
-  const int64_t blocks = (p.length + kGatedKeepTokens - 1) / kGatedKeepTokens;
-  S* y = (S*)yv + b * p.length * p.channels + c;
-  for (int64_t t = 0; t < p.length; ++t) {
-    if (starts != nullptr && t % kGatedKeepTokens == 0)
-      starts[(b * blocks + t / kGatedKeepTokens) * p.channels + c] = h;
-    float out = 0.0f;
-    if (t < n) {
-      const S* ig = p.input_gate == nullptr
-                        ? nullptr
-                        : (const S*)p.input_gate + b * p.input_batch + t * p.input_token + c;
-      h = gated_token<F, RATE>(h, ((const S*)p.x)[b * p.x_batch + t * p.x_token + c],
-                               ((const S*)p.forget)[b * p.forget_batch + t * p.forget_token + c],
-                               ig, nr);
-      out = p.z == nullptr ? h
-                           : h * silu(widen<F>(((const S*)p.z)[b * p.z_batch + t * p.z_token + c]));
-    }
-    y[t * p.channels] = narrow<F>(out);
-  }
-  if (final_state != nullptr) final_state[b * p.channels + c] = h;
-}
-
-size_t gated_scan_scratch(const GatedProblem&) { return 0; }
-
-template <class F>
-static hipError_t launch_gated_f(const GatedProblem& p, void* y, float* final_state, float* starts,
-                                 hipStream_t stream) {
-  const int64_t parts = (p.channels + 63) / 64;
-  const int64_t step = kMaxGroups / parts;
-  for (int64_t b0 = 0; b0 < p.batch; b0 += step) {
-    const int64_t nb = p.batch - b0 < step ? p.batch - b0 : step;
-    const dim3 grid((unsigned)(nb * parts));
-    if (p.rate != nullptr)
-      gated_scan_kernel<F, true><<<grid, dim3(64), 0, stream>>>(p, y, final_state, starts, b0);
-    else
-      gated_scan_kernel<F, false><<<grid, dim3(64), 0, stream>>>(p, y, final_state, starts, b0);
-  }
-  return hipGetLastError();
-}
-
-hipError_t launch_gated_scan(const GatedProblem& p, Fmt fmt, void* y, float* final_state,
-                             float* starts, void*, hipStream_t stream) {
-  switch (fmt) {
-    case Fmt::F32: return launch_gated_f<FmtF32>(p, y, final_state, starts, stream);
-    case Fmt::F16: return launch_gated_f<FmtF16>(p, y, final_state, starts, stream);
-    case Fmt::BF16: return launch_gated_f<FmtBF16>(p, y, final_state, starts, stream);
-    default: return hipErrorInvalidValue;
-  }
 }
 
 // One token: a thread per channel.

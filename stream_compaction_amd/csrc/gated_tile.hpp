@@ -1,0 +1,279 @@
+// What the gated scan's forward and gradient share: a workgroup's tile of tokens
+// and channels, the maps that carry a state over a run of tokens, and their
+// exchange between workgroups.
+//
+// A tile is 128 channels, two to a lane, and a run of consecutive tokens for each
+// of the 8 waves, kept in registers: the inputs are read once.  A state crosses a
+// run by h -> 2^l h + b, where l sums the tokens' log2 decays.  Waves exchange
+// their maps through LDS, workgroups through memory: each writes its tile's map as
+// soon as it has read its tokens, and reads those of the tiles before it (after it,
+// in the gradient) in its group of 16, and one state at the group's border.  So no
+// tile waits for more than its neighbours' reading and one link a group, and what
+// is added in which order does not depend on timing.
+#pragma once
+
+#include "gated.hpp"
+
+namespace sca {
+
+constexpr int kTileWaves = 8;
+constexpr int kTileThreads = 64 * kTileWaves;
+constexpr int kTileChannels = 128;           // two to a lane
+constexpr int kTileGroup = 16;               // tiles from one passed-on state to the next
+constexpr int64_t kTileHeader = 16;          // words before the slots: the ticket
+
+// The launch's tiles: `cols` columns (a sequence's 128 channels) of `chunks` runs.
+struct Tiles {
+  int64_t parts, cols, chunks;
+  int64_t b0 = 0;                            // the first sequence
+  __host__ __device__ int64_t count() const { return cols * chunks; }
+  int64_t words() const {                    // of scratch, 8 bytes each
+    if (chunks <= 1) return 0;
+    return kTileHeader + (chunks + (chunks + kTileGroup - 1) / kTileGroup) * cols * kTileChannels;
+  }
+};
+inline Tiles gated_tiles(const GatedProblem& p, int tokens) {
+  Tiles t;
+  t.parts = (p.channels + kTileChannels - 1) / kTileChannels;
+  t.cols = p.batch * t.parts;
+  t.chunks = p.length <= tokens ? 1 : (p.length + tokens - 1) / tokens;
+  return t;
+}
+hipError_t launch_tile_clear(uint64_t* scratch, int64_t words, hipStream_t stream);
+
+// Launches `kernel(grid, tiles)` over all tiles.  With several chunks workgroups
+// draw their tiles (a grid of two axes may start some that find none left);
+// otherwise they are counted, and a large batch goes out in parts.
+constexpr int64_t kTileGroups = 1ll << 22;   // workgroups along the first axis
+template <class Kernel>
+hipError_t launch_tiles(Tiles t, int64_t batch, uint64_t* scratch, hipStream_t stream, Kernel&& kernel) {
+  if (t.chunks > 1) {
+    const hipError_t e = launch_tile_clear(scratch, t.words(), stream);
+    if (e != hipSuccess) return e;
+    const int64_t n = t.count(), x = n < kTileGroups ? n : kTileGroups;
+    kernel(dim3((unsigned)x, (unsigned)((n + x - 1) / x)), t);
+    return hipGetLastError();
+  }
+  const int64_t step = kTileGroups / t.parts;
+  for (int64_t b0 = 0; b0 < batch; b0 += step) {
+    Tiles part = t;
+    part.b0 = b0;
+    part.cols = (batch - b0 < step ? batch - b0 : step) * t.parts;
+    kernel(dim3((unsigned)part.cols), part);
+  }
+  return hipGetLastError();
+}
+
+// A sequence's rows, one token after the other, as wave-uniform addresses.
+struct Rows {
+  uintptr_t at, step;
+  __device__ __forceinline__ Rows(uintptr_t base, int64_t batch, int64_t token, int64_t b, int64_t t, int eb)
+      : at(base + (uintptr_t)((b * batch + t * token) * eb)), step((uintptr_t)(token * eb)) {}
+  __device__ __forceinline__ void next(bool more) { at += more ? step : 0; }
+};
+
+// Two neighbouring channels of a row as one access, or, where the number of
+// channels is odd, as one access each (a pair may then lie across a row's end).
+template <class F, bool ODD> struct PairIO {
+  using S = typename F::S;
+  using IO = RowIO<F, 2>;
+  using Raw = typename IO::Raw;
+  typedef Raw Loose __attribute__((aligned(sizeof(S))));
+  // o0, o1: byte offsets of the two channels, inside the row
+  static __device__ __forceinline__ Raw load(uintptr_t row, uint32_t o0, uint32_t o1) {
+    if constexpr (ODD) {
+      typename IO::Elems e;
+      e.e[0] = *(const __attribute__((address_space(1))) S*)(gptr<const char>(row) + o0);
+      e.e[1] = *(const __attribute__((address_space(1))) S*)(gptr<const char>(row) + o1);
+      return __builtin_bit_cast(Raw, e);
+    } else {
+      return *(const __attribute__((address_space(1))) Loose*)(gptr<const char>(row) + o0);
+    }
+  }
+  // n: how many of the two exist
+  static __device__ __forceinline__ void store(uintptr_t row, uint32_t o0, Raw r, int n) {
+    if constexpr (ODD) {
+      const typename IO::Elems e = __builtin_bit_cast(typename IO::Elems, r);
+      if (n > 0) *(__attribute__((address_space(1))) S*)(gptr<char>(row) + o0) = e.e[0];
+      if (n > 1)
+        *(__attribute__((address_space(1))) S*)(gptr<char>(row) + o0 + (uint32_t)sizeof(S)) = e.e[1];
+    } else {
+      if (n > 0) *(__attribute__((address_space(1))) Loose*)(gptr<char>(row) + o0) = r;
+    }
+  }
+  static __device__ __forceinline__ Raw splat(float v) {
+    const float x[2] = {v, v};
+    return IO::pack(x);
+  }
+};
+
+// sqrt(2^l) of a run's decay, by which a state is multiplied twice: 2^l itself may
+// leave float32's range where its product with a large state does not.  What is
+// below 2^-252 leaves nothing of any finite state, and an infinite one stays so; l
+// = -inf (a decay of 0) gives 0.
+__device__ __forceinline__ float half_decay(float l) {
+  const float m = at_least(exp2_hw(0.5f * l), 1.17549435e-38f);
+  return l == -__builtin_huge_valf() ? 0.0f : m;
+}
+__device__ __forceinline__ float carry_over(float m, float b, float h) {
+  return __builtin_fmaf(h * m, m, b);
+}
+
+// Slots: a map or a state as one 64-bit word, written and read whole, whose upper
+// half is never all ones; the launch before fills them with ones.
+constexpr uint32_t kNoWord = 0xffffffffu;
+__device__ __forceinline__ uint64_t map_word(float l, float b) {
+  uint32_t hi = __builtin_bit_cast(uint32_t, l);
+  if (hi == kNoWord) hi = 0x7fc00000u;       // that one NaN becomes another
+  return ((uint64_t)hi << 32) | __builtin_bit_cast(uint32_t, b);
+}
+__device__ __forceinline__ float word_l(uint64_t w) { return __builtin_bit_cast(float, (uint32_t)(w >> 32)); }
+__device__ __forceinline__ float word_b(uint64_t w) { return __builtin_bit_cast(float, (uint32_t)w); }
+__device__ __forceinline__ uint64_t state_word(float h) { return __builtin_bit_cast(uint32_t, h); }
+
+// Two channels' words, once they are there.
+struct Words { uint64_t w[2]; };
+__device__ __forceinline__ Words peek_words(const uint64_t* at) {
+  return Words{{ld_relaxed(at), ld_relaxed(at + 1)}};
+}
+__device__ __forceinline__ Words await_words(const uint64_t* at, Words w) {
+  while (__ballot((uint32_t)(w.w[0] >> 32) == kNoWord || (uint32_t)(w.w[1] >> 32) == kNoWord)) {
+    __builtin_amdgcn_s_sleep(4);
+    w = peek_words(at);
+  }
+  return w;
+}
+
+// The tile a workgroup takes next: by a ticket, so that the tiles it will wait for
+// are with workgroups that run already, whatever order the hardware starts them in.
+// (Only the lowest unfinished tile must be able to go on, and it waits for none.)
+__device__ __forceinline__ int64_t next_tile(uint64_t* ticket, uint64_t* shared) {
+  if (threadIdx.x == 0)
+    *shared = __hip_atomic_fetch_add(ticket, 1ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  return (int64_t)readlane(*shared, 0);
+}
+
+struct TileMaps {                            // a workgroup's exchange
+  float l[kTileWaves][kTileChannels], m[kTileWaves][kTileChannels], b[kTileWaves][kTileChannels];
+  float fm[kTileWaves][kTileChannels], fb[kTileWaves][kTileChannels];   // tiles looked back to
+  float base[kTileChannels];
+  uint64_t tile;
+};
+
+__device__ __forceinline__ void put2(float* row, float a, float b) {
+  *(f32x2*)(row + 2 * lane_id()) = f32x2{a, b};
+}
+__device__ __forceinline__ void get2(const float* row, float (&v)[2]) {
+  const f32x2 r = *(const f32x2*)(row + 2 * lane_id());
+  v[0] = r.x;
+  v[1] = r.y;
+}
+
+// The state that enters tile `step` of its column's `steps` (both counted in the
+// direction of the walk), and what the tile leaves to others: called by every wave
+// when all maps are in LDS (before a barrier), with the state `first` that enters
+// the column.  slots + tile index * 128 words, borders likewise by group.
+__device__ __forceinline__ void tile_entry(TileMaps& s, int wave, int64_t step, int64_t steps,
+                                           int64_t col, int64_t cols, uint64_t* scratch,
+                                           int64_t chunks, const float (&first)[2], float (&h)[2]) {
+  const int lane2 = 2 * lane_id();
+  uint64_t* slots = scratch + kTileHeader;
+  uint64_t* borders = slots + chunks * cols * kTileChannels;
+  auto slot = [&](int64_t i) { return slots + (i * cols + col) * kTileChannels + lane2; };
+  auto border = [&](int64_t g) { return borders + (g * cols + col) * kTileChannels + lane2; };
+  const int64_t group = step / kTileGroup, begin = group * kTileGroup;
+  const int before = (int)(step - begin);
+  constexpr int kEach = (kTileGroup - 1 + kTileWaves - 1) / kTileWaves;
+  static_assert(kEach == 2, "each wave looks at two tiles");
+  const int i0 = wave * kEach;
+  const bool on0 = i0 < before, on1 = i0 + 1 < before;
+  Words w0 = {}, w1 = {}, wb = {};
+  if (on0) w0 = peek_words(slot(begin + i0));
+  if (on1) w1 = peek_words(slot(begin + i0 + 1));
+  const bool passes = wave == kTileWaves - 1 && group > 0;
+  if (passes) wb = peek_words(border(group));
+  if (wave == 0 && step + 1 < steps) {       // this tile's own map
+    float l[2] = {0.0f, 0.0f}, b[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int w = 0; w < kTileWaves; ++w) {
+      float wl[2], wm[2], wb2[2];
+      get2(s.l[w], wl);
+      get2(s.m[w], wm);
+      get2(s.b[w], wb2);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        l[c] += wl[c];
+        b[c] = carry_over(wm[c], wb2[c], b[c]);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) st_relaxed(slot(step) + c, map_word(l[c], b[c]));
+  }
+  float m[2] = {1.0f, 1.0f}, b[2] = {0.0f, 0.0f};
+  if (on0) {
+    w0 = await_words(slot(begin + i0), w0);
+    float l[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      l[c] = word_l(w0.w[c]);
+      b[c] = word_b(w0.w[c]);
+    }
+    if (on1) {
+      w1 = await_words(slot(begin + i0 + 1), w1);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        b[c] = carry_over(half_decay(word_l(w1.w[c])), word_b(w1.w[c]), b[c]);
+        l[c] += word_l(w1.w[c]);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) m[c] = half_decay(l[c]);
+  }
+  put2(s.fm[wave], m[0], m[1]);
+  put2(s.fb[wave], b[0], b[1]);
+  if (wave == kTileWaves - 1) {
+    float v[2] = {first[0], first[1]};
+    if (passes) {
+      wb = await_words(border(group), wb);
+      v[0] = word_b(wb.w[0]);
+      v[1] = word_b(wb.w[1]);
+    }
+    put2(s.base, v[0], v[1]);
+  }
+  lds_barrier();
+  get2(s.base, h);
+  const int used = (before + kEach - 1) / kEach;
+  for (int w = 0; w < used; ++w) {
+    get2(s.fm[w], m);
+    get2(s.fb[w], b);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) h[c] = carry_over(m[c], b[c], h[c]);
+  }
+  // the group's last tile passes the state on
+  if (wave == kTileWaves - 1 && before == kTileGroup - 1 && step + 1 < steps) {
+    float v[2] = {h[0], h[1]};
+#pragma unroll
+    for (int w = 0; w < kTileWaves; ++w) {
+      get2(s.m[w], m);
+      get2(s.b[w], b);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) v[c] = carry_over(m[c], b[c], v[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) st_relaxed(border(group + 1) + c, state_word(v[c]));
+  }
+}
+
+// The state that enters this wave's run, from the one that enters the tile.
+__device__ __forceinline__ void wave_entry(const TileMaps& s, int wave, float (&h)[2]) {
+  for (int w = 0; w < wave; ++w) {
+    float m[2], b[2];
+    get2(s.m[w], m);
+    get2(s.b[w], b);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) h[c] = carry_over(m[c], b[c], h[c]);
+  }
+}
+
+}  // namespace sca
