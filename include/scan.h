@@ -436,7 +436,7 @@ scan_status selective_scan_step(const selective_scan_args* args, const float* st
  *   h = a h + w v x[b,t,c],   y[b,t,c] = h z sigmoid(z)  (y = h when z is NULL).
  *   x, forget, input_gate, z   activations, each with its {batch, token} strides
  *   rate           float32 [channels]; a rate below 0 counts as 0, which holds
- *                  the state and takes no input
+ *                  the state and takes no input, one above 1e38 as 1e38
  *   initial_state  float32 [batch, channels], h before t = 0 (NULL: zeros)
  * The state is float32 throughout.
  */

@@ -54,7 +54,10 @@ __device__ __forceinline__ Gate gate(float forget, float nr) {
   return g;
 }
 
-// -log2(e) r of a rate, a negative one counting as 0 (a NaN stays one).
-__device__ __forceinline__ float rate_log2(float r) { return at_least(r, 0.0f) * -kLog2e; }
+// -log2(e) r of a rate, a negative one counting as 0 and an infinite one as 1e38, so
+// that a closed gate (s = 0) holds the state under any rate (a NaN stays one).
+__device__ __forceinline__ float rate_log2(float r) {
+  return at_most(at_least(r, 0.0f), 1e38f) * -kLog2e;
+}
 
 }  // namespace sca

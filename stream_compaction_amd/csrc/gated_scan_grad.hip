@@ -8,120 +8,319 @@
 //                  dforget = E (1 - s),   drate = (sum of E over tokens) / rate,
 // as p = rate s enters through log p alone.  p / w tends to 0 with p.
 //
-// A thread per channel goes through the blocks of 64 tokens from the last one on:
-// each block's states are found again from its start, which the forward kept.
-#include "gated.hpp"
+// What is carried is c[t] = a[t] g[t], from the last token to the first: the same
+// maps as the forward's, c -> 2^l c + b, in tiles of 64 tokens (gated_tile.hpp).  The
+// states are found again from the tile's first, which the forward kept.  A wave has 8
+// tokens: decay, weight and state of each stay in registers with the inputs, the
+// sigmoids are computed a second time (all of it kept would leave room for half as
+// many waves).
+#include "gated_tile.hpp"
 
 namespace sca {
 
-template <class F, bool RATE>
-__global__ __launch_bounds__(64) void gated_scan_grad_kernel(GatedProblem p, GatedGrads g,
-                                                             float* partial, int64_t b0) {
+constexpr int kGradTokens = 8;                              // of a wave
+constexpr int kGradTile = kGradTokens * kTileWaves;         // of a workgroup
+static_assert(kGradTile == kGatedKeepTokens, "a tile starts from a kept state");
+
+// Waves a SIMD: float32's inputs take twice the registers, and with two workgroups a
+// CU some of them would go to memory.
+template <class F, bool RATE, bool IG, bool Z>
+constexpr int kGradWaves = sizeof(typename F::S) == 4 && (RATE || IG || Z) ? 2 : 4;
+
+template <class F, bool RATE, bool IG, bool Z, bool ODD>
+__global__ __launch_bounds__(kTileThreads)
+__attribute__((amdgpu_waves_per_eu(kGradWaves<F, RATE, IG, Z>, kGradWaves<F, RATE, IG, Z>)))
+void gated_scan_grad_kernel(GatedProblem p, GatedGrads g, uint64_t* scratch, float* partial, Tiles tiles) {
   using S = typename F::S;
-  constexpr int K = kGatedKeepTokens;
-  int64_t part;
-  const int64_t parts = (p.channels + 63) / 64;
-  const int64_t b = b0 + divide((int64_t)blockIdx.x, parts, &part), c = part * 64 + threadIdx.x;
-  if (c >= p.channels) return;
-  const float nr = RATE ? rate_log2(p.rate[c]) : 0.0f;
+  using PIO = PairIO<F, ODD>;
+  using IO = typename PIO::IO;
+  using Raw = typename PIO::Raw;
+  constexpr int T = kGradTokens;
+  constexpr int eb = sizeof(S);
+  __shared__ TileMaps sh;
+  __shared__ float forward_b[kTileWaves][kTileChannels];
+  const int wave = wave_id(), turn = kTileWaves - 1 - wave;  // its turn in the walk
+  const int D = (int)p.channels;
+  const int64_t tile = tiles.chunks > 1 ? next_tile(scratch, &sh.tile) : blockIdx.x;
+  if (tile >= tiles.count()) return;
+  int64_t col, part;
+  const int64_t chunk = tiles.chunks - 1 - divide(tile, tiles.cols, &col);
+  const int64_t b = tiles.b0 + divide(col, tiles.parts, &part);
+  const int ch = (int)part * kTileChannels + 2 * lane_id();
+  const int have = D - ch >= 2 ? 2 : (D - ch == 1 ? 1 : 0);
+  // lanes past the last channel work on the last one (pair), unheard
+  const int c0 = ODD ? (ch < D ? ch : D - 1) : (ch < D ? ch : D - 2);
+  const int c1 = ch + 1 < D ? ch + 1 : D - 1;
+  const uint32_t o0 = (uint32_t)c0 * eb, o1 = (uint32_t)c1 * eb;
   const int64_t n = p.lengths == nullptr ? p.length : live_count(p.length, p.lengths + b);
-  const int64_t blocks = (p.length + K - 1) / K;
-  const S* x = (const S*)p.x + b * p.x_batch + c;
-  const S* f = (const S*)p.forget + b * p.forget_batch + c;
-  const S* ig = (const S*)p.input_gate + b * p.input_batch + c;
-  const S* z = (const S*)p.z + b * p.z_batch + c;
-  const S* dy = (const S*)g.dy + b * g.dy_batch + c;
-  const int64_t row = b * p.length * p.channels + c;
-  float carry = g.dfinal == nullptr ? 0.0f : g.dfinal[b * p.channels + c], total = 0.0f;
-  for (int64_t t = n; t < p.length; ++t) {
-    ((S*)g.dx)[row + t * p.channels] = ((S*)g.dforget)[row + t * p.channels] = narrow<F>(0.0f);
-    if (p.input_gate != nullptr) ((S*)g.dinput_gate)[row + t * p.channels] = narrow<F>(0.0f);
-    if (p.z != nullptr) ((S*)g.dz)[row + t * p.channels] = narrow<F>(0.0f);
+  const int64_t t0 = chunk * kGradTile + wave * T;         // this wave's first token
+  uintptr_t out = ((b * p.length + t0) * D) * eb;
+  const int room = (int)(p.length - t0 < T ? p.length - t0 : T);
+  float c[2] = {0.0f, 0.0f};
+  if (g.dfinal != nullptr) {
+    c[0] = g.dfinal[b * D + c0];
+    c[1] = g.dfinal[b * D + c1];
   }
-  for (int64_t blk = (n + K - 1) / K - 1; blk >= 0; --blk) {
-    const int64_t t0 = blk * K;
-    const int count = (int)(n - t0 < K ? n - t0 : K);
-    float hs[K];
-    float h = g.starts[(b * blocks + blk) * p.channels + c];
-    for (int k = 0; k < count; ++k) {
-      const int64_t t = t0 + k;
-      hs[k] = h;
-      const Gate gt = gate<RATE>(widen<F>(f[t * p.forget_token]), nr);
-      const float v = p.input_gate == nullptr ? 1.0f : sigmoid(widen<F>(ig[t * p.input_token]));
-      h = __builtin_fmaf(gt.a, h, gt.w * v * widen<F>(x[t * p.x_token]));
+  if (chunk * kGradTile >= n) {                            // no token of this tile exists
+    const Raw zero = PIO::splat(0.0f);
+    for (int k = 0; k < room; ++k, out += D * eb) {
+      PIO::store((uintptr_t)g.dx + out, o0, zero, have);
+      PIO::store((uintptr_t)g.dforget + out, o0, zero, have);
+      if constexpr (IG) PIO::store((uintptr_t)g.dinput_gate + out, o0, zero, have);
+      if constexpr (Z) PIO::store((uintptr_t)g.dz + out, o0, zero, have);
     }
-    for (int k = count - 1; k >= 0; --k) {
-      const int64_t t = t0 + k, at = row + t * p.channels;
-      const float fv = widen<F>(f[t * p.forget_token]), xv = widen<F>(x[t * p.x_token]);
-      const Gate gt = gate<RATE>(fv, nr);
-      const Sides s = sides(fv);
-      const float d = widen<F>(dy[t * g.dy_token]);
-      float q = d;
-      if (p.z != nullptr) {
-        const float zv = widen<F>(z[t * p.z_token]);
-        q = d * silu(zv);
-        ((S*)g.dz)[at] = narrow<F>(d * h * silu_slope(zv));
+    if (wave == 0) {
+      float* at = partial + (b * tiles.chunks + chunk) * D + ch;
+      if (RATE && have > 0) at[0] = 0.0f;
+      if (RATE && have > 1) at[1] = 0.0f;
+      if (chunk == 0 && g.dinitial != nullptr) {
+        if (have > 0) g.dinitial[b * D + ch] = c[0];
+        if (have > 1) g.dinitial[b * D + ch + 1] = c[1];
       }
-      Sides v = {1.0f, 0.0f};
-      if (p.input_gate != nullptr) v = sides(widen<F>(ig[t * p.input_token]));
-      const float grad = q + carry, dx = grad * gt.w * v.up;
-      ((S*)g.dx)[at] = narrow<F>(dx);
-      if (p.input_gate != nullptr) ((S*)g.dinput_gate)[at] = narrow<F>(dx * xv * v.down);
+    }
+    return;
+  }
+  const int count = (int)(n - t0 <= 0 ? 0 : (n - t0 < T ? n - t0 : T));
+  // (past the last token it is read again)
+  const int64_t first_token = count > 0 ? t0 : n - 1;
+  Rows ax((uintptr_t)p.x, p.x_batch, p.x_token, b, first_token, eb);
+  Rows af((uintptr_t)p.forget, p.forget_batch, p.forget_token, b, first_token, eb);
+  Rows ai((uintptr_t)p.input_gate, p.input_batch, p.input_token, b, first_token, eb);
+  Rows az((uintptr_t)p.z, p.z_batch, p.z_token, b, first_token, eb);
+  Rows ad((uintptr_t)g.dy, g.dy_batch, g.dy_token, b, first_token, eb);
+  Raw rx[T], rf[T], ri[IG ? T : 1], rz[Z ? T : 1], rd[T];
+#pragma unroll
+  for (int k = 0; k < T; ++k) {
+    rx[k] = PIO::load(ax.at, o0, o1);
+    rf[k] = PIO::load(af.at, o0, o1);
+    if constexpr (IG) ri[k] = PIO::load(ai.at, o0, o1);
+    if constexpr (Z) rz[k] = PIO::load(az.at, o0, o1);
+    rd[k] = PIO::load(ad.at, o0, o1);
+    const bool more = k + 1 < count;
+    ax.next(more);
+    af.next(more);
+    ai.next(more);
+    az.next(more);
+    ad.next(more);
+  }
+  float nr[2] = {0.0f, 0.0f}, h[2];
+  if constexpr (RATE) {
+    nr[0] = rate_log2(p.rate[c0]);
+    nr[1] = rate_log2(p.rate[c1]);
+  }
+  {
+    const int64_t blocks = (p.length + kGatedKeepTokens - 1) / kGatedKeepTokens;
+    const float* at = g.starts + (b * blocks + chunk) * D;
+    h[0] = at[c0];
+    h[1] = at[c1];
+  }
+  if (count < T) {                                         // tokens that do not exist: a = 1, u = q = 0
+#pragma unroll
+    for (int k = 0; k < T; ++k) {
+      if (k < count) continue;
+      rx[k] = rd[k] = PIO::splat(0.0f);
+      rf[k] = PIO::splat(RATE ? -__builtin_huge_valf() : __builtin_huge_valf());
+      if constexpr (IG) ri[k] = PIO::splat(0.0f);
+      if constexpr (Z) rz[k] = PIO::splat(0.0f);
+    }
+  }
+  // hs: first the input's part of each token, then the state before it
+  float a[T][2], w[RATE ? T : 1][2], hs[T][2];
+  float l[2] = {0.0f, 0.0f}, least[2] = {1.0f, 1.0f}, last[2] = {0.0f, 0.0f}, back[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int k = 0; k < T; ++k) {
+    float x[2], f[2], v[2];
+    IO::unpack(rx[k], x);
+    IO::unpack(rf[k], f);
+    if constexpr (IG) IO::unpack(ri[k], v);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const Gate gt = gate<RATE>(f[j], nr[j]);
+      a[k][j] = gt.a;
+      if constexpr (RATE) w[k][j] = gt.w;
+      hs[k][j] = gt.w * x[j];
+      if constexpr (IG) hs[k][j] *= sigmoid(v[j]);
+      l[j] += gt.log_a;
+      least[j] = __builtin_fminf(least[j], gt.a);
+      last[j] = __builtin_fmaf(gt.a, last[j], hs[k][j]);
+    }
+    __builtin_amdgcn_sched_barrier(0);                     // token after token, as in the forward
+  }
+#pragma unroll
+  for (int k = T - 1; k >= 0; --k) {
+    float q[2], z[2];
+    IO::unpack(rd[k], q);
+    if constexpr (Z) IO::unpack(rz[k], z);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if constexpr (Z) q[j] *= silu(z[j]);
+      back[j] = a[k][j] * (q[j] + back[j]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (least[j] == 0.0f) l[j] = -__builtin_huge_valf();
+  put2(sh.l[turn], l[0], l[1]);
+  put2(sh.m[turn], half_decay(l[0]), half_decay(l[1]));
+  put2(sh.b[turn], back[0], back[1]);
+  put2(forward_b[wave], last[0], last[1]);
+  lds_barrier();
+  if (tiles.chunks > 1) {
+    const float first[2] = {c[0], c[1]};
+    const int64_t steps = (n + kGradTile - 1) / kGradTile;
+    tile_entry(sh, turn, steps - 1 - chunk, steps, col, tiles.cols, scratch, tiles.chunks, first, c);
+  }
+  wave_entry(sh, turn, c);
+  for (int i = 0; i < wave; ++i) {                         // the state that enters this wave's run
+    float m[2], fb[2];
+    get2(sh.m[kTileWaves - 1 - i], m);
+    get2(forward_b[i], fb);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) h[j] = carry_over(m[j], fb[j], h[j]);
+  }
+#pragma unroll
+  for (int k = 0; k < T; ++k)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float u = hs[k][j];
+      hs[k][j] = h[j];
+      h[j] = __builtin_fmaf(a[k][j], h[j], u);
+    }
+  float total[2] = {0.0f, 0.0f};
+  out += (uintptr_t)(T - 1) * D * eb;
+#pragma unroll
+  for (int k = T - 1; k >= 0; --k) {
+    float x[2], f[2], v[2], z[2], d[2], dx[2], df[2], di[2], dz[2];
+    IO::unpack(PIO::again(rx[k]), x);
+    IO::unpack(PIO::again(rf[k]), f);
+    IO::unpack(PIO::again(rd[k]), d);
+    if constexpr (IG) IO::unpack(PIO::again(ri[k]), v);
+    if constexpr (Z) IO::unpack(PIO::again(rz[k]), z);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float q = d[j];
+      if constexpr (Z) {
+        q *= silu(z[j]);
+        dz[j] = d[j] * h[j] * silu_slope(z[j]);
+        h[j] = hs[k][j];
+      }
+      const Sides s = sides(f[j]);
+      Sides vs = {1.0f, 0.0f};
+      if constexpr (IG) vs = sides(v[j]);
+      const float grad = q + c[j], gv = grad * vs.up;
+      const float weight = RATE ? w[RATE ? k : 0][j] : s.down;
+      dx[j] = gv * weight;
+      if constexpr (IG) di[j] = dx[j] * x[j] * vs.down;
       if constexpr (RATE) {
-        const float P = at_most(gt.log_a * -kLn2, 128.0f);   // exp(-128) is 0 in float32
-        const float pw = gt.w > 0.0f ? P / gt.w : 0.0f;
-        const float E = grad * (v.up * xv * gt.a * gt.a * pw - P * gt.a * hs[k]);
-        ((S*)g.dforget)[at] = narrow<F>(E * s.down);
-        total += E;
+        const float P = at_most(nr[j] * s.up * -kLn2, 128.0f);   // exp(-128) is 0 in float32
+        const float pw = weight > 0.0f ? P * rcp_hw(weight) : 0.0f;
+        const float A = a[k][j];
+        const float E = gv * x[j] * (A * A * pw) - grad * (P * A * hs[k][j]);
+        df[j] = E * s.down;
+        total[j] += E;
       } else {
-        ((S*)g.dforget)[at] = narrow<F>(grad * (hs[k] - v.up * xv) * s.up * s.down);
+        df[j] = (grad * hs[k][j] - gv * x[j]) * (s.up * s.down);
       }
-      carry = gt.a * grad;
-      h = hs[k];
+      c[j] = a[k][j] * grad;
+      if (k >= count) dx[j] = df[j] = di[j] = dz[j] = 0.0f;
+    }
+    if (k < room) {
+      PIO::store((uintptr_t)g.dx + out, o0, IO::pack(dx), have);
+      PIO::store((uintptr_t)g.dforget + out, o0, IO::pack(df), have);
+      if constexpr (IG) PIO::store((uintptr_t)g.dinput_gate + out, o0, IO::pack(di), have);
+      if constexpr (Z) PIO::store((uintptr_t)g.dz + out, o0, IO::pack(dz), have);
+    }
+    out -= (uintptr_t)D * eb;
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  if (g.dinitial != nullptr && t0 == 0) {
+    if (have > 0) g.dinitial[b * D + ch] = c[0];
+    if (have > 1) g.dinitial[b * D + ch + 1] = c[1];
+  }
+  if constexpr (RATE) {                                    // the tile's sums, wave after wave
+    __syncthreads();
+    put2(sh.l[wave], total[0], total[1]);
+    __syncthreads();
+    if (wave == 0) {
+      float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < kTileWaves; ++i) {
+        float e[2];
+        get2(sh.l[i], e);
+        sum[0] += e[0];
+        sum[1] += e[1];
+      }
+      float* at = partial + (b * tiles.chunks + chunk) * D + ch;
+      if (have > 0) at[0] = sum[0];
+      if (have > 1) at[1] = sum[1];
     }
   }
-  if (g.dinitial != nullptr) g.dinitial[b * p.channels + c] = carry;
-  if constexpr (RATE) partial[b * p.channels + c] = total;
 }
 
-__global__ __launch_bounds__(64) void gated_rate_kernel(const float* partial, const float* rate,
-                                                        float* drate, int64_t rows,
-                                                        int64_t channels) {
-  const int64_t c = (int64_t)blockIdx.x * 64 + threadIdx.x;
-  if (c >= channels) return;
+// drate from the tiles' sums: 64 channels a workgroup, 16 strands of tiles each.
+__global__ __launch_bounds__(1024) void gated_rate_kernel(const float* partial, const float* rate,
+                                                          float* drate, int64_t rows, int64_t channels) {
+  __shared__ float strand[16][64];
+  const int64_t c = (int64_t)blockIdx.x * 64 + lane_id();
   float sum = 0.0f;
-  for (int64_t i = 0; i < rows; ++i) sum += partial[i * channels + c];
-  drate[c] = rate[c] <= 0.0f ? 0.0f : sum / rate[c];
+  if (c < channels) {
+#pragma unroll 8
+    for (int64_t i = threadIdx.x / 64; i < rows; i += 16) sum += partial[i * channels + c];
+  }
+  strand[threadIdx.x / 64][lane_id()] = sum;
+  __syncthreads();
+  if (threadIdx.x >= 64 || c >= channels) return;
+  for (int i = 1; i < 16; ++i) sum += strand[i][lane_id()];
+  const float r = rate[c];
+  drate[c] = r <= 0.0f ? 0.0f : sum / r;
 }
 
 size_t gated_scan_grad_scratch(const GatedProblem& p) {
-  return p.rate == nullptr ? 0 : (size_t)(p.batch * p.channels) * 4;
+  const Tiles t = gated_tiles(p, kGradTile);
+  const size_t sums = p.rate == nullptr ? 0 : (size_t)(p.batch * t.chunks * p.channels) * 4;
+  return (size_t)t.words() * 8 + sums;
+}
+
+template <class F, bool RATE, bool IG, bool Z>
+static hipError_t launch_grad_z(const GatedProblem& p, const GatedGrads& g, void* scratch, hipStream_t stream) {
+  const Tiles tiles = gated_tiles(p, kGradTile);
+  uint64_t* words = (uint64_t*)scratch;
+  float* partial = (float*)(words + tiles.words());
+  hipError_t e = hipSuccess;
+  if (p.batch > 0)
+    e = launch_tiles(tiles, p.batch, words, stream, [&](dim3 grid, const Tiles& t) {
+      if (p.channels % 2 == 0)
+        gated_scan_grad_kernel<F, RATE, IG, Z, false><<<grid, dim3(kTileThreads), 0, stream>>>(p, g, words, partial, t);
+      else
+        gated_scan_grad_kernel<F, RATE, IG, Z, true><<<grid, dim3(kTileThreads), 0, stream>>>(p, g, words, partial, t);
+    });
+  if (e != hipSuccess || !RATE) return e;
+  gated_rate_kernel<<<dim3((unsigned)((p.channels + 63) / 64)), dim3(1024), 0, stream>>>(
+      partial, p.rate, g.drate, p.batch * tiles.chunks, p.channels);
+  return hipGetLastError();
+}
+
+template <class F, bool RATE>
+static hipError_t launch_grad_r(const GatedProblem& p, const GatedGrads& g, void* s, hipStream_t stream) {
+  if (p.input_gate != nullptr)
+    return p.z != nullptr ? launch_grad_z<F, RATE, true, true>(p, g, s, stream)
+                          : launch_grad_z<F, RATE, true, false>(p, g, s, stream);
+  return p.z != nullptr ? launch_grad_z<F, RATE, false, true>(p, g, s, stream)
+                        : launch_grad_z<F, RATE, false, false>(p, g, s, stream);
 }
 
 template <class F>
-static hipError_t launch_grad_f(const GatedProblem& p, const GatedGrads& g, float* partial,
-                                hipStream_t stream) {
-  const int64_t parts = (p.channels + 63) / 64, step = (1ll << 21) / parts;
-  for (int64_t b0 = 0; b0 < p.batch; b0 += step) {
-    const int64_t nb = p.batch - b0 < step ? p.batch - b0 : step;
-    const dim3 grid((unsigned)(nb * parts));
-    if (p.rate != nullptr)
-      gated_scan_grad_kernel<F, true><<<grid, dim3(64), 0, stream>>>(p, g, partial, b0);
-    else
-      gated_scan_grad_kernel<F, false><<<grid, dim3(64), 0, stream>>>(p, g, partial, b0);
-  }
-  if (p.rate != nullptr)
-    gated_rate_kernel<<<dim3((unsigned)parts), dim3(64), 0, stream>>>(partial, p.rate, g.drate,
-                                                                      p.batch, p.channels);
-  return hipGetLastError();
+static hipError_t launch_grad_f(const GatedProblem& p, const GatedGrads& g, void* s, hipStream_t stream) {
+  return p.rate != nullptr ? launch_grad_r<F, true>(p, g, s, stream)
+                           : launch_grad_r<F, false>(p, g, s, stream);
 }
 
 hipError_t launch_gated_scan_grad(const GatedProblem& p, Fmt fmt, const GatedGrads& g,
                                   void* scratch, hipStream_t stream) {
   switch (fmt) {
-    case Fmt::F32: return launch_grad_f<FmtF32>(p, g, (float*)scratch, stream);
-    case Fmt::F16: return launch_grad_f<FmtF16>(p, g, (float*)scratch, stream);
-    case Fmt::BF16: return launch_grad_f<FmtBF16>(p, g, (float*)scratch, stream);
+    case Fmt::F32: return launch_grad_f<FmtF32>(p, g, scratch, stream);
+    case Fmt::F16: return launch_grad_f<FmtF16>(p, g, scratch, stream);
+    case Fmt::BF16: return launch_grad_f<FmtBF16>(p, g, scratch, stream);
     default: return hipErrorInvalidValue;
   }
 }

@@ -101,6 +101,21 @@ template <class F, bool ODD> struct PairIO {
       if (n > 0) *(__attribute__((address_space(1))) Loose*)(gptr<char>(row) + o0) = r;
     }
   }
+  // The same bits, of which the compiler knows nothing any more: what is computed
+  // from them is computed again, not kept in registers since the first time.
+  static __device__ __forceinline__ Raw again(Raw r) {
+    if constexpr (sizeof(Raw) == 4) {
+      uint32_t w = __builtin_bit_cast(uint32_t, r);
+      materialize(w);
+      return __builtin_bit_cast(Raw, w);
+    } else {
+      u32x2 w = __builtin_bit_cast(u32x2, r);
+      uint32_t lo = w.x, hi = w.y;
+      materialize(lo);
+      materialize(hi);
+      return __builtin_bit_cast(Raw, u32x2{lo, hi});
+    }
+  }
   static __device__ __forceinline__ Raw splat(float v) {
     const float x[2] = {v, v};
     return IO::pack(x);

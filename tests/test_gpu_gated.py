@@ -339,6 +339,7 @@ def test_infinities_and_rates_at_their_ends():
         assert bool((y[0, :, c] == init[0, c]).all()) and float(state[0, c]) == float(init[0, c])
     v = torch.sigmoid(i[0, :, 3].double()) * x2[0, :, 3].double()
     assert torch.allclose(y[0, :, 3].double(), v, rtol=1e-6, atol=1e-7)
+    assert bool(torch.isfinite(state[:, [0, 1, 2, 3, 4, 6, 8, 9, 10, 11]]).all())
     assert bool(torch.isfinite(y[0, :200, 5]).all()) and bool(torch.isinf(y[0, 200:, 5]).all())
     assert bool(torch.isfinite(y[0, :300, 7]).all()) and bool(torch.isnan(y[0, 300:, 7]).all())
     assert float(y[0, 100, 8]) == float(y[0, 99, 8]) and bool(torch.isfinite(y[..., [8, 9]]).all())
