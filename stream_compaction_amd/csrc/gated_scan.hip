@@ -25,10 +25,10 @@ void gated_scan_kernel(GatedProblem p, void* yv, float* final_state, float* star
   __shared__ TileMaps sh;
   const int wave = wave_id();
   const int D = (int)p.channels;
-  const int64_t tile = tiles.chunks > 1 ? next_tile(scratch, &sh.tile) : blockIdx.x;
-  if (tile >= tiles.count()) return;
+  if (group_number() >= tiles.count()) return;
   int64_t col, part;
-  const int64_t chunk = divide(tile, tiles.cols, &col);
+  divide(group_number(), tiles.cols, &col);
+  const int64_t chunk = tiles.chunks > 1 ? draw_chunk(scratch, col, &sh.tile) : 0;
   const int64_t b = tiles.b0 + divide(col, tiles.parts, &part);
   const int ch = (int)part * kTileChannels + 2 * lane_id();
   const int have = D - ch >= 2 ? 2 : (D - ch == 1 ? 1 : 0);
@@ -154,15 +154,18 @@ void gated_scan_kernel(GatedProblem p, void* yv, float* final_state, float* star
   }
 }
 
-__global__ __launch_bounds__(256) void tile_clear_kernel(uint64_t* scratch, int64_t words) {
+__global__ __launch_bounds__(256) void tile_clear_kernel(uint64_t* scratch, int64_t tickets,
+                                                         int64_t words) {
   typedef uint64_t two __attribute__((ext_vector_type(2)));
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < words / 2; i += (int64_t)gridDim.x * 256)
-    *gptr<two>((uintptr_t)(scratch + 2 * i)) = i == 0 ? two{0, 0} : two{~0ull, ~0ull};
+    *gptr<two>((uintptr_t)(scratch + 2 * i)) =
+        2 * i < tickets ? two{0, 0} : two{~0ull, ~0ull};
 }
 
-hipError_t launch_tile_clear(uint64_t* scratch, int64_t words, hipStream_t stream) {
+hipError_t launch_tile_clear(uint64_t* scratch, int64_t tickets, int64_t words, hipStream_t stream) {
   const int64_t blocks = (words / 2 + 255) / 256;
-  tile_clear_kernel<<<dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), 0, stream>>>(scratch, words);
+  tile_clear_kernel<<<dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), 0, stream>>>(scratch, tickets,
+                                                                                          words);
   return hipGetLastError();
 }
 

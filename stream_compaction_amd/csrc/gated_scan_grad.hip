@@ -41,10 +41,10 @@ void gated_scan_grad_kernel(GatedProblem p, GatedGrads g, uint64_t* scratch, flo
   __shared__ float forward_b[kTileWaves][kTileChannels];
   const int wave = wave_id(), turn = kTileWaves - 1 - wave;  // its turn in the walk
   const int D = (int)p.channels;
-  const int64_t tile = tiles.chunks > 1 ? next_tile(scratch, &sh.tile) : blockIdx.x;
-  if (tile >= tiles.count()) return;
+  if (group_number() >= tiles.count()) return;
   int64_t col, part;
-  const int64_t chunk = tiles.chunks - 1 - divide(tile, tiles.cols, &col);
+  divide(group_number(), tiles.cols, &col);
+  const int64_t chunk = tiles.chunks > 1 ? tiles.chunks - 1 - draw_chunk(scratch, col, &sh.tile) : 0;
   const int64_t b = tiles.b0 + divide(col, tiles.parts, &part);
   const int ch = (int)part * kTileChannels + 2 * lane_id();
   const int have = D - ch >= 2 ? 2 : (D - ch == 1 ? 1 : 0);
