@@ -514,6 +514,64 @@ scan_status embedding_grad(const void* dout, const void* ids, void* dweight, int
                            scan_dtype id_dtype, scan_dtype out_dtype, float scale, void* scratch,
                            size_t scratch_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Beam search: what follows the last product of each token, and moves the
+ * states that the steps above keep.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * The `count` best continuations of each batch entry, over its beams and the
+ * vocabulary.  A continuation of beam j by token v has the score
+ *   S[j,v] = scores[b,j] + log softmax(logits[b,j,:])[v],
+ * formed in 64 bits.  Chosen are the greatest: of equal scores the lower beam
+ * first, in a beam the greater logit, then the lower token.
+ *   logits        [batch, beams, vocab] of `dtype` (SCAN_F32, SCAN_F16 or
+ *                 SCAN_BF16, else SCAN_ENOTSUP), contiguous along the vocabulary;
+ *                 logits_stride = {batch, beam} strides in elements
+ *   scores        float32 [batch, beams], the beams' own
+ *   finished      NULL, or uint8 [batch, beams]: a beam with a nonzero flag has one
+ *                 continuation, by end_token, whose score is the beam's own; its
+ *                 logits are not read
+ * A logit of -infinity, or one that is no number, is masked: its continuation has
+ * score -infinity, as has one whose score is no number.  One of +infinity has the
+ * whole probability (shared by all such).  Continuations of score -infinity are
+ * chosen last, in the order of beam and token, so that the outputs always hold
+ * `count` different ones.
+ *   1 <= beams <= 64 and 1 <= count <= 64 (else SCAN_ENOTSUP), count <= beams *
+ *   vocab, 1 <= vocab <= INT32_MAX, 0 <= batch <= INT32_MAX, 0 <= end_token <
+ *   vocab.
+ *   out_scores    float32 [batch, count], in descending order
+ *   parents       int32 [batch, count], the beam that goes on
+ *   tokens        int32 [batch, count], by which token
+ * Scratch needs no initialization.  Results do not depend on timing.
+ */
+typedef struct {
+    const void* logits;
+    const float* scores;
+    const uint8_t* finished;
+    int64_t batch, beams, vocab, count, end_token;
+    int64_t logits_stride[2];
+    scan_dtype dtype;
+} beam_select_args;
+size_t beam_select_scratch_bytes(const beam_select_args* args);
+scan_status beam_select(const beam_select_args* args, float* out_scores, int32_t* parents,
+                        int32_t* tokens, void* scratch, size_t scratch_bytes, void* stream);
+
+/*
+ * The beams' states follow them: in each of `tensors` arrays of [batch, beams]
+ * rows, new[b,j] = old[b, parents[b,j]] (a parent outside [0, beams) counts as j).
+ *   states, new_states   `tensors` device pointers each (arrays on the host):
+ *                        contiguous rows of row_bytes[i] bytes.  new_states[i] is
+ *                        states[i], which is then moved in place, or overlaps
+ *                        nothing of this call.
+ *   parents              int32 [batch, beams] on the device
+ *   1 <= beams <= 64 (else SCAN_ENOTSUP), 0 <= tensors <= 1024, 0 <= batch <=
+ *   INT32_MAX, no array of 2^47 bytes or more.
+ */
+scan_status beam_reorder(const void* const* states, void* const* new_states,
+                         const int64_t* row_bytes, int64_t tensors, const int32_t* parents,
+                         int64_t batch, int64_t beams, void* stream);
+
 /* Static string naming a status code (never NULL). */
 const char* scan_status_str(scan_status s);
 

@@ -39,6 +39,9 @@ Sequence operators (module ``sequence``, reached by the same names from here; ea
 described there): ``causal_conv``, ``causal_conv_grad``, ``causal_conv_step``,
 ``selective_scan``, ``selective_scan_grad``, ``selective_scan_step``, ``gated_scan``,
 ``gated_scan_grad``, ``gated_scan_step``, ``embedding``, ``embedding_grad``; module ``autograd`` has the differentiable forms.
+
+Beam search (module ``beam``, likewise): ``beam_select``, the best continuations over beams
+and vocabulary, and ``beam_reorder``, which moves the beams' states to where they go on.
 """
 import ctypes
 import os
@@ -63,12 +66,14 @@ EXPORTS = ("scan_rows", "scan_device", "scan_device_inclusive", "scan_device_scr
            "selective_scan_grad_scratch_bytes", "selective_scan_step", "gated_scan",
            "gated_scan_starts_bytes", "gated_scan_scratch_bytes", "gated_scan_grad",
            "gated_scan_grad_scratch_bytes", "gated_scan_step", "embedding",
-           "embedding_grad", "embedding_grad_scratch_bytes", "scan_status_str",
+           "embedding_grad", "embedding_grad_scratch_bytes", "beam_select",
+           "beam_select_scratch_bytes", "beam_reorder", "scan_status_str",
            "scan_last_hip_error")
 # entry points whose wrappers live in the module `sequence`, loaded on first use
 _SEQUENCE = ("causal_conv", "causal_conv_grad", "causal_conv_step", "selective_scan",
              "selective_scan_grad", "selective_scan_step", "gated_scan", "gated_scan_grad",
              "gated_scan_step", "embedding", "embedding_grad")
+_BEAM = ("beam_select", "beam_reorder")      # and in the module `beam`
 
 _lib = None
 
@@ -140,6 +145,10 @@ def __getattr__(name):
     if name in _SEQUENCE:
         from . import sequence
         globals()[name] = getattr(sequence, name)
+        return globals()[name]
+    if name in _BEAM:
+        from . import beam
+        globals()[name] = getattr(beam, name)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 

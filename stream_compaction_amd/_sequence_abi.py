@@ -1,4 +1,4 @@
-"""ctypes mirror of the sequence operators in ``include/scan.h`` (needs no torch)."""
+"""ctypes mirror of the sequence operators and of beam search in ``include/scan.h`` (needs no torch)."""
 import ctypes
 
 _vp, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
@@ -38,11 +38,18 @@ class GatedGrads(ctypes.Structure):
                 ("dinitial", _vp)]
 
 
+class BeamArgs(ctypes.Structure):
+    _fields_ = [("logits", _vp), ("scores", _vp), ("finished", _vp), ("batch", _i64),
+                ("beams", _i64), ("vocab", _i64), ("count", _i64), ("end_token", _i64),
+                ("logits_stride", _i64 * 2), ("dtype", _i32)]
+
+
 def declare(L):
     """C signatures of the sequence entry points on a loaded library."""
     sz, f32 = ctypes.c_size_t, ctypes.c_float
     conv, scan = ctypes.POINTER(ConvArgs), ctypes.POINTER(ScanArgs)
-    gated = ctypes.POINTER(GatedArgs)
+    gated, beam = ctypes.POINTER(GatedArgs), ctypes.POINTER(BeamArgs)
+    many = ctypes.POINTER(_vp)
     for name, args in (
             ("causal_conv", [conv, _vp, _vp, _vp]),
             ("causal_conv_grad", [conv, _vp, ctypes.POINTER(_i64), _vp, _vp, _vp, _vp, _vp, _vp,
@@ -55,6 +62,8 @@ def declare(L):
             ("gated_scan", [gated, _vp, _vp, _vp, _vp, sz, _vp]),
             ("gated_scan_grad", [gated, ctypes.POINTER(GatedGrads), _vp, sz, _vp]),
             ("gated_scan_step", [gated, _vp, _vp, _vp, _vp]),
+            ("beam_select", [beam, _vp, _vp, _vp, _vp, sz, _vp]),
+            ("beam_reorder", [many, many, ctypes.POINTER(_i64), _i64, _vp, _i64, _i64, _vp]),
             ("embedding", [_vp, _vp, _vp, _i64, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int, f32,
                            _vp]),
             ("embedding_grad", [_vp, _vp, _vp, _i64, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int,
@@ -68,6 +77,7 @@ def declare(L):
                        ("gated_scan_starts_bytes", [gated]),
                        ("gated_scan_scratch_bytes", [gated]),
                        ("gated_scan_grad_scratch_bytes", [gated]),
+                       ("beam_select_scratch_bytes", [beam]),
                        ("embedding_grad_scratch_bytes", [_i64, _i64, _i64])):
         getattr(L, name).argtypes = args
         getattr(L, name).restype = sz

@@ -1,0 +1,95 @@
+"""Beam search over the library: the choice of the best continuations, and the beams' states
+moved to where they go on.
+
+Thin wrappers over the C ABI (``include/scan.h`` has every definition and rule), in the manner
+of the sequence operators: they check shapes, types and devices, allocate what is not given, and
+pass pointers and the current HIP stream, which must be of the data's GPU.
+"""
+import ctypes
+
+import torch
+
+from . import check, lib
+from ._sequence_abi import BeamArgs
+from .sequence import _code, _like, _out, _queue, _require, _scratch
+
+_i64, _vp = ctypes.c_int64, ctypes.c_void_p
+
+
+def beam_select(logits, scores, count, finished=None, end_token=0, out_scores=None, parents=None,
+                tokens=None, scratch=None, stream=None):
+    """The ``count`` best continuations (1 to 64) of each batch entry over its beams (1 to 64) and
+    the vocabulary.
+
+    ``logits`` is ``[batch, beams, vocab]`` float32, float16 or bfloat16, contiguous along the
+    vocabulary, and ``scores`` (float32 ``[batch, beams]``) the beams' own.  A continuation's score
+    is its beam's plus the token's log softmax, formed in 64 bits.  ``finished`` (uint8 or bool
+    ``[batch, beams]``) marks beams that have ended: such a beam goes on by ``end_token`` alone, at
+    its own score.  Logits of -infinity (or NaN) are masked.
+
+    Returns ``(out_scores, parents, tokens)``, each ``[batch, count]`` (float32, int32, int32), the
+    best first; of equal scores the lower beam, then the greater logit, then the lower token.
+    """
+    _require(logits.dim() == 3, "logits must be [batch, beams, vocab]")
+    _require(logits.is_cuda, "logits must be a GPU tensor")
+    code, dev = _code(logits, "logits"), logits.get_device()
+    b, k, v = logits.shape
+    _require(v <= 1 or logits.stride(2) == 1, "logits must have a contiguous last axis")
+    count = int(count)
+    _require(count >= 1, "count must be at least 1")
+    sp = _like(scores, "scores", (b, k), torch.float32, dev)
+    fp = None
+    if finished is not None:
+        if finished.dtype is torch.bool:
+            finished = finished.view(torch.uint8)
+        fp = _like(finished, "finished", (b, k), torch.uint8, dev)
+    a = BeamArgs(logits.data_ptr(), sp, fp, b, k, v, count, int(end_token), logits.stride()[:2], code)
+    chosen = (b, count)
+    out_scores = _out(out_scores, "out_scores", chosen, torch.float32, scores, stream)
+    parents = _out(parents, "parents", chosen, torch.int32, scores, stream)
+    tokens = _out(tokens, "tokens", chosen, torch.int32, scores, stream)
+    L = lib()
+    scratch, room = _scratch(scratch, L.beam_select_scratch_bytes(a), scores, stream)
+    check(L.beam_select(a, out_scores.data_ptr(), parents.data_ptr(), tokens.data_ptr(),
+                        scratch.data_ptr(), room, _queue(stream, dev)))
+    return out_scores, parents, tokens
+
+
+def _row_bytes(t, what, b, k, dev):
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous tensors on cuda:{dev}")
+    shape = t.shape
+    if not (shape[:2] == (b, k) or (t.dim() > 0 and shape[0] == b * k)):
+        raise ValueError(f"{what} must be [batch, beams, ...] or [batch * beams, ...]")
+    rows = b * k
+    return t.numel() // rows * t.element_size() if rows else 0
+
+
+def beam_reorder(states, parents, new_states=None, stream=None):
+    """The beams' states follow them: ``new[b, j] = old[b, parents[b, j]]`` in each of ``states``,
+    a list of contiguous tensors of any type, ``[batch, beams, ...]`` or ``[batch * beams, ...]``
+    (at most 1024, moved together).
+
+    ``parents`` is int32 ``[batch, beams]`` (1 to 64 beams); an entry outside ``[0, beams)`` counts
+    as the beam's own.  The states are moved in place, where beams that go on as themselves are
+    neither read nor written, or into ``new_states``, tensors of the same shapes and types that
+    overlap nothing.  Returns the list of the moved tensors.
+    """
+    _require(parents.dim() == 2 and parents.is_cuda, "parents must be a GPU tensor [batch, beams]")
+    dev = parents.get_device()
+    b, k = parents.shape
+    pp = _like(parents, "parents", (b, k), torch.int32, dev)
+    states = list(states)
+    out = states if new_states is None else list(new_states)
+    _require(len(out) == len(states), "new_states must have as many tensors as states")
+    n = len(states)
+    _require(n <= 1024, "at most 1024 states")
+    from_, to, size = (_vp * n)(), (_vp * n)(), (_i64 * n)()
+    for i, t in enumerate(states):
+        size[i] = _row_bytes(t, "states", b, k, dev)
+        from_[i] = to[i] = t.data_ptr()
+    if new_states is not None:
+        for i, (t, o) in enumerate(zip(states, out)):
+            to[i] = _like(o, "new_states", t.shape, t.dtype, dev)
+    check(lib().beam_reorder(from_, to, size, n, pp, b, k, _queue(stream, dev)))
+    return out
