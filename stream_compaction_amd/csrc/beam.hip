@@ -44,32 +44,48 @@ __device__ __forceinline__ double key_value64(uint64_t k) {
   return __builtin_bit_cast(double, (k >> 63) ? k & 0x7fffffffffffffffull : ~k);
 }
 
-// 2^t for -1000 <= t <= 0, to 4e-11 of it: t = n + f with |f| <= 1/2, a polynomial of
-// degree 7 (least maximum of the relative error, fitted there), n to the exponent.
+// 2^t for -1000 <= t <= 1000, to 5e-11 of it: t = n + f with |f| <= 1/2, a polynomial
+// of degree 7 that is 1 at 0 (least maximum of the relative error, fitted there), n to
+// the exponent.
 __device__ __forceinline__ double exp2_64(double t) {
   const double shift = 6755399441055744.0;   // 1.5 x 2^52: the sum's last digits are n
   const double r = t + shift, f = t - (r - shift);
-  double v = __builtin_fma(f, 1.5201921452474336e-05, 0.00015469291140648007);
-  v = __builtin_fma(f, v, 0.0013333922564236862);
-  v = __builtin_fma(f, v, 0.009618027253677558);
-  v = __builtin_fma(f, v, 0.05550410353447074);
-  v = __builtin_fma(f, v, 0.24022651198157435);
-  v = __builtin_fma(f, v, 0.6931471807284468);
-  v = __builtin_fma(f, v, 0.9999999999616814);
+  double v = __builtin_fma(f, 1.5196156538658058e-05, 0.00015466756316955186);
+  v = __builtin_fma(f, v, 0.0013333935055508488);
+  v = __builtin_fma(f, v, 0.009618038132060329);
+  v = __builtin_fma(f, v, 0.05550410365991636);
+  v = __builtin_fma(f, v, 0.240226510665611);
+  v = __builtin_fma(f, v, 0.6931471807045305);
+  v = __builtin_fma(f, v, 1.0);
   const uint64_t b = __builtin_bit_cast(uint64_t, v) + (__builtin_bit_cast(uint64_t, r) << 52);
   return __builtin_bit_cast(double, b);
 }
 constexpr double kLog2e64 = 1.4426950408889634074;
 
+// All lanes' sum and maximum, in every lane.
 __device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int m = 32; m > 0; m /= 2) v += __shfl_xor(v, m);
-  return v;
+  return readlane(wave_scan_incl<Op::Add>(v), 63);
 }
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int m = 32; m > 0; m /= 2) v = __builtin_fmaxf(v, __shfl_xor(v, m));
-  return v;
+  return readlane(wave_scan_incl<Op::Max>(v), 63);
+}
+
+// The ranks of n entries of `list` by `threads` threads, added up in `rank`, which is
+// zero: several threads an entry where there are fewer entries than threads.  The
+// caller waits before it reads them.
+template <class T>
+__device__ __forceinline__ void add_ranks(const T* list, uint32_t* rank, uint32_t n, uint32_t threads) {
+  uint32_t wide = 32;
+  while (wide < n && wide < threads) wide *= 2;
+  const uint32_t parts = threads / wide, part = threadIdx.x / wide;
+  for (uint32_t i = threadIdx.x % wide; i < n; i += wide) {
+    const T mine = list[i];
+    uint32_t above = 0;
+#pragma unroll 4
+    for (uint32_t k = part; k < n; k += parts) above += list[k] > mine ? 1u : 0u;
+    if (above != 0)
+      __hip_atomic_fetch_add(&rank[i], above, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+  }
 }
 
 // The greatest T, a multiple of 2^LOW, that at least `count` lanes' keys are not below.
@@ -85,18 +101,21 @@ __device__ __forceinline__ uint32_t lanes_bound(uint32_t key, int count) {
   return (t >> 31) ? t : t | ((1u << LOW) - 1);
 }
 
-struct Found {                               // of a segment
-  float most;
-  float pad;
+// Of a segment: its greatest logit, and its sum of exp(l - from).
+struct Found {
+  float most, from;
   double sum;
 };
+// Logits up to here in size need no maximum taken off before the exponential: in 64
+// bits their exponentials and sums stay inside the range, 260 digits from its ends.
+constexpr float kPlainLogit = 600.0f;
 
 struct SegmentShared {
-  uint64_t list[kListed];
+  uint64_t by_wave[kBeamWaves][kListed / kBeamWaves], list[kListed];
+  uint32_t rank[kListed];
   double sum[kBeamWaves];
   float most[kBeamWaves];
-  uint32_t bound[kBeamWaves], part[kBeamWaves];
-  uint32_t listed;
+  uint32_t bound[kBeamWaves], part[kBeamWaves], listed[kBeamWaves];
 };
 
 // A workgroup's sum of a number of each thread.
@@ -114,12 +133,12 @@ __device__ __forceinline__ uint32_t group_sum(uint32_t v, SegmentShared& s, int 
 
 }  // namespace
 
-// A segment: 256 NV vectors of 16 bytes.  Entries are (order_key << 32 | ~token), so that the greater entry
+// A segment: `length` vectors of 16 bytes, at most 256 NV.  Entries are (order_key << 32 | ~token), so that the greater entry
 // comes first; 0 is none.
 template <class F, int NV>
 __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem p, uint64_t* best,
                                                                    Found* found, int64_t row0,
-                                                                   int64_t segments) {
+                                                                   int64_t segments, int64_t length) {
   using S = typename F::S;
   constexpr int E = kVecElems<F>;
   constexpr int kBits = std::is_same_v<F, FmtBF16> ? 16 : (std::is_same_v<F, FmtF16> ? 13 : 0);
@@ -130,43 +149,63 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
   const int64_t b = divide(row, p.beams, &j);
   if (p.finished != nullptr && p.finished[row] != 0) return;     // none of its logits is asked for
   const S* logits = (const S*)p.logits + b * p.logits_batch + j * p.logits_beam;
-  if (tid == 0) sh.listed = 0;
   // The row's last vector ends with it and may begin among those of the one before,
   // which are left out.  What a thread adds up depends on the vocabulary alone, not
   // on where the row lies: equal rows have equal sums.
-  const int64_t v0 = seg * (kBeamThreads * NV) + tid;
+  const int64_t v0 = seg * length + tid, vend = (seg + 1) * length;
   auto begin = [&](int64_t vec) { return vec * E < p.vocab - E ? vec * E : p.vocab - E; };
-  float v[NV][E];
+  using IO = RowIO<F, E>;
+  u32x4 raw[NV];                             // as they are: 16-bit logits two to a register
   if (p.vocab >= E) {
-    u32x4 raw[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      raw[i] = RowIO<F, E>::load_any(logits + begin(v0 + i * kBeamThreads), E);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      RowIO<F, E>::unpack(raw[i], v[i]);
-      const int64_t skip = (v0 + i * kBeamThreads) * E - begin(v0 + i * kBeamThreads);
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        v[i][e] = e >= skip && v[i][e] == v[i][e] ? v[i][e] : -__builtin_huge_valf();
-    }
+    for (int i = 0; i < NV; ++i) raw[i] = IO::load_any(logits + begin(v0 + i * kBeamThreads), E);
   } else {                                   // less than a vector: the first thread's
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      float v[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        v[i][e] = -__builtin_huge_valf();
-        if (i == 0 && v0 == 0 && e >= E - p.vocab) {
-          const float l = widen<F>(logits[e - (E - p.vocab)]);
-          v[i][e] = l == l ? l : v[i][e];
-        }
+        v[e] = -__builtin_huge_valf();
+        if (i == 0 && tid == 0 && e >= E - p.vocab) v[e] = widen<F>(logits[e - (E - p.vocab)]);
       }
+      raw[i] = IO::pack(v);
+    }
   }
-  float most = v[0][0];
+  // Vector i's logits.  A NaN is smaller and greater than nothing and equal to
+  // nothing, and a maximum is the other's, so that it counts for nothing below.
+  auto values = [&](int i, float (&v)[E]) {
+    uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+    for (int k = 0; k < 4; ++k) materialize(w[k]);         // unpacked each time, not kept so
+    IO::unpack(u32x4{w[0], w[1], w[2], w[3]}, v);
+  };
+  // maximum and sum of exponentials at once, for logits of ordinary size
+  // (what is 2^-1000 adds nothing, as do masked logits)
+  auto exponential = [&](float v, double off) {
+    return exp2_64(__builtin_fmax(__builtin_fma((double)v, kLog2e64, off), -1000.0));
+  };
+  float most = -__builtin_huge_valf();
+  double sum = 0.0;
 #pragma unroll
-    for (int e = 0; e < E; ++e) most = __builtin_fmaxf(most, v[i][e]);
+  for (int i = 0; i < NV; ++i) {
+    float v[E];
+    const int64_t vec = v0 + i * kBeamThreads, skip = vec < vend ? vec * E - begin(vec) : E;
+    if (skip > 0 && p.vocab >= E) {
+      IO::unpack(raw[i], v);
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = e >= skip ? v[e] : -__builtin_huge_valf();
+      raw[i] = IO::pack(v);
+    }
+    values(i, v);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      most = __builtin_fmaxf(most, v[e]);
+      sum += exponential(v[e], 0.0);
+    }
+    // vector after vector: each when it is there, with the registers of one
+    materialize(sum);
+    __builtin_amdgcn_sched_barrier(0);
+  }
   const uint32_t mine = order_key(most);
   const uint32_t bound = lanes_bound<kBits>(mine, count);
   const float wmost = wave_max(most);
@@ -185,79 +224,111 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
   uint64_t* out = best + (row * segments + seg) * count;
   if (top == -__builtin_huge_valf()) {                           // all masked
     if (tid < count) out[tid] = 0;
-    if (tid == 0) found[row * segments + seg] = Found{top, 0.0f, 0.0};
+    if (tid == 0) found[row * segments + seg] = Found{top, top, 0.0};
     return;
   }
   // what is above the bound, then what is equal to it
   least = least > kMaskedKey ? least : kMaskedKey + 1;
-  auto entry = [&](int i, int e) {
+  auto entry = [&](int i, int e, float v) {
     const uint32_t token = (uint32_t)(begin(v0 + i * kBeamThreads) + e);
-    return ((uint64_t)order_key(v[i][e]) << 32) | (uint32_t)~token;
+    return ((uint64_t)order_key(v) << 32) | (uint32_t)~token;
   };
   float edge = key_value(least);
+  // each wave lists what is above the edge for itself: how many there were
   auto above = [&]() {
+    uint32_t n = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      float v[E];
+      values(i, v);
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (v[i][e] > edge) {
-          const uint32_t k = __hip_atomic_fetch_add(&sh.listed, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-          if (k < (uint32_t)kListed) sh.list[k] = entry(i, e);
-        }
+      for (int e = 0; e < E; ++e) {
+        const uint64_t on = __ballot(v[e] > edge);
+        if (on == 0) continue;
+        const uint32_t k = n + (uint32_t)__builtin_popcountll(on & ((1ull << lane_id()) - 1));
+        if (v[e] > edge && k < (uint32_t)(kListed / kBeamWaves)) sh.by_wave[wave][k] = entry(i, e, v[e]);
+        n += (uint32_t)__builtin_popcountll(on);
+      }
+    }
+    return n;
   };
-  if (most > edge) above();
-  double sum = 0.0;
-  if (top == __builtin_huge_valf()) {
+  uint32_t listed = wmost > edge ? above() : 0;
+  float from = 0.0f;
+  if (!(__builtin_fabsf(top) <= kPlainLogit)) {
+    const bool infinite = top == __builtin_huge_valf();
+    const double off = infinite ? 0.0 : -(double)top * kLog2e64;
+    from = top;
+    sum = 0.0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      float v[E];
+      values(i, v);
 #pragma unroll
-      for (int e = 0; e < E; ++e) sum += v[i][e] == top ? 1.0 : 0.0;
-  } else {
-    const double off = -(double)top * kLog2e64;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        sum += exp2_64(__builtin_fmax(__builtin_fma((double)v[i][e], kLog2e64, off), -1000.0));
+      for (int e = 0; e < E; ++e) {
+        // (beside an infinite logit: 2^0 for each such, nothing for others)
+        const float l = infinite ? (v[e] == top ? 0.0f : -__builtin_huge_valf()) : v[e];
+        sum += exponential(l, off);
+      }
+      materialize(sum);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
   sum = wave_sum(sum);
-  if (lane_id() == 0) sh.sum[wave] = sum;
+  if (lane_id() == 0) {
+    sh.sum[wave] = sum;
+    sh.listed[wave] = listed;
+  }
+  for (int i = tid; i < kListed; i += kBeamThreads) sh.rank[i] = 0;
   __syncthreads();
   if (tid == 0) {
     double all = sh.sum[0];
 #pragma unroll
     for (int w = 1; w < kBeamWaves; ++w) all += sh.sum[w];
-    found[row * segments + seg] = Found{top, 0.0f, all};
+    found[row * segments + seg] = Found{top, from, all};
   }
-  uint32_t n = sh.listed;
-  if (n > (uint32_t)kListed) {
+  bool over = false;
+#pragma unroll
+  for (int w = 0; w < kBeamWaves; ++w) over |= sh.listed[w] > (uint32_t)(kListed / kBeamWaves);
+  if (over) {
     // too much above the bound (great logits side by side): the count-th greatest
     // itself, bit by bit
     uint32_t t = 0;
     for (int bit = 31; bit >= 0; --bit) {
       const uint32_t c = t | (1u << bit);
+      const float low = key_value(c > kMaskedKey ? c : kMaskedKey + 1);
       uint32_t k = 0;
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
+      for (int i = 0; i < NV; ++i) {
+        float v[E];
+        values(i, v);
 #pragma unroll
-        for (int e = 0; e < E; ++e) k += order_key(v[i][e]) >= c ? 1u : 0u;
+        for (int e = 0; e < E; ++e) k += v[e] >= low ? 1u : 0u;
+      }
       if (group_sum(k, sh, wave) >= (uint32_t)count) t = c;
     }
     edge = key_value(t > kMaskedKey ? t : kMaskedKey + 1);
-    if (tid == 0) sh.listed = 0;
+    listed = above();                        // fewer than `count`
     __syncthreads();
-    above();
+    if (lane_id() == 0) sh.listed[wave] = listed;
     __syncthreads();
-    n = sh.listed;
   }
+  uint32_t n = 0, place = 0;                 // the waves' lists, one behind the other
+#pragma unroll
+  for (int w = 0; w < kBeamWaves; ++w) {
+    place += w < wave ? sh.listed[w] : 0;
+    n += sh.listed[w];
+  }
+  for (uint32_t i = lane_id(); i < listed; i += 64) sh.list[place + i] = sh.by_wave[wave][i];
   if (n < (uint32_t)count) {
     // those equal to the bound, in token order, as many as are asked for
     uint32_t open = (uint32_t)count - n, taken = n;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
+      float v[E];
+      values(i, v);
       uint32_t k = 0;
 #pragma unroll
-      for (int e = 0; e < E; ++e) k += v[i][e] == edge ? 1u : 0u;
+      for (int e = 0; e < E; ++e) k += v[e] == edge ? 1u : 0u;
       uint32_t before = wave_scan_incl<Op::Add>(k);
       __syncthreads();
       if (lane_id() == 63) sh.part[wave] = before;
@@ -271,8 +342,8 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
       }
 #pragma unroll
       for (int e = 0; e < E; ++e)
-        if (v[i][e] == edge) {
-          if (before < open) sh.list[taken + before] = entry(i, e);
+        if (v[e] == edge) {
+          if (before < open) sh.list[taken + before] = entry(i, e, v[e]);
           ++before;
         }
       const uint32_t got = all < open ? all : open;
@@ -282,12 +353,10 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
     n = taken;
   }
   __syncthreads();
-  for (uint32_t i = tid; i < n; i += kBeamThreads) {
-    const uint64_t mine64 = sh.list[i];
-    uint32_t rank = 0;
-    for (uint32_t k = 0; k < n; ++k) rank += sh.list[k] > mine64 ? 1u : 0u;
-    if (rank < (uint32_t)count) out[rank] = mine64;
-  }
+  add_ranks(sh.list, sh.rank, n, kBeamThreads);
+  __syncthreads();
+  for (uint32_t i = tid; i < n; i += kBeamThreads)
+    if (sh.rank[i] < (uint32_t)count) out[sh.rank[i]] = sh.list[i];
   if (tid >= (int)n && tid < count) out[tid] = 0;
 }
 
@@ -296,11 +365,10 @@ namespace {
 // A candidate in the order of the choice: score, lower beam, greater logit, lower token.
 struct Candidate {
   uint64_t score;                            // order_key64; 0 is none
-  uint32_t beam;
-  uint32_t pad;
   uint64_t entry;
+  uint32_t beam;
 };
-__device__ __forceinline__ bool beats(const Candidate& a, const Candidate& b) {
+__device__ __forceinline__ bool operator>(const Candidate& a, const Candidate& b) {
   if (a.score != b.score) return a.score > b.score;
   if (a.beam != b.beam) return a.beam < b.beam;
   return a.entry > b.entry;
@@ -308,7 +376,8 @@ __device__ __forceinline__ bool beats(const Candidate& a, const Candidate& b) {
 
 struct JoinShared {
   Candidate list[kJoined];
-  double lse[64];                            // log of the sum of exponentials
+  uint32_t rank[kJoined];
+  double lse[64];                            // log of the sum of exponentials of the logits
   float most[64], score[64];
   uint32_t bound[kJoinWaves];
   uint32_t listed;
@@ -324,36 +393,50 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(BeamProblem p, 
   __shared__ JoinShared sh;
   const int wave = wave_id(), tid = (int)threadIdx.x, count = (int)p.count, beams = (int)p.beams;
   const int64_t b = b0 + blockIdx.x, row0 = b * beams;
+  const int64_t per = segments * count, total = per * beams;
+  // a thread's first candidates, read while the beams' sums are joined
+  constexpr int R = 4;
+  uint64_t held[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t i = tid + r * kJoinThreads;
+    held[r] = best[row0 * per + (i < total ? i : total - 1)];
+  }
   if (tid == 0) sh.listed = 0;
+  for (int i = tid; i < kJoined; i += kJoinThreads) sh.rank[i] = 0;
   for (int j = wave; j < beams; j += kJoinWaves) {
     const Found* f = found + (row0 + j) * segments;
     const bool done = p.finished != nullptr && p.finished[row0 + j] != 0;
-    float most = -__builtin_huge_valf();
+    float most = -__builtin_huge_valf(), from = most;
     double sum = 0.0;
     if (!done) {
-      for (int64_t s = lane_id(); s < segments; s += 64) most = __builtin_fmaxf(most, f[s].most);
-      most = wave_max(most);
       for (int64_t s = lane_id(); s < segments; s += 64) {
-        const float m = f[s].most;
+        most = __builtin_fmaxf(most, f[s].most);
+        from = __builtin_fmaxf(from, f[s].from);
+      }
+      most = wave_max(most);
+      from = wave_max(from);
+      for (int64_t s = lane_id(); s < segments; s += 64) {
+        const float m = f[s].from;
         const double part = f[s].sum;
-        if (m == most) sum += part;
-        else if (m > -__builtin_huge_valf()) sum += part * exp((double)m - (double)most);
+        if (m == from) sum += part;
+        else if (m > -__builtin_huge_valf()) sum += part * exp((double)m - (double)from);
       }
       sum = wave_sum(sum);
     }
     if (lane_id() == 0) {
       sh.most[j] = most;
-      sh.lse[j] = done ? 0.0 : log(sum);
+      // (beside an infinite logit the sum is the number of such)
+      sh.lse[j] = done ? 0.0 : log(sum) + (most == __builtin_huge_valf() ? 0.0 : (double)from);
       sh.score[j] = p.scores[row0 + j];
     }
   }
   __syncthreads();
-  const int64_t per = segments * count, total = per * beams;
-  // candidate i of the batch entry
-  auto candidate = [&](int64_t i) {
+  // candidate i of the batch entry, whose entry is known
+  auto candidate = [&](int64_t i, uint64_t entry) {
     int64_t k;
     const int j = (int)divide(i, per, &k);
-    Candidate c{0, (uint32_t)j, 0, 0};
+    Candidate c{0, entry, (uint32_t)j};
     const double base = (double)sh.score[j];
     double s;
     if (p.finished != nullptr && p.finished[row0 + j] != 0) {
@@ -361,17 +444,22 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(BeamProblem p, 
       c.entry = (uint32_t)~(uint32_t)p.end_token;
       s = base;
     } else {
-      c.entry = best[row0 * per + i];
-      if (c.entry == 0) return c;
-      const float l = key_value((uint32_t)(c.entry >> 32)), m = sh.most[j];
-      s = base + ((l == m ? 0.0 : (double)l - (double)m) - sh.lse[j]);
+      if (entry == 0) return c;
+      const float l = key_value((uint32_t)(entry >> 32)), m = sh.most[j];
+      s = base + ((m < __builtin_huge_valf() ? (double)l : (l == m ? 0.0 : -__builtin_huge_val())) - sh.lse[j]);
     }
     if (s > -__builtin_huge_val()) c.score = order_key64(s);      // (no NaN)
     return c;
   };
-  uint64_t mine = 0;
-  for (int64_t i = tid; i < total; i += kJoinThreads) {
-    const uint64_t s = candidate(i).score;
+  uint64_t mine = 0, first[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t i = tid + r * kJoinThreads;
+    first[r] = i < total ? candidate(i, held[r]).score : 0;
+    mine = mine > first[r] ? mine : first[r];
+  }
+  for (int64_t i = tid + R * kJoinThreads; i < total; i += kJoinThreads) {
+    const uint64_t s = candidate(i, best[row0 * per + i]).score;
     mine = mine > s ? mine : s;
   }
   const uint32_t bound = lanes_bound<0>((uint32_t)(mine >> 32), count);
@@ -380,36 +468,43 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(BeamProblem p, 
   uint32_t least = 1;
 #pragma unroll
   for (int w = 0; w < kJoinWaves; ++w) least = least > sh.bound[w] ? least : sh.bound[w];
-  if ((uint32_t)(mine >> 32) >= least)
-    for (int64_t i = tid; i < total; i += kJoinThreads) {
-      const Candidate c = candidate(i);
-      if ((uint32_t)(c.score >> 32) < least) continue;
-      const uint32_t k = __hip_atomic_fetch_add(&sh.listed, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-      if (k < (uint32_t)kJoined) sh.list[k] = c;
+  auto list = [&](const Candidate& c) {
+    const uint32_t k = __hip_atomic_fetch_add(&sh.listed, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    if (k < (uint32_t)kJoined) sh.list[k] = c;
+  };
+  if ((uint32_t)(mine >> 32) >= least) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if ((uint32_t)(first[r] >> 32) >= least) list(candidate(tid + r * kJoinThreads, held[r]));
+    for (int64_t i = tid + R * kJoinThreads; i < total; i += kJoinThreads) {
+      const Candidate c = candidate(i, best[row0 * per + i]);
+      if ((uint32_t)(c.score >> 32) >= least) list(c);
     }
+  }
   __syncthreads();
   uint32_t n = sh.listed;
   if (n > (uint32_t)kJoined) {
     // too many: one after the other, the best of those behind the one before
-    Candidate last{~0ull, 0, 0, ~0ull};
+    Candidate last{~0ull, ~0ull, 0};
     n = 0;
     for (int k = 0; k < count; ++k) {
-      Candidate top{0, 0, 0, 0};
+      Candidate top{0, 0, 0};
       for (int64_t i = tid; i < total; i += kJoinThreads) {
-        const Candidate c = candidate(i);
-        if (c.score != 0 && beats(last, c) && beats(c, top)) top = c;
+        const Candidate c = candidate(i, best[row0 * per + i]);
+        if (c.score != 0 && last > c && c > top) top = c;
       }
       for (int m = 32; m > 0; m /= 2) {
-        Candidate o{__shfl_xor((unsigned long long)top.score, m), (uint32_t)__shfl_xor((int)top.beam, m), 0,
-                    __shfl_xor((unsigned long long)top.entry, m)};
-        if (beats(o, top)) top = o;
+        const Candidate o{__shfl_xor((unsigned long long)top.score, m),
+                          __shfl_xor((unsigned long long)top.entry, m),
+                          (uint32_t)__shfl_xor((int)top.beam, m)};
+        if (o > top) top = o;
       }
       __syncthreads();
       if (lane_id() == 0) sh.wave_best[wave] = top;
       __syncthreads();
       top = sh.wave_best[0];
       for (int w = 1; w < kJoinWaves; ++w)
-        if (beats(sh.wave_best[w], top)) top = sh.wave_best[w];
+        if (sh.wave_best[w] > top) top = sh.wave_best[w];
       if (top.score == 0) break;
       if (tid == 0) sh.list[n] = top;
       ++n;
@@ -417,11 +512,12 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(BeamProblem p, 
     }
     __syncthreads();
   }
+  add_ranks(sh.list, sh.rank, n, kJoinThreads);
+  __syncthreads();
   const int64_t out = b * count;
   for (uint32_t i = tid; i < n; i += kJoinThreads) {
     const Candidate c = sh.list[i];
-    uint32_t rank = 0;
-    for (uint32_t k = 0; k < n; ++k) rank += beats(sh.list[k], c) ? 1u : 0u;
+    const uint32_t rank = sh.rank[i];
     if (rank >= (uint32_t)count) continue;
     scores[out + rank] = (float)key_value64(c.score);
     parents[out + rank] = (int32_t)c.beam;
@@ -450,48 +546,66 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(BeamProblem p, 
 
 namespace {
 
-// Vectors a thread: as many as still leave a workgroup for every CU, so that a few
-// rows are read by the whole chip.
-template <class F> int beam_vectors(const BeamProblem& p) {
+// How rows are cut: segments of equal length, at most 8 vectors a thread.  A
+// workgroup costs what 2 (float32: 4) vectors a thread cost beside its own, and a CU
+// goes through its workgroups one after the other as far as arithmetic is concerned,
+// the first few waits apart.  So a few rows are cut fine, for the whole chip, many
+// rows coarse, where their length fits whole vectors best: 256 rows of 50000 in
+// bfloat16 take 5 segments of 1250.
+struct Cut { int64_t segments, length; int vectors; };
+template <class F> Cut beam_cut(const BeamProblem& p) {
   const int64_t vecs = (p.vocab + kVecElems<F> - 1) / kVecElems<F>, rows = p.batch * p.beams;
-  for (int nv = 4; nv > 1; nv /= 2)
-    if (rows * (vecs / (kBeamThreads * nv)) >= 512) return nv;
-  return 1;
-}
-template <class F> int64_t beam_segments(const BeamProblem& p, int nv) {
-  const int64_t vecs = (p.vocab + kVecElems<F> - 1) / kVecElems<F>;
-  return (vecs + kBeamThreads * nv - 1) / (kBeamThreads * nv);
+  const int64_t least = (vecs + 8 * kBeamThreads - 1) / (8 * kBeamThreads);
+  const int64_t most = (vecs + kBeamThreads - 1) / kBeamThreads;
+  constexpr int64_t own = sizeof(typename F::S) == 4 ? 4 : 2;
+  Cut best{};
+  int64_t lowest = 0;
+  for (int64_t s = least; s <= most; ++s) {
+    const int64_t length = (vecs + s - 1) / s, nv = (length + kBeamThreads - 1) / kBeamThreads;
+    const int64_t cost = (own + nv) * ((rows * s + 255) / 256 + 4);
+    if (best.segments == 0 || cost < lowest) {
+      best = Cut{(vecs + length - 1) / length, length, (int)nv};
+      lowest = cost;
+    }
+    if (s >= least + 64 && s < most) s = most - 1;     // (a very long row: no need to look at all)
+  }
+  return best;
 }
 
 template <class F, int NV>
 hipError_t launch_segments(const BeamProblem& p, uint64_t* best, Found* found, int64_t segments,
-                           hipStream_t stream) {
+                           int64_t length, hipStream_t stream) {
   const int64_t rows = p.batch * p.beams, most = (1ll << 22) / segments, step = most < 1 ? 1 : most;
   for (int64_t r = 0; r < rows; r += step) {
     const int64_t n = rows - r < step ? rows - r : step;
     beam_segment_kernel<F, NV><<<dim3((unsigned)(n * segments)), dim3(kBeamThreads), 0, stream>>>(
-        p, best, found, r, segments);
+        p, best, found, r, segments, length);
   }
   return hipGetLastError();
 }
 
 template <class F> size_t beam_scratch_f(const BeamProblem& p) {
-  const size_t segs = (size_t)(p.batch * p.beams) * (size_t)beam_segments<F>(p, beam_vectors<F>(p));
+  const size_t segs = (size_t)(p.batch * p.beams) * (size_t)beam_cut<F>(p).segments;
   return segs * (sizeof(Found) + 8 * (size_t)p.count);
 }
 
 template <class F>
 hipError_t launch_beam_f(const BeamProblem& p, float* scores, int32_t* parents, int32_t* tokens,
                          void* scratch, hipStream_t stream) {
-  const int nv = beam_vectors<F>(p);
-  const int64_t segments = beam_segments<F>(p, nv);
+  const Cut cut = beam_cut<F>(p);
+  const int64_t segments = cut.segments;
   Found* found = (Found*)scratch;
   uint64_t* best = (uint64_t*)(found + p.batch * p.beams * segments);
   hipError_t e;
-  switch (nv) {
-    case 4: e = launch_segments<F, 4>(p, best, found, segments, stream); break;
-    case 2: e = launch_segments<F, 2>(p, best, found, segments, stream); break;
-    default: e = launch_segments<F, 1>(p, best, found, segments, stream); break;
+  switch (cut.vectors) {
+    case 8: e = launch_segments<F, 8>(p, best, found, segments, cut.length, stream); break;
+    case 7: e = launch_segments<F, 7>(p, best, found, segments, cut.length, stream); break;
+    case 6: e = launch_segments<F, 6>(p, best, found, segments, cut.length, stream); break;
+    case 5: e = launch_segments<F, 5>(p, best, found, segments, cut.length, stream); break;
+    case 4: e = launch_segments<F, 4>(p, best, found, segments, cut.length, stream); break;
+    case 3: e = launch_segments<F, 3>(p, best, found, segments, cut.length, stream); break;
+    case 2: e = launch_segments<F, 2>(p, best, found, segments, cut.length, stream); break;
+    default: e = launch_segments<F, 1>(p, best, found, segments, cut.length, stream); break;
   }
   if (e != hipSuccess) return e;
   for (int64_t b = 0; b < p.batch; b += 1 << 21) {
@@ -545,12 +659,20 @@ template <class V> __device__ __forceinline__ V load_loose(uintptr_t a) {
   typedef V Loose __attribute__((aligned(1)));
   return *gptr<const Loose>(a);
 }
-template <class V> __device__ __forceinline__ void store_loose(uintptr_t a, V v) {
+template <bool PAST, class V> __device__ __forceinline__ void store_loose(uintptr_t a, V v) {
   typedef V Loose __attribute__((aligned(1)));
-  *gptr<Loose>(a) = v;
+  if constexpr (PAST) {
+    __builtin_nontemporal_store(v, gptr<Loose>(a));
+  } else {
+    *gptr<Loose>(a) = v;
+  }
 }
 
-template <int NB, class V>
+// States that the 256 MB last-level cache cannot hold are stored past the caches: 587
+// MB of new states 164 us, by other stores 172.
+inline bool states_past_caches(int64_t bytes) { return bytes > (256ll << 20); }
+
+template <int NB, bool PAST, class V>
 __device__ __forceinline__ void move_column(uintptr_t from, uintptr_t to, int64_t bytes, const int* parent,
                                             uint64_t moves) {
   // (every load is issued: a register that only a branch writes costs many more)
@@ -559,12 +681,12 @@ __device__ __forceinline__ void move_column(uintptr_t from, uintptr_t to, int64_
   for (int j = 0; j < NB; ++j) v[j] = load_loose<V>(from + (uintptr_t)(parent[j] * bytes));
 #pragma unroll
   for (int j = 0; j < NB; ++j)
-    if ((moves >> j) & 1) store_loose<V>(to + (uintptr_t)(j * bytes), v[j]);
+    if ((moves >> j) & 1) store_loose<PAST, V>(to + (uintptr_t)(j * bytes), v[j]);
 }
 
 }  // namespace
 
-template <int NB, class V>
+template <int NB, class V, bool PAST>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4, 8)))
 void beam_reorder_kernel(Moves m, const int32_t* parents, int64_t b0,
                                                            int beams) {
@@ -594,10 +716,10 @@ void beam_reorder_kernel(Moves m, const int32_t* parents, int64_t b0,
   const uintptr_t skip = (uintptr_t)(b * beams * bytes);
   const uintptr_t from = m.from[t] + skip, to = m.to[t] + skip;
   if (col < whole) {
-    move_column<NB, V>(from + (uintptr_t)col * sizeof(V), to + (uintptr_t)col * sizeof(V), bytes, parent, moves);
+    move_column<NB, PAST, V>(from + (uintptr_t)col * sizeof(V), to + (uintptr_t)col * sizeof(V), bytes, parent, moves);
   } else if (col - whole < bytes % (int64_t)sizeof(V)) {         // a row's last bytes, one a thread
     const uintptr_t at = (uintptr_t)(whole * (int64_t)sizeof(V) + (col - whole));
-    move_column<NB, uint8_t>(from + at, to + at, bytes, parent, moves);
+    move_column<NB, PAST, uint8_t>(from + at, to + at, bytes, parent, moves);
   }
 }
 
@@ -606,6 +728,9 @@ static hipError_t launch_moves(const void* const* states, void* const* new_state
                                int64_t tensors, const int32_t* parents, int64_t batch, int64_t beams,
                                hipStream_t stream) {
   constexpr int64_t kMostBlocks = 1ll << 23;
+  int64_t all = 0;
+  for (int64_t t = 0; t < tensors; ++t) all += batch * beams * row_bytes[t];
+  const bool past = states_past_caches(all);
   for (int64_t t = 0; t < tensors;) {
     Moves m{};
     int64_t blocks = 0;
@@ -625,7 +750,11 @@ static hipError_t launch_moves(const void* const* states, void* const* new_state
     const int64_t step = blocks >= kMostBlocks ? 1 : kMostBlocks / blocks;
     for (int64_t b = 0; b < batch; b += step) {
       const int64_t n = batch - b < step ? batch - b : step;
-      beam_reorder_kernel<NB, V><<<dim3((unsigned)(n * blocks)), dim3(256), 0, stream>>>(m, parents, b, (int)beams);
+      const dim3 grid((unsigned)(n * blocks));
+      if (past)
+        beam_reorder_kernel<NB, V, true><<<grid, dim3(256), 0, stream>>>(m, parents, b, (int)beams);
+      else
+        beam_reorder_kernel<NB, V, false><<<grid, dim3(256), 0, stream>>>(m, parents, b, (int)beams);
     }
   }
   return hipGetLastError();
