@@ -25,11 +25,13 @@ class ScanGrads(ctypes.Structure):
                 ("dD", _vp), ("ddt_bias", _vp), ("dinitial", _vp)]
 
 
+# (strides one by one: a step for one token is bound by this side, and arrays cost more)
 class GatedArgs(ctypes.Structure):
     _fields_ = [("x", _vp), ("forget", _vp), ("input_gate", _vp), ("z", _vp), ("rate", _vp),
                 ("initial_state", _vp), ("lengths", _vp), ("batch", _i64), ("length", _i64),
-                ("channels", _i64), ("x_stride", _i64 * 2), ("forget_stride", _i64 * 2),
-                ("input_gate_stride", _i64 * 2), ("z_stride", _i64 * 2), ("dtype", _i32)]
+                ("channels", _i64), ("x_batch", _i64), ("x_token", _i64), ("forget_batch", _i64),
+                ("forget_token", _i64), ("input_gate_batch", _i64), ("input_gate_token", _i64),
+                ("z_batch", _i64), ("z_token", _i64), ("dtype", _i32)]
 
 
 class GatedGrads(ctypes.Structure):
@@ -41,7 +43,7 @@ class GatedGrads(ctypes.Structure):
 class BeamArgs(ctypes.Structure):
     _fields_ = [("logits", _vp), ("scores", _vp), ("finished", _vp), ("batch", _i64),
                 ("beams", _i64), ("vocab", _i64), ("count", _i64), ("end_token", _i64),
-                ("logits_stride", _i64 * 2), ("dtype", _i32)]
+                ("logits_batch", _i64), ("logits_beam", _i64), ("dtype", _i32)]
 
 
 def declare(L):

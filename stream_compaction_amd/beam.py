@@ -34,7 +34,8 @@ def beam_select(logits, scores, count, finished=None, end_token=0, out_scores=No
     _require(logits.is_cuda, "logits must be a GPU tensor")
     code, dev = _code(logits, "logits"), logits.get_device()
     b, k, v = logits.shape
-    _require(v <= 1 or logits.stride(2) == 1, "logits must have a contiguous last axis")
+    stride = logits.stride()
+    _require(v <= 1 or stride[2] == 1, "logits must have a contiguous last axis")
     count = int(count)
     _require(count >= 1, "count must be at least 1")
     sp = _like(scores, "scores", (b, k), torch.float32, dev)
@@ -43,7 +44,7 @@ def beam_select(logits, scores, count, finished=None, end_token=0, out_scores=No
         if finished.dtype is torch.bool:
             finished = finished.view(torch.uint8)
         fp = _like(finished, "finished", (b, k), torch.uint8, dev)
-    a = BeamArgs(logits.data_ptr(), sp, fp, b, k, v, count, int(end_token), logits.stride()[:2], code)
+    a = BeamArgs(logits.data_ptr(), sp, fp, b, k, v, count, int(end_token), stride[0], stride[1], code)
     chosen = (b, count)
     out_scores = _out(out_scores, "out_scores", chosen, torch.float32, scores, stream)
     parents = _out(parents, "parents", chosen, torch.int32, scores, stream)
@@ -53,16 +54,6 @@ def beam_select(logits, scores, count, finished=None, end_token=0, out_scores=No
     check(L.beam_select(a, out_scores.data_ptr(), parents.data_ptr(), tokens.data_ptr(),
                         scratch.data_ptr(), room, _queue(stream, dev)))
     return out_scores, parents, tokens
-
-
-def _row_bytes(t, what, b, k, dev):
-    if t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous tensors on cuda:{dev}")
-    shape = t.shape
-    if not (shape[:2] == (b, k) or (t.dim() > 0 and shape[0] == b * k)):
-        raise ValueError(f"{what} must be [batch, beams, ...] or [batch * beams, ...]")
-    rows = b * k
-    return t.numel() // rows * t.element_size() if rows else 0
 
 
 def beam_reorder(states, parents, new_states=None, stream=None):
@@ -84,12 +75,19 @@ def beam_reorder(states, parents, new_states=None, stream=None):
     _require(len(out) == len(states), "new_states must have as many tensors as states")
     n = len(states)
     _require(n <= 1024, "at most 1024 states")
-    from_, to, size = (_vp * n)(), (_vp * n)(), (_i64 * n)()
-    for i, t in enumerate(states):
-        size[i] = _row_bytes(t, "states", b, k, dev)
-        from_[i] = to[i] = t.data_ptr()
+    rows, batched = b * k, (b, k)
+    pointers, sizes = [], []
+    for t in states:
+        # (at most a thousand of them a token: what is cheap to ask is asked first)
+        shape = t.shape
+        if not (len(shape) > 0 and (shape[0] == rows or shape[:2] == batched)):
+            raise ValueError("states must be [batch, beams, ...] or [batch * beams, ...]")
+        if t.get_device() != dev or not t.is_contiguous():
+            raise ValueError(f"states must be contiguous tensors on cuda:{dev}")
+        pointers.append(t.data_ptr())
+        sizes.append(t.nbytes // rows if rows else 0)
+    from_ = to = (_vp * n)(*pointers)
     if new_states is not None:
-        for i, (t, o) in enumerate(zip(states, out)):
-            to[i] = _like(o, "new_states", t.shape, t.dtype, dev)
-    check(lib().beam_reorder(from_, to, size, n, pp, b, k, _queue(stream, dev)))
+        to = (_vp * n)(*[_like(o, "new_states", t.shape, t.dtype, dev) for t, o in zip(states, out)])
+    check(lib().beam_reorder(from_, to, (_i64 * n)(*sizes), n, pp, b, k, _queue(stream, dev)))
     return out

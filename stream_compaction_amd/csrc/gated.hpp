@@ -20,17 +20,17 @@ __device__ __forceinline__ Sides sides(float v) {
   return v >= 0.0f ? Sides{r, er} : Sides{er, r};
 }
 
-// 1 - exp(-t) for t >= 0, exp(-t) = q being known.  Below 1/2, where the
-// difference loses digits, a polynomial of (1 - exp(-t)) / t that is within 8e-8
-// of it (least maximum of the relative error, fitted on [0, 1/2]).
-__device__ __forceinline__ float one_minus_exp(float t, float q) {
-  float s = __builtin_fmaf(t, 0.00677103782f, -0.0410012789f);
-  s = __builtin_fmaf(t, s, 0.166548148f);
-  s = __builtin_fmaf(t, s, -0.49999249f);
-  s = __builtin_fmaf(t, s, 0.99999994f);
-  s *= t;
+// 1 - 4^l for l <= 0, 4^l = q being known.  Above -0.36 (q above 0.6), where the
+// difference loses digits, a polynomial that is within 9e-8 of it (least maximum of the
+// relative error of its quotient by l, fitted there).
+__device__ __forceinline__ float one_minus_4(float l, float q) {
+  float s = __builtin_fmaf(l, -0.0346682966f, -0.151432544f);
+  s = __builtin_fmaf(l, s, -0.443717122f);
+  s = __builtin_fmaf(l, s, -0.960891604f);
+  s = __builtin_fmaf(l, s, -1.38629425f);
+  s *= l;
   materialize(s);                            // a select, not a branch around the polynomial
-  return t < 0.5f ? s : 1.0f - q;
+  return l > -0.36067376f ? s : 1.0f - q;
 }
 
 // What a token's gate does: decay a, log2 of it, the input's weight w.
@@ -43,7 +43,7 @@ __device__ __forceinline__ Gate gate(float forget, float nr) {
   if constexpr (RATE) {
     g.log_a = nr * sigmoid(forget);
     g.a = exp2_hw(g.log_a);
-    g.w = __builtin_amdgcn_sqrtf(one_minus_exp(g.log_a * (-2.0f * kLn2), g.a * g.a));
+    g.w = __builtin_amdgcn_sqrtf(one_minus_4(g.log_a, g.a * g.a));
   } else {
     const Sides s = sides(forget);
     g.a = s.up;

@@ -21,39 +21,41 @@ void gated_scan_kernel(GatedProblem p, void* yv, float* final_state, float* star
   using Raw = typename PIO::Raw;
   constexpr int T = kFwdTokens;
   constexpr int eb = sizeof(S);
-  constexpr bool kLateZ = sizeof(S) == 4;    // four float32 inputs at once have no room in registers
+  // four inputs at once have no room in registers in float32, nor as single channels
+  constexpr bool kLateZ = sizeof(S) == 4 || ODD;
   __shared__ TileMaps sh;
   const int wave = wave_id();
   const int D = (int)p.channels;
-  if (group_number() >= tiles.count()) return;
-  int64_t col, part;
-  divide(group_number(), tiles.cols, &col);
-  const int64_t chunk = tiles.chunks > 1 ? draw_chunk(scratch, col, &sh.tile) : 0;
-  const int64_t b = tiles.b0 + divide(col, tiles.parts, &part);
-  const int ch = (int)part * kTileChannels + 2 * lane_id();
+  const int64_t n = sequence_tokens(p, tiles.b0 + blockIdx.y);
+  const Place place = draw_place(tiles, scratch, &sh.tile);
+  if (place.run < 0) return;
+  const int64_t b = place.b, col = place.col, chunk = place.run;
+  const int ch = place.part * kTileChannels + 2 * lane_id();
   const int have = D - ch >= 2 ? 2 : (D - ch == 1 ? 1 : 0);
   // lanes past the last channel work on the last one (pair), unheard
   const int c0 = ODD ? (ch < D ? ch : D - 1) : (ch < D ? ch : D - 2);
   const int c1 = ch + 1 < D ? ch + 1 : D - 1;
   const uint32_t o0 = (uint32_t)c0 * eb, o1 = (uint32_t)c1 * eb;
-  const int64_t n = p.lengths == nullptr ? p.length : live_count(p.length, p.lengths + b);
   const int64_t t0 = chunk * kFwdTile + wave * T;          // this wave's first token
   uintptr_t yrow = (uintptr_t)yv + ((b * p.length + t0) * D) * eb;
-  float h[2] = {0.0f, 0.0f};
-  if (p.initial_state != nullptr) {
-    h[0] = p.initial_state[b * D + c0];
-    h[1] = p.initial_state[b * D + c1];
-  }
   const int room = (int)(p.length - t0 < T ? p.length - t0 : T);   // tokens of the output
   if (chunk * kFwdTile >= n) {                             // no token of this tile exists
     for (int k = 0; k < room; ++k, yrow += D * eb) PIO::store(yrow, o0, PIO::splat(0.0f), have);
     if (chunk == 0 && wave == 0 && final_state != nullptr) {
-      if (have > 0) final_state[b * D + ch] = h[0];
-      if (have > 1) final_state[b * D + ch + 1] = h[1];
+      const float* s0 = p.initial_state == nullptr ? nullptr : p.initial_state + b * D + ch;
+      if (have > 0) final_state[b * D + ch] = s0 == nullptr ? 0.0f : s0[0];
+      if (have > 1) final_state[b * D + ch + 1] = s0 == nullptr ? 0.0f : s0[1];
     }
     return;
   }
   const int count = (int)(n - t0 <= 0 ? 0 : (n - t0 < T ? n - t0 : T));
+  // the rates first: loads return in order, and the first token must not wait for the
+  // last one's
+  float nr[2] = {0.0f, 0.0f};
+  if constexpr (RATE) {
+    nr[0] = rate_log2(p.rate[c0]);
+    nr[1] = rate_log2(p.rate[c1]);
+  }
   // (past the last token it is read again)
   const int64_t first_token = count > 0 ? t0 : n - 1;
   Rows ax((uintptr_t)p.x, p.x_batch, p.x_token, b, first_token, eb);
@@ -73,10 +75,10 @@ void gated_scan_kernel(GatedProblem p, void* yv, float* final_state, float* star
     ai.next(more);
     if constexpr (!kLateZ) az.next(more);
   }
-  float nr[2] = {0.0f, 0.0f};
-  if constexpr (RATE) {
-    nr[0] = rate_log2(p.rate[c0]);
-    nr[1] = rate_log2(p.rate[c1]);
+  float h[2] = {0.0f, 0.0f};                               // what enters the sequence
+  if (p.initial_state != nullptr && chunk < kTileGroup) {
+    h[0] = p.initial_state[b * D + c0];
+    h[1] = p.initial_state[b * D + c1];
   }
   if (count < T) {                                       // tokens that do not exist: a = 1, u = 0
 #pragma unroll
@@ -87,7 +89,7 @@ void gated_scan_kernel(GatedProblem p, void* yv, float* final_state, float* star
       if constexpr (IG) ri[k] = PIO::splat(0.0f);
     }
   }
-  float a[T][2], u[T][2], l[2] = {0.0f, 0.0f}, least[2] = {1.0f, 1.0f}, last[2] = {0.0f, 0.0f};
+  float a[T][2], u[T][2], l[2] = {0.0f, 0.0f}, last[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int k = 0; k < T; ++k) {
     float x[2], f[2], v[2];
@@ -101,16 +103,12 @@ void gated_scan_kernel(GatedProblem p, void* yv, float* final_state, float* star
       u[k][c] = g.w * x[c];
       if constexpr (IG) u[k][c] *= sigmoid(v[c]);
       l[c] += g.log_a;
-      least[c] = __builtin_fminf(least[c], g.a);
       last[c] = __builtin_fmaf(g.a, last[c], u[k][c]);
     }
     // token after token: left alone, the compiler starts many at once and runs out
     // of registers
     __builtin_amdgcn_sched_barrier(0);
   }
-#pragma unroll
-  for (int c = 0; c < 2; ++c)
-    if (least[c] == 0.0f) l[c] = -__builtin_huge_valf();
   if constexpr (Z && kLateZ) {
 #pragma unroll
     for (int k = 0; k < T; ++k) {
@@ -124,7 +122,7 @@ void gated_scan_kernel(GatedProblem p, void* yv, float* final_state, float* star
   lds_barrier();
   if (tiles.chunks > 1) {
     const float first[2] = {h[0], h[1]};
-    tile_entry(sh, wave, chunk, (n + kFwdTile - 1) / kFwdTile, col, tiles.cols, scratch,
+    tile_entry(sh, wave, chunk, (n + kFwdTile - 1) / kFwdTile, col, tiles.cols(), scratch,
                tiles.chunks, first, h);
   }
   wave_entry(sh, wave, h);
@@ -143,9 +141,9 @@ void gated_scan_kernel(GatedProblem p, void* yv, float* final_state, float* star
       h[c] = __builtin_fmaf(a[k][c], h[c], u[k][c]);
       y[c] = h[c];
       if constexpr (Z) y[c] *= silu(z[c]);
-      if (k >= count) y[c] = 0.0f;
     }
-    if (k < room) PIO::store(yrow, o0, PIO::IO::pack(y), have);
+    const Raw packed = PIO::IO::pack(y);
+    if (k < room) PIO::store(yrow, o0, k < count ? packed : PIO::splat(0.0f), have);
     yrow += D * eb;
   }
   if (final_state != nullptr && count > 0 && t0 + count == n) {

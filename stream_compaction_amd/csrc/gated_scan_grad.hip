@@ -41,26 +41,19 @@ void gated_scan_grad_kernel(GatedProblem p, GatedGrads g, uint64_t* scratch, flo
   __shared__ float forward_b[kTileWaves][kTileChannels];
   const int wave = wave_id(), turn = kTileWaves - 1 - wave;  // its turn in the walk
   const int D = (int)p.channels;
-  if (group_number() >= tiles.count()) return;
-  int64_t col, part;
-  divide(group_number(), tiles.cols, &col);
-  const int64_t chunk = tiles.chunks > 1 ? tiles.chunks - 1 - draw_chunk(scratch, col, &sh.tile) : 0;
-  const int64_t b = tiles.b0 + divide(col, tiles.parts, &part);
-  const int ch = (int)part * kTileChannels + 2 * lane_id();
+  const int64_t n = sequence_tokens(p, tiles.b0 + blockIdx.y);
+  const Place place = draw_place(tiles, scratch, &sh.tile);
+  if (place.run < 0) return;
+  const int64_t b = place.b, col = place.col, chunk = tiles.chunks - 1 - place.run;
+  const int ch = place.part * kTileChannels + 2 * lane_id();
   const int have = D - ch >= 2 ? 2 : (D - ch == 1 ? 1 : 0);
   // lanes past the last channel work on the last one (pair), unheard
   const int c0 = ODD ? (ch < D ? ch : D - 1) : (ch < D ? ch : D - 2);
   const int c1 = ch + 1 < D ? ch + 1 : D - 1;
   const uint32_t o0 = (uint32_t)c0 * eb, o1 = (uint32_t)c1 * eb;
-  const int64_t n = p.lengths == nullptr ? p.length : live_count(p.length, p.lengths + b);
   const int64_t t0 = chunk * kGradTile + wave * T;         // this wave's first token
   uintptr_t out = ((b * p.length + t0) * D) * eb;
   const int room = (int)(p.length - t0 < T ? p.length - t0 : T);
-  float c[2] = {0.0f, 0.0f};
-  if (g.dfinal != nullptr) {
-    c[0] = g.dfinal[b * D + c0];
-    c[1] = g.dfinal[b * D + c1];
-  }
   if (chunk * kGradTile >= n) {                            // no token of this tile exists
     const Raw zero = PIO::splat(0.0f);
     for (int k = 0; k < room; ++k, out += D * eb) {
@@ -74,13 +67,27 @@ void gated_scan_grad_kernel(GatedProblem p, GatedGrads g, uint64_t* scratch, flo
       if (RATE && have > 0) at[0] = 0.0f;
       if (RATE && have > 1) at[1] = 0.0f;
       if (chunk == 0 && g.dinitial != nullptr) {
-        if (have > 0) g.dinitial[b * D + ch] = c[0];
-        if (have > 1) g.dinitial[b * D + ch + 1] = c[1];
+        const float* s0 = g.dfinal == nullptr ? nullptr : g.dfinal + b * D + ch;
+        if (have > 0) g.dinitial[b * D + ch] = s0 == nullptr ? 0.0f : s0[0];
+        if (have > 1) g.dinitial[b * D + ch + 1] = s0 == nullptr ? 0.0f : s0[1];
       }
     }
     return;
   }
   const int count = (int)(n - t0 <= 0 ? 0 : (n - t0 < T ? n - t0 : T));
+  // the rates and the state first: loads return in order, and the first token must not
+  // wait for the last one's
+  float nr[2] = {0.0f, 0.0f}, h[2];
+  if constexpr (RATE) {
+    nr[0] = rate_log2(p.rate[c0]);
+    nr[1] = rate_log2(p.rate[c1]);
+  }
+  {
+    const int64_t blocks = (p.length + kGatedKeepTokens - 1) / kGatedKeepTokens;
+    const float* at = g.starts + (b * blocks + chunk) * D;
+    h[0] = at[c0];
+    h[1] = at[c1];
+  }
   // (past the last token it is read again)
   const int64_t first_token = count > 0 ? t0 : n - 1;
   Rows ax((uintptr_t)p.x, p.x_batch, p.x_token, b, first_token, eb);
@@ -103,16 +110,11 @@ void gated_scan_grad_kernel(GatedProblem p, GatedGrads g, uint64_t* scratch, flo
     az.next(more);
     ad.next(more);
   }
-  float nr[2] = {0.0f, 0.0f}, h[2];
-  if constexpr (RATE) {
-    nr[0] = rate_log2(p.rate[c0]);
-    nr[1] = rate_log2(p.rate[c1]);
-  }
-  {
-    const int64_t blocks = (p.length + kGatedKeepTokens - 1) / kGatedKeepTokens;
-    const float* at = g.starts + (b * blocks + chunk) * D;
-    h[0] = at[c0];
-    h[1] = at[c1];
+  const int64_t steps = (n + kGradTile - 1) / kGradTile;
+  float c[2] = {0.0f, 0.0f};                               // what enters the sequence from behind
+  if (g.dfinal != nullptr && steps - 1 - chunk < kTileGroup) {
+    c[0] = g.dfinal[b * D + c0];
+    c[1] = g.dfinal[b * D + c1];
   }
   if (count < T) {                                         // tokens that do not exist: a = 1, u = q = 0
 #pragma unroll
@@ -126,7 +128,7 @@ void gated_scan_grad_kernel(GatedProblem p, GatedGrads g, uint64_t* scratch, flo
   }
   // hs: first the input's part of each token, then the state before it
   float a[T][2], w[RATE ? T : 1][2], hs[T][2];
-  float l[2] = {0.0f, 0.0f}, least[2] = {1.0f, 1.0f}, last[2] = {0.0f, 0.0f}, back[2] = {0.0f, 0.0f};
+  float l[2] = {0.0f, 0.0f}, last[2] = {0.0f, 0.0f}, back[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int k = 0; k < T; ++k) {
     float x[2], f[2], v[2];
@@ -141,7 +143,6 @@ void gated_scan_grad_kernel(GatedProblem p, GatedGrads g, uint64_t* scratch, flo
       hs[k][j] = gt.w * x[j];
       if constexpr (IG) hs[k][j] *= sigmoid(v[j]);
       l[j] += gt.log_a;
-      least[j] = __builtin_fminf(least[j], gt.a);
       last[j] = __builtin_fmaf(gt.a, last[j], hs[k][j]);
     }
     __builtin_amdgcn_sched_barrier(0);                     // token after token, as in the forward
@@ -157,9 +158,6 @@ void gated_scan_grad_kernel(GatedProblem p, GatedGrads g, uint64_t* scratch, flo
       back[j] = a[k][j] * (q[j] + back[j]);
     }
   }
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-    if (least[j] == 0.0f) l[j] = -__builtin_huge_valf();
   put2(sh.l[turn], l[0], l[1]);
   put2(sh.m[turn], half_decay(l[0]), half_decay(l[1]));
   put2(sh.b[turn], back[0], back[1]);
@@ -167,8 +165,7 @@ void gated_scan_grad_kernel(GatedProblem p, GatedGrads g, uint64_t* scratch, flo
   lds_barrier();
   if (tiles.chunks > 1) {
     const float first[2] = {c[0], c[1]};
-    const int64_t steps = (n + kGradTile - 1) / kGradTile;
-    tile_entry(sh, turn, steps - 1 - chunk, steps, col, tiles.cols, scratch, tiles.chunks, first, c);
+    tile_entry(sh, turn, steps - 1 - chunk, steps, col, tiles.cols(), scratch, tiles.chunks, first, c);
   }
   wave_entry(sh, turn, c);
   for (int i = 0; i < wave; ++i) {                         // the state that enters this wave's run
@@ -222,13 +219,17 @@ void gated_scan_grad_kernel(GatedProblem p, GatedGrads g, uint64_t* scratch, flo
         df[j] = (grad * hs[k][j] - gv * x[j]) * (s.up * s.down);
       }
       c[j] = a[k][j] * grad;
-      if (k >= count) dx[j] = df[j] = di[j] = dz[j] = 0.0f;
     }
     if (k < room) {
-      PIO::store((uintptr_t)g.dx + out, o0, IO::pack(dx), have);
-      PIO::store((uintptr_t)g.dforget + out, o0, IO::pack(df), have);
-      if constexpr (IG) PIO::store((uintptr_t)g.dinput_gate + out, o0, IO::pack(di), have);
-      if constexpr (Z) PIO::store((uintptr_t)g.dz + out, o0, IO::pack(dz), have);
+      const bool on = k < count;
+      auto kept = [&](const float (&v)[2]) {
+        const Raw r = IO::pack(v);
+        return on ? r : PIO::splat(0.0f);
+      };
+      PIO::store((uintptr_t)g.dx + out, o0, kept(dx), have);
+      PIO::store((uintptr_t)g.dforget + out, o0, kept(df), have);
+      if constexpr (IG) PIO::store((uintptr_t)g.dinput_gate + out, o0, kept(di), have);
+      if constexpr (Z) PIO::store((uintptr_t)g.dz + out, o0, kept(dz), have);
     }
     out -= (uintptr_t)D * eb;
     __builtin_amdgcn_sched_barrier(0);

@@ -22,46 +22,49 @@ constexpr int kTileChannels = 128;           // two to a lane
 constexpr int kTileGroup = 16;               // tiles from one passed-on state to the next
 constexpr int64_t kTicketWords = 16;         // a column's ticket, on a cache line of its own
 
-// The launch's tiles: `cols` columns (a sequence's 128 channels) of `chunks` runs.
+// A launch's tiles: columns (a sequence's 128 channels) of `chunks` runs.  Its grid is
+// the parts of the channels, the sequences, and the chunks (those beyond the third
+// axis beside the parts), so that no workgroup divides to find its column.
 struct Tiles {
-  int64_t parts, cols, chunks;
-  int64_t b0 = 0;                            // the first sequence
-  __host__ __device__ int64_t count() const { return cols * chunks; }
+  int64_t parts, batch, chunks;              // of the launch
+  int64_t b0;                                // its first sequence
+  __host__ __device__ int64_t cols() const { return parts * batch; }
   int64_t words() const {                    // of scratch, 8 bytes each
     if (chunks <= 1) return 0;
-    return cols * (kTicketWords + (chunks + (chunks + kTileGroup - 1) / kTileGroup) * kTileChannels);
+    return cols() * (kTicketWords + (chunks + (chunks + kTileGroup - 1) / kTileGroup) * kTileChannels);
   }
 };
+constexpr int64_t kAxis = 65535;             // a grid's second and third axis
 inline Tiles gated_tiles(const GatedProblem& p, int tokens) {
   Tiles t;
   t.parts = (p.channels + kTileChannels - 1) / kTileChannels;
-  t.cols = p.batch * t.parts;
+  t.batch = p.batch < kAxis ? p.batch : kAxis;
   t.chunks = p.length <= tokens ? 1 : (p.length + tokens - 1) / tokens;
+  t.b0 = 0;
   return t;
 }
 // Fills `tickets` words with zeros and the others with ones.
 hipError_t launch_tile_clear(uint64_t* scratch, int64_t tickets, int64_t words, hipStream_t stream);
 
-// Launches `kernel(grid, tiles)` over all tiles, on a grid of two axes where one
-// does not hold them; a large batch of single tiles goes out in parts.
-constexpr int64_t kTileGroups = 1ll << 22;   // workgroups along the first axis
+// Launches `kernel(grid, tiles)` over all tiles; a batch beyond the second axis goes
+// out in parts, one after the other in the same scratch.
 template <class Kernel>
 hipError_t launch_tiles(Tiles t, int64_t batch, uint64_t* scratch, hipStream_t stream, Kernel&& kernel) {
-  if (t.chunks > 1) {
-    const hipError_t e = launch_tile_clear(scratch, t.cols * kTicketWords, t.words(), stream);
-    if (e != hipSuccess) return e;
-    const int64_t n = t.count(), x = n < kTileGroups ? n : kTileGroups;
-    kernel(dim3((unsigned)x, (unsigned)((n + x - 1) / x)), t);
-    return hipGetLastError();
-  }
-  const int64_t step = kTileGroups / t.parts;
-  for (int64_t b0 = 0; b0 < batch; b0 += step) {
-    Tiles part = t;
-    part.b0 = b0;
-    part.cols = (batch - b0 < step ? batch - b0 : step) * t.parts;
-    kernel(dim3((unsigned)part.cols), part);
+  const int64_t z = t.chunks < kAxis ? t.chunks : kAxis, x = (t.chunks + z - 1) / z;
+  for (; t.b0 < batch; t.b0 += kAxis) {
+    if (batch - t.b0 < t.batch) t.batch = batch - t.b0;
+    if (t.chunks > 1) {
+      const hipError_t e = launch_tile_clear(scratch, t.cols() * kTicketWords, t.words(), stream);
+      if (e != hipSuccess) return e;
+    }
+    kernel(dim3((unsigned)(t.parts * x), (unsigned)t.batch, (unsigned)z), t);
   }
   return hipGetLastError();
+}
+
+// The tokens of a sequence that exist.
+__device__ __forceinline__ int64_t sequence_tokens(const GatedProblem& p, int64_t b) {
+  return p.lengths == nullptr ? p.length : live_count(p.length, p.lengths + b);
 }
 
 // A sequence's rows, one token after the other, as wave-uniform addresses.
@@ -170,9 +173,21 @@ __device__ __forceinline__ int64_t draw_chunk(uint64_t* scratch, int64_t col, ui
   __syncthreads();
   return (int64_t)readlane(*shared, 0);
 }
-// The workgroup's number in a grid of two axes.
-__device__ __forceinline__ int64_t group_number() {
-  return (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+// A workgroup's place: its part of the channels, its sequence and their column, and
+// which of the column's runs it takes (-1: none is left).
+struct Place { int part; int64_t col, b, run; };
+__device__ __forceinline__ Place draw_place(const Tiles& t, uint64_t* scratch, uint64_t* shared) {
+  Place p;
+  const uint32_t parts = (uint32_t)t.parts;
+  p.part = (int)(gridDim.x == parts ? blockIdx.x : blockIdx.x % parts);
+  p.b = t.b0 + blockIdx.y;
+  p.col = (int64_t)blockIdx.y * parts + p.part;
+  p.run = 0;
+  if (t.chunks > 1) {
+    p.run = draw_chunk(scratch, p.col, shared);
+    if (p.run >= t.chunks) p.run = -1;
+  }
+  return p;
 }
 
 struct TileMaps {                            // a workgroup's exchange
@@ -194,7 +209,7 @@ __device__ __forceinline__ void get2(const float* row, float (&v)[2]) {
 // The state that enters tile `step` of its column's `steps` (both counted in the
 // direction of the walk), and what the tile leaves to others: called by every wave
 // when all maps are in LDS (before a barrier), with the state `first` that enters
-// the column.  slots + tile index * 128 words, borders likewise by group.
+// the column (of which the last wave asks in a column's first group).
 __device__ __forceinline__ void tile_entry(TileMaps& s, int wave, int64_t step, int64_t steps,
                                            int64_t col, int64_t cols, uint64_t* scratch,
                                            int64_t chunks, const float (&first)[2], float (&h)[2]) {

@@ -293,30 +293,29 @@ def selective_scan_step(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, sof
 
 
 def _gated_args(x, forget, rate, input_gate, z, initial_state, lengths, step):
-    if x.dim() != (2 if step else 3):
+    shape = x.shape
+    if len(shape) != (2 if step else 3):
         raise ValueError("x must be [batch, channels]" if step else
                          "x must be [batch, length, channels]")
     _require(x.is_cuda, "x must be a GPU tensor")
     code = _code(x, "x")
-    dev, ty, shape, f32 = x.get_device(), x.dtype, x.shape, torch.float32
+    dev, ty, f32 = x.get_device(), x.dtype, torch.float32
     b, d = shape[0], shape[-1]
     # (shapes before strides: an argument of another rank has not as many)
     xp, fp = _rows(x, "x", shape, ty, dev), _rows(forget, "forget", shape, ty, dev)
-    ip = None if input_gate is None else _rows(input_gate, "input_gate", shape, ty, dev)
-    zp = None if z is None else _rows(z, "z", shape, ty, dev)
-
-    def strides(t):
-        if t is None:
-            return (0, 0)
-        return (t.stride(0), 0) if step else t.stride()[:2]
-
+    xs, fs, gs, zs = x.stride(), forget.stride(), (0, 0), (0, 0)
+    ip = zp = None
+    if input_gate is not None:
+        ip, gs = _rows(input_gate, "input_gate", shape, ty, dev), input_gate.stride()
+    if z is not None:
+        zp, zs = _rows(z, "z", shape, ty, dev), z.stride()
+    # (a step has no token axis; what stands in its place is not used)
     return GatedArgs(
         xp, fp, ip, zp, None if rate is None else _like(rate, "rate", (d,), f32, dev),
         None if initial_state is None else
         _like(initial_state, "initial_state", (b, d), f32, dev),
         None if lengths is None else _like(lengths, "lengths", (b,), torch.int32, dev),
-        b, 1 if step else shape[1], d, strides(x), strides(forget), strides(input_gate),
-        strides(z), code)
+        b, 1 if step else shape[1], d, xs[0], xs[1], fs[0], fs[1], gs[0], gs[1], zs[0], zs[1], code)
 
 
 def gated_scan(x, forget, rate=None, input_gate=None, z=None, initial_state=None, lengths=None,

@@ -97,7 +97,7 @@ def test_data_of_another_gpu_than_the_stream(monkeypatch):
 
 
 def args(**more):
-    k = dict(logits=S[0], scores=S[1], batch=2, beams=3, vocab=100, count=6, logits_stride=(300, 100),
+    k = dict(logits=S[0], scores=S[1], batch=2, beams=3, vocab=100, count=6, logits_batch=300, logits_beam=100,
              dtype=sc.DTYPE_CODES["f32"])
     k.update(more)
     return BeamArgs(**k)
@@ -109,8 +109,8 @@ def test_refused_selections():
     assert call(args(batch=0), None, None, None, None, 0) == OK
     for wrong in (dict(batch=-1), dict(batch=1 << 31), dict(beams=0), dict(vocab=0), dict(vocab=1 << 31), dict(count=0),
                   dict(count=7, beams=1, vocab=6), dict(logits=None), dict(scores=None), dict(logits=S[0] + 2),
-                  dict(logits_stride=(-300, 100)), dict(finished=S[2], end_token=100), dict(finished=S[2], end_token=-1),
-                  dict(batch=1 << 30, logits_stride=(1 << 30, 1))):
+                  dict(logits_batch=-300), dict(finished=S[2], end_token=100), dict(finished=S[2], end_token=-1),
+                  dict(batch=1 << 30, logits_batch=1 << 30, logits_beam=1)):
         assert call(args(**wrong)) == EINVAL, wrong
     for wrong in (dict(beams=65), dict(count=65), dict(dtype=sc.DTYPE_CODES["f64"])):
         assert call(args(**wrong)) == ENOTSUP, wrong

@@ -95,7 +95,7 @@ class TestPython:
 
 def args(**more):
     k = dict(x=S[0], forget=S[1], batch=2, length=200, channels=48,
-             x_stride=(200 * 48, 48), forget_stride=(200 * 48, 48), dtype=sc.DTYPE_CODES["f32"])
+             x_batch=200 * 48, x_token=48, forget_batch=200 * 48, forget_token=48, dtype=sc.DTYPE_CODES["f32"])
     k.update(more)
     return GatedArgs(**k)
 
@@ -104,11 +104,11 @@ def test_refused_sizes_and_types():
     L = sc.lib()
     for wrong in (dict(batch=-1), dict(batch=1 << 31), dict(length=-1), dict(length=1 << 31),
                   dict(channels=0), dict(channels=(1 << 22) + 1), dict(x=None), dict(forget=None),
-                  dict(x=S[0] + 2), dict(rate=S[2] + 1), dict(x_stride=(-1, 48)),
+                  dict(x=S[0] + 2), dict(rate=S[2] + 1), dict(x_batch=-1),
                   dict(batch=1 << 30, length=1 << 30, channels=16)):
         a = args(**wrong)
         assert L.gated_scan(a, S[10], S[11], None, S[12], 1 << 46, None) == EINVAL, wrong
-        if "length" not in wrong and "x_stride" not in wrong:
+        if "length" not in wrong:
             assert L.gated_scan_step(a, S[4], S[4], S[10], None) == EINVAL, wrong
     for code in ("f64", "i32"):
         a = args(dtype=sc.DTYPE_CODES[code])
@@ -124,7 +124,7 @@ def test_refused_overlap_and_scratch():
     L = sc.lib()
     a = args(batch=0)
     assert L.gated_scan(a, None, None, None, None, 0, None) == OK
-    a = args(rate=S[2], z=S[3], z_stride=(200 * 48, 48))
+    a = args(rate=S[2], z=S[3], z_batch=200 * 48, z_token=48)
     room = 1 << 46
     assert L.gated_scan(a, S[0], None, None, S[12], room, None) == EALIAS
     assert L.gated_scan(a, S[10], S[10] + 64, None, S[12], room, None) == EALIAS
