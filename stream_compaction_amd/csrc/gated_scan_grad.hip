@@ -184,6 +184,7 @@ void gated_scan_grad_kernel(GatedProblem p, GatedGrads g, uint64_t* scratch, flo
       h[j] = __builtin_fmaf(a[k][j], h[j], u);
     }
   float total[2] = {0.0f, 0.0f};
+  const float p_rate[2] = {nr[0] * -kLn2, nr[1] * -kLn2};  // the rates again, at most 1e38: P stays finite
   out += (uintptr_t)(T - 1) * D * eb;
 #pragma unroll
   for (int k = T - 1; k >= 0; --k) {
@@ -209,8 +210,8 @@ void gated_scan_grad_kernel(GatedProblem p, GatedGrads g, uint64_t* scratch, flo
       dx[j] = gv * weight;
       if constexpr (IG) di[j] = dx[j] * x[j] * vs.down;
       if constexpr (RATE) {
-        const float P = at_most(nr[j] * s.up * -kLn2, 128.0f);   // exp(-128) is 0 in float32
-        const float pw = weight > 0.0f ? P * rcp_hw(weight) : 0.0f;
+        // (p / w is 0 where both are)
+        const float P = p_rate[j] * s.up, pw = P * rcp_hw(__builtin_fmaxf(weight, 1e-30f));
         const float A = a[k][j];
         const float E = gv * x[j] * (A * A * pw) - grad * (P * A * hs[k][j]);
         df[j] = E * s.down;
