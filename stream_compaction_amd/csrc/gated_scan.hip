@@ -12,12 +12,13 @@ constexpr int kFwdTokens = 16;                              // of a wave
 constexpr int kFwdTile = kFwdTokens * kTileWaves;           // of a workgroup
 static_assert(kGatedKeepTokens % kFwdTokens == 0, "a kept state is a wave's first");
 
-template <class F, bool RATE, bool IG, bool Z, bool ODD>
+template <class F, bool RATE, bool IG, bool Z, Rows2 ROWS>
 __global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(4, 4)))
 void gated_scan_kernel(GatedProblem p, void* yv, float* final_state, float* starts, uint64_t* scratch,
                        Tiles tiles) {
   using S = typename F::S;
-  using PIO = PairIO<F, ODD>;
+  using PIO = PairIO<F, ROWS>;
+  constexpr bool ODD = PIO::ODD;
   using Raw = typename PIO::Raw;
   constexpr int T = kFwdTokens;
   constexpr int eb = sizeof(S);
@@ -172,12 +173,17 @@ size_t gated_scan_scratch(const GatedProblem& p) { return (size_t)gated_tiles(p,
 template <class F, bool RATE, bool IG, bool Z>
 static hipError_t launch_gated_z(const GatedProblem& p, void* y, float* final_state, float* starts,
                                  uint64_t* scratch, hipStream_t stream) {
+  const bool past = past_caches(p.batch * p.length * p.channels * (int64_t)sizeof(typename F::S));
   return launch_tiles(gated_tiles(p, kFwdTile), p.batch, scratch, stream, [&](dim3 grid, const Tiles& t) {
-    if (p.channels % 2 == 0)
-      gated_scan_kernel<F, RATE, IG, Z, false><<<grid, dim3(kTileThreads), 0, stream>>>(
+    const dim3 block(kTileThreads);
+    if (p.channels % 2 != 0)
+      gated_scan_kernel<F, RATE, IG, Z, Rows2::Singles><<<grid, block, 0, stream>>>(
+          p, y, final_state, starts, scratch, t);
+    else if (past)
+      gated_scan_kernel<F, RATE, IG, Z, Rows2::PairsPast><<<grid, block, 0, stream>>>(
           p, y, final_state, starts, scratch, t);
     else
-      gated_scan_kernel<F, RATE, IG, Z, true><<<grid, dim3(kTileThreads), 0, stream>>>(
+      gated_scan_kernel<F, RATE, IG, Z, Rows2::Pairs><<<grid, block, 0, stream>>>(
           p, y, final_state, starts, scratch, t);
   });
 }

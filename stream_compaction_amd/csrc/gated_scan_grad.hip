@@ -27,12 +27,13 @@ static_assert(kGradTile == kGatedKeepTokens, "a tile starts from a kept state");
 template <class F, bool RATE, bool IG, bool Z>
 constexpr int kGradWaves = sizeof(typename F::S) == 4 && (RATE || IG || Z) ? 2 : 4;
 
-template <class F, bool RATE, bool IG, bool Z, bool ODD>
+template <class F, bool RATE, bool IG, bool Z, Rows2 ROWS>
 __global__ __launch_bounds__(kTileThreads)
 __attribute__((amdgpu_waves_per_eu(kGradWaves<F, RATE, IG, Z>, kGradWaves<F, RATE, IG, Z>)))
 void gated_scan_grad_kernel(GatedProblem p, GatedGrads g, uint64_t* scratch, float* partial, Tiles tiles) {
   using S = typename F::S;
-  using PIO = PairIO<F, ODD>;
+  using PIO = PairIO<F, ROWS>;
+  constexpr bool ODD = PIO::ODD;
   using IO = typename PIO::IO;
   using Raw = typename PIO::Raw;
   constexpr int T = kGradTokens;
@@ -286,15 +287,19 @@ size_t gated_scan_grad_scratch(const GatedProblem& p) {
 template <class F, bool RATE, bool IG, bool Z>
 static hipError_t launch_grad_z(const GatedProblem& p, const GatedGrads& g, void* scratch, hipStream_t stream) {
   const Tiles tiles = gated_tiles(p, kGradTile);
+  const bool past = past_caches(p.batch * p.length * p.channels * (int64_t)sizeof(typename F::S));
   uint64_t* words = (uint64_t*)scratch;
   float* partial = (float*)(words + tiles.words());
   hipError_t e = hipSuccess;
   if (p.batch > 0)
     e = launch_tiles(tiles, p.batch, words, stream, [&](dim3 grid, const Tiles& t) {
-      if (p.channels % 2 == 0)
-        gated_scan_grad_kernel<F, RATE, IG, Z, false><<<grid, dim3(kTileThreads), 0, stream>>>(p, g, words, partial, t);
+      const dim3 block(kTileThreads);
+      if (p.channels % 2 != 0)
+        gated_scan_grad_kernel<F, RATE, IG, Z, Rows2::Singles><<<grid, block, 0, stream>>>(p, g, words, partial, t);
+      else if (past)
+        gated_scan_grad_kernel<F, RATE, IG, Z, Rows2::PairsPast><<<grid, block, 0, stream>>>(p, g, words, partial, t);
       else
-        gated_scan_grad_kernel<F, RATE, IG, Z, true><<<grid, dim3(kTileThreads), 0, stream>>>(p, g, words, partial, t);
+        gated_scan_grad_kernel<F, RATE, IG, Z, Rows2::Pairs><<<grid, block, 0, stream>>>(p, g, words, partial, t);
     });
   if (e != hipSuccess || !RATE) return e;
   gated_rate_kernel<<<dim3((unsigned)((p.channels + 63) / 64)), dim3(1024), 0, stream>>>(
