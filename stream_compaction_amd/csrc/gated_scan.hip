@@ -38,10 +38,13 @@ void gated_scan_kernel(GatedProblem p, void* yv, float* final_state, float* star
   const int c1 = ch + 1 < D ? ch + 1 : D - 1;
   const uint32_t o0 = (uint32_t)c0 * eb, o1 = (uint32_t)c1 * eb;
   const int64_t t0 = chunk * kFwdTile + wave * T;          // this wave's first token
-  uintptr_t yrow = (uintptr_t)yv + ((b * p.length + t0) * D) * eb;
+  const uintptr_t yrow = (uintptr_t)yv + ((b * p.length + t0) * D) * eb, ystep = (uintptr_t)D * eb;
   const int room = (int)(p.length - t0 < T ? p.length - t0 : T);   // tokens of the output
   if (chunk * kFwdTile >= n) {                             // no token of this tile exists
-    for (int k = 0; k < room; ++k, yrow += D * eb) PIO::store(yrow, o0, PIO::splat(0.0f), have);
+    Raw zeros[T];
+#pragma unroll
+    for (int k = 0; k < T; ++k) zeros[k] = PIO::splat(0.0f);
+    PIO::store_rows(yrow, ystep, o0, zeros, room, have);
     if (chunk == 0 && wave == 0 && final_state != nullptr) {
       const float* s0 = p.initial_state == nullptr ? nullptr : p.initial_state + b * D + ch;
       if (have > 0) final_state[b * D + ch] = s0 == nullptr ? 0.0f : s0[0];
@@ -70,18 +73,18 @@ void gated_scan_kernel(GatedProblem p, void* yv, float* final_state, float* star
     rf[k] = PIO::load(af.at, o0, o1);
     if constexpr (IG) ri[k] = PIO::load(ai.at, o0, o1);
     if constexpr (Z && !kLateZ) rz[k] = PIO::load(az.at, o0, o1);
-    const bool more = k + 1 < count;
-    ax.next(more);
-    af.next(more);
-    ai.next(more);
-    if constexpr (!kLateZ) az.next(more);
+    const uintptr_t on = k + 1 < count ? ~(uintptr_t)0 : 0;
+    ax.next(on);
+    af.next(on);
+    ai.next(on);
+    if constexpr (!kLateZ) az.next(on);
   }
   float h[2] = {0.0f, 0.0f};                               // what enters the sequence
   if (p.initial_state != nullptr && chunk < kTileGroup) {
     h[0] = p.initial_state[b * D + c0];
     h[1] = p.initial_state[b * D + c1];
   }
-  if (count < T) {                                       // tokens that do not exist: a = 1, u = 0
+  if (count < T) {                                         // tokens that do not exist: a = 1, u = 0
 #pragma unroll
     for (int k = 0; k < T; ++k) {
       if (k < count) continue;
@@ -114,7 +117,7 @@ void gated_scan_kernel(GatedProblem p, void* yv, float* final_state, float* star
 #pragma unroll
     for (int k = 0; k < T; ++k) {
       rz[k] = PIO::load(az.at, o0, o1);
-      az.next(k + 1 < count);
+      az.next(k + 1 < count ? ~(uintptr_t)0 : 0);
     }
   }
   put2(sh.l[wave], l[0], l[1]);
@@ -133,6 +136,7 @@ void gated_scan_kernel(GatedProblem p, void* yv, float* final_state, float* star
     if (have > 0) at[0] = h[0];
     if (have > 1) at[1] = h[1];
   }
+  Raw out[T];
 #pragma unroll
   for (int k = 0; k < T; ++k) {
     float y[2], z[2];
@@ -143,10 +147,13 @@ void gated_scan_kernel(GatedProblem p, void* yv, float* final_state, float* star
       y[c] = h[c];
       if constexpr (Z) y[c] *= silu(z[c]);
     }
-    const Raw packed = PIO::IO::pack(y);
-    if (k < room) PIO::store(yrow, o0, k < count ? packed : PIO::splat(0.0f), have);
-    yrow += D * eb;
+    out[k] = PIO::IO::pack(y);
   }
+  if (count < T) {
+#pragma unroll
+    for (int k = 0; k < T; ++k) out[k] = k < count ? out[k] : PIO::splat(0.0f);
+  }
+  PIO::store_rows(yrow, ystep, o0, out, room, have);
   if (final_state != nullptr && count > 0 && t0 + count == n) {
     if (have > 0) final_state[b * D + ch] = h[0];
     if (have > 1) final_state[b * D + ch + 1] = h[1];

@@ -53,16 +53,16 @@ void gated_scan_grad_kernel(GatedProblem p, GatedGrads g, uint64_t* scratch, flo
   const int c1 = ch + 1 < D ? ch + 1 : D - 1;
   const uint32_t o0 = (uint32_t)c0 * eb, o1 = (uint32_t)c1 * eb;
   const int64_t t0 = chunk * kGradTile + wave * T;         // this wave's first token
-  uintptr_t out = ((b * p.length + t0) * D) * eb;
+  const uintptr_t out = ((b * p.length + t0) * D) * eb, ostep = (uintptr_t)D * eb;
   const int room = (int)(p.length - t0 < T ? p.length - t0 : T);
   if (chunk * kGradTile >= n) {                            // no token of this tile exists
-    const Raw zero = PIO::splat(0.0f);
-    for (int k = 0; k < room; ++k, out += D * eb) {
-      PIO::store((uintptr_t)g.dx + out, o0, zero, have);
-      PIO::store((uintptr_t)g.dforget + out, o0, zero, have);
-      if constexpr (IG) PIO::store((uintptr_t)g.dinput_gate + out, o0, zero, have);
-      if constexpr (Z) PIO::store((uintptr_t)g.dz + out, o0, zero, have);
-    }
+    Raw zeros[T];
+#pragma unroll
+    for (int k = 0; k < T; ++k) zeros[k] = PIO::splat(0.0f);
+    PIO::store_rows((uintptr_t)g.dx + out, ostep, o0, zeros, room, have);
+    PIO::store_rows((uintptr_t)g.dforget + out, ostep, o0, zeros, room, have);
+    if constexpr (IG) PIO::store_rows((uintptr_t)g.dinput_gate + out, ostep, o0, zeros, room, have);
+    if constexpr (Z) PIO::store_rows((uintptr_t)g.dz + out, ostep, o0, zeros, room, have);
     if (wave == 0) {
       float* at = partial + (b * tiles.chunks + chunk) * D + ch;
       if (RATE && have > 0) at[0] = 0.0f;
@@ -104,12 +104,12 @@ void gated_scan_grad_kernel(GatedProblem p, GatedGrads g, uint64_t* scratch, flo
     if constexpr (IG) ri[k] = PIO::load(ai.at, o0, o1);
     if constexpr (Z) rz[k] = PIO::load(az.at, o0, o1);
     rd[k] = PIO::load(ad.at, o0, o1);
-    const bool more = k + 1 < count;
-    ax.next(more);
-    af.next(more);
-    ai.next(more);
-    az.next(more);
-    ad.next(more);
+    const uintptr_t on = k + 1 < count ? ~(uintptr_t)0 : 0;
+    ax.next(on);
+    af.next(on);
+    ai.next(on);
+    az.next(on);
+    ad.next(on);
   }
   const int64_t steps = (n + kGradTile - 1) / kGradTile;
   float c[2] = {0.0f, 0.0f};                               // what enters the sequence from behind
@@ -186,7 +186,7 @@ void gated_scan_grad_kernel(GatedProblem p, GatedGrads g, uint64_t* scratch, flo
     }
   float total[2] = {0.0f, 0.0f};
   const float p_rate[2] = {nr[0] * -kLn2, nr[1] * -kLn2};  // the rates again, at most 1e38: P stays finite
-  out += (uintptr_t)(T - 1) * D * eb;
+  Raw ox[T], of[T], oi[IG ? T : 1], oz[Z ? T : 1];
 #pragma unroll
   for (int k = T - 1; k >= 0; --k) {
     float x[2], f[2], v[2], z[2], d[2], dx[2], df[2], di[2], dz[2];
@@ -222,20 +222,26 @@ void gated_scan_grad_kernel(GatedProblem p, GatedGrads g, uint64_t* scratch, flo
       }
       c[j] = a[k][j] * grad;
     }
-    if (k < room) {
-      const bool on = k < count;
-      auto kept = [&](const float (&v)[2]) {
-        const Raw r = IO::pack(v);
-        return on ? r : PIO::splat(0.0f);
-      };
-      PIO::store((uintptr_t)g.dx + out, o0, kept(dx), have);
-      PIO::store((uintptr_t)g.dforget + out, o0, kept(df), have);
-      if constexpr (IG) PIO::store((uintptr_t)g.dinput_gate + out, o0, kept(di), have);
-      if constexpr (Z) PIO::store((uintptr_t)g.dz + out, o0, kept(dz), have);
-    }
-    out -= (uintptr_t)D * eb;
+    ox[k] = IO::pack(dx);
+    of[k] = IO::pack(df);
+    if constexpr (IG) oi[k] = IO::pack(di);
+    if constexpr (Z) oz[k] = IO::pack(dz);
     __builtin_amdgcn_sched_barrier(0);
   }
+  if (count < T) {
+#pragma unroll
+    for (int k = 0; k < T; ++k) {
+      const bool on = k < count;
+      ox[k] = on ? ox[k] : PIO::splat(0.0f);
+      of[k] = on ? of[k] : PIO::splat(0.0f);
+      if constexpr (IG) oi[k] = on ? oi[k] : PIO::splat(0.0f);
+      if constexpr (Z) oz[k] = on ? oz[k] : PIO::splat(0.0f);
+    }
+  }
+  PIO::store_rows((uintptr_t)g.dx + out, ostep, o0, ox, room, have);
+  PIO::store_rows((uintptr_t)g.dforget + out, ostep, o0, of, room, have);
+  if constexpr (IG) PIO::store_rows((uintptr_t)g.dinput_gate + out, ostep, o0, oi, room, have);
+  if constexpr (Z) PIO::store_rows((uintptr_t)g.dz + out, ostep, o0, oz, room, have);
   if (g.dinitial != nullptr && t0 == 0) {
     if (have > 0) g.dinitial[b * D + ch] = c[0];
     if (have > 1) g.dinitial[b * D + ch + 1] = c[1];

@@ -72,7 +72,8 @@ struct Rows {
   uintptr_t at, step;
   __device__ __forceinline__ Rows(uintptr_t base, int64_t batch, int64_t token, int64_t b, int64_t t, int eb)
       : at(base + (uintptr_t)((b * batch + t * token) * eb)), step((uintptr_t)(token * eb)) {}
-  __device__ __forceinline__ void next(bool more) { at += more ? step : 0; }
+  // on: all ones, or zero past the last token, which is read again
+  __device__ __forceinline__ void next(uintptr_t on) { at += step & on; }
 };
 
 // Two neighbouring channels of a row as one access, or, where the number of
@@ -97,19 +98,37 @@ template <class F, Rows2 ROWS> struct PairIO {
       return *(const __attribute__((address_space(1))) Loose*)(gptr<const char>(row) + o0);
     }
   }
-  // n: how many of the two exist
-  static __device__ __forceinline__ void store(uintptr_t row, uint32_t o0, Raw r, int n) {
+  static __device__ __forceinline__ void put(uintptr_t row, uint32_t o0, Raw r) {
+    auto at = (__attribute__((address_space(1))) Loose*)(gptr<char>(row) + o0);
+    if constexpr (ROWS == Rows2::PairsPast) {
+      __builtin_nontemporal_store(r, at);
+    } else {
+      *at = r;
+    }
+  }
+  template <class E> static __device__ __forceinline__ void put_one(uintptr_t at, uint32_t o, E e) {
+    *(__attribute__((address_space(1))) E*)(gptr<char>(at) + o) = e;
+  }
+  // `room` of T rows, `step` bytes apart; n: how many of the two channels exist.  (One
+  // decision for all rows of a whole run: one for each cost a tenth of the kernel.)
+  template <int T>
+  static __device__ __forceinline__ void store_rows(uintptr_t row, uintptr_t step, uint32_t o0, const Raw (&r)[T],
+                                                    int room, int n) {
     if constexpr (ODD) {
-      const typename IO::Elems e = __builtin_bit_cast(typename IO::Elems, r);
-      if (n > 0) *(__attribute__((address_space(1))) S*)(gptr<char>(row) + o0) = e.e[0];
-      if (n > 1)
-        *(__attribute__((address_space(1))) S*)(gptr<char>(row) + o0 + (uint32_t)sizeof(S)) = e.e[1];
+#pragma unroll
+      for (int k = 0; k < T; ++k, row += step) {
+        const typename IO::Elems e = __builtin_bit_cast(typename IO::Elems, r[k]);
+        if (k < room && n > 0) put_one(row, o0, e.e[0]);
+        if (k < room && n > 1) put_one(row, o0 + (uint32_t)sizeof(S), e.e[1]);
+      }
     } else if (n > 0) {
-      auto at = (__attribute__((address_space(1))) Loose*)(gptr<char>(row) + o0);
-      if constexpr (ROWS == Rows2::PairsPast) {
-        __builtin_nontemporal_store(r, at);
+      if (room == T) {
+#pragma unroll
+        for (int k = 0; k < T; ++k, row += step) put(row, o0, r[k]);
       } else {
-        *at = r;
+#pragma unroll
+        for (int k = 0; k < T; ++k, row += step)
+          if (k < room) put(row, o0, r[k]);
       }
     }
   }
