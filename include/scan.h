@@ -539,7 +539,7 @@ scan_status embedding_grad(const void* dout, const void* ids, void* dweight, int
  * `count` different ones.
  *   1 <= beams <= 64 and 1 <= count <= 64 (else SCAN_ENOTSUP), count <= beams *
  *   vocab, 1 <= vocab <= INT32_MAX, 0 <= batch <= INT32_MAX, 0 <= end_token <
- *   vocab.
+ *   vocab, and less than 2^47 bytes of logits, broadcast ones counted in full.
  *   out_scores    float32 [batch, count], in descending order
  *   parents       int32 [batch, count], the beam that goes on
  *   tokens        int32 [batch, count], by which token

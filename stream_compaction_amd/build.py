@@ -23,9 +23,10 @@ COPY_LIB_PATH = os.path.join(HERE, "libscan_copy.so")
 COPY_SOURCES = ["copy_ceiling.hip"]
 # test-only build of the scan library whose look-back never waits: any
 # predecessor descriptor not yet published is recomputed from the input at
-# once, so the tests exercise that recovery path on every call
+# once, so the tests exercise that recovery path on every call; and whose gated
+# scan asks for a state once and then takes it as lost
 FALLBACK_LIB_PATH = os.path.join(HERE, "libscan_amd_lbtest.so")
-FALLBACK_DEFINES = ["-DSCA_LOOKBACK_TIMEOUT_TICKS=0ull"]
+FALLBACK_DEFINES = ["-DSCA_LOOKBACK_TIMEOUT_TICKS=0ull", "-DSCA_TILE_POLLS=0u"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

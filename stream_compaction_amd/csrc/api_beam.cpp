@@ -23,6 +23,8 @@ scan_status beam_problem(const beam_select_args* a, sca::BeamProblem* p, sca::Fm
   if (a->count > a->beams * a->vocab) return SCAN_EINVAL;
   if (a->batch < 0 || a->batch > kMaxN) return SCAN_EINVAL;
   if (a->finished != nullptr && (a->end_token < 0 || a->end_token >= a->vocab)) return SCAN_EINVAL;
+  // (the logits' size counts whatever their strides, so that no product below passes 64 bits)
+  if ((unsigned __int128)a->batch * (uint64_t)a->beams * (uint64_t)a->vocab * *eb >= kMaxBytes) return SCAN_EINVAL;
   *p = sca::BeamProblem{a->logits, a->scores, a->finished, a->batch, a->beams, a->vocab, a->count,
                         a->end_token, a->batch > 1 ? a->logits_stride[0] : 0,
                         a->beams > 1 ? a->logits_stride[1] : 0};

@@ -177,13 +177,24 @@ __device__ __forceinline__ float word_l(uint64_t w) { return __builtin_bit_cast(
 __device__ __forceinline__ float word_b(uint64_t w) { return __builtin_bit_cast(float, (uint32_t)w); }
 __device__ __forceinline__ uint64_t state_word(float h) { return __builtin_bit_cast(uint32_t, h); }
 
-// Two channels' words, once they are there.
+// Two channels' words, once they are there.  Every wait ends: a word that is not
+// there after some seconds of asking never comes (two calls in flight have shared
+// their scratch, which is not allowed), and stands for a state that is no number.
+#ifndef SCA_TILE_POLLS
+#define SCA_TILE_POLLS (1u << 22)
+#endif
+constexpr uint64_t kLostWord = 0x7fc000007fc00000ull;
 struct Words { uint64_t w[2]; };
 __device__ __forceinline__ Words peek_words(const uint64_t* at) {
   return Words{{ld_relaxed(at), ld_relaxed(at + 1)}};
 }
+__device__ __forceinline__ bool no_word(uint64_t w) { return (uint32_t)(w >> 32) == kNoWord; }
 __device__ __forceinline__ Words await_words(const uint64_t* at, Words w) {
-  while (__ballot((uint32_t)(w.w[0] >> 32) == kNoWord || (uint32_t)(w.w[1] >> 32) == kNoWord)) {
+  for (uint32_t polls = 0; __ballot(no_word(w.w[0]) || no_word(w.w[1])); ++polls) {
+    if (polls >= SCA_TILE_POLLS) {
+      for (uint64_t& v : w.w) v = no_word(v) ? kLostWord : v;
+      break;
+    }
     __builtin_amdgcn_s_sleep(4);
     w = peek_words(at);
   }

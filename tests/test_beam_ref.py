@@ -110,8 +110,10 @@ def test_refused_selections():
     for wrong in (dict(batch=-1), dict(batch=1 << 31), dict(beams=0), dict(vocab=0), dict(vocab=1 << 31), dict(count=0),
                   dict(count=7, beams=1, vocab=6), dict(logits=None), dict(scores=None), dict(logits=S[0] + 2),
                   dict(logits_batch=-300), dict(finished=S[2], end_token=100), dict(finished=S[2], end_token=-1),
-                  dict(batch=1 << 30, logits_batch=1 << 30, logits_beam=1)):
+                  dict(batch=1 << 30, logits_batch=1 << 30, logits_beam=1),
+                  dict(batch=(1 << 31) - 1, beams=64, vocab=(1 << 31) - 1, logits_batch=0, logits_beam=0)):
         assert call(args(**wrong)) == EINVAL, wrong
+    assert L.beam_select_scratch_bytes(args(batch=(1 << 31) - 1, beams=64, vocab=(1 << 31) - 1)) == 0
     for wrong in (dict(beams=65), dict(count=65), dict(dtype=sc.DTYPE_CODES["f64"])):
         assert call(args(**wrong)) == ENOTSUP, wrong
         assert L.beam_select_scratch_bytes(args(**wrong)) == 0

@@ -171,6 +171,20 @@ def test_far_rows():
     torch.cuda.empty_cache()
 
 
+def test_more_rows_than_a_launch_takes():
+    # 2^22 workgroups a launch: the rows at its end and behind it
+    b, k, v = 65540, 64, 3
+    g = torch.Generator(device="cuda").manual_seed(13)
+    x = torch.randn((b, k, v), generator=g, device="cuda").bfloat16()
+    s = torch.randn((b, k), generator=g, device="cuda")
+    got = sc.beam_select(x, s, 2)
+    for lo, hi in ((0, 30000), (30000, b)):
+        part = sc.beam_select(x[lo:hi], s[lo:hi].contiguous(), 2)
+        assert all(torch.equal(a[lo:hi], c) for a, c in zip(got, part))
+    full = s.double()[..., None] + torch.log_softmax(x.double(), -1)
+    assert bool(((got[0][:, 0].double() - full.view(b, -1).max(-1).values).abs() < 1e-6).all())
+
+
 # batch, beams, rows' shapes and types
 REORDERS = [(1, 1, [((5,), "f32")]), (1, 4, [((3, 768), "bf16"), ((768, 16), "f32")]), (3, 2, [((), "i64"), ((1,), "u8")]),
             (2, 8, [((16,), "u8"), ((17,), "u8"), ((15,), "f16"), ((333, 3), "f32")]),

@@ -371,6 +371,68 @@ def test_states_beyond_a_chunks_decay():
     assert bool(torch.isinf(y).all()) and bool(torch.isinf(state).all())
 
 
+@pytest.mark.parametrize("l", [3, 131])
+def test_more_sequences_than_an_axis_holds(l):
+    # 65535 sequences a launch: the ones at its end and behind it, in one tile and in several
+    b, d = 65538, 3
+    r = torch.Generator(device="cuda").manual_seed(l)
+    x, f = (torch.randn((b, l, d), generator=r, device="cuda") for _ in range(2))
+    rate = torch.rand(d, generator=r, device="cuda")
+    init = torch.randn((b, d), generator=r, device="cuda")
+    y, state, starts = sc.gated_scan(x, f, rate, initial_state=init, keep_starts=True)
+    g = sc.gated_scan_grad(x, x, f, starts, rate)
+    total = torch.zeros(d, dtype=torch.float64, device="cuda")
+    for lo, hi in ((0, 40000), (40000, b)):
+        s = slice(lo, hi)
+        y2, state2, starts2 = sc.gated_scan(x[s], f[s], rate, initial_state=init[s].contiguous(), keep_starts=True)
+        g2 = sc.gated_scan_grad(x[s], x[s], f[s], starts2, rate)
+        assert torch.equal(y[s], y2) and torch.equal(state[s], state2)
+        assert all(torch.equal(g[n][s], g2[n]) for n in ("dx", "dforget", "dstate"))
+        total += g2["drate"].double()
+    # (sums of 2^16 x l terms in another order: 16 strands of 4096 tiles, some 2^12 roundings of a sum)
+    size = (g["dforget"].double().abs().sum((0, 1)) / rate).clamp(min=1.0)
+    assert bool(((g["drate"].double() - total).abs() <= size * 2.0 ** -12 * 8).all())
+
+
+def test_more_runs_than_an_axis_holds():
+    # one channel, tiles beyond 65535 in both directions: the whole against its parts
+    l, cut = 8_500_000, 5_000_001
+    r = torch.Generator(device="cuda").manual_seed(5)
+    x, f = (torch.randn((1, l, 1), generator=r, device="cuda").bfloat16() for _ in range(2))
+    rate = torch.full((1,), 1e-3, device="cuda")
+    y, state, starts = sc.gated_scan(x, f, rate, keep_starts=True)
+    g = sc.gated_scan_grad(x, x, f, starts, rate)
+    y1, mid, starts1 = sc.gated_scan(x[:, :cut], f[:, :cut], rate, keep_starts=True)
+    y2, last, starts2 = sc.gated_scan(x[:, cut:], f[:, cut:], rate, initial_state=mid, keep_starts=True)
+    g2 = sc.gated_scan_grad(x[:, cut:], x[:, cut:], f[:, cut:], starts2, rate)
+    g1 = sc.gated_scan_grad(x[:, :cut], x[:, :cut], f[:, :cut], starts1, rate, dfinal=g2["dstate"])
+    # states of about 30 (1 over the root of the rate) that differ by roundings of 2^-24 over some thousand tokens
+    near = lambda a, b: bool(((a.float() - b.float()).abs() <= a.float().abs() * 2.0 ** -7 + 1e-2).all())  # noqa: E731
+    assert near(y, torch.cat([y1, y2], 1)) and near(state, last)
+    assert near(g["dx"], torch.cat([g1["dx"], g2["dx"]], 1)) and near(g["dstate"], g1["dstate"])
+    # where a part begins with the whole, it is the same to the bit
+    assert torch.equal(y[:, :4096], y1[:, :4096])
+
+
+def test_a_state_that_never_comes():
+    # a build that asks for a state once and then takes it as lost: the call ends, the first tile is right and
+    # what follows is right or no number
+    from stream_compaction_amd import build
+    from stream_compaction_amd.sequence import _gated_args
+    k, _ = inputs((2, 900, 300, "f32", None, "rate in"), 160)
+    want, _ = sc.gated_scan(**k)
+    L = sc.load(build.FALLBACK_LIB_PATH)
+    a = _gated_args(k["x"], k["forget"], k["rate"], k["input_gate"], None, None, None, False)
+    y = torch.empty_like(want)
+    scratch = torch.empty(L.gated_scan_scratch_bytes(a), dtype=torch.uint8, device="cuda")
+    sc.check(L.gated_scan(a, y.data_ptr(), None, None, scratch.data_ptr(), scratch.numel(),
+                          torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    assert torch.equal(y[:, :128], want[:, :128])
+    lost = torch.isnan(y)
+    assert torch.equal(y[~lost], want[~lost])
+
+
 def test_refusals_leave_outputs():
     x = torch.randn(2, 8, 16, device="cuda")
     rate = torch.rand(16, device="cuda")
