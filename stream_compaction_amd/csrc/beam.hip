@@ -44,12 +44,13 @@ __device__ __forceinline__ double key_value64(uint64_t k) {
   return __builtin_bit_cast(double, (k >> 63) ? k & 0x7fffffffffffffffull : ~k);
 }
 
-// 2^t for -1000 <= t <= 1000, to 5e-11 of it: t = n + f with |f| <= 1/2, a polynomial
-// of degree 7 that is 1 at 0 (least maximum of the relative error, fitted there), n to
-// the exponent.
-__device__ __forceinline__ double exp2_64(double t) {
-  const double shift = 6755399441055744.0;   // 1.5 x 2^52: the sum's last digits are n
-  const double r = t + shift, f = t - (r - shift);
+// exp(x) for -690 <= x <= 690, to 5e-11 of it.  x log2(e) is n + f with |f| <= 1/2: n
+// comes from the last digits of a sum with 1.5 x 2^52, f from the same product with n
+// taken off in one rounding; 2^f is a polynomial of degree 7 that is 1 at 0 (least
+// maximum of the relative error, fitted there), and n is added to its exponent.
+__device__ __forceinline__ double exp_64(double x) {
+  const double shift = 6755399441055744.0, log2e = 1.4426950408889634074;
+  const double r = __builtin_fma(x, log2e, shift), f = __builtin_fma(x, log2e, shift - r);
   double v = __builtin_fma(f, 1.5196156538658058e-05, 0.00015466756316955186);
   v = __builtin_fma(f, v, 0.0013333935055508488);
   v = __builtin_fma(f, v, 0.009618038132060329);
@@ -57,10 +58,10 @@ __device__ __forceinline__ double exp2_64(double t) {
   v = __builtin_fma(f, v, 0.240226510665611);
   v = __builtin_fma(f, v, 0.6931471807045305);
   v = __builtin_fma(f, v, 1.0);
-  const uint64_t b = __builtin_bit_cast(uint64_t, v) + (__builtin_bit_cast(uint64_t, r) << 52);
+  u32x2 b = __builtin_bit_cast(u32x2, v);
+  b.y += __builtin_bit_cast(u32x2, r).x << 20;
   return __builtin_bit_cast(double, b);
 }
-constexpr double kLog2e64 = 1.4426950408889634074;
 
 // All lanes' sum and maximum, in every lane.
 __device__ __forceinline__ double wave_sum(double v) {
@@ -97,8 +98,30 @@ __device__ __forceinline__ uint32_t lanes_bound(uint32_t key, int count) {
     const uint32_t c = t | (1u << bit);
     if (__builtin_popcountll(__ballot(key >= c)) >= count) t = c;
   }
-  // (a 16-bit type's keys end in zeros, below 0 in ones)
-  return (t >> 31) ? t : t | ((1u << LOW) - 1);
+  return t;
+}
+// Two bounds for the `count` greatest of a segment, from its waves' lanes: a wave in
+// which `count` lanes reach a value gives one alone; the least of what a quarter of them
+// reach in each of the four gives another.  The greater holds: as a rule the second,
+// which leaves some 20 entries for 16 (the first 50); where all that is great lies in one
+// wave the first.  The low bits of the keys are left out as far as a 16-bit type has
+// none (its keys end in zeros, below 0 in ones), and in float32 the last 12.
+struct Bounds { uint32_t alone, together; };
+template <class F>
+__device__ __forceinline__ Bounds lanes_bounds(uint32_t key, int count) {
+  constexpr int LOW = std::is_same_v<F, FmtBF16> ? 16 : (std::is_same_v<F, FmtF16> ? 13 : 12);
+  constexpr uint32_t ones = sizeof(typename F::S) == 2 ? (1u << LOW) - 1 : 0;
+  const uint32_t t = lanes_bound<LOW>(key, count), u = lanes_bound<LOW>(key, (count + kBeamWaves - 1) / kBeamWaves);
+  return Bounds{(t >> 31) ? t : t | ones, (u >> 31) ? u : u | ones};
+}
+__device__ __forceinline__ uint32_t joint_bound(const Bounds* waves) {
+  uint32_t alone = waves[0].alone, together = waves[0].together;
+#pragma unroll
+  for (int w = 1; w < kBeamWaves; ++w) {
+    alone = alone > waves[w].alone ? alone : waves[w].alone;
+    together = together < waves[w].together ? together : waves[w].together;
+  }
+  return alone > together ? alone : together;
 }
 
 // Of a segment: its greatest logit, and its sum of exp(l - from).
@@ -115,7 +138,8 @@ struct SegmentShared {
   uint32_t rank[kListed];
   double sum[kBeamWaves];
   float most[kBeamWaves];
-  uint32_t bound[kBeamWaves], part[kBeamWaves], listed[kBeamWaves];
+  Bounds bound[kBeamWaves];
+  uint32_t part[kBeamWaves], listed[kBeamWaves];
 };
 
 // A workgroup's sum of a number of each thread.
@@ -141,7 +165,6 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
                                                                    int64_t segments, int64_t length) {
   using S = typename F::S;
   constexpr int E = kVecElems<F>;
-  constexpr int kBits = std::is_same_v<F, FmtBF16> ? 16 : (std::is_same_v<F, FmtF16> ? 13 : 0);
   __shared__ SegmentShared sh;
   const int wave = wave_id(), tid = (int)threadIdx.x, count = (int)p.count;
   int64_t seg, j;
@@ -180,10 +203,6 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
     IO::unpack(u32x4{w[0], w[1], w[2], w[3]}, v);
   };
   // maximum and sum of exponentials at once, for logits of ordinary size
-  // (what is 2^-1000 adds nothing, as do masked logits)
-  auto exponential = [&](float v, double off) {
-    return exp2_64(__builtin_fmax(__builtin_fma((double)v, kLog2e64, off), -1000.0));
-  };
   float most = -__builtin_huge_valf();
   double sum = 0.0;
 #pragma unroll
@@ -200,14 +219,15 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       most = __builtin_fmaxf(most, v[e]);
-      sum += exponential(v[e], 0.0);
+      // (exp(-690) adds nothing, and stands for masked logits)
+      sum += exp_64((double)__builtin_fmaxf(v[e], -690.0f));
     }
     // vector after vector: each when it is there, with the registers of one
     materialize(sum);
     __builtin_amdgcn_sched_barrier(0);
   }
   const uint32_t mine = order_key(most);
-  const uint32_t bound = lanes_bound<kBits>(mine, count);
+  const Bounds bound = lanes_bounds<F>(mine, count);
   const float wmost = wave_max(most);
   if (lane_id() == 0) {
     sh.most[wave] = wmost;
@@ -215,12 +235,9 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
   }
   __syncthreads();
   float top = sh.most[0];
-  uint32_t least = sh.bound[0];
+  uint32_t least = joint_bound(sh.bound);
 #pragma unroll
-  for (int w = 1; w < kBeamWaves; ++w) {
-    top = __builtin_fmaxf(top, sh.most[w]);
-    least = least > sh.bound[w] ? least : sh.bound[w];
-  }
+  for (int w = 1; w < kBeamWaves; ++w) top = __builtin_fmaxf(top, sh.most[w]);
   uint64_t* out = best + (row * segments + seg) * count;
   if (top == -__builtin_huge_valf()) {                           // all masked
     if (tid < count) out[tid] = 0;
@@ -256,7 +273,6 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
   float from = 0.0f;
   if (!(__builtin_fabsf(top) <= kPlainLogit)) {
     const bool infinite = top == __builtin_huge_valf();
-    const double off = infinite ? 0.0 : -(double)top * kLog2e64;
     from = top;
     sum = 0.0;
 #pragma unroll
@@ -265,9 +281,9 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
       values(i, v);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        // (beside an infinite logit: 2^0 for each such, nothing for others)
-        const float l = infinite ? (v[e] == top ? 0.0f : -__builtin_huge_valf()) : v[e];
-        sum += exponential(l, off);
+        // (beside an infinite logit: exp(0) for each such, nothing for others)
+        const double d = infinite ? (v[e] == top ? 0.0 : -690.0) : (double)v[e] - (double)top;
+        sum += exp_64(__builtin_fmax(d, -690.0));
       }
       materialize(sum);
       __builtin_amdgcn_sched_barrier(0);
@@ -278,7 +294,6 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
     sh.sum[wave] = sum;
     sh.listed[wave] = listed;
   }
-  for (int i = tid; i < kListed; i += kBeamThreads) sh.rank[i] = 0;
   __syncthreads();
   if (tid == 0) {
     double all = sh.sum[0];
@@ -318,7 +333,24 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
     place += w < wave ? sh.listed[w] : 0;
     n += sh.listed[w];
   }
+  if (n >= (uint32_t)count && n <= 64) {
+    // as a rule: one wave ranks an entry a lane, the others are done
+    if (wave != 0) return;
+    uint32_t k = (uint32_t)lane_id(), w = 0;
+#pragma unroll
+    for (int i = 0; i + 1 < kBeamWaves; ++i) {
+      const bool beyond = w == (uint32_t)i && k >= sh.listed[i];
+      k -= beyond ? sh.listed[i] : 0;
+      w += beyond ? 1 : 0;
+    }
+    const uint64_t own = (uint32_t)lane_id() < n ? sh.by_wave[w][k] : 0;
+    uint32_t rank = 0;
+    for (uint32_t i = 0; i < n; ++i) rank += readlane(own, (int)i) > own ? 1u : 0u;
+    if ((uint32_t)lane_id() < n && rank < (uint32_t)count) out[rank] = own;
+    return;
+  }
   for (uint32_t i = lane_id(); i < listed; i += 64) sh.list[place + i] = sh.by_wave[wave][i];
+  for (int i = tid; i < kListed; i += kBeamThreads) sh.rank[i] = 0;
   if (n < (uint32_t)count) {
     // those equal to the bound, in token order, as many as are asked for
     uint32_t open = (uint32_t)count - n, taken = n;
@@ -462,7 +494,7 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(BeamProblem p, 
     const uint64_t s = candidate(i, best[row0 * per + i]).score;
     mine = mine > s ? mine : s;
   }
-  const uint32_t bound = lanes_bound<0>((uint32_t)(mine >> 32), count);
+  const uint32_t bound = lanes_bound<8>((uint32_t)(mine >> 32), count);
   if (lane_id() == 0) sh.bound[wave] = bound;
   __syncthreads();
   uint32_t least = 1;
