@@ -1,12 +1,15 @@
 """A small state space language model on the library's sequence operators.
 
-    python examples/state_space_lm.py [--steps 100] [--dtype bf16]
+    python examples/state_space_lm.py [--steps 100] [--dtype bf16] [--mixer gated] [--beams 4]
 
-Embedding, causal convolution and selective scan make the model; it learns a rule that gives
-each token from the one three places before (sequences padded to unequal lengths), forward and
-backward through the library's kernels, and then answers token by token with the single-token steps, captured into one HIP
-graph.  Prints the loss on the way, how far the steps' logits are from the whole sequence's,
-and the share of tokens that the model continues right.
+Embedding, causal convolution and selective scan (or, with ``--mixer gated``, the gated scan) make
+the model; it learns a rule that gives each token from the one three places before (sequences
+padded to unequal lengths), forward and backward through the library's kernels, and then answers
+token by token with the single-token steps, captured into one HIP graph.  Prints the loss on the
+way, how far the steps' logits are from the whole sequence's, and the share of tokens that the
+model continues right.  With ``--beams`` it also searches for the likeliest answers, several
+at a time, the states following their beams, and prints how far their scores are from the whole
+sequences' log probabilities.
 """
 import argparse
 import math
@@ -64,13 +67,44 @@ class Layer(nn.Module):
         return u + self.leave(y)
 
 
+class GatedLayer(nn.Module):
+    """The same with a gated scan: one state per channel, both of its gates from one projection."""
+
+    def __init__(self, model, inner, width, dtype):
+        super().__init__()
+        self.norm = nn.LayerNorm(model, dtype=dtype)
+        self.enter = nn.Linear(model, 2 * inner, bias=False, dtype=dtype)
+        self.gates = nn.Linear(inner, 2 * inner, dtype=dtype)
+        self.leave = nn.Linear(inner, model, bias=False, dtype=dtype)
+        self.filter = nn.Parameter((torch.rand(inner, width) * 2 - 1) / math.sqrt(width))
+        self.filter_bias = nn.Parameter(torch.zeros(inner))
+        # rates that leave 0.9 to 0.999 of the state at half a gate
+        self.log_rate = nn.Parameter(torch.log(-2 * torch.log(0.9 + 0.099 * torch.rand(inner))))
+
+    def forward(self, u, lengths=None):
+        x, z = self.enter(self.norm(u)).chunk(2, -1)
+        c, window = ops.causal_conv(x, self.filter, self.filter_bias, lengths=lengths)
+        forget, input_gate = self.gates(c).chunk(2, -1)
+        y, state = ops.gated_scan(c, forget, self.log_rate.exp(), input_gate, z, lengths=lengths)
+        return u + self.leave(y), (window, state)
+
+    def step(self, u, cache):
+        window, state = cache
+        x, z = self.enter(self.norm(u)).chunk(2, -1)
+        c = sc.causal_conv_step(window, x, self.filter, self.filter_bias)
+        forget, input_gate = self.gates(c).chunk(2, -1)
+        y = sc.gated_scan_step(state, c, forget, self.log_rate.exp(), input_gate, z)
+        return u + self.leave(y)
+
+
 class Model(nn.Module):
     def __init__(self, vocabulary, model=64, inner=128, states=16, rank=8, width=4, layers=2,
-                 dtype=torch.float32):
+                 dtype=torch.float32, mixer="selective"):
         super().__init__()
         self.table = nn.Parameter((torch.randn(vocabulary, model) / math.sqrt(model)).to(dtype))
         self.scale = math.sqrt(model)
-        self.layers = nn.ModuleList(Layer(model, inner, states, rank, width, dtype)
+        self.layers = nn.ModuleList(GatedLayer(model, inner, width, dtype) if mixer == "gated" else
+                                    Layer(model, inner, states, rank, width, dtype)
                                     for _ in range(layers))
         self.norm = nn.LayerNorm(model, dtype=dtype)
 
@@ -146,11 +180,47 @@ def answer(model, prompt, count):
     return torch.stack(tokens, 1), torch.stack(seen, 1)
 
 
-def run(steps=100, dtype="f32", vocabulary=32, seed=0):
+@torch.no_grad()
+def search(model, prompt, count, beams):
+    """The ``beams`` likeliest continuations of ``prompt`` that beam search finds, one captured
+    step per token: their tokens ``[batch, beams, count]`` and log probabilities, the best first."""
+    b, v = prompt.shape[0], model.table.shape[0]
+    logits, cache = model(prompt)
+    # each prompt has one beam; its states are every chosen continuation's
+    scores, _, tokens = sc.beam_select(logits[:, -1:], torch.zeros(b, 1, device="cuda"), beams)
+    cache = [(w.repeat_interleave(beams, 0), s.repeat_interleave(beams, 0)) for w, s in cache]
+    text = torch.zeros((b, beams, count), dtype=torch.int32, device="cuda")
+    text[..., 0] = tokens
+    at = torch.ones(1, dtype=torch.int64, device="cuda")
+
+    def step(cache, text, at, scores, tokens):
+        logits = model.step(tokens.view(-1), cache).view(b, beams, v)
+        new_scores, parents, new_tokens = sc.beam_select(logits, scores, beams)
+        sc.beam_reorder([t for layer in cache for t in layer] + [text], parents)
+        scores.copy_(new_scores)
+        tokens.copy_(new_tokens)
+        text.index_copy_(2, at, new_tokens[..., None])
+        at.add_(1)
+
+    held = cache, text, at, scores, tokens
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step([(w.clone(), s.clone()) for w, s in cache], *(t.clone() for t in held[1:]))
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(*held)
+    for _ in range(count - 1):
+        graph.replay()
+    return text, scores
+
+
+def run(steps=100, dtype="f32", vocabulary=32, seed=0, mixer="selective", beams=0):
     torch.manual_seed(seed)
     gen = torch.Generator().manual_seed(seed)
     kind = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[dtype]
-    model = Model(vocabulary, dtype=kind).cuda()
+    model = Model(vocabulary, dtype=kind, mixer=mixer).cuda()
     rule = torch.randperm(vocabulary, generator=gen)
     first, last = train(model, steps, gen, rule)
     whole = sequences(gen, rule, 16, 48).cuda()
@@ -163,12 +233,26 @@ def run(steps=100, dtype="f32", vocabulary=32, seed=0):
     right = float((tokens == whole[:, prompt.shape[1]:prompt.shape[1] + 20]).float().mean())
     print(f"loss {first:.3f} -> {last:.3f}; steps' logits off by {off:.2e} of {span:.1f}; "
           f"{100 * right:.0f}% of tokens continued right", flush=True)
-    return {"first": first, "last": last, "off": off, "span": span, "right": right}
+    result = {"first": first, "last": last, "off": off, "span": span, "right": right}
+    if beams:
+        text, scores = search(model, prompt, 20, beams)
+        with torch.no_grad():
+            whole = torch.cat([prompt.repeat_interleave(beams, 0), text.flatten(0, 1).long()], 1)
+            logits, _ = model(whole[:, :-1].contiguous())
+            each = torch.log_softmax(logits[:, prompt.shape[1] - 1:].double(), -1)
+            sums = each.gather(-1, whole[:, prompt.shape[1]:, None]).sum((1, 2)).view(scores.shape)
+        result["search_off"] = float((sums - scores).abs().max())
+        result["found"] = float((text[:, 0].long() == tokens).float().mean())
+        print(f"scores off by {result['search_off']:.2e}; {100 * result['found']:.0f}% of the best beams' tokens "
+              "are the greedy answers'", flush=True)
+    return result
 
 
 if __name__ == "__main__":
     parser = argparse.ArgumentParser()
     parser.add_argument("--steps", type=int, default=100)
     parser.add_argument("--dtype", choices=("f32", "f16", "bf16"), default="f32")
+    parser.add_argument("--mixer", choices=("selective", "gated"), default="selective")
+    parser.add_argument("--beams", type=int, default=0)
     args = parser.parse_args()
-    run(args.steps, args.dtype)
+    run(args.steps, args.dtype, mixer=args.mixer, beams=args.beams)
