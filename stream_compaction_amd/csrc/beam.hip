@@ -411,6 +411,7 @@ struct JoinShared {
   uint32_t rank[kJoined];
   double lse[64];                            // log of the sum of exponentials of the logits
   float most[64], score[64];
+  bool done[64];
   uint32_t bound[kJoinWaves];
   uint32_t listed;
   Candidate wave_best[kJoinWaves];
@@ -437,30 +438,32 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(BeamProblem p, 
   if (tid == 0) sh.listed = 0;
   for (int i = tid; i < kJoined; i += kJoinThreads) sh.rank[i] = 0;
   for (int j = wave; j < beams; j += kJoinWaves) {
+    // (a finished beam's segments hold nothing, and are read all the same: their loads
+    // need not wait for the mark's)
     const Found* f = found + (row0 + j) * segments;
+    const Found own = f[lane_id() < segments ? lane_id() : 0];
+    const float score = p.scores[row0 + j];
     const bool done = p.finished != nullptr && p.finished[row0 + j] != 0;
-    float most = -__builtin_huge_valf(), from = most;
-    double sum = 0.0;
-    if (!done) {
-      for (int64_t s = lane_id(); s < segments; s += 64) {
-        most = __builtin_fmaxf(most, f[s].most);
-        from = __builtin_fmaxf(from, f[s].from);
-      }
-      most = wave_max(most);
-      from = wave_max(from);
-      for (int64_t s = lane_id(); s < segments; s += 64) {
-        const float m = f[s].from;
-        const double part = f[s].sum;
-        if (m == from) sum += part;
-        else if (m > -__builtin_huge_valf()) sum += part * exp((double)m - (double)from);
-      }
-      sum = wave_sum(sum);
+    float most = own.most, from = own.from;
+    for (int64_t s = lane_id() + 64; s < segments; s += 64) {
+      most = __builtin_fmaxf(most, f[s].most);
+      from = __builtin_fmaxf(from, f[s].from);
     }
+    most = wave_max(most);
+    from = wave_max(from);
+    // (beside an infinite logit the sum is the number of such)
+    auto part = [&](const Found& v) {
+      if (v.from == from) return v.sum;
+      return v.from > -__builtin_huge_valf() ? v.sum * exp((double)v.from - (double)from) : 0.0;
+    };
+    double sum = lane_id() < segments ? part(own) : 0.0;
+    for (int64_t s = lane_id() + 64; s < segments; s += 64) sum += part(f[s]);
+    sum = wave_sum(sum);
     if (lane_id() == 0) {
       sh.most[j] = most;
-      // (beside an infinite logit the sum is the number of such)
-      sh.lse[j] = done ? 0.0 : log(sum) + (most == __builtin_huge_valf() ? 0.0 : (double)from);
-      sh.score[j] = p.scores[row0 + j];
+      sh.lse[j] = log(sum) + (most == __builtin_huge_valf() ? 0.0 : (double)from);
+      sh.score[j] = score;
+      sh.done[j] = done;
     }
   }
   __syncthreads();
@@ -471,7 +474,7 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(BeamProblem p, 
     Candidate c{0, entry, (uint32_t)j};
     const double base = (double)sh.score[j];
     double s;
-    if (p.finished != nullptr && p.finished[row0 + j] != 0) {
+    if (sh.done[j]) {
       if (k != 0) return c;
       c.entry = (uint32_t)~(uint32_t)p.end_token;
       s = base;
@@ -494,7 +497,7 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(BeamProblem p, 
     const uint64_t s = candidate(i, best[row0 * per + i]).score;
     mine = mine > s ? mine : s;
   }
-  const uint32_t bound = lanes_bound<8>((uint32_t)(mine >> 32), count);
+  const uint32_t bound = lanes_bound<12>((uint32_t)(mine >> 32), count);
   if (lane_id() == 0) sh.bound[wave] = bound;
   __syncthreads();
   uint32_t least = 1;
