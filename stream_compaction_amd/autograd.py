@@ -4,7 +4,9 @@
 functions of these names in ``stream_compaction_amd.sequence`` and can be differentiated with respect to
 every floating input, through the output and the final state.  Both directions run in the
 library's kernels on the current stream; work space comes from torch's allocator, so a
-forward and backward pass can be captured into a HIP graph.  Gradients are taken once, in
+forward and backward pass can be captured into a HIP graph (of leaves that no output of
+eager work still refers to: torch takes a leaf's gradient to the stream of the first graph that
+holds it, and a capture that waits for another stream fails).  Gradients are taken once, in
 reverse: there are no second derivatives, no forward mode and no ``torch.func`` transforms
 (``grad``, ``vmap``, ...), which torch refuses with an error of its own.
 """
