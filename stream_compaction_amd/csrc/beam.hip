@@ -179,11 +179,14 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
   // The row's last vector ends with it and may begin among those of the one before,
   // which are left out.  What a thread adds up depends on the vocabulary alone, not
   // on where the row lies: equal rows have equal sums.
-  const int64_t v0 = seg * length + tid, vend = (seg + 1) * length;
-  auto begin = [&](int64_t vec) { return vec * E < p.vocab - E ? vec * E : p.vocab - E; };
+  // (below 2^31 logits and a segment more: 32 bits without a sign)
+  const uint32_t vocab = (uint32_t)p.vocab;
+  const uint32_t s0 = (uint32_t)(seg * length), v0 = s0 + (uint32_t)tid, vend = s0 + (uint32_t)length;
+  const bool whole = vocab >= E;
+  auto begin = [&](uint32_t vec) { return whole && vec * E < vocab - E ? vec * E : vocab - E; };
   using IO = RowIO<F, E>;
   u32x4 raw[NV];                             // as they are: 16-bit logits two to a register
-  if (p.vocab >= E) {
+  if (whole) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) raw[i] = IO::load_any(logits + begin(v0 + i * kBeamThreads), E);
   } else {                                   // less than a vector: the first thread's
@@ -193,7 +196,7 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         v[e] = -__builtin_huge_valf();
-        if (i == 0 && tid == 0 && e >= E - p.vocab) v[e] = widen<F>(logits[e - (E - p.vocab)]);
+        if (i == 0 && tid == 0 && e + (int)vocab >= E) v[e] = widen<F>(logits[e + (int)vocab - E]);
       }
       raw[i] = IO::pack(v);
     }
@@ -213,11 +216,11 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     float v[E];
-    const int64_t vec = v0 + i * kBeamThreads, skip = vec < vend ? vec * E - begin(vec) : E;
-    if (skip > 0 && p.vocab >= E) {
+    const uint32_t vec = v0 + i * kBeamThreads, skip = vec < vend ? vec * E - begin(vec) : E;
+    if (skip > 0 && whole) {
       IO::unpack(raw[i], v);
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = e >= skip ? v[e] : -__builtin_huge_valf();
+      for (int e = 0; e < E; ++e) v[e] = (uint32_t)e >= skip ? v[e] : -__builtin_huge_valf();
       raw[i] = IO::pack(v);
     }
     values(i, v);
@@ -252,9 +255,16 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
   }
   // what is above the bound, then what is equal to it
   least = least > kMaskedKey ? least : kMaskedKey + 1;
-  auto entry = [&](int i, int e, float v) {
-    const uint32_t token = (uint32_t)(begin(v0 + i * kBeamThreads) + e);
-    return ((uint64_t)order_key(v) << 32) | (uint32_t)~token;
+  // What is chosen is first held as its value and where it lies (the thread, and which
+  // of its logits), a few instructions each; the entry is made of that by a lane each.
+  auto hold = [&](int ie, float v) {
+    return ((uint64_t)__builtin_bit_cast(uint32_t, v) << 32) | ((uint32_t)ie * kBeamThreads + (uint32_t)tid);
+  };
+  auto entry = [&](uint64_t held) {
+    const uint32_t at = (uint32_t)held, ie = at / kBeamThreads;
+    const uint32_t vec = s0 + at % kBeamThreads + ie / E * kBeamThreads;
+    const uint32_t token = begin(vec) + ie % E;
+    return ((uint64_t)order_key(__builtin_bit_cast(float, (uint32_t)(held >> 32))) << 32) | (uint32_t)~token;
   };
   float edge = key_value(least);
   // each wave lists what is above the edge for itself: how many there were
@@ -269,7 +279,7 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
         const uint64_t on = __ballot(v[e] > edge);
         if (on == 0) continue;
         const uint32_t k = n + (uint32_t)__builtin_popcountll(on & ((1ull << lane_id()) - 1));
-        if (v[e] > edge && k < (uint32_t)(kListed / kBeamWaves)) sh.by_wave[wave][k] = entry(i, e, v[e]);
+        if (v[e] > edge && k < (uint32_t)(kListed / kBeamWaves)) sh.by_wave[wave][k] = hold(i * E + e, v[e]);
         n += (uint32_t)__builtin_popcountll(on);
       }
     }
@@ -349,13 +359,13 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
       k -= beyond ? sh.listed[i] : 0;
       w += beyond ? 1 : 0;
     }
-    const uint64_t own = (uint32_t)lane_id() < n ? sh.by_wave[w][k] : 0;
+    const uint64_t own = (uint32_t)lane_id() < n ? entry(sh.by_wave[w][k]) : 0;
     uint32_t rank = 0;
     for (uint32_t i = 0; i < n; ++i) rank += readlane(own, (int)i) > own ? 1u : 0u;
     if ((uint32_t)lane_id() < n && rank < (uint32_t)count) out[rank] = own;
     return;
   }
-  for (uint32_t i = lane_id(); i < listed; i += 64) sh.list[place + i] = sh.by_wave[wave][i];
+  for (uint32_t i = lane_id(); i < listed; i += 64) sh.list[place + i] = entry(sh.by_wave[wave][i]);
   for (int i = tid; i < kListed; i += kBeamThreads) sh.rank[i] = 0;
   if (n < (uint32_t)count) {
     // those equal to the bound, in token order, as many as are asked for
@@ -381,7 +391,7 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
 #pragma unroll
       for (int e = 0; e < E; ++e)
         if (v[e] == edge) {
-          if (before < open) sh.list[taken + before] = entry(i, e, v[e]);
+          if (before < open) sh.list[taken + before] = entry(hold(i * E + e, v[e]));
           ++before;
         }
       const uint32_t got = all < open ? all : open;
