@@ -51,7 +51,6 @@ def declare(L):
     sz, f32 = ctypes.c_size_t, ctypes.c_float
     conv, scan = ctypes.POINTER(ConvArgs), ctypes.POINTER(ScanArgs)
     gated, beam = ctypes.POINTER(GatedArgs), ctypes.POINTER(BeamArgs)
-    many = ctypes.POINTER(_vp)
     for name, args in (
             ("causal_conv", [conv, _vp, _vp, _vp]),
             ("causal_conv_grad", [conv, _vp, ctypes.POINTER(_i64), _vp, _vp, _vp, _vp, _vp, _vp,
@@ -65,7 +64,7 @@ def declare(L):
             ("gated_scan_grad", [gated, ctypes.POINTER(GatedGrads), _vp, sz, _vp]),
             ("gated_scan_step", [gated, _vp, _vp, _vp, _vp]),
             ("beam_select", [beam, _vp, _vp, _vp, _vp, sz, _vp]),
-            ("beam_reorder", [many, many, ctypes.POINTER(_i64), _i64, _vp, _i64, _i64, _vp]),
+            ("beam_reorder", [_vp, _vp, _vp, _i64, _vp, _i64, _i64, _vp]),
             ("embedding", [_vp, _vp, _vp, _i64, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int, f32,
                            _vp]),
             ("embedding_grad", [_vp, _vp, _vp, _i64, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int,

@@ -5,15 +5,13 @@ Thin wrappers over the C ABI (``include/scan.h`` has every definition and rule),
 of the sequence operators: they check shapes, types and devices, allocate what is not given, and
 pass pointers and the current HIP stream, which must be of the data's GPU.
 """
-import ctypes
+from array import array
 
 import torch
 
 from . import check, lib
 from ._sequence_abi import BeamArgs
 from .sequence import _code, _like, _out, _queue, _require, _scratch
-
-_i64, _vp = ctypes.c_int64, ctypes.c_void_p
 
 
 def beam_select(logits, scores, count, finished=None, end_token=0, out_scores=None, parents=None,
@@ -56,6 +54,13 @@ def beam_select(logits, scores, count, finished=None, end_token=0, out_scores=No
     return out_scores, parents, tokens
 
 
+def _pointers(tensors, what, dev):
+    for t in tensors:
+        if t.get_device() != dev or not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous tensors on cuda:{dev}")
+    return array("Q", [t.data_ptr() for t in tensors])
+
+
 def beam_reorder(states, parents, new_states=None, stream=None):
     """The beams' states follow them: ``new[b, j] = old[b, parents[b, j]]`` in each of ``states``,
     a list of contiguous tensors of any type, ``[batch, beams, ...]`` or ``[batch * beams, ...]``
@@ -75,19 +80,17 @@ def beam_reorder(states, parents, new_states=None, stream=None):
     _require(len(out) == len(states), "new_states must have as many tensors as states")
     n = len(states)
     _require(n <= 1024, "at most 1024 states")
-    rows, batched = b * k, (b, k)
-    pointers, sizes = [], []
-    for t in states:
-        # (at most a thousand of them a token: what is cheap to ask is asked first)
-        shape = t.shape
-        if not (len(shape) > 0 and (shape[0] == rows or shape[:2] == batched)):
+    # (up to a thousand tensors a token: each is asked little, and the pointers go out in arrays)
+    rows, shapes = b * k, [t.shape for t in states]
+    for shape in set(shapes):
+        if not (len(shape) > 0 and (shape[0] == rows or shape[:2] == (b, k))):
             raise ValueError("states must be [batch, beams, ...] or [batch * beams, ...]")
-        if t.get_device() != dev or not t.is_contiguous():
-            raise ValueError(f"states must be contiguous tensors on cuda:{dev}")
-        pointers.append(t.data_ptr())
-        sizes.append(t.nbytes // rows if rows else 0)
-    from_ = to = (_vp * n)(*pointers)
+    from_ = to = _pointers(states, "states", dev)
     if new_states is not None:
-        to = (_vp * n)(*[_like(o, "new_states", t.shape, t.dtype, dev) for t, o in zip(states, out)])
-    check(lib().beam_reorder(from_, to, (_i64 * n)(*sizes), n, pp, b, k, _queue(stream, dev)))
+        if [t.shape for t in out] != shapes or [t.dtype for t in out] != [t.dtype for t in states]:
+            raise ValueError("new_states must have the shapes and types of states")
+        to = _pointers(out, "new_states", dev)
+    sizes = array("q", [t.nbytes // rows for t in states] if rows else [0] * n)
+    check(lib().beam_reorder(from_.buffer_info()[0], to.buffer_info()[0], sizes.buffer_info()[0], n, pp, b, k,
+                             _queue(stream, dev)))
     return out
