@@ -45,7 +45,7 @@ def beam_select(logits, scores, count, finished=None, end_token=0, out_scores=No
     a = BeamArgs(logits.data_ptr(), sp, fp, b, k, v, count, int(end_token), stride[0], stride[1], code)
     chosen = (b, count)
     out_scores = _out(out_scores, "out_scores", chosen, torch.float32, scores, stream)
-    parents = _out(parents, "parents", chosen, torch.int32, scores, stream)
+    parents = _out(parents, "parents", chosen, torch.int32, out_scores, stream)
     tokens = _out(tokens, "tokens", chosen, torch.int32, parents, stream)
     L = lib()
     scratch, room = _scratch(scratch, L.beam_select_scratch_bytes(a), scores, stream)

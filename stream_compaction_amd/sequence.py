@@ -76,9 +76,9 @@ def _new(shape, dtype, like, stream):
     if stream is not None:
         with torch.cuda.stream(stream):
             return torch.empty(shape, dtype=dtype, device=like.device)
+    if like.shape == shape and like.is_contiguous():
+        return torch.empty_like(like) if like.dtype is dtype else torch.empty_like(like, dtype=dtype)
     if like.dtype is dtype:
-        if like.shape == shape and like.is_contiguous():
-            return torch.empty_like(like)
         return like.new_empty(shape)
     return torch.empty(shape, dtype=dtype, device=like.device)
 
@@ -336,7 +336,7 @@ def gated_scan(x, forget, rate=None, input_gate=None, z=None, initial_state=None
     a = _gated_args(x, forget, rate, input_gate, z, initial_state, lengths, False)
     y = _out(out, "out", x.shape, x.dtype, x, stream)
     f32 = torch.float32
-    fs = _out(final_state, "final_state", (a.batch, a.channels), f32, x, stream)
+    fs = _out(final_state, "final_state", (a.batch, a.channels), f32, x if rate is None else rate, stream)
     L = lib()
     starts = None
     if keep_starts:
