@@ -201,8 +201,8 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
       raw[i] = IO::pack(v);
     }
   }
-  // Vector i's logits.  A NaN is smaller and greater than nothing and equal to
-  // nothing, and a maximum is the other's, so that it counts for nothing below.
+  // Vector i's logits.  A NaN is smaller and greater than nothing and equal to nothing,
+  // so that it counts for nothing below.
   auto values = [&](int i, float (&v)[E]) {
     uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
@@ -226,7 +226,7 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
     values(i, v);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      most = __builtin_fmaxf(most, v[e]);
+      most = __builtin_elementwise_maximum(most, v[e]);
       // (exp(-690) adds nothing, and stands for masked logits; in 64 bits a NaN is quiet,
       // and the maximum one instruction)
       sum += exp_64(__builtin_fmax((double)v[e], -690.0));
@@ -234,6 +234,18 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
     // vector after vector: each when it is there, with the registers of one
     materialize(sum);
     __builtin_amdgcn_sched_barrier(0);
+  }
+  // (that maximum is a NaN's wherever there is one: the other kind takes a signalling
+  // one for a number's end, or an instruction more a logit)
+  if (__ballot(most != most) != 0) {
+    most = -__builtin_huge_valf();
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float v[E];
+      values(i, v);
+#pragma unroll
+      for (int e = 0; e < E; ++e) most = v[e] > most ? v[e] : most;
+    }
   }
   const uint32_t mine = order_key(most);
   const Bounds bound = lanes_bounds<F>(mine, count);

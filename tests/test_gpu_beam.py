@@ -1,5 +1,7 @@
 """Beam search on the GPU against the float64 oracle of ``beam_ref``: choices are equal, scores are
 within a float32 rounding of it; states move to the bit."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -158,6 +160,24 @@ def test_strides_and_streams(dt):
     assert all(torch.equal(p, q) for o in outs for p, q in zip(want, o))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+def test_every_nan_is_masked(dt):
+    # quiet and signalling ones of either sign, in the first, inner and last vectors, count for nothing
+    v, bits = 2311, {"bf16": (torch.int16, 0x7f80, 0x40), "f16": (torch.int16, 0x7c00, 0x200),
+                     "f32": (torch.int32, 0x7f800000, 0x400000)}[dt]
+    kind, top, quiet = bits
+    x = normal(gen(14), (2, 3, v), dt)
+    masked = x.clone()
+    sign = torch.iinfo(kind).min
+    for i, at in enumerate((0, 1, 2, 700, 701, 1333, v - 2, v - 1)):
+        nan = (top | (quiet if i % 2 else 1)) + (sign if i % 4 > 1 else 0)
+        x.view(kind)[:, :, at] = nan
+        masked[:, :, at] = -INF
+    assert int(x.isnan().sum()) == 8 * 6
+    s = -torch.rand((2, 3), generator=gen(15)).cuda()
+    assert all(torch.equal(a, b) for a, b in zip(sc.beam_select(x, s, 16), sc.beam_select(masked, s, 16)))
+
+
 def test_far_rows():
     # beams whose rows pass 2^32 bytes
     step = (1 << 30) + 5
@@ -168,6 +188,22 @@ def test_far_rows():
     s = torch.zeros(1, 3, device="cuda")
     assert all(torch.equal(a, b) for a, b in zip(sc.beam_select(far, s, 16), sc.beam_select(x0, s, 16)))
     del big, far
+    torch.cuda.empty_cache()
+
+
+def test_largest_vocabulary():
+    # places up to 2^31 - 2 in a row of 4 GiB; all but four logits are 0, which the first of them win
+    v = 2 ** 31 - 1
+    x = torch.zeros((1, 1, v), dtype=torch.bfloat16, device="cuda")
+    great = {v - 1: 4.0, 0: 3.0, 5: 2.0, 2 ** 30 + 1: 1.0}
+    for at, value in great.items():
+        x[0, 0, at] = value
+    got = sc.beam_select(x, torch.zeros(1, 1, device="cuda"), 6)
+    assert got[2].tolist() == [list(great) + [1, 2]] and got[1].tolist() == [[0] * 6]
+    lse = math.log(v - 4 + sum(math.exp(l) for l in great.values()))
+    want = torch.tensor(list(great.values()) + [0.0, 0.0], dtype=torch.float64) - lse
+    assert bool(((got[0][0].cpu().double() - want).abs() <= want.abs() * 2.0 ** -24 + 1e-9).all())
+    del x
     torch.cuda.empty_cache()
 
 
