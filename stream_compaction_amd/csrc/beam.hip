@@ -235,8 +235,8 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
     materialize(sum);
     __builtin_amdgcn_sched_barrier(0);
   }
-  // (that maximum is a NaN's wherever there is one: the other kind takes a signalling
-  // one for a number's end, or an instruction more a logit)
+  // (that maximum is NaN wherever an operand is; one that passes NaNs over would need the
+  // signalling ones made quiet first, an instruction more a logit)
   if (__ballot(most != most) != 0) {
     most = -__builtin_huge_valf();
 #pragma unroll
