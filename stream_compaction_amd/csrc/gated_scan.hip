@@ -34,7 +34,7 @@ void gated_scan_kernel(GatedProblem p, void* yv, float* final_state, float* star
   const int wave = wave_id();
   const int D = (int)p.channels;
   const int64_t n = sequence_tokens(p, tiles.b0 + blockIdx.y);
-  const Place place = draw_place(tiles, scratch, &sh.tile);
+  const Place place = draw_place<true>(tiles, scratch, &sh.tile);
   if (place.run < 0) return;
   const int64_t b = place.b, col = place.col, chunk = place.run;
   const int ch = place.part * kTileChannels + 2 * lane_id();

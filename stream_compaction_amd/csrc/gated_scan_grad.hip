@@ -46,7 +46,7 @@ void gated_scan_grad_kernel(GatedProblem p, GatedGrads g, uint64_t* scratch, flo
   const int wave = wave_id(), turn = kTileWaves - 1 - wave;  // its turn in the walk
   const int D = (int)p.channels;
   const int64_t n = sequence_tokens(p, tiles.b0 + blockIdx.y);
-  const Place place = draw_place(tiles, scratch, &sh.tile);
+  const Place place = draw_place<false>(tiles, scratch, &sh.tile);
   if (place.run < 0) return;
   const int64_t b = place.b, col = place.col, chunk = tiles.chunks - 1 - place.run;
   const int ch = place.part * kTileChannels + 2 * lane_id();

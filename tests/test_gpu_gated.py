@@ -132,6 +132,30 @@ def test_strides(how, dt, channels):
     assert torch.equal(st, st2)
 
 
+@pytest.mark.parametrize("channels,dt", [(4096, "bf16"), (4090, "f16"), (8190, "f32"), (8191, "bf16"), (3968, "bf16")])
+def test_wide_rows(channels, dt):
+    # many channels a row; each is its own, with the same bits as in a row of a few (an odd row
+    # goes by another kernel, whose sums and products the compiler may join otherwise)
+    test_scan((2, 300, channels, dt, [300, 190], "rate in gate init"))
+    test_grad((2, 300, channels, dt, [300, 190], "rate in gate init"))
+    if channels % 2:
+        return
+    k, _, dy, dfinal = inputs((2, 300, channels, dt, [300, 190], "rate in gate init"), 35, grads=True)
+    y, state, starts = sc.gated_scan(keep_starts=True, **k)
+    initial = k.pop("initial_state")
+    g = sc.gated_scan_grad(dy, starts=starts, dfinal=dfinal, **k)
+    starts = starts.view(2, -1, channels)
+    for lo, hi in ((0, 130), (900, 1156), (channels - 390, channels)):
+        part = {n: v if n == "lengths" else v[..., lo:hi].contiguous() for n, v in k.items()}
+        y2, state2, starts2 = sc.gated_scan(keep_starts=True, initial_state=initial[:, lo:hi].contiguous(), **part)
+        assert torch.equal(y[..., lo:hi], y2) and torch.equal(state[:, lo:hi], state2), (lo, hi)
+        for i, blocks in ((0, 5), (1, 3)):                   # (none is written for blocks without a token)
+            assert torch.equal(starts[i, :blocks, lo:hi], starts2.view(2, 5, -1)[i, :blocks]), (lo, hi)
+        g2 = sc.gated_scan_grad(dy[..., lo:hi].contiguous(), starts=starts2, dfinal=dfinal[:, lo:hi].contiguous(), **part)
+        for name in g:
+            assert torch.equal(g[name][..., lo:hi], g2[name]), (lo, hi, name)
+
+
 def test_broadcast_strides():
     # one token of the gate and one batch of z, repeated with stride 0; a row of one value
     k, _ = inputs((3, 170, 20, "f32", None, "rate in gate"), 40)
