@@ -192,6 +192,9 @@ static hipError_t launch_gated_z(const GatedProblem& p, void* y, float* final_st
     if (p.channels % 2 != 0)
       gated_scan_kernel<F, RATE, IG, Z, Rows2::Singles><<<grid, block, 0, stream>>>(
           p, y, final_state, starts, scratch, t);
+    else if (past && starts == nullptr)
+      gated_scan_kernel<F, RATE, IG, Z, Rows2::PairsOnce><<<grid, block, 0, stream>>>(
+          p, y, final_state, starts, scratch, t);
     else if (past)
       gated_scan_kernel<F, RATE, IG, Z, Rows2::PairsPast><<<grid, block, 0, stream>>>(
           p, y, final_state, starts, scratch, t);

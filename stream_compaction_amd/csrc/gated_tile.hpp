@@ -79,8 +79,12 @@ struct Rows {
 // Two neighbouring channels of a row as one access, or, where the number of
 // channels is odd, as one access each (a pair may then lie across a row's end).
 // Pairs are stored past the caches where the outputs are large (past_caches):
-// forward and gradient of 4 x 2048 x 2048 bf16, 34 MB an output, 108 to 102 us.
-enum class Rows2 { Pairs, PairsPast, Singles };
+// forward and gradient of 4 x 2048 x 2048 bf16, 34 MB an output, 108 to 102 us.  Once:
+// loaded so, too, by the gradient and by a forward that keeps no states for one (after
+// which nobody is known to read the inputs again): forward of 4 x 4096 x 4096 bf16 114.3
+// to 111.9 us, of 4 x 2048 x 2304 f32 73.7 to 70.6; forward and gradient of 4 x 2048 x 4096
+// 175 to 172; with the keeping forward's loads, too, 2 x 4096 x 2048 f32 159.5 to 166.
+enum class Rows2 { Pairs, PairsPast, PairsOnce, Singles };
 template <class F, Rows2 ROWS> struct PairIO {
   static constexpr bool ODD = ROWS == Rows2::Singles;
   using S = typename F::S;
@@ -95,12 +99,17 @@ template <class F, Rows2 ROWS> struct PairIO {
       e.e[1] = *(const __attribute__((address_space(1))) S*)(gptr<const char>(row) + o1);
       return __builtin_bit_cast(Raw, e);
     } else {
-      return *(const __attribute__((address_space(1))) Loose*)(gptr<const char>(row) + o0);
+      const auto at = (const __attribute__((address_space(1))) Loose*)(gptr<const char>(row) + o0);
+      if constexpr (ROWS == Rows2::PairsOnce) {
+        return __builtin_nontemporal_load(at);
+      } else {
+        return *at;
+      }
     }
   }
   static __device__ __forceinline__ void put(uintptr_t row, uint32_t o0, Raw r) {
     auto at = (__attribute__((address_space(1))) Loose*)(gptr<char>(row) + o0);
-    if constexpr (ROWS == Rows2::PairsPast) {
+    if constexpr (ROWS == Rows2::PairsPast || ROWS == Rows2::PairsOnce) {
       __builtin_nontemporal_store(r, at);
     } else {
       *at = r;
