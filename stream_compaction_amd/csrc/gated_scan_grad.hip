@@ -307,7 +307,7 @@ static hipError_t launch_grad_z(const GatedProblem& p, const GatedGrads& g, void
       if (p.channels % 2 != 0)
         gated_scan_grad_kernel<F, RATE, IG, Z, Rows2::Singles><<<grid, block, 0, stream>>>(p, g, words, partial, t);
       else if (past)
-        gated_scan_grad_kernel<F, RATE, IG, Z, Rows2::PairsPast><<<grid, block, 0, stream>>>(p, g, words, partial, t);
+        gated_scan_grad_kernel<F, RATE, IG, Z, Rows2::PairsOnce><<<grid, block, 0, stream>>>(p, g, words, partial, t);
       else
         gated_scan_grad_kernel<F, RATE, IG, Z, Rows2::Pairs><<<grid, block, 0, stream>>>(p, g, words, partial, t);
     });
