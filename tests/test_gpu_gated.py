@@ -222,6 +222,25 @@ def test_far_offsets():
     torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("opts", ["rate in init", "gate"])
+def test_past_the_caches(opts):
+    # 34 MB an output, loaded and stored past the caches: with states kept and without, against some channels alone
+    k, w, dy, dfinal = inputs((2, 2100, 4096, "bf16", [2100, 1300], opts), 105, grads=True)
+    y, state, starts = sc.gated_scan(keep_starts=True, **k)
+    y2, state2 = sc.gated_scan(**k)
+    k.pop("initial_state", None)
+    g = sc.gated_scan_grad(dy, starts=starts, dfinal=dfinal, **k)
+    for lo, hi in ((0, 20), (2040, 2060), (4076, 4096)):
+        want = ref.gated(**{n: v if n == "lengths" or v is None else v[..., lo:hi] for n, v in w.items()})
+        for what, got in (("y", y), ("y", y2), ("dx", g["dx"]), ("dforget", g["dforget"]),
+                          ("dinput_gate", g["dinput_gate"]), ("dz", g["dz"])):
+            if got is not None:
+                agree(got[..., lo:hi], want[what], "bf16", what)
+        for what, got in (("state", state), ("state", state2), ("drate", g["drate"]), ("dstate", g["dstate"])):
+            if got is not None:
+                agree(got[..., lo:hi], want[what], "f32", what)
+
+
 def test_far_outputs():
     # an output that passes 2^32 bytes; the sequence's end against the end alone
     l, d = 40001, 54001
