@@ -7,7 +7,7 @@
 //
 // 8192 tokens x 4096 channels, bfloat16, rate and input gate: 67 us, 268 MB at 4.0 TB/s
 // (the same loads and stores without arithmetic 49 us; vector units 60% busy); 4 x 4096 x
-// 4096 float16 with output gate, half of it padding: 72 us, 335 MB at 4.6 TB/s; 45 x 768:
+// 4096 float16 with output gate, half of it padding: 71 us, 335 MB at 4.7 TB/s; 45 x 768:
 // 7.5 us.  Runs of 16 tokens by 8 waves measured best: 8 tokens 85 us for the first, 4
 // waves 82, 16 waves 76.
 #include "gated_tile.hpp"
