@@ -5,11 +5,13 @@
 //   S[j, v] = score[j] + ((l[v] - m) - log(sum over u of exp(l[u] - m))),
 // l being the beam's logits and m their maximum; formed in 64 bits, as the scores
 // that compete lie closer together than float32's rounding of a sum over a
-// vocabulary.  The `count` greatest are chosen in a total order: score, then the
-// lower beam, the greater logit, the lower token.
+// vocabulary.  Every exponential is of a difference from a maximum, so that rows
+// which are one another plus a constant have equal scores, and a token that is
+// certain has its beam's own.  The `count` greatest are chosen in a total order:
+// score, then the lower beam, the greater logit, the lower token.
 //
 // Two launches.  The first reads each logit once: a workgroup keeps a segment of a
-// beam's row in registers, finds its maximum and its sum of exponentials, and its
+// beam's row in registers, finds its maximum, then its sum of exponentials and its
 // `count` greatest logits (within a beam the order by score is that by logit).  A
 // bound for these comes from the lanes' maxima: in a wave where `count` lanes hold
 // something as great as T, T bounds the choice from below, and what is not below it
@@ -44,23 +46,32 @@ __device__ __forceinline__ double key_value64(uint64_t k) {
   return __builtin_bit_cast(double, (k >> 63) ? k & 0x7fffffffffffffffull : ~k);
 }
 
-// exp(x) for -690 <= x <= 690, to 5e-11 of it.  x log2(e) is n + f with |f| <= 1/2: n
-// comes from the last digits of a sum with 1.5 x 2^52, f from the same product with n
-// taken off in one rounding; 2^f is a polynomial of degree 7 that is 1 at 0 (least
-// maximum of the relative error, fitted there), and n is added to its exponent.
+// exp(x) for -690 <= x <= 0: 1 at 0, and within (5e-16 + 2e-17 |x|) of itself (the second
+// by log2(e)'s own rounding).  x log2(e) is n + f with |f| <= 1/2: n comes from the last
+// digits of a sum with 1.5 x 2^52, f from the same product with n taken off in one
+// rounding; 2^f is a polynomial of degree 10 that is 1 at 0 (relative error 3e-16, fitted
+// there by exchange), and n is added to its exponent.
 __device__ __forceinline__ double exp_64(double x) {
   const double shift = 6755399441055744.0, log2e = 1.4426950408889634074;
   const double r = __builtin_fma(x, log2e, shift), f = __builtin_fma(x, log2e, shift - r);
-  double v = __builtin_fma(f, 1.5196156538658058e-05, 0.00015466756316955186);
-  v = __builtin_fma(f, v, 0.0013333935055508488);
-  v = __builtin_fma(f, v, 0.009618038132060329);
-  v = __builtin_fma(f, v, 0.05550410365991636);
-  v = __builtin_fma(f, v, 0.240226510665611);
-  v = __builtin_fma(f, v, 0.6931471807045305);
+  double v = __builtin_fma(f, 7.1117595466171784e-09, 1.0210506490815314e-07);
+  v = __builtin_fma(f, v, 1.3215235630301141e-06);
+  v = __builtin_fma(f, v, 1.5252647747511752e-05);
+  v = __builtin_fma(f, v, 0.0001540353080082534);
+  v = __builtin_fma(f, v, 0.001333355824648106);
+  v = __builtin_fma(f, v, 0.009618129107380713);
+  v = __builtin_fma(f, v, 0.05550410866434658);
+  v = __builtin_fma(f, v, 0.24022650695910472);
+  v = __builtin_fma(f, v, 0.6931471805599516);
   v = __builtin_fma(f, v, 1.0);
   u32x2 b = __builtin_bit_cast(u32x2, v);
   b.y += __builtin_bit_cast(u32x2, r).x << 20;
   return __builtin_bit_cast(double, b);
+}
+// exp(x - most) for x <= most; 1e-300, which adds nothing, for what is masked (-infinity
+// or NaN) or much smaller.
+__device__ __forceinline__ double exp_below(double x, double most) {
+  return exp_64(__builtin_fmax(x - most, -690.0));
 }
 
 // All lanes' sum and maximum, in every lane.
@@ -124,14 +135,12 @@ __device__ __forceinline__ uint32_t joint_bound(const Bounds* waves) {
   return alone > together ? alone : together;
 }
 
-// Of a segment: its greatest logit, and its sum of exp(l - from).
+// Of a segment: its greatest logit, and its sum of exp(l - most); of +infinity, how many
+// logits are that.
 struct Found {
-  float most, from;
+  float most;
   double sum;
 };
-// Logits up to here in size need no maximum taken off before the exponential: in 64
-// bits their exponentials and sums stay inside the range, 260 digits from its ends.
-constexpr float kPlainLogit = 600.0f;
 
 struct SegmentShared {
   uint64_t by_wave[kBeamWaves][kListed / kBeamWaves], list[kListed];
@@ -160,9 +169,11 @@ __device__ __forceinline__ uint32_t group_sum(uint32_t v, SegmentShared& s, int 
 // A segment: `length` vectors of 16 bytes, at most 256 NV.  Entries are (order_key << 32
 // | ~token), so that the greater entry comes first; 0 is none.
 //
-// 32 x 8 rows of 50000 bfloat16 logits, count 16: 17 us, of which some 4 the 64-bit
-// exponentials (15 instructions a logit) and 5 the choice; the vector units are 70%
-// busy.  128 x 4 rows in float32, a fifth of them finished: 25 us, 3.3 TB/s.
+// 32 x 8 rows of 50000 bfloat16 logits, count 16: 19.4 us, of which some 6 the 64-bit
+// exponentials (19 instructions a logit) and 5 the choice; 128 x 4 rows in float32, a fifth
+// of them finished: 28.4 us, 2.9 TB/s.  (Exponentials of the logits as they are, with 4
+// instructions fewer, took 17.2 and 25: a row plus a constant then had another sum.
+// Relative to a wave's maximum, before the barrier, 19.8 and 28.8.)
 template <class F, int NV>
 __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem p, uint64_t* best,
                                                                    Found* found, int64_t row0,
@@ -210,9 +221,7 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
     raw[i] = u32x4{w[0], w[1], w[2], w[3]};
     IO::unpack(raw[i], v);
   };
-  // maximum and sum of exponentials at once, for logits of ordinary size
   float most = -__builtin_huge_valf();
-  double sum = 0.0;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     float v[E];
@@ -225,14 +234,8 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
     }
     values(i, v);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      most = __builtin_elementwise_maximum(most, v[e]);
-      // (exp(-690) adds nothing, and stands for masked logits; in 64 bits a NaN is quiet,
-      // and the maximum one instruction)
-      sum += exp_64(__builtin_fmax((double)v[e], -690.0));
-    }
+    for (int e = 0; e < E; ++e) most = __builtin_elementwise_maximum(most, v[e]);
     // vector after vector: each when it is there, with the registers of one
-    materialize(sum);
     __builtin_amdgcn_sched_barrier(0);
   }
   // (that maximum is NaN wherever an operand is; one that passes NaNs over would need the
@@ -262,7 +265,7 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
   uint64_t* out = best + (row * segments + seg) * count;
   if (top == -__builtin_huge_valf()) {                           // all masked
     if (tid < count) out[tid] = 0;
-    if (tid == 0) found[row * segments + seg] = Found{top, top, 0.0};
+    if (tid == 0) found[row * segments + seg] = Found{top, 0.0};
     return;
   }
   // what is above the bound, then what is equal to it
@@ -279,42 +282,39 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
     return ((uint64_t)order_key(__builtin_bit_cast(float, (uint32_t)(held >> 32))) << 32) | (uint32_t)~token;
   };
   float edge = key_value(least);
-  // each wave lists what is above the edge for itself: how many there were
-  auto above = [&]() {
-    uint32_t n = 0;
+  // each wave lists what is above the edge for itself; n: how many there were
+  auto above = [&](int i, const float (&v)[E], uint32_t& n) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float v[E];
-      values(i, v);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const uint64_t on = __ballot(v[e] > edge);
-        if (on == 0) continue;
-        const uint32_t k = n + (uint32_t)__builtin_popcountll(on & ((1ull << lane_id()) - 1));
-        if (v[e] > edge && k < (uint32_t)(kListed / kBeamWaves)) sh.by_wave[wave][k] = hold(i * E + e, v[e]);
-        n += (uint32_t)__builtin_popcountll(on);
-      }
+    for (int e = 0; e < E; ++e) {
+      const uint64_t on = __ballot(v[e] > edge);
+      if (on == 0) continue;
+      const uint32_t k = n + (uint32_t)__builtin_popcountll(on & ((1ull << lane_id()) - 1));
+      if (v[e] > edge && k < (uint32_t)(kListed / kBeamWaves)) sh.by_wave[wave][k] = hold(i * E + e, v[e]);
+      n += (uint32_t)__builtin_popcountll(on);
     }
-    return n;
   };
-  uint32_t listed = wmost > edge ? above() : 0;
-  float from = 0.0f;
-  if (!(__builtin_fabsf(top) <= kPlainLogit)) {
-    const bool infinite = top == __builtin_huge_valf();
-    from = top;
+  // the exponentials and the list, in one walk
+  const bool some = wmost > edge;
+  uint32_t listed = 0;
+  double sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float v[E];
+    values(i, v);
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum += exp_below((double)v[e], (double)top);
+    materialize(sum);
+    __builtin_amdgcn_sched_barrier(0);
+    if (some) above(i, v, listed);
+  }
+  if (top == __builtin_huge_valf()) {
     sum = 0.0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float v[E];
       values(i, v);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        // (beside an infinite logit: exp(0) for each such, nothing for others)
-        const double d = infinite ? (v[e] == top ? 0.0 : -690.0) : (double)v[e] - (double)top;
-        sum += exp_64(__builtin_fmax(d, -690.0));
-      }
-      materialize(sum);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int e = 0; e < E; ++e) sum += v[e] == top ? 1.0 : 0.0;
     }
   }
   sum = wave_sum(sum);
@@ -327,7 +327,7 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
     double all = sh.sum[0];
 #pragma unroll
     for (int w = 1; w < kBeamWaves; ++w) all += sh.sum[w];
-    found[row * segments + seg] = Found{top, from, all};
+    found[row * segments + seg] = Found{top, all};
   }
   bool over = false;
 #pragma unroll
@@ -350,7 +350,13 @@ __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem 
       if (group_sum(k, sh, wave) >= (uint32_t)count) t = c;
     }
     edge = key_value(t > kMaskedKey ? t : kMaskedKey + 1);
-    listed = above();                        // fewer than `count`
+    listed = 0;                              // fewer than `count`
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float v[E];
+      values(i, v);
+      above(i, v, listed);
+    }
     __syncthreads();
     if (lane_id() == 0) sh.listed[wave] = listed;
     __syncthreads();
@@ -437,7 +443,7 @@ __device__ __forceinline__ bool operator>(const Candidate& a, const Candidate& b
 struct JoinShared {
   Candidate list[kJoined];
   uint32_t rank[kJoined];
-  double lse[64];                            // log of the sum of exponentials of the logits
+  double lse[64];                            // log of the sum of exp(logit - most)
   float most[64], score[64];
   bool done[64];
   uint32_t bound[kJoinWaves];
@@ -474,24 +480,18 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(BeamProblem p, 
     const Found own = f[lane_id() < segments ? lane_id() : 0];
     const float score = p.scores[row0 + j];
     const bool done = p.finished != nullptr && p.finished[row0 + j] != 0;
-    float most = own.most, from = own.from;
-    for (int64_t s = lane_id() + 64; s < segments; s += 64) {
-      most = __builtin_fmaxf(most, f[s].most);
-      from = __builtin_fmaxf(from, f[s].from);
-    }
+    float most = own.most;
+    for (int64_t s = lane_id() + 64; s < segments; s += 64) most = __builtin_fmaxf(most, f[s].most);
     most = wave_max(most);
-    from = wave_max(from);
-    // (beside an infinite logit the sum is the number of such)
     auto part = [&](const Found& v) {
-      if (v.from == from) return v.sum;
-      return v.from > -__builtin_huge_valf() ? v.sum * exp((double)v.from - (double)from) : 0.0;
+      return v.most == most ? v.sum : v.sum * exp_below((double)v.most, (double)most);
     };
     double sum = lane_id() < segments ? part(own) : 0.0;
     for (int64_t s = lane_id() + 64; s < segments; s += 64) sum += part(f[s]);
     sum = wave_sum(sum);
     if (lane_id() == 0) {
       sh.most[j] = most;
-      sh.lse[j] = log(sum) + (most == __builtin_huge_valf() ? 0.0 : (double)from);
+      sh.lse[j] = log(sum);
       sh.score[j] = score;
       sh.done[j] = done;
     }
@@ -511,7 +511,8 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(BeamProblem p, 
     } else {
       if (entry == 0) return c;
       const float l = key_value((uint32_t)(entry >> 32)), m = sh.most[j];
-      s = base + ((m < __builtin_huge_valf() ? (double)l : (l == m ? 0.0 : -__builtin_huge_val())) - sh.lse[j]);
+      // (beside an infinite logit only such have a chance)
+      s = base + ((l == m ? 0.0 : (double)l - (double)m) - sh.lse[j]);
     }
     if (s > -__builtin_huge_val()) c.score = order_key64(s);      // (no NaN)
     return c;
