@@ -269,23 +269,25 @@ void gated_scan_grad_kernel(GatedProblem p, GatedGrads g, uint64_t* scratch, flo
   }
 }
 
-// drate from the tiles' sums: 64 channels a workgroup, 16 strands of tiles each (4.7 us
-// for 128 tiles of 2048 channels; latency).
+// drate from the tiles' sums: 64 channels a workgroup, 16 strands of tiles each, added up in
+// 64 bits: a strand has thousands of rows where sequences are many, and in 32 bits equal
+// terms drift by as many roundings of the sum.  (4.7 us for 128 tiles of 2048 channels;
+// latency.)
 __global__ __launch_bounds__(1024) void gated_rate_kernel(const float* partial, const float* rate,
                                                           float* drate, int64_t rows, int64_t channels) {
-  __shared__ float strand[16][64];
+  __shared__ double strand[16][64];
   const int64_t c = (int64_t)blockIdx.x * 64 + lane_id();
-  float sum = 0.0f;
+  double sum = 0.0;
   if (c < channels) {
 #pragma unroll 8
-    for (int64_t i = threadIdx.x / 64; i < rows; i += 16) sum += partial[i * channels + c];
+    for (int64_t i = threadIdx.x / 64; i < rows; i += 16) sum += (double)partial[i * channels + c];
   }
   strand[threadIdx.x / 64][lane_id()] = sum;
   __syncthreads();
   if (threadIdx.x >= 64 || c >= channels) return;
   for (int i = 1; i < 16; ++i) sum += strand[i][lane_id()];
   const float r = rate[c];
-  drate[c] = r <= 0.0f ? 0.0f : sum / r;
+  drate[c] = r <= 0.0f ? 0.0f : (float)(sum / (double)r);
 }
 
 size_t gated_scan_grad_scratch(const GatedProblem& p) {
