@@ -566,7 +566,7 @@ scan_status beam_select(const beam_select_args* args, float* out_scores, int32_t
  *                        nothing of this call.
  *   parents              int32 [batch, beams] on the device
  *   1 <= beams <= 64 (else SCAN_ENOTSUP), 0 <= tensors <= 1024, 0 <= batch <=
- *   INT32_MAX, no array of 2^47 bytes or more.
+ *   INT32_MAX, no row of 2^43 bytes or more, no array of 2^47.
  */
 scan_status beam_reorder(const void* const* states, void* const* new_states,
                          const int64_t* row_bytes, int64_t tensors, const int32_t* parents,

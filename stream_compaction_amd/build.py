@@ -23,12 +23,14 @@ COPY_LIB_PATH = os.path.join(HERE, "libscan_copy.so")
 COPY_SOURCES = ["copy_ceiling.hip"]
 # test-only build of the scan library whose look-back never waits: any
 # predecessor descriptor not yet published is recomputed from the input at
-# once, so the tests exercise that recovery path on every call; and whose gated
-# scan asks for a state once and then takes it as lost
+# once, so the tests exercise that recovery path on every call; whose gated
+# scan asks for a state once and then takes it as lost; and whose launches of
+# beam_reorder hold three workgroups, so that rows go out in several
 FALLBACK_LIB_PATH = os.path.join(HERE, "libscan_amd_lbtest.so")
-FALLBACK_DEFINES = ["-DSCA_LOOKBACK_TIMEOUT_TICKS=0ull", "-DSCA_TILE_POLLS=0u"]
-# the sources that wait so; the others' objects are the library's own
-FALLBACK_SOURCES = ("scan_device.hip", "select.hip", "reduce_by_key.hip", "gated_scan.hip", "gated_scan_grad.hip")
+FALLBACK_DEFINES = ["-DSCA_LOOKBACK_TIMEOUT_TICKS=0ull", "-DSCA_TILE_POLLS=0u", "-DSCA_REORDER_BLOCKS=3"]
+# the sources that these are of; the others' objects are the library's own
+FALLBACK_SOURCES = ("scan_device.hip", "select.hip", "reduce_by_key.hip", "gated_scan.hip", "gated_scan_grad.hip",
+                    "beam.hip")
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -14,6 +14,7 @@ namespace {
 using namespace sca::api;
 
 constexpr int64_t kMostBeams = 64, kMostCount = 64, kMostTensors = 1024;
+constexpr int64_t kMostRowBytes = 1ll << 43;   // its columns' workgroups are counted in 32 bits
 
 scan_status beam_problem(const beam_select_args* a, sca::BeamProblem* p, sca::Fmt* fmt, size_t* eb) {
   if (a == nullptr) return SCAN_EINVAL;
@@ -89,7 +90,7 @@ scan_status beam_reorder(const void* const* states, void* const* new_states,
   int n = 0;
   spans[n++] = Span{(uintptr_t)parents, (uintptr_t)parents + 4 * rows, false};
   for (int64_t i = 0; i < tensors; ++i) {
-    if (row_bytes[i] < 0) return SCAN_EINVAL;
+    if (row_bytes[i] < 0 || row_bytes[i] >= kMostRowBytes) return SCAN_EINVAL;
     const unsigned __int128 bytes = (unsigned __int128)row_bytes[i] * rows;
     if (bytes >= kMaxBytes) return SCAN_EINVAL;
     if (bytes == 0) continue;

@@ -715,6 +715,9 @@ hipError_t launch_beam_select(const BeamProblem& p, Fmt fmt, float* scores, int3
 namespace {
 
 constexpr int kMoved = 64;                   // tensors a launch
+#ifndef SCA_REORDER_BLOCKS
+#define SCA_REORDER_BLOCKS (1ll << 23)
+#endif
 struct Moves {
   uintptr_t from[kMoved], to[kMoved];
   int64_t bytes[kMoved];                     // of a row
@@ -755,10 +758,12 @@ __device__ __forceinline__ void move_column(uintptr_t from, uintptr_t to, int64_
 
 template <int NB, class V, bool PAST>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4, 8)))
-void beam_reorder_kernel(Moves m, const int32_t* parents, int64_t b0, int beams) {
-  const int64_t blocks = m.first[m.count];
+void beam_reorder_kernel(Moves m, const int32_t* parents, int64_t b0, uint32_t first, uint32_t blocks,
+                         int beams) {
+  // blocks: of a batch entry in this launch, from the first one on
   int64_t block;
   const int64_t b = b0 + divide((int64_t)blockIdx.x, blocks, &block);
+  block += first;
   int t = 0;
   while (t + 1 < m.count && (uint32_t)block >= m.first[t + 1]) ++t;
   const bool in_place = m.from[t] == m.to[t];
@@ -793,7 +798,9 @@ template <int NB, class V>
 static hipError_t launch_moves(const void* const* states, void* const* new_states, const int64_t* row_bytes,
                                int64_t tensors, const int32_t* parents, int64_t batch, int64_t beams,
                                hipStream_t stream) {
-  constexpr int64_t kMostBlocks = 1ll << 23;
+  // Workgroups of a launch: 2^31 threads, where an axis ends at 2^32.  A longer row (32 GB)
+  // goes out in several launches: no column reads what another writes, in place either.
+  constexpr int64_t kMostBlocks = SCA_REORDER_BLOCKS;
   int64_t all = 0;
   for (int64_t t = 0; t < tensors; ++t) all += batch * beams * row_bytes[t];
   const bool past = states_past_caches(all);
@@ -816,11 +823,16 @@ static hipError_t launch_moves(const void* const* states, void* const* new_state
     const int64_t step = blocks >= kMostBlocks ? 1 : kMostBlocks / blocks;
     for (int64_t b = 0; b < batch; b += step) {
       const int64_t n = batch - b < step ? batch - b : step;
-      const dim3 grid((unsigned)(n * blocks));
-      if (past)
-        beam_reorder_kernel<NB, V, true><<<grid, dim3(256), 0, stream>>>(m, parents, b, (int)beams);
-      else
-        beam_reorder_kernel<NB, V, false><<<grid, dim3(256), 0, stream>>>(m, parents, b, (int)beams);
+      for (int64_t first = 0; first < blocks; first += kMostBlocks) {
+        const int64_t part = blocks - first < kMostBlocks ? blocks - first : kMostBlocks;
+        const dim3 grid((unsigned)(n * part));
+        if (past)
+          beam_reorder_kernel<NB, V, true><<<grid, dim3(256), 0, stream>>>(m, parents, b, (uint32_t)first,
+                                                                           (uint32_t)part, (int)beams);
+        else
+          beam_reorder_kernel<NB, V, false><<<grid, dim3(256), 0, stream>>>(m, parents, b, (uint32_t)first,
+                                                                            (uint32_t)part, (int)beams);
+      }
     }
   }
   return hipGetLastError();
