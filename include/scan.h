@@ -287,7 +287,8 @@ scan_status select_compact_devn(const void* in, const uint8_t* flags, void* out,
  *    inputs may have any non-negative batch and token strides (in elements; 0
  *    repeats), the arrays a call writes are contiguous.  Parameters and states
  *    of the scans are contiguous float32.  All arithmetic and every sum is
- *    float32; each output is rounded once, to nearest even.
+ *    float32 (float64 where a sum over the batch says so); each output is
+ *    rounded once, to nearest even.
  *  - Inputs may overlap one another; outputs and scratch overlap nothing
  *    (SCAN_EALIAS), but a step may update its state in place.
  *  - lengths: NULL, or device pointer to `batch` int32, read by the kernels and
@@ -457,7 +458,10 @@ typedef struct {
  * not written).  starts (NULL: not written): what the gradient needs,
  * gated_scan_starts_bytes(args) bytes, the states before each block of 64 tokens.
  * Scratch carries the state between workgroups that share a sequence (0 bytes for
- * short ones: then scratch may be NULL). */
+ * short ones: then scratch may be NULL); calls in flight at the same time share none.
+ * A workgroup waits for a state that another one is about to write.  Every wait ends: a
+ * state that has not come after some seconds (calls have shared scratch) stands for no
+ * number, and so do the outputs that depend on it, of the gradient likewise. */
 size_t gated_scan_starts_bytes(const gated_scan_args* args);
 size_t gated_scan_scratch_bytes(const gated_scan_args* args);
 scan_status gated_scan(const gated_scan_args* args, void* y, float* final_state, float* starts,
@@ -467,8 +471,8 @@ scan_status gated_scan(const gated_scan_args* args, void* y, float* final_state,
  * (strides {batch, token}) and dfinal (of final_state's shape; NULL: zeros).
  * dx, dforget, dinput_gate and dz: [batch, length, channels] of dtype, the last
  * two required exactly when their input is given; drate: float32 [channels],
- * likewise (0 for a rate of 0 and below, where w has no derivative); dinitial:
- * float32 [batch, channels], not written when NULL. */
+ * likewise (0 for a rate of 0 and below, where w has no derivative), summed over
+ * sequences in float64; dinitial: float32 [batch, channels], not written when NULL. */
 typedef struct {
     const void* dy;
     int64_t dy_stride[2];

@@ -24,10 +24,12 @@ COPY_SOURCES = ["copy_ceiling.hip"]
 # test-only build of the scan library whose look-back never waits: any
 # predecessor descriptor not yet published is recomputed from the input at
 # once, so the tests exercise that recovery path on every call; whose gated
-# scan asks for a state once and then takes it as lost; and whose launches of
-# beam_reorder hold three workgroups, so that rows go out in several
+# scan asks for a state once and then takes it as lost, and does not write some;
+# and whose launches of beam_reorder hold three workgroups, so that rows go out
+# in several
 FALLBACK_LIB_PATH = os.path.join(HERE, "libscan_amd_lbtest.so")
-FALLBACK_DEFINES = ["-DSCA_LOOKBACK_TIMEOUT_TICKS=0ull", "-DSCA_TILE_POLLS=0u", "-DSCA_REORDER_BLOCKS=3"]
+FALLBACK_DEFINES = ["-DSCA_LOOKBACK_TIMEOUT_TICKS=0ull", "-DSCA_TILE_POLLS=0u", "-DSCA_TILE_MUTE",
+                    "-DSCA_REORDER_BLOCKS=3"]
 # the sources that these are of; the others' objects are the library's own
 FALLBACK_SOURCES = ("scan_device.hip", "select.hip", "reduce_by_key.hip", "gated_scan.hip", "gated_scan_grad.hip",
                     "beam.hip")

@@ -193,6 +193,22 @@ __device__ __forceinline__ uint64_t state_word(float h) { return __builtin_bit_c
 #define SCA_TILE_POLLS (1u << 22)
 #endif
 constexpr uint64_t kLostWord = 0x7fc000007fc00000ull;
+// Whether a column's word is written: the library's always; of a test build, not the map of
+// step 3 in every second column, nor the state at the first border in the others.
+__device__ __forceinline__ bool map_comes(int64_t col, int64_t step) {
+#ifdef SCA_TILE_MUTE
+  return col % 2 != 0 || step != 3;
+#else
+  return true;
+#endif
+}
+__device__ __forceinline__ bool border_comes(int64_t col, int64_t group) {
+#ifdef SCA_TILE_MUTE
+  return col % 2 == 0 || group != 1;
+#else
+  return true;
+#endif
+}
 struct Words { uint64_t w[2]; };
 __device__ __forceinline__ Words peek_words(const uint64_t* at) {
   return Words{{ld_relaxed(at), ld_relaxed(at + 1)}};
@@ -283,7 +299,7 @@ __device__ __forceinline__ void tile_entry(TileMaps& s, int wave, int64_t step, 
   if (on1) w1 = peek_words(slot(begin + i0 + 1));
   const bool passes = wave == kTileWaves - 1 && group > 0;
   if (passes) wb = peek_words(border(group));
-  if (wave == 0 && step + 1 < steps) {       // this tile's own map
+  if (wave == 0 && step + 1 < steps && map_comes(col, step)) {   // this tile's own map
     float l[2] = {0.0f, 0.0f}, b[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int w = 0; w < kTileWaves; ++w) {
@@ -341,7 +357,7 @@ __device__ __forceinline__ void tile_entry(TileMaps& s, int wave, int64_t step, 
     for (int c = 0; c < 2; ++c) h[c] = carry_over(m[c], b[c], h[c]);
   }
   // the group's last tile passes the state on
-  if (wave == kTileWaves - 1 && before == kTileGroup - 1 && step + 1 < steps) {
+  if (wave == kTileWaves - 1 && before == kTileGroup - 1 && step + 1 < steps && border_comes(col, group + 1)) {
     float v[2] = {h[0], h[1]};
 #pragma unroll
     for (int w = 0; w < kTileWaves; ++w) {
