@@ -11,8 +11,9 @@
 
 namespace sca {
 
-// sigmoid(v) and sigmoid(-v), each to a few units in its last place: 1 minus a
-// rounded sigmoid would lose the digits of the smaller one.
+// sigmoid(v) and sigmoid(-v).  The greater one is within a few units of its last place,
+// the smaller within (|v| + 8) 2^-24 of itself, as the exponent's product is rounded; 1
+// minus a rounded sigmoid would lose its digits altogether.
 struct Sides { float up, down; };
 __device__ __forceinline__ Sides sides(float v) {
   const float e = exp2_hw(-__builtin_fabsf(v) * kLog2e);   // in (0, 1]
@@ -21,8 +22,8 @@ __device__ __forceinline__ Sides sides(float v) {
 }
 
 // 1 - 4^l for l <= 0, 4^l = q being known.  Above -0.36 (q above 0.6), where the
-// difference loses digits, a polynomial that is within 9e-8 of it (least maximum of the
-// relative error of its quotient by l, fitted there).
+// difference loses digits, a polynomial (least maximum of the relative error of its quotient
+// by l, 9e-8, fitted there) that in float32 is within 2e-7 of it.
 __device__ __forceinline__ float one_minus_4(float l, float q) {
   float s = __builtin_fmaf(l, -0.0346682966f, -0.151432544f);
   s = __builtin_fmaf(l, s, -0.443717122f);

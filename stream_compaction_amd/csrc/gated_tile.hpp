@@ -164,8 +164,8 @@ template <class F, Rows2 ROWS> struct PairIO {
 
 // sqrt(2^l) of a run's decay, by which a state is multiplied twice: 2^l itself may
 // leave float32's range where its product with a large state does not.  What is
-// below 2^-252 leaves nothing of any finite state, and an infinite one stays so; l
-// = -inf (a decay of 0) gives 0.
+// below 2^-252 counts as that, which leaves less than 2^-124 of any finite state, and an
+// infinite one stays so; l = -inf (a decay of 0) gives 0.
 __device__ __forceinline__ float half_decay(float l) {
   const float m = at_least(exp2_hw(0.5f * l), 1.17549435e-38f);
   return l == -__builtin_huge_valf() ? 0.0f : m;
