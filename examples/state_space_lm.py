@@ -191,6 +191,8 @@ def search(model, prompt, count, beams):
     cache = [(w.repeat_interleave(beams, 0), s.repeat_interleave(beams, 0)) for w, s in cache]
     text = torch.zeros((b, beams, count), dtype=torch.int32, device="cuda")
     text[..., 0] = tokens
+    if count == 1:
+        return text, scores
     at = torch.ones(1, dtype=torch.int64, device="cuda")
 
     def step(cache, text, at, scores, tokens):
