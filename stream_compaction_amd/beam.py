@@ -87,8 +87,12 @@ def beam_reorder(states, parents, new_states=None, stream=None):
             raise ValueError("states must be [batch, beams, ...] or [batch * beams, ...]")
     from_ = to = _pointers(states, "states", dev)
     if new_states is not None:
-        if [t.shape for t in out] != shapes or [t.dtype for t in out] != [t.dtype for t in states]:
+        types = [t.dtype for t in states]
+        if [t.shape for t in out] != shapes or [t.dtype for t in out] != types:
             raise ValueError("new_states must have the shapes and types of states")
+        # (what is moved is memory, which holds the conjugate of a lazily conjugated view's values)
+        if any(ty.is_complex for ty in set(types)) and [t.is_conj() for t in out] != [t.is_conj() for t in states]:
+            raise ValueError("new_states must be conjugated views exactly where states are")
         to = _pointers(out, "new_states", dev)
     sizes = array("q", [t.nbytes // rows for t in states] if rows else [0] * n)
     check(lib().beam_reorder(from_.buffer_info()[0], to.buffer_info()[0], sizes.buffer_info()[0], n, pp, b, k,
