@@ -42,7 +42,12 @@ def beam_select(logits, scores, count, finished=None, end_token=0, out_scores=No
         if finished.dtype is torch.bool:
             finished = finished.view(torch.uint8)
         fp = _like(finished, "finished", (b, k), torch.uint8, dev)
-    a = BeamArgs(logits.data_ptr(), sp, fp, b, k, v, count, int(end_token), stride[0], stride[1], code)
+        end_token = int(end_token)
+        # (here, as a number beyond 64 bits would reach the library as another)
+        _require(0 <= end_token < v, "end_token must be in the vocabulary")
+    else:
+        end_token = 0
+    a = BeamArgs(logits.data_ptr(), sp, fp, b, k, v, count, end_token, stride[0], stride[1], code)
     chosen = (b, count)
     out_scores = _out(out_scores, "out_scores", chosen, torch.float32, scores, stream)
     parents = _out(parents, "parents", chosen, torch.int32, out_scores, stream)

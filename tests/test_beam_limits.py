@@ -39,3 +39,28 @@ def test_conjugated_views(monkeypatch):
     beam.beam_reorder([view], p)                         # in place it stays what it is
     beam.beam_reorder([plain], p, [other])
     assert len(reached) == 2
+
+
+def test_end_tokens(monkeypatch):
+    reached = []
+
+    class Library:
+        def beam_select(self, args, *more):
+            reached.append(args.end_token)
+            return 0
+
+        def beam_select_scratch_bytes(self, args):
+            return 64
+    monkeypatch.setattr(beam, "lib", Library)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 0)
+    x, s, done = OnGpu(2, 3, 50), OnGpu(2, 3), OnGpu(2, 3, dtype=torch.uint8)
+    more = {"out_scores": OnGpu(2, 4), "parents": OnGpu(2, 4, dtype=torch.int32), "tokens": OnGpu(2, 4, dtype=torch.int32),
+            "scratch": OnGpu(64, dtype=torch.uint8)}
+    for wrong in (-1, 50, 1 << 64, (1 << 64) + 7, -(1 << 64) + 7):
+        with pytest.raises(ValueError, match="end_token"):
+            beam.beam_select(x, s, 4, finished=done, end_token=wrong, **more)
+        beam.beam_select(x, s, 4, end_token=wrong, **more)   # not used without ended beams
+    assert reached == [0] * 5
+    beam.beam_select(x, s, 4, finished=done, end_token=49, **more)
+    assert reached[-1] == 49
