@@ -169,11 +169,11 @@ __device__ __forceinline__ uint32_t group_sum(uint32_t v, SegmentShared& s, int 
 // A segment: `length` vectors of 16 bytes, at most 256 NV.  Entries are (order_key << 32
 // | ~token), so that the greater entry comes first; 0 is none.
 //
-// 32 x 8 rows of 50000 bfloat16 logits, count 16: 19.4 us, of which some 6 the 64-bit
-// exponentials (19 instructions a logit) and 5 the choice; 128 x 4 rows in float32, a fifth
-// of them finished: 28.4 us, 2.9 TB/s.  (Exponentials of the logits as they are, with 4
-// instructions fewer, took 17.2 and 25: a row plus a constant then had another sum.
-// Relative to a wave's maximum, before the barrier, 19.8 and 28.8.)
+// 32 x 8 rows of 50000 bfloat16 logits, count 16: 20 us, of which some 7 the 64-bit
+// exponentials (19 instructions a logit) and 4 the choice; the vector units are 69% busy.
+// 128 x 4 rows in float32, a fifth of them finished: 28.5 us, 2.9 TB/s.  (Exponentials of the
+// logits as they are, with 4 instructions fewer, took 17.2 and 25, but a row plus a constant
+// had another sum.  Relative to a wave's maximum, before the barrier, 19.8 and 28.8.)
 template <class F, int NV>
 __global__ __launch_bounds__(kBeamThreads) void beam_segment_kernel(BeamProblem p, uint64_t* best,
                                                                    Found* found, int64_t row0,
@@ -453,7 +453,7 @@ struct JoinShared {
 
 }  // namespace
 
-// A workgroup a batch entry: 5 us for one of 4 beams and 12 segments, 6.4 for 32 of 8
+// A workgroup a batch entry: 5 us for one of 4 beams and 12 segments, 6.5 for 32 of 8
 // beams and 5 segments; latency, as three steps read what the one before found.
 __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(BeamProblem p, const uint64_t* best,
                                                                  const Found* found, float* scores,

@@ -26,7 +26,8 @@ constexpr int kGradTile = kGradTokens * kTileWaves;         // of a workgroup
 static_assert(kGradTile == kGatedKeepTokens, "a tile starts from a kept state");
 
 // Waves a SIMD: float32's inputs take twice the registers, and with two workgroups a
-// CU some of them would go to memory.
+// CU some of them would go to memory (4 x 2048 x 2304, rate and input gate: 110 us, in four
+// waves 136; 4 x 2048 x 2048, output gate: 95 and 100).
 template <class F, bool RATE, bool IG, bool Z>
 constexpr int kGradWaves = sizeof(typename F::S) == 4 && (RATE || IG || Z) ? 2 : 4;
 

@@ -77,7 +77,9 @@ struct Rows {
 };
 
 // Two neighbouring channels of a row as one access, or, where the number of
-// channels is odd, as one access each (a pair may then lie across a row's end).
+// channels is odd, as one access each (a pair may then lie across a row's end).  An odd
+// width costs as much again: 8 x 2048 bfloat16 tokens of 2303 channels 131 us and in the
+// gradient 236, of 2304 65 and 129; 4 x 2048 in float32 87 and 177, 58 and 110.
 // Pairs are stored past the caches where the outputs are large (past_caches):
 // forward and gradient of 4 x 2048 x 2048 bf16, 34 MB an output, 108 to 102 us.  Once:
 // loaded so, too, by the gradient and by a forward that keeps no states for one (after
@@ -242,8 +244,9 @@ __device__ __forceinline__ int64_t draw_chunk(uint64_t* scratch, int64_t col, ui
 struct Place { int part; int64_t col, b, run; };
 // Workgroups go to the 8 XCDs in turn; with `near` one XCD takes four neighbouring parts of
 // 32, 1 KB of a 16-bit row, where the parts are a multiple of 32.  (The forward of 4 x 4096 x
-// 4096 77.0 to 74.6 us, 8192 x 8192 114.6 to 111.6, 4 x 2048 x 8192 with both gates 144 to
-// 145.5; two of 16 parts gained nothing at 2048 channels, nor did the gradient.)
+// 4096 77.0 to 74.6 us, 8192 x 8192 114.6 to 111.6; in float32 8192 x 8192 143 to 140, 2 x 4096 x
+// 4096 and 4 x 4096 x 4096 the same; with both gates 4 x 2048 x 8192 lost, 148 to 151.  Two of
+// 16 parts gained nothing at 2048 channels, nor did the gradient.)
 template <bool near>
 __device__ __forceinline__ Place draw_place(const Tiles& t, uint64_t* scratch, uint64_t* shared) {
   Place p;
