@@ -527,8 +527,10 @@ scan_status embedding_grad(const void* dout, const void* ids, void* dweight, int
  * The `count` best continuations of each batch entry, over its beams and the
  * vocabulary.  A continuation of beam j by token v has the score
  *   S[j,v] = scores[b,j] + log softmax(logits[b,j,:])[v],
- * formed in 64 bits.  Chosen are the greatest: of equal scores the lower beam
- * first, in a beam the greater logit, then the lower token.
+ * formed in 64 bits from differences to the row's greatest logit, so that rows
+ * which are one another plus a constant have equal scores, and a token that is
+ * certain has its beam's own.  Chosen are the greatest: of equal scores the lower
+ * beam first, in a beam the greater logit, then the lower token.
  *   logits        [batch, beams, vocab] of `dtype` (SCAN_F32, SCAN_F16 or
  *                 SCAN_BF16, else SCAN_ENOTSUP), contiguous along the vocabulary;
  *                 logits_stride = {batch, beam} strides in elements
